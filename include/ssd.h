@@ -17,8 +17,14 @@
  *   ssd_chunk_scan_backward
  *                   the gradients of ssd_chunk_scan with respect to all of
  *                   its inputs (the backward pass of a training step).
+ *   ssd_add_norm, ssd_gated_norm (and their gradients), ssd_quantize_q8,
+ *   ssd_linear_q8, ssd_conv1d_backward
+ *                   what stands between two scans of a Mamba-2 stack: the
+ *                   residual add with the norm before a block, the gated norm
+ *                   after its scan, the block's projections in 8-bit
+ *                   integers, and the gradients of its convolution.
  *
- * Both compute, for every batch row b and head h (g = h / (H/G) is the B/C
+ * The scan and the step compute, for every batch row b and head h (g = h / (H/G) is the B/C
  * group of head h), the selective diagonal SSM
  *
  *   d_t      = clip(softplus(dt[b,t,h] + dt_bias[h]), dt_min, dt_max)
@@ -372,6 +378,192 @@ ssd_status ssd_conv1d(const ssd_conv_desc* desc, const void* x, const float* w,
  */
 ssd_status ssd_conv1d_step(const ssd_conv_desc* desc, void* state, const void* x_t,
                            const float* w, const float* bias, void* y_t, hipStream_t stream);
+
+/*
+ * Gradients of ssd_conv1d (same descriptor, x, w, bias and state_in) for the
+ * loss sum(dy * y) + sum(dstate_out * state_out): with z the convolution
+ * (recomputed here) and xp the window followed by x, as above,
+ *
+ *   dz[t]      = dy[t] * (silu ? s (1 + z (1 - s)), s = logistic(z[t]) : 1)
+ *   dxp[u]     = sum_i w[i] dz[u - i]  (+ dstate_out[j] at u = T + j)
+ *   dx[t]      = dxp[t + k - 1];  dstate[j] = dxp[j], j < k-1
+ *   dw[c][i]   = sum_{b,t} dz[t] xp[t + i];  dbias[c] = sum_{b,t} dz[t]
+ *
+ *   dy [Bt,T,D] in dy_dtype, float32 or io_dtype (the scan's gradients are
+ *   float32); dstate_out [Bt,D,k-1] io_dtype or NULL (zero);
+ *   dx [Bt,T,D] and dstate [Bt,D,k-1] io_dtype (written; dstate may be NULL);
+ *   dw [D,k] and dbias [D] float32 (written; dbias may be NULL)
+ *   workspace: at least ssd_conv1d_backward_workspace_bytes(desc), 16-byte
+ *   aligned
+ *
+ * All sums are float32 in an order that depends on the shape alone (no
+ * atomics).  Shapes and grid limits as ssd_conv1d.  Outputs may not overlap
+ * any input, the workspace or each other.  batch == 0 or seqlen == 0 writes
+ * zeros to dw and dbias; with seqlen == 0 dstate is dstate_out (or zeros).
+ */
+size_t ssd_conv1d_backward_workspace_bytes(const ssd_conv_desc* desc);
+ssd_status ssd_conv1d_backward(const ssd_conv_desc* desc, int32_t dy_dtype, const void* x,
+                               const float* w, const float* bias, const void* state_in,
+                               const void* dy, const void* dstate_out, void* dx, float* dw,
+                               float* dbias, void* dstate, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+
+/* Problem description of the residual add and norm before a block. */
+typedef struct {
+  int64_t rows;      /* R >= 0: tokens */
+  int64_t cols;      /* D: width of the residual stream, 1 <= D <= SSD_NORM_MAX_COLS */
+  int32_t io_dtype;  /* ssd_dtype of x, y, dy and dx */
+  float scale;       /* s: the residual scale, multiplies x (finite) */
+  float eps;         /* added to the mean square, >= 0 */
+} ssd_add_norm_desc;
+
+/* The widest row (residual stream, or one group of the gated norm). */
+#define SSD_NORM_MAX_COLS 16384
+/* 8-bit rows are padded with zeros to a multiple of this many columns. */
+#define SSD_Q8_PAD 128
+/* The widest 8-bit row: 2^14 times this stays below 2^31. */
+#define SSD_Q8_MAX_COLS 130944
+
+/*
+ * The residual add and the RMS norm before a block, in one pass.
+ *
+ * Source: "Compiler-First State Space Duality and Portable O(1) Autoregressive
+ * Caching", Implementation choices, "precision management": the residual
+ * stream and the norm are kept in float32.  Per row:
+ *
+ *   r' = residual + s * x;   y = r' / sqrt(mean(r'^2) + eps) * weight
+ *
+ *   x [R,D] io_dtype      residual [R,D] f32 or NULL (zeros: the first block)
+ *   weight [D] f32        y [R,D] io_dtype (written)
+ *   residual_out [R,D] f32 (written) or NULL (not returned); it may be
+ *   `residual` itself (updated in place)
+ *
+ * Buffers need the alignment of their elements only.  Sums are float32; the
+ * order depends on D alone, so a row gives the same bits in any batch.
+ */
+ssd_status ssd_add_norm(const ssd_add_norm_desc* desc, const void* x, const float* residual,
+                        const float* weight, void* y, float* residual_out, hipStream_t stream);
+
+/*
+ * ssd_add_norm with y as 8-bit rows for ssd_linear_q8, quantised in the same
+ * pass from the float32 values (see ssd_quantize_q8):
+ *   q [R, Dp] int8, Dp = D rounded up to a multiple of SSD_Q8_PAD (written,
+ *   padding included); qscale [R] f32 (written)
+ */
+ssd_status ssd_add_norm_q8(const ssd_add_norm_desc* desc, const void* x, const float* residual,
+                           const float* weight, int8_t* q, float* qscale, float* residual_out,
+                           hipStream_t stream);
+
+/*
+ * Gradients of ssd_add_norm for the loss sum(dy * y) + sum(dresidual_out *
+ * residual_out).  With c = 1/sqrt(mean(r'^2) + eps), p = dy * weight:
+ *
+ *   dresidual = dresidual_out + c (p - r' c mean(p r' c));  dx = s * dresidual
+ *   dweight   = sum over rows of dy r' c
+ *
+ *   residual_out [R,D] f32: r' as the forward wrote it; weight [D] f32
+ *   dy [R,D] io_dtype; dresidual_out [R,D] f32 or NULL (zero)
+ *   dx [R,D] io_dtype (written) or NULL; dresidual [R,D] f32 (written) or
+ *   NULL; it may be dresidual_out itself (updated in place)
+ *   dweight [D] f32 (written)
+ *   workspace: at least ssd_add_norm_backward_workspace_bytes(desc)
+ *
+ * No atomics: the order of dweight's sum depends on the shape alone.  rows ==
+ * 0 writes zeros to dweight.
+ */
+size_t ssd_add_norm_backward_workspace_bytes(const ssd_add_norm_desc* desc);
+ssd_status ssd_add_norm_backward(const ssd_add_norm_desc* desc, const float* residual_out,
+                                 const float* weight, const void* dy, const float* dresidual_out,
+                                 void* dx, float* dresidual, float* dweight, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+
+/* Problem description of the gated norm after the scan. */
+typedef struct {
+  int64_t rows;      /* R >= 0: tokens */
+  int64_t cols;      /* D: the scan's H * P columns */
+  int64_t groups;    /* G >= 1 divides D; a mean square per D/G adjacent columns */
+  int64_t z_stride;  /* elements between rows of z, >= D (the gate is a slice of the projection) */
+  int64_t dz_stride; /* the same for dz (the gradients only) */
+  int32_t io_dtype;  /* ssd_dtype of y, z, out and their gradients */
+  float eps;
+} ssd_gated_norm_desc;
+
+/*
+ * The gated RMS norm after a block's scan, in one pass.  Per row:
+ *
+ *   g = y * silu(z);   out = g / sqrt(mean over its group(g^2) + eps) * weight
+ *
+ *   y [R,D] io_dtype (the scan's output)    z [R,D] io_dtype, rows z_stride apart
+ *   weight [D] f32                          out [R,D] io_dtype (written)
+ *
+ * Groups up to SSD_NORM_MAX_COLS wide.  Alignment and order of sums as
+ * ssd_add_norm.
+ */
+ssd_status ssd_gated_norm(const ssd_gated_norm_desc* desc, const void* y, const void* z,
+                          const float* weight, void* out, hipStream_t stream);
+
+/* ssd_gated_norm with out as 8-bit rows, as ssd_add_norm_q8 (one scale per
+ * row, over all its groups; at most SSD_NORM_MAX_GROUPS_Q8 of them, D at most
+ * SSD_NORM_MAX_COLS). */
+#define SSD_NORM_MAX_GROUPS_Q8 1024
+ssd_status ssd_gated_norm_q8(const ssd_gated_norm_desc* desc, const void* y, const void* z,
+                             const float* weight, int8_t* q, float* qscale, hipStream_t stream);
+
+/*
+ * Gradients of ssd_gated_norm for the loss sum(dout * out).  With ghat = g c,
+ * c = 1/sqrt(mean(g^2) + eps), p = dout * weight, and the means over a group:
+ *
+ *   dg = c (p - ghat mean(p ghat));   dy = dg silu(z);   dz = dg y silu'(z)
+ *   dweight = sum over rows of dout ghat
+ *
+ *   dout [R,D], dy [R,D] io_dtype; dz [R,D] io_dtype, rows dz_stride apart
+ *   (written between the columns of a row only); dweight [D] f32
+ *   workspace: at least ssd_gated_norm_backward_workspace_bytes(desc)
+ */
+size_t ssd_gated_norm_backward_workspace_bytes(const ssd_gated_norm_desc* desc);
+ssd_status ssd_gated_norm_backward(const ssd_gated_norm_desc* desc, const void* y, const void* z,
+                                   const float* weight, const void* dout, void* dy, void* dz,
+                                   float* dweight, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
+
+/*
+ * Rows in 8 bits: of a weight [N,K] (a scale per output channel, laid out once)
+ * or of activations [M,K] (a scale per token).  Per row v:
+ *
+ *   a = max |v|;  scale = a / 127;  q = clamp(round_to_even(v * (127 / a)), -127, 127)
+ *
+ * in float32.  A row with a < 2^-100 gets q = 0 and scale 0; a row with a NaN
+ * or an infinity gets q = 0 and scale NaN, so that everything made from it is
+ * NaN.  Columns K .. Kp-1 (Kp: K rounded up to a multiple of SSD_Q8_PAD) are
+ * zeros.  K <= SSD_Q8_MAX_COLS.
+ *
+ *   v [R,K] in dtype      q [R,Kp] int8, 16-byte aligned      qscale [R] f32
+ */
+ssd_status ssd_quantize_q8(int64_t rows, int64_t cols, int32_t dtype, const void* v, int8_t* q,
+                           float* qscale, hipStream_t stream);
+
+/* Problem description of a product of 8-bit rows. */
+typedef struct {
+  int64_t rows;      /* M >= 0: tokens */
+  int64_t cols;      /* Kp: padded columns of both operands, a multiple of SSD_Q8_PAD */
+  int64_t outs;      /* N >= 1: output channels */
+  int32_t out_dtype; /* ssd_dtype of out */
+} ssd_linear_q8_desc;
+
+/*
+ * The product of 8-bit activations and weights on the integer matrix cores:
+ *
+ *   out[m][n] = qscale[m] * wscale[n] * sum_k q[m][k] wq[n][k]
+ *
+ * with the sum exact in 32-bit integers (Kp <= SSD_Q8_MAX_COLS cannot overflow
+ * them) and the result rounded to out_dtype once.
+ *
+ *   q [M,Kp] int8, qscale [M] f32      wq [N,Kp] int8, wscale [N] f32
+ *   out [M,N] out_dtype (written; element alignment)
+ *   q and wq 16-byte aligned
+ */
+ssd_status ssd_linear_q8(const ssd_linear_q8_desc* desc, const int8_t* q, const float* qscale,
+                         const int8_t* wq, const float* wscale, void* out, hipStream_t stream);
 
 /* Static description of a status code (never NULL). */
 const char* ssd_status_string(ssd_status status);

@@ -9,6 +9,14 @@ PyTorch fallback -- if libssd.so is missing, importing this package raises.
   ssd_step(state, x_t, dt_t, A, B_t, C_t, D=None, ...)      -> y_t  (state updated in place)
   ssd_chunk_scan_workspace_bytes(...)                        -> int
 
+and, for the rest of a block between two scans,
+
+  ssd_add_norm(x, weight, residual=None, ...)   -> (y, residual_out)   residual add + RMS norm
+  ssd_gated_norm(y, z, weight, ...)             -> out                 gated RMS norm
+  ssd_add_norm_q8, ssd_gated_norm_q8, ssd_quantize_q8 -> (q, qscale, ...)  8-bit rows
+  ssd_linear_q8(q, qscale, wq, wscale)          -> out                 product of 8-bit rows
+  ssd_add_norm_backward, ssd_gated_norm_backward, ssd_conv1d_backward -> dict of gradients
+
 Source: "Compiler-First State Space Duality and Portable O(1) Autoregressive
 Caching" (Background, Eq. 2-3; O(1) cache).
 """
@@ -36,10 +44,16 @@ SSD_VARIANT_DEFAULT = 0
 SSD_VARIANT_BF16_DECAY = 1
 SSD_VARIANT_LOADED_MASK = 2
 SSD_NOALLOC_MAX_WORKSPACE = 96 << 20
+SSD_Q8_PAD = 128
 EXPORTED = ("ssd_chunk_scan", "ssd_chunk_scan_timed", "ssd_chunk_scan_workspace_bytes",
             "ssd_chunk_scan_schedule", "ssd_chunk_scan_ablation", "ssd_chunk_scan_noalloc",
             "ssd_step", "ssd_conv1d", "ssd_conv1d_step",
             "ssd_chunk_scan_backward", "ssd_chunk_scan_backward_workspace_bytes",
+            "ssd_conv1d_backward", "ssd_conv1d_backward_workspace_bytes",
+            "ssd_add_norm", "ssd_add_norm_q8", "ssd_add_norm_backward",
+            "ssd_add_norm_backward_workspace_bytes", "ssd_gated_norm", "ssd_gated_norm_q8",
+            "ssd_gated_norm_backward", "ssd_gated_norm_backward_workspace_bytes",
+            "ssd_quantize_q8", "ssd_linear_q8",
             "ssd_status_string", "ssd_abi_version")
 
 
@@ -64,6 +78,22 @@ class ConvDesc(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
                 ("channels", ctypes.c_int64), ("width", ctypes.c_int64),
                 ("io_dtype", ctypes.c_int32), ("silu", ctypes.c_int32)]
+
+
+class AddNormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class GatedNormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("groups", ctypes.c_int64),
+                ("z_stride", ctypes.c_int64), ("dz_stride", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class LinearQ8Desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("outs", ctypes.c_int64),
+                ("out_dtype", ctypes.c_int32)]
 
 
 class SSDError(RuntimeError):
@@ -104,6 +134,29 @@ def _load() -> ctypes.CDLL:
     L.ssd_conv1d.argtypes = [ctypes.POINTER(ConvDesc)] + [vp] * 6 + [vp]
     L.ssd_conv1d_step.restype = i32
     L.ssd_conv1d_step.argtypes = [ctypes.POINTER(ConvDesc)] + [vp] * 5 + [vp]
+    L.ssd_conv1d_backward.restype = i32
+    L.ssd_conv1d_backward.argtypes = ([ctypes.POINTER(ConvDesc), i32] + [vp] * 11 + [sz, vp])
+    L.ssd_add_norm.restype = i32
+    L.ssd_add_norm.argtypes = [ctypes.POINTER(AddNormDesc)] + [vp] * 5 + [vp]
+    L.ssd_add_norm_q8.restype = i32
+    L.ssd_add_norm_q8.argtypes = [ctypes.POINTER(AddNormDesc)] + [vp] * 6 + [vp]
+    L.ssd_add_norm_backward.restype = i32
+    L.ssd_add_norm_backward.argtypes = [ctypes.POINTER(AddNormDesc)] + [vp] * 8 + [sz, vp]
+    L.ssd_gated_norm.restype = i32
+    L.ssd_gated_norm.argtypes = [ctypes.POINTER(GatedNormDesc)] + [vp] * 4 + [vp]
+    L.ssd_gated_norm_q8.restype = i32
+    L.ssd_gated_norm_q8.argtypes = [ctypes.POINTER(GatedNormDesc)] + [vp] * 5 + [vp]
+    L.ssd_gated_norm_backward.restype = i32
+    L.ssd_gated_norm_backward.argtypes = [ctypes.POINTER(GatedNormDesc)] + [vp] * 8 + [sz, vp]
+    for name, desc in (("ssd_conv1d_backward", ConvDesc), ("ssd_add_norm_backward", AddNormDesc),
+                       ("ssd_gated_norm_backward", GatedNormDesc)):
+        query = getattr(L, name + "_workspace_bytes")
+        query.restype = sz
+        query.argtypes = [ctypes.POINTER(desc)]
+    L.ssd_quantize_q8.restype = i32
+    L.ssd_quantize_q8.argtypes = [ctypes.c_int64, ctypes.c_int64, i32] + [vp] * 3 + [vp]
+    L.ssd_linear_q8.restype = i32
+    L.ssd_linear_q8.argtypes = [ctypes.POINTER(LinearQ8Desc)] + [vp] * 5 + [vp]
     L.ssd_status_string.restype = ctypes.c_char_p
     L.ssd_status_string.argtypes = [i32]
     L.ssd_abi_version.restype = i32
@@ -467,6 +520,342 @@ def ssd_conv1d_step(state: torch.Tensor, x_t: torch.Tensor, weight: torch.Tensor
     if st != SSD_OK:
         raise SSDError(st, "ssd_conv1d_step")
     return y_t
+
+
+def ssd_conv1d_backward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                        *, dy: torch.Tensor, state: Optional[torch.Tensor] = None,
+                        dstate_out: Optional[torch.Tensor] = None, silu: bool = True,
+                        workspace: Optional[torch.Tensor] = None,
+                        grads: Optional[dict] = None) -> dict:
+    """Gradients of ssd_conv1d for L = sum(dy * y) + sum(dstate_out * state_out),
+    on the current stream.  dy [Bt,T,D] float32 (as the scan's gradients are) or
+    x's dtype; dstate_out [Bt,D,k-1] in x's dtype or None.  Returns a dict: dx
+    [Bt,T,D] and dstate [Bt,D,k-1] in x's dtype, dweight [D,k] and dbias [D]
+    float32 (all four always computed)."""
+    if x.dim() != 3 or weight.dim() != 2 or weight.shape[0] != x.shape[2]:
+        raise ValueError("x [Bt,T,D], weight [D,k]")
+    Bt, T, Dc = x.shape
+    K = weight.shape[1]
+    io = x.dtype
+    code = _io_code(io)
+    g = _grad_buffers(grads, {"dx": ((Bt, T, Dc), io), "dweight": ((Dc, K), torch.float32),
+                              "dbias": ((Dc,), torch.float32), "dstate": ((Bt, Dc, K - 1), io)})
+    _shape(dy, "dy", (Bt, T, Dc))
+    _shape(bias, "bias", (Dc,))
+    _shape(state, "state", (Bt, Dc, K - 1))
+    _shape(dstate_out, "dstate_out", (Bt, Dc, K - 1))
+    for t, n, dt_ in ((x, "x", None), (weight, "weight", torch.float32),
+                      (bias, "bias", torch.float32), (state, "state", io),
+                      (dy, "dy", torch.float32 if dy.dtype == torch.float32 else io),
+                      (dstate_out, "dstate_out", io)):
+        _check(t, n, dt_)
+    out = _allocate(g, x.device)
+    desc = ConvDesc(Bt, T, Dc, K, code, int(bool(silu)))
+    workspace = _workspace(workspace, lib.ssd_conv1d_backward_workspace_bytes, desc, x.device)
+    st = lib.ssd_conv1d_backward(
+        ctypes.byref(desc), _io_code(dy.dtype), _ptr(x), _ptr(weight), _ptr(bias), _ptr(state),
+        _ptr(dy), _ptr(dstate_out), _ptr(out["dx"]), _ptr(out["dweight"]), _ptr(out["dbias"]),
+        _ptr(out["dstate"]), _ptr(workspace), _nbytes(workspace), _stream(x.device))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_conv1d_backward")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Norms, 8-bit rows and their product.  Tensors are [..., columns]: the leading
+# dimensions are rows.
+# ---------------------------------------------------------------------------
+def _grad_buffers(grads: Optional[dict], want: dict) -> dict:
+    """The caller's gradient buffers checked against {name: (shape, dtype)}, the
+    rest left to _allocate; shapes are checked here, before device placement."""
+    grads = grads or {}
+    unknown = set(grads) - set(want)
+    if unknown:
+        raise ValueError(f"unknown gradient names {sorted(unknown)}")
+    for k, v in grads.items():
+        _shape(v, k, want[k][0])
+    return {k: (grads.get(k), *want[k]) for k in want}
+
+
+def _allocate(buffers: dict, device) -> dict:
+    out = {}
+    for k, (v, shape, dtype) in buffers.items():
+        if v is None:
+            v = torch.empty(shape, device=device, dtype=dtype)
+        else:
+            _check(v, k, dtype)
+        out[k] = v
+    return out
+
+
+def _workspace(workspace: Optional[torch.Tensor], query, desc, device) -> torch.Tensor:
+    if workspace is None:
+        workspace = torch.empty(max(int(query(ctypes.byref(desc))), 1), dtype=torch.uint8,
+                                device=device)
+    _check(workspace, "workspace")
+    return workspace
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the rows of t [..., D], whose rows must be dense and
+    evenly spaced (a slice of a projection's columns is)."""
+    if t.dim() < 2:
+        return t.shape[-1]
+    if t.numel() == 0:
+        return max(t.stride(-2), t.shape[-1])
+    ok = t.stride(-1) == 1 or t.shape[-1] == 1
+    rows, step = 1, None
+    for d in range(t.dim() - 2, -1, -1):
+        if t.shape[d] == 1:
+            continue
+        if step is None:
+            step = t.stride(d)
+        ok = ok and t.stride(d) == step * rows
+        rows *= t.shape[d]
+    step = t.shape[-1] if step is None else step
+    if not ok or step < t.shape[-1]:
+        raise ValueError(f"{name} must have dense, evenly spaced rows (shape {tuple(t.shape)}, "
+                         f"strides {tuple(t.stride())})")
+    return step
+
+
+def _check_rows(t: Optional[torch.Tensor], name: str, dtype) -> int:
+    """_check for a tensor that may be a slice of columns; its row stride."""
+    if t is None:
+        return 0
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor (got {t.device}); there is no CPU path")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return _row_stride(t, name)
+
+
+def q8_cols(cols: int) -> int:
+    """Columns of an 8-bit row that holds `cols` values (padded with zeros)."""
+    return (cols + SSD_Q8_PAD - 1) // SSD_Q8_PAD * SSD_Q8_PAD
+
+
+def _add_norm_call(x, weight, residual, scale, eps, residual_out, **outs):
+    if x.dim() < 1 or weight.dim() != 1:
+        raise ValueError("x [..., D], weight [D]")
+    D = x.shape[-1]
+    _shape(weight, "weight", (D,))
+    _shape(residual, "residual", x.shape)
+    _shape(residual_out, "residual_out", x.shape)
+    want = {"y": (x.shape, x.dtype), "q": ((*x.shape[:-1], q8_cols(D)), torch.int8),
+            "qscale": (x.shape[:-1], torch.float32)}
+    for k, v in outs.items():
+        _shape(v, k, want[k][0])
+    code = _io_code(x.dtype)
+    for t, n, dt_ in ((x, "x", None), (weight, "weight", torch.float32),
+                      (residual, "residual", torch.float32),
+                      (residual_out, "residual_out", torch.float32)):
+        _check(t, n, dt_)
+    dev = x.device
+    outs = _allocate({k: (v, *want[k]) for k, v in outs.items()}, dev)
+    if residual_out is None:
+        residual_out = torch.empty(x.shape, dtype=torch.float32, device=dev)
+    desc = AddNormDesc(x.numel() // max(D, 1), D, code, float(scale), float(eps))
+    head = (ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(weight))
+    call = lib.ssd_add_norm if "y" in outs else lib.ssd_add_norm_q8
+    st = call(*head, *[_ptr(v) for v in outs.values()], _ptr(residual_out), _stream(dev))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_add_norm" if "y" in outs else "ssd_add_norm_q8")
+    return (*outs.values(), residual_out)
+
+
+def ssd_add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
+                 scale: float = 1.0, eps: float = 1e-5, y: Optional[torch.Tensor] = None,
+                 residual_out: Optional[torch.Tensor] = None
+                 ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Residual add and RMS norm before a block, on the current stream:
+    residual_out = residual + scale * x, y = residual_out / rms * weight.
+
+    x [..., D] float32 or bfloat16, residual [..., D] float32 or None (zeros),
+    weight [D] float32.  Returns (y in x's dtype, residual_out float32).
+    residual_out may be `residual` itself (updated in place)."""
+    return _add_norm_call(x, weight, residual, scale, eps, residual_out, y=y)
+
+
+def ssd_add_norm_q8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                    *, scale: float = 1.0, eps: float = 1e-5, q: Optional[torch.Tensor] = None,
+                    qscale: Optional[torch.Tensor] = None,
+                    residual_out: Optional[torch.Tensor] = None
+                    ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """ssd_add_norm with y quantised to 8-bit rows in the same pass: returns
+    (q [..., q8_cols(D)] int8, qscale [...] float32, residual_out)."""
+    return _add_norm_call(x, weight, residual, scale, eps, residual_out, q=q, qscale=qscale)
+
+
+def ssd_add_norm_backward(residual_out: torch.Tensor, weight: torch.Tensor, *, dy: torch.Tensor,
+                          dresidual_out: Optional[torch.Tensor] = None, scale: float = 1.0,
+                          eps: float = 1e-5, workspace: Optional[torch.Tensor] = None,
+                          grads: Optional[dict] = None) -> dict:
+    """Gradients of ssd_add_norm for L = sum(dy * y) + sum(dresidual_out *
+    residual_out), on the current stream, from the residual_out it returned.
+    Returns a dict: dx [..., D] in dy's dtype, dresidual [..., D] and dweight
+    [D] float32.  grads["dresidual"] may be dresidual_out itself."""
+    if residual_out.dim() < 1 or weight.dim() != 1:
+        raise ValueError("residual_out [..., D], weight [D]")
+    shape, D = residual_out.shape, residual_out.shape[-1]
+    f32 = torch.float32
+    _shape(weight, "weight", (D,))
+    _shape(dy, "dy", shape)
+    _shape(dresidual_out, "dresidual_out", shape)
+    code = _io_code(dy.dtype)
+    g = _grad_buffers(grads, {"dx": (shape, dy.dtype), "dresidual": (shape, f32),
+                              "dweight": ((D,), f32)})
+    for t, n, dt_ in ((residual_out, "residual_out", f32), (weight, "weight", f32),
+                      (dy, "dy", None), (dresidual_out, "dresidual_out", f32)):
+        _check(t, n, dt_)
+    dev = dy.device
+    out = _allocate(g, dev)
+    desc = AddNormDesc(dy.numel() // max(D, 1), D, code, float(scale), float(eps))
+    workspace = _workspace(workspace, lib.ssd_add_norm_backward_workspace_bytes, desc, dev)
+    st = lib.ssd_add_norm_backward(
+        ctypes.byref(desc), _ptr(residual_out), _ptr(weight), _ptr(dy), _ptr(dresidual_out),
+        _ptr(out["dx"]), _ptr(out["dresidual"]), _ptr(out["dweight"]), _ptr(workspace),
+        _nbytes(workspace), _stream(dev))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_add_norm_backward")
+    return out
+
+
+def _gated_norm_call(y, z, weight, groups, eps, **outs):
+    if y.dim() < 1 or weight.dim() != 1:
+        raise ValueError("y [..., D], z [..., D], weight [D]")
+    D = y.shape[-1]
+    _shape(z, "z", y.shape)
+    _shape(weight, "weight", (D,))
+    want = {"out": (y.shape, y.dtype), "q": ((*y.shape[:-1], q8_cols(D)), torch.int8),
+            "qscale": (y.shape[:-1], torch.float32)}
+    for k, v in outs.items():
+        _shape(v, k, want[k][0])
+    code = _io_code(y.dtype)
+    _check(y, "y")
+    _check(weight, "weight", torch.float32)
+    stride = _check_rows(z, "z", y.dtype)
+    dev = y.device
+    outs = _allocate({k: (v, *want[k]) for k, v in outs.items()}, dev)
+    desc = GatedNormDesc(y.numel() // max(D, 1), D, int(groups), stride, 0, code, float(eps))
+    call = lib.ssd_gated_norm if "out" in outs else lib.ssd_gated_norm_q8
+    st = call(ctypes.byref(desc), _ptr(y), _ptr(z), _ptr(weight),
+              *[_ptr(v) for v in outs.values()], _stream(dev))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_gated_norm" if "out" in outs else "ssd_gated_norm_q8")
+    return tuple(outs.values())
+
+
+def ssd_gated_norm(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *, groups: int = 1,
+                   eps: float = 1e-5, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gated RMS norm after a block's scan, on the current stream: g = y * silu(z),
+    out = g / rms(g over each of `groups` equal parts of a row) * weight.
+
+    y [..., D] float32 or bfloat16, z [..., D] in y's dtype with evenly spaced
+    rows (a slice of the projection's columns), weight [D] float32."""
+    return _gated_norm_call(y, z, weight, groups, eps, out=out)[0]
+
+
+def ssd_gated_norm_q8(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *, groups: int = 1,
+                      eps: float = 1e-5, q: Optional[torch.Tensor] = None,
+                      qscale: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """ssd_gated_norm with its output quantised to 8-bit rows in the same pass:
+    returns (q [..., q8_cols(D)] int8, qscale [...] float32)."""
+    return _gated_norm_call(y, z, weight, groups, eps, q=q, qscale=qscale)
+
+
+def ssd_gated_norm_backward(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *,
+                            dout: torch.Tensor, groups: int = 1, eps: float = 1e-5,
+                            workspace: Optional[torch.Tensor] = None,
+                            grads: Optional[dict] = None) -> dict:
+    """Gradients of ssd_gated_norm for L = sum(dout * out), on the current
+    stream.  Returns a dict: dy, dz [..., D] in y's dtype, dweight [D] float32.
+    grads["dz"] may be a slice of a larger tensor's columns, like z."""
+    if y.dim() < 1 or weight.dim() != 1:
+        raise ValueError("y [..., D], z [..., D], weight [D]")
+    shape, D, io = y.shape, y.shape[-1], y.dtype
+    _shape(z, "z", shape)
+    _shape(weight, "weight", (D,))
+    _shape(dout, "dout", shape)
+    code = _io_code(io)
+    g = _grad_buffers(grads, {"dy": (shape, io), "dz": (shape, io),
+                              "dweight": ((D,), torch.float32)})
+    _check(y, "y")
+    _check(weight, "weight", torch.float32)
+    _check(dout, "dout", io)
+    z_stride = _check_rows(z, "z", io)
+    dev = y.device
+    dz = g["dz"][0]
+    if dz is not None:
+        dz_stride = _check_rows(dz, "dz", io)
+    else:
+        dz, dz_stride = torch.empty(shape, dtype=io, device=dev), D
+    del g["dz"]
+    out = _allocate(g, dev)
+    out["dz"] = dz
+    desc = GatedNormDesc(y.numel() // max(D, 1), D, int(groups), z_stride, dz_stride, code,
+                         float(eps))
+    workspace = _workspace(workspace, lib.ssd_gated_norm_backward_workspace_bytes, desc, dev)
+    st = lib.ssd_gated_norm_backward(
+        ctypes.byref(desc), _ptr(y), _ptr(z), _ptr(weight), _ptr(dout), _ptr(out["dy"]), _ptr(dz),
+        _ptr(out["dweight"]), _ptr(workspace), _nbytes(workspace), _stream(dev))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_gated_norm_backward")
+    return out
+
+
+def ssd_quantize_q8(v: torch.Tensor, *, q: Optional[torch.Tensor] = None,
+                    qscale: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Rows of v [..., K] (float32 or bfloat16) in 8 bits, on the current stream:
+    a weight's output channels (laid out once) or tokens.  Returns (q [...,
+    q8_cols(K)] int8, zero-padded, and qscale [...] float32)."""
+    if v.dim() < 1:
+        raise ValueError("v [..., K]")
+    K = v.shape[-1]
+    want = {"q": ((*v.shape[:-1], q8_cols(K)), torch.int8), "qscale": (v.shape[:-1], torch.float32)}
+    _shape(q, "q", want["q"][0])
+    _shape(qscale, "qscale", want["qscale"][0])
+    code = _io_code(v.dtype)
+    _check(v, "v")
+    out = _allocate({"q": (q, *want["q"]), "qscale": (qscale, *want["qscale"])}, v.device)
+    st = lib.ssd_quantize_q8(v.numel() // max(K, 1), K, code, _ptr(v), _ptr(out["q"]),
+                             _ptr(out["qscale"]), _stream(v.device))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_quantize_q8")
+    return out["q"], out["qscale"]
+
+
+def ssd_linear_q8(q: torch.Tensor, qscale: torch.Tensor, wq: torch.Tensor, wscale: torch.Tensor, *,
+                  out_dtype: torch.dtype = torch.bfloat16,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Product of 8-bit activations and weights on the current stream:
+    out[..., n] = qscale * wscale[n] * sum_k q[..., k] wq[n, k], summed exactly.
+
+    q [..., Kp] int8 and qscale [...] float32 (tokens), wq [N, Kp] int8 and
+    wscale [N] float32 (output channels), Kp a multiple of SSD_Q8_PAD, as
+    ssd_quantize_q8 and the norms' _q8 forms return them."""
+    if q.dim() < 1 or wq.dim() != 2:
+        raise ValueError("q [..., Kp], wq [N, Kp]")
+    Kp, N = q.shape[-1], wq.shape[0]
+    if out is not None:
+        out_dtype = out.dtype
+    shape = (*q.shape[:-1], N)
+    _shape(wq, "wq", (N, Kp))
+    _shape(qscale, "qscale", q.shape[:-1])
+    _shape(wscale, "wscale", (N,))
+    _shape(out, "out", shape)
+    code = _io_code(out_dtype)
+    for t, n, dt_ in ((q, "q", torch.int8), (qscale, "qscale", torch.float32),
+                      (wq, "wq", torch.int8), (wscale, "wscale", torch.float32), (out, "out", None)):
+        _check(t, n, dt_)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=q.device)
+    desc = LinearQ8Desc(q.numel() // max(Kp, 1), Kp, N, code)
+    st = lib.ssd_linear_q8(ctypes.byref(desc), _ptr(q), _ptr(qscale), _ptr(wq), _ptr(wscale),
+                           _ptr(out), _stream(q.device))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_linear_q8")
+    return out
 
 
 def abi_version() -> int:

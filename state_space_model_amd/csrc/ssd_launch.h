@@ -125,6 +125,73 @@ struct BwdArgs {
   float dt_min, dt_max;
 };
 
+// The residual add and norm, and its gradients (ssd_norm.hip).
+struct AddNormArgs {
+  const void* x;            // [R,D] io
+  const float* residual;    // [R,D] or null
+  const float* weight;      // [D]
+  void* y;                  // [R,D] io, or null when q is written
+  int8_t* q;                // [R,Dp] or null
+  float* qscale;            // [R] with q
+  float* residual_out;      // [R,D] or null; the gradients read it (never null there)
+  const void* dy;           // [R,D] io
+  const float* dres_out;    // [R,D] or null
+  void* dx;                 // [R,D] io or null
+  float* dres;              // [R,D] or null
+  float* dweight;           // [D]
+  float* part;              // [parts,D] partial sums of dweight
+  int64_t R;
+  int32_t D, Dp;            // Dp: columns of q
+  float scale, eps;
+};
+
+// The gated norm and its gradients (ssd_norm.hip).
+struct GatedNormArgs {
+  const void* y;            // [R,D] io
+  const void* z;            // [R,D] io, rows z_stride apart
+  const float* weight;      // [D]
+  void* out;                // [R,D] io, or null when q is written
+  int8_t* q;                // [R,Dp] or null
+  float* qscale;            // [R] with q
+  const void* dout;         // [R,D] io
+  void* dy;                 // [R,D] io
+  void* dz;                 // [R,D] io, rows dz_stride apart
+  float* dweight;           // [D]
+  float* part;              // [parts,D] partial sums of dweight
+  int64_t R, D, z_stride, dz_stride;
+  int32_t G, W, Dp;         // groups, columns per group, columns of q
+  float eps;
+};
+
+// Product of 8-bit rows (ssd_linear_q8.hip).
+struct LinearQ8Args {
+  const int8_t* q;          // [M,K]
+  const float* qscale;      // [M]
+  const int8_t* wq;         // [N,K]
+  const float* wscale;      // [N]
+  void* out;                // [M,N] io
+  int64_t M, N;
+  int32_t K;
+};
+
+// Gradients of the depthwise causal convolution (ssd_conv_backward.hip).
+struct ConvBwdArgs {
+  const void* x;            // [Bt,T,D] io
+  const float* w;           // [D,K]
+  const float* bias;        // [D] or null
+  const void* state_in;     // [Bt,D,K-1] io or null
+  const void* dy;           // [Bt,T,D] io or float32
+  const void* dstate_out;   // [Bt,D,K-1] io or null
+  void* dx;                 // [Bt,T,D] io
+  float* dw;                // [D,K]
+  float* dbias;             // [D] or null
+  void* dstate;             // [Bt,D,K-1] io or null
+  float* part;              // [parts,K+1,D] partial sums of dw and dbias
+  int64_t Bt, T, D;
+  int32_t K;
+  int32_t silu;
+};
+
 // Compiled shape variants.
 bool scan_shape_supported(int64_t P, int64_t N, int64_t L, bool bf16);
 
@@ -168,6 +235,22 @@ hipError_t launch_step_bf16(const StepArgs& a, hipStream_t stream);
 bool conv_width_supported(int64_t K);
 bool conv_shape_supported(int64_t Bt, int64_t T, int64_t D);
 hipError_t launch_conv(const ConvArgs& a, bool io_bf16, bool step, hipStream_t stream);
+
+// Rows of partial sums of dweight / (dw, dbias) the gradients leave in their
+// workspace, from the shape alone.
+int64_t add_norm_backward_parts(int64_t R, int64_t D);
+int64_t gated_norm_backward_parts(int64_t R, int64_t G, int64_t W);
+int64_t conv_backward_parts(int64_t Bt, int64_t T, int64_t D);
+
+hipError_t launch_add_norm(const AddNormArgs& a, bool io_bf16, hipStream_t stream);
+hipError_t launch_add_norm_backward(const AddNormArgs& a, bool io_bf16, hipStream_t stream);
+hipError_t launch_gated_norm(const GatedNormArgs& a, bool io_bf16, hipStream_t stream);
+hipError_t launch_gated_norm_backward(const GatedNormArgs& a, bool io_bf16, hipStream_t stream);
+hipError_t launch_quantize_q8(const void* v, bool v_bf16, int64_t R, int32_t K, int32_t Kp,
+                              int8_t* q, float* qscale, hipStream_t stream);
+hipError_t launch_linear_q8(const LinearQ8Args& a, bool out_bf16, hipStream_t stream);
+hipError_t launch_conv_backward(const ConvBwdArgs& a, bool io_bf16, bool dy_bf16,
+                                hipStream_t stream);
 
 // Backward pass pieces: phase 0 prepares Delta, its chunk-local prefix and the
 // reversed operands and initial state of R1; phase 1 (after the forward state
