@@ -147,7 +147,7 @@ ssd_status ssd_add_norm_q8(const ssd_add_norm_desc* d, const void* x, const floa
 size_t ssd_add_norm_backward_workspace_bytes(const ssd_add_norm_desc* d) {
   int64_t n = 0;
   if (check_add_norm(d, &n) != SSD_OK) return 0;
-  return round_up((size_t)(add_norm_backward_parts(d->rows, d->cols) * d->cols) * 4, kAlign);
+  return round_up((size_t)(add_norm_backward_parts(d->rows, d->cols, d->io_dtype == SSD_BF16) * d->cols) * 4, kAlign);
 }
 
 ssd_status ssd_add_norm_backward(const ssd_add_norm_desc* d, const float* residual_out,
@@ -198,7 +198,8 @@ ssd_status ssd_gated_norm_q8(const ssd_gated_norm_desc* d, const void* y, const 
 size_t ssd_gated_norm_backward_workspace_bytes(const ssd_gated_norm_desc* d) {
   int64_t n = 0, nz = 0, ndz = 0;
   if (check_gated_norm(d, true, &n, &nz, &ndz) != SSD_OK) return 0;
-  return round_up((size_t)(gated_norm_backward_parts(d->rows, d->groups, d->cols / d->groups) *
+  return round_up((size_t)(gated_norm_backward_parts(d->rows, d->groups, d->cols / d->groups,
+                                                       d->io_dtype == SSD_BF16) *
                            d->cols) * 4, kAlign);
 }
 

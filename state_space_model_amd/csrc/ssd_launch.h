@@ -238,8 +238,8 @@ hipError_t launch_conv(const ConvArgs& a, bool io_bf16, bool step, hipStream_t s
 
 // Rows of partial sums of dweight / (dw, dbias) the gradients leave in their
 // workspace, from the shape alone.
-int64_t add_norm_backward_parts(int64_t R, int64_t D);
-int64_t gated_norm_backward_parts(int64_t R, int64_t G, int64_t W);
+int64_t add_norm_backward_parts(int64_t R, int64_t D, bool io_bf16);
+int64_t gated_norm_backward_parts(int64_t R, int64_t G, int64_t W, bool io_bf16);
 int64_t conv_backward_parts(int64_t Bt, int64_t T, int64_t D);
 
 hipError_t launch_add_norm(const AddNormArgs& a, bool io_bf16, hipStream_t stream);

@@ -435,6 +435,30 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(gr["dy"][-2:], g1["dy"]) and torch.equal(gr["dz"][-2:], g1["dz"])
 
 
+def test_more_rows_than_one_grid_holds():
+    """2^21 + 3 rows: the rows past the first launch's equal a small call."""
+    need_gpu()
+    import state_space_model_amd as ssd
+    announce("rows beyond one launch")
+    g = torch.Generator(device="cuda").manual_seed(6)
+    rows, d = (1 << 21) + 3, 64
+    x = torch.randn(rows, d, generator=g, device="cuda").bfloat16()
+    r = torch.randn(rows, d, generator=g, device="cuda")
+    zf = torch.randn(rows, d + 6, generator=g, device="cuda").bfloat16()
+    w = torch.rand(d, generator=g, device="cuda")
+    tail = slice(rows - 5, rows)
+    t = lambda v: v[tail].contiguous()
+    for full, part in ((ssd.ssd_add_norm(x, w, r), ssd.ssd_add_norm(t(x), w, t(r))),
+                       (ssd.ssd_add_norm_q8(x, w, r), ssd.ssd_add_norm_q8(t(x), w, t(r))),
+                       ([ssd.ssd_gated_norm(x, zf[:, :d], w, groups=2)],
+                        [ssd.ssd_gated_norm(t(x), zf[tail, :d], w, groups=2)]),
+                       (ssd.ssd_gated_norm_q8(x, zf[:, :d], w, groups=2),
+                        ssd.ssd_gated_norm_q8(t(x), zf[tail, :d], w, groups=2)),
+                       (ssd.ssd_quantize_q8(x), ssd.ssd_quantize_q8(t(x)))):
+        for a, b in zip(full, part):
+            assert torch.equal(a[tail], b)
+
+
 # --------------------------------------------------------------------------
 # convolution gradients
 # --------------------------------------------------------------------------
