@@ -1,47 +1,530 @@
 // Product of 8-bit rows on the integer matrix cores of gfx950:
 //   out[m][n] = sx[m] sw[n] sum_k x[m][k] w[n][k]
 //
-// v_mfma_i32_16x16x64_i8 contracts 64 columns: lane l holds 16 adjacent bytes
-// of row l % 16 of each operand, columns 16 (l / 16) ..., and register r of
-// lane l is element [4 (l / 16) + r][l % 16] of the product, as for the
-// float matrix instructions.  The sum is exact, so its order is free.
-#include "ssd_device.h"
+// The weight is the instruction's first operand, so that a lane ends with
+// four adjacent outputs of one token.  Both matrix instructions used contract
+// 16 adjacent bytes per lane, any assignment of columns to lanes being valid
+// as long as both operands share it; the integer sum is exact, so its order is
+// free and every shape gives the same bits.
+//   v_mfma_i32_16x16x64_i8  lane l: row l % 16, bytes 16 (l / 16) of 64;
+//                           register r: element [4 (l / 16) + r][l % 16]
+//   v_mfma_i32_32x32x32_i8  lane l: row l % 32, bytes 16 (l / 32) of 32;
+//                           register r: [8 (r / 4) + 4 (l / 32) + r % 4][l % 32]
 #include "ssd_launch.h"
+#include "ssd_rows.h"
 
 namespace ssd {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 
-// one wavefront per 16 x 16 tile
+__device__ __forceinline__ i32x4 load16(const int8_t* p) { return *reinterpret_cast<const i32x4*>(p); }
+
+// four adjacent outputs of one token, of which `n` exist
 template <typename T>
-__global__ __launch_bounds__(64) void k_linear_q8(LinearQ8Args a, int64_t nt) {
-  const int l = threadIdx.x, i = l & 15, g = l >> 4;
-  const int64_t m0 = (int64_t)(blockIdx.x / nt) * 16, n0 = (int64_t)(blockIdx.x % nt) * 16;
-  const int64_t m = m0 + i < a.M ? m0 + i : a.M - 1, n = n0 + i < a.N ? n0 + i : a.N - 1;
-  const int8_t* x = a.q + m * a.K + g * 16;
-  const int8_t* w = a.wq + n * a.K + g * 16;
-  i32x4 acc = {0, 0, 0, 0};
-  for (int k = 0; k < a.K; k += 64)
-    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(*reinterpret_cast<const i32x4*>(x + k),
-                                                *reinterpret_cast<const i32x4*>(w + k), acc, 0, 0, 0);
+__device__ __forceinline__ void store_quad(T* p, i32x4 acc, const float* ws, float xs, int n) {
+  if (n >= 4) {
+    const fvec<4> w = load_pack<4>(ws);
+    fvec<4> v;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int64_t mm = m0 + 4 * g + r;
-    if (mm < a.M && n0 + i < a.N)
-      reinterpret_cast<T*>(a.out)[mm * a.N + n0 + i] =
-          to_io<T>((float)acc[r] * a.wscale[n0 + i] * a.qscale[mm]);
+    for (int e = 0; e < 4; ++e) v[e] = (float)acc[e] * xs * w[e];
+    store_pack<4>(p, convert_pack<T, 4>(v));
+  } else {
+    for (int e = 0; e < n; ++e) p[e] = to_io<T>((float)acc[e] * xs * ws[e]);
   }
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: the weights stream once from memory.  A workgroup of NW
+// wavefronts owns 16 outputs and all tokens (MT tiles of 16); the wavefronts
+// split the columns, 128 bytes (a line of each weight row) at a time, load
+// straight into registers and add up through LDS.
+// ---------------------------------------------------------------------------
+template <typename T, int NW, int UN>
+__global__ __launch_bounds__(64 * NW) void k_linear_q8_stream(LinearQ8Args a) {
+  __shared__ i32x4 part[NW - 1][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t n = n0 + i < a.N ? n0 + i : a.N - 1, m = i < a.M ? i : a.M - 1;
+  const int units = a.K / 128;
+  const int u0 = units * wave / NW, u1 = units * (wave + 1) / NW;
+  const int8_t* w = a.wq + n * a.K + g * 16;
+  const int8_t* x = a.q + m * a.K + g * 16;
+  i32x4 acc = {};
+  // UN units at a time; past the end of the share the last one is loaded again
+  // and its activations are taken as zeros
+  for (int u = u0; u < u1; u += UN) {
+    i32x4 wr[2 * UN], xr[2 * UN];
+#pragma unroll
+    for (int j = 0; j < 2 * UN; ++j) {
+      const int k = min(u + j / 2, u1 - 1) * 128 + j % 2 * 64;
+      wr[j] = load16(w + k);
+      xr[j] = load16(x + k);
+    }
+#pragma unroll
+    for (int j = 0; j < 2 * UN; ++j) {
+      const i32x4 xv = u + j / 2 < u1 ? xr[j] : i32x4{0, 0, 0, 0};
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wr[j], xv, acc, 0, 0, 0);
+    }
+  }
+  if (wave > 0) part[wave - 1][lane] = acc;
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int o = 0; o < NW - 1; ++o) acc += part[o][lane];
+  const int64_t nn = n0 + 4 * g;
+  if (i < a.M && nn < a.N)
+    store_quad(reinterpret_cast<T*>(a.out) + i * a.N + nn, acc, a.wscale + nn, a.qscale[i],
+               (int)(a.N - nn < 4 ? a.N - nn : 4));
+}
+
+// The tile of a workgroup, of nt x mt: consecutive tiles run on one XCD, in
+// groups of 8 tile rows, so that the tiles it holds at a time share both
+// operands' panels in its L2.
+struct TileOf {
+  int32_t n, m;
+  __device__ __forceinline__ TileOf(int32_t nt, int32_t mt) {
+    constexpr int32_t kRows = 8;
+    const uint32_t id = (uint32_t)xcd_remap(blockIdx.x, (int64_t)nt * mt);
+    const uint32_t per = kRows * nt, group = id / per, in = id % per, first = group * kRows;
+    const uint32_t size = min((uint32_t)mt - first, (uint32_t)kRows);
+    // divisions are done on the vector unit; the results are the same in every lane
+    m = __builtin_amdgcn_readfirstlane((int)(first + in % size));
+    n = __builtin_amdgcn_readfirstlane((int)(in / size));
+  }
+};
+
+// A wavefront's 32 TN x 32 TM outputs, through its own kOutBytes of LDS: 64
+// columns of 32 tokens at a time, scaled by the token on the way in and by the
+// column on the way out, where a lane's four columns stay the same; each
+// token's columns then leave as whole lines.
+constexpr int kOutPitch = 256 + 16, kOutBytes = 32 * kOutPitch;
+template <typename T, int TN, int TM>
+__device__ __forceinline__ void store_tile(const LinearQ8Args& a, const i32x16 (&acc)[TN][TM],
+                                           int8_t* lds, int64_t n0, int64_t m0, int lane) {
+  const int half = lane >> 5, tok = lane & 31, c = (lane & 15) * 4;
+  float xs[TM];
+#pragma unroll
+  for (int tm = 0; tm < TM; ++tm) {
+    const int64_t m = m0 + 32 * tm + tok;
+    xs[tm] = a.qscale[m < a.M ? m : a.M - 1];
+  }
+#pragma unroll
+  for (int t0 = 0; t0 < TN; t0 += 2) {
+    const int64_t n = n0 + 32 * t0 + c;
+    const int left = (TN - t0 >= 2 || c < 32) && n < a.N ? (int)(a.N - n < 4 ? a.N - n : 4) : 0;
+    fvec<4> ws;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ws[e] = a.wscale[e < left ? n + e : a.N - 1];
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm) {
+#pragma unroll
+      for (int t = t0; t < t0 + 2 && t < TN; ++t)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          fvec<4> v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = (float)acc[t][tm][4 * p + e] * xs[tm];
+          *reinterpret_cast<fvec<4>*>(lds + tok * kOutPitch + (32 * (t - t0) + 8 * p + 4 * half) * 4) = v;
+        }
+      // (LDS operations of one wavefront complete in order)
+#pragma unroll
+      for (int r = 0; r < 32; r += 4) {
+        const int row = r + lane / 16;
+        const fvec<4> v = *reinterpret_cast<const fvec<4>*>(lds + row * kOutPitch + c * 4) * ws;
+        const int64_t m = m0 + 32 * tm + row;
+        if (m < a.M) {
+          T* out = reinterpret_cast<T*>(a.out) + m * a.N + n;
+          const typename Pack<T, 4>::V o = convert_pack<T, 4>(v);
+          if (left == 4) {
+            store_pack<4>(out, o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+              if (e < left) out[e] = o[e];
+          }
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many tokens: BN outputs x BM tokens per workgroup, WN x WM wavefronts, the
+// operands staged through LDS 128 columns at a time in two buffers.
+//
+// Global loads write LDS directly, 16 bytes per lane: a wavefront's load fills
+// 8 rows of 128 bytes.  The 16-byte chunk c of row r is kept at position
+// c ^ (r / 2 % 8) of its row, so that the 16 lanes of a read phase, which take
+// one chunk of 16 adjacent rows, meet 16 different quarter-banks; the swizzle
+// is applied to the global address, as the LDS side of such a load is linear.
+// ---------------------------------------------------------------------------
+template <typename T, int BN, int BM, int WN, int WM, int NS>
+__global__ __launch_bounds__(64 * WN * WM) void k_linear_q8_tile(LinearQ8Args a, int32_t nt,
+                                                                  int32_t mt) {
+  constexpr int NW = WN * WM, BK = 128;
+  constexpr int TN = BN / WN / 32, TM = BM / WM / 32;   // 32 x 32 tiles of a wavefront
+  constexpr int ROWS = BN + BM, CPR = BK / 16, RPL = 64 / CPR;   // chunks per row, rows per load
+  constexpr int LOADS = ROWS / RPL / NW;
+  static_assert(BM % (RPL * NW) == 0 && BN % (RPL * NW) == 0);
+  static_assert((NS - 2) * LOADS < 64);
+  constexpr int STAGE = ROWS * BK, BYTES = NS * STAGE > NW * kOutBytes ? NS * STAGE : NW * kOutBytes;
+  __shared__ __align__(1024) int8_t sm[BYTES];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const TileOf at(nt, mt);
+  const int64_t m0 = (int64_t)at.m * BM, n0 = (int64_t)at.n * BN;
+
+  const int8_t* wp = a.wq + n0 * a.K;
+  const int8_t* xp = a.q + m0 * a.K;
+  const int nlast = (int)(a.N - n0 < BN ? a.N - n0 : BN) - 1, mlast = (int)(a.M - m0 < BM ? a.M - m0 : BM) - 1;
+  uint32_t off[LOADS];
+#pragma unroll
+  for (int j = 0; j < LOADS; ++j) {
+    const int r = (j * NW + wave) * RPL + lane / CPR;
+    const int chunk = (lane % CPR) ^ (r / (16 / CPR) % CPR);
+    const int row = j * NW * RPL < BN ? min(r, nlast) : min(r - BN, mlast);
+    off[j] = (uint32_t)row * (uint32_t)a.K + chunk * 16;
+  }
+  auto stage_part = [&](int buf, int j0, int j1) {
+#pragma unroll
+    for (int j = j0; j < j1; ++j) {
+      const int8_t* base = j * NW * RPL < BN ? wp : xp;
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)(base + off[j]),
+          (__attribute__((address_space(3))) void*)(sm + buf * STAGE + (j * NW + wave) * 1024), 16, 0, 0);
+    }
+  };
+  auto stage = [&](int buf) {
+    stage_part(buf, 0, LOADS);
+    wp += BK;
+    xp += BK;
+  };
+  const int wn = wave % WN, wm = wave / WN;
+  const int rw = wn * (BN / WN) + (lane & 31), rx = BN + wm * (BM / WM) + (lane & 31);
+  const int half = lane >> 5;
+  i32x16 acc[TN][TM] = {};
+  const int steps = a.K / BK;
+#pragma unroll
+  for (int p = 0; p < NS - 1; ++p) {
+    stage_part(p, 0, LOADS);
+    wp += p + 1 < steps ? BK : 0;
+    xp += p + 1 < steps ? BK : 0;
+  }
+  int cur = 0, nxt = NS - 1;
+  for (int s = 0; s < steps; ++s) {
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * LOADS) : "memory");
+    const int8_t* b = sm + cur * STAGE;
+    i32x4 wf[BK / 32][TN], xf[BK / 32][TM];
+    auto frags = [&](int kk) {
+#pragma unroll
+      for (int t = 0; t < TN; ++t)
+        wf[kk][t] = load16(b + (rw + 32 * t) * BK + (((2 * kk + half) ^ (rw / (16 / CPR) % CPR)) << 4));
+#pragma unroll
+      for (int t = 0; t < TM; ++t)
+        xf[kk][t] = load16(b + (rx + 32 * t) * BK + (((2 * kk + half) ^ (rx / (16 / CPR) % CPR)) << 4));
+    };
+    frags(0);
+    // (the last steps load the final columns again into a buffer that no one reads)
+    constexpr int KK = BK / 32, SP = NS == 2 ? (KK + 1) / 2 : KK;
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      auto product = [&](int i0, int i1) {
+#pragma unroll
+        for (int i = i0; i < i1; ++i) {
+          const int tn = i / TM, tm = i % TM;
+          acc[tn][tm] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[kk][tn], xf[kk][tm], acc[tn][tm], 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      constexpr int HEAD = 1;
+      product(0, HEAD);
+      if (kk + 1 < KK) frags(kk + 1);
+      if (kk < SP) stage_part(nxt, LOADS * kk / SP, LOADS * (kk + 1) / SP);
+      __builtin_amdgcn_sched_barrier(0);
+      product(HEAD, TN * TM);
+    }
+    wp += s + NS < steps ? BK : 0;
+    xp += s + NS < steps ? BK : 0;
+    cur = cur + 1 == NS ? 0 : cur + 1;
+    nxt = nxt + 1 == NS ? 0 : nxt + 1;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load may reach LDS after this
+  __syncthreads();
+  store_tile<T, TN, TM>(a, acc, sm + wave * kOutBytes, n0 + wn * (BN / WN), m0 + wm * (BM / WM), lane);
+}
+
+// Few tiles: the KS wavefronts of a workgroup share one BN x BM tile and split
+// its columns; each stages its part through a ring of its own, without
+// barriers, and the sums meet in LDS.
+template <typename T, int BN, int BM, int KS, int NS>
+__global__ __launch_bounds__(64 * KS) void k_linear_q8_split(LinearQ8Args a, int32_t nt, int32_t mt) {
+  constexpr int BK = 128, TN = BN / 32, TM = BM / 32, LOADS = (BN + BM) / 8;
+  constexpr int STAGE = (BN + BM) * BK, RING = KS * NS * STAGE;
+  constexpr int SUMS = KS * TN * TM * 4096, OUT = SUMS + KS * kOutBytes;
+  static_assert((NS - 1) * LOADS < 64);
+  __shared__ __align__(1024) int8_t sm[RING > OUT ? RING : OUT];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const TileOf at(nt, mt);
+  const int64_t m0 = (int64_t)at.m * BM, n0 = (int64_t)at.n * BN;
+  const int nlast = (int)(a.N - n0 < BN ? a.N - n0 : BN) - 1;
+  const int mlast = (int)(a.M - m0 < BM ? a.M - m0 : BM) - 1;
+  uint32_t off[LOADS];
+#pragma unroll
+  for (int j = 0; j < LOADS; ++j) {
+    const int r = j * 8 + lane / 8, chunk = (lane % 8) ^ (r / 2 % 8);
+    const int row = j * 8 < BN ? min(r, nlast) : min(r - BN, mlast);
+    off[j] = (uint32_t)row * (uint32_t)a.K + chunk * 16;
+  }
+  const int8_t* wp = a.wq + n0 * a.K;
+  const int8_t* xp = a.q + m0 * a.K;
+  const int steps = a.K / BK, s0 = steps * wave / KS, s1 = steps * (wave + 1) / KS;
+  int8_t* ring = sm + wave * NS * STAGE;
+  auto stage = [&](int s, int buf) {   // past the end: the last step again, read by no one
+    const int64_t k = (int64_t)(s < s1 ? s : steps - 1) * BK;
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j)
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)((j * 8 < BN ? wp : xp) + k + off[j]),
+          (__attribute__((address_space(3))) void*)(ring + buf * STAGE + j * 1024), 16, 0, 0);
+  };
+  const int r32 = lane & 31, half = lane >> 5;
+  i32x16 acc[TN][TM] = {};
+#pragma unroll
+  for (int p = 0; p < NS - 1; ++p) stage(s0 + p, p);
+  int cur = 0;
+  for (int s = s0; s < s1; ++s) {
+    // step s has landed, and the reads of step s - 1 are done
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)" ::"n"((NS - 2) * LOADS) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    const int8_t* b = ring + cur * STAGE;
+    i32x4 wf[4][TN], xf[4][TM];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const int pos = ((2 * kk + half) ^ (r32 / 2 % 8)) << 4;
+#pragma unroll
+      for (int t = 0; t < TN; ++t) wf[kk][t] = load16(b + (32 * t + r32) * BK + pos);
+#pragma unroll
+      for (int t = 0; t < TM; ++t) xf[kk][t] = load16(b + (BN + 32 * t + r32) * BK + pos);
+    }
+    stage(s + NS - 1, cur == 0 ? NS - 1 : cur - 1);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm)
+          acc[tn][tm] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[kk][tn], xf[kk][tm], acc[tn][tm], 0, 0, 0);
+    cur = cur + 1 == NS ? 0 : cur + 1;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load may reach LDS after this
+  __syncthreads();
+  i32x16* sums = reinterpret_cast<i32x16*>(sm);
+#pragma unroll
+  for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm) sums[((wave * TN + tn) * TM + tm) * 64 + lane] = acc[tn][tm];
+  __syncthreads();
+  for (int t = wave; t < TN * TM; t += KS) {
+    i32x16 sum[1][1] = {{sums[t * 64 + lane]}};
+#pragma unroll
+    for (int o = 1; o < KS; ++o) sum[0][0] += sums[(o * TN * TM + t) * 64 + lane];
+    store_tile<T, 1, 1>(a, sum, sm + SUMS + wave * kOutBytes, n0 + t / TM * 32, m0 + t % TM * 32, lane);
+  }
+}
+
+template <typename T, int BN, int BM, int KS, int NS>
+hipError_t split(const LinearQ8Args& a, hipStream_t s) {
+  const int32_t nt = (int32_t)((a.N + BN - 1) / BN), mt = (int32_t)((a.M + BM - 1) / BM);
+  hipLaunchKernelGGL((k_linear_q8_split<T, BN, BM, KS, NS>), dim3((unsigned)(nt * mt)), dim3(64 * KS), 0, s, a, nt, mt);
+  return hipGetLastError();
+}
+
+// Two groups of four wavefronts, one of each group per SIMD, take turns.
+template <typename T, int TN, int TM>
+__global__ __launch_bounds__(512) void k_linear_q8_turns(LinearQ8Args a, int32_t nt, int32_t mt) {
+  constexpr int WN = 2, WM = 4, NW = 8, BK = 128, BN = WN * TN * 32, BM = WM * TM * 32;
+  constexpr int ROWS = BN + BM, LOADS = ROWS / 8 / NW;
+  static_assert(BN % 64 == 0 && BM % 64 == 0);
+  // two buffers of ROWS x BK bytes; the outputs pass through the same memory
+  constexpr int STAGE = ROWS * BK, BYTES = 2 * STAGE > NW * kOutBytes ? 2 * STAGE : NW * kOutBytes;
+  __shared__ __align__(1024) int8_t sm[BYTES];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const TileOf at(nt, mt);
+  const int64_t m0 = (int64_t)at.m * BM, n0 = (int64_t)at.n * BN;
+
+  const int nlast = (int)(a.N - n0 < BN ? a.N - n0 : BN) - 1;
+  const int mlast = (int)(a.M - m0 < BM ? a.M - m0 : BM) - 1;
+  uint32_t off[LOADS];
+#pragma unroll
+  for (int j = 0; j < LOADS; ++j) {
+    const int r = (j * NW + wave) * 8 + lane / 8;
+    const int chunk = (lane % 8) ^ (r / 2 % 8);
+    const int row = j * NW * 8 < BN ? min(r, nlast) : min(r - BN, mlast);
+    off[j] = (uint32_t)row * (uint32_t)a.K + chunk * 16;
+  }
+  const int8_t* wp = a.wq + n0 * a.K;
+  const int8_t* xp = a.q + m0 * a.K;
+  const int steps = a.K / BK;
+  // this wavefront's part of step s; past the last step it loads that step
+  // again, into a buffer that no one reads any more
+  auto stage = [&](int s) {
+    const int64_t k = (int64_t)(s < steps ? s : steps - 1) * BK;
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j)
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)((j * NW * 8 < BN ? wp : xp) + k + off[j]),
+          (__attribute__((address_space(3))) void*)(sm + (s & 1) * STAGE + (j * NW + wave) * 1024), 16, 0, 0);
+  };
+  const int wn = wave % WN, wm = wave / WN;
+  const int rw = wn * (BN / WN) + (lane & 31), rx = BN + wm * (BM / WM) + (lane & 31);
+  const int half = lane >> 5;
+  i32x16 acc[TN][TM] = {};
+  i32x4 wf[4][TN], xf[4][TM];
+  auto frags = [&](int s) {
+    const int8_t* b = sm + (s & 1) * STAGE;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+      for (int t = 0; t < TN; ++t)
+        wf[kk][t] = load16(b + (rw + 32 * t) * BK + (((2 * kk + half) ^ (rw / 2 % 8)) << 4));
+#pragma unroll
+      for (int t = 0; t < TM; ++t)
+        xf[kk][t] = load16(b + (rx + 32 * t) * BK + (((2 * kk + half) ^ (rx / 2 % 8)) << 4));
+    }
+  };
+  auto product = [&](int k0) {
+#pragma unroll
+    for (int kk = k0; kk < k0 + 2; ++kk)
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm)
+          acc[tn][tm] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[kk][tn], xf[kk][tm], acc[tn][tm], 0, 0, 0);
+  };
+#define SSD_FENCE(text)                     \
+  __builtin_amdgcn_sched_barrier(0);        \
+  asm volatile(text ::: "memory");          \
+  __builtin_amdgcn_sched_barrier(0)
+  stage(0);
+  if (wave < 4) {
+    SSD_FENCE("s_waitcnt vmcnt(0)\n\ts_barrier");
+    for (int s = 0; s < steps; ++s) {
+      frags(s);
+      stage(s + 1);
+      SSD_FENCE("s_waitcnt lgkmcnt(0)\n\ts_barrier");
+      product(0);
+      SSD_FENCE("s_barrier");
+      product(2);
+      SSD_FENCE("s_waitcnt vmcnt(0)\n\ts_barrier");
+    }
+  } else {
+    stage(1);
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LOADS) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    SSD_FENCE("s_barrier");
+    frags(0);
+    SSD_FENCE("s_waitcnt vmcnt(0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier");
+    stage(2);
+    SSD_FENCE("s_barrier");
+    for (int s = 1; s < steps; ++s) {
+      product(0);
+      product(2);
+      SSD_FENCE("s_barrier");
+      frags(s);
+      SSD_FENCE("s_waitcnt vmcnt(0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier");
+      stage(s + 2);
+      SSD_FENCE("s_barrier");
+    }
+    product(0);
+    product(2);
+  }
+  SSD_FENCE("s_waitcnt vmcnt(0)");   // no load may reach LDS after the end
+  SSD_FENCE("s_barrier");            // every wavefront has read its operands
+  store_tile<T, TN, TM>(a, acc, sm + wave * kOutBytes, n0 + wn * (BN / WN), m0 + wm * (BM / WM), lane);
+}
+
+template <typename T, int TN, int TM>
+hipError_t turns(const LinearQ8Args& a, hipStream_t s) {
+  constexpr int BN = 64 * TN, BM = 128 * TM;
+  const int32_t nt = (int32_t)((a.N + BN - 1) / BN), mt = (int32_t)((a.M + BM - 1) / BM);
+  hipLaunchKernelGGL((k_linear_q8_turns<T, TN, TM>), dim3((unsigned)(nt * mt)), dim3(512), 0, s, a, nt, mt);
+  return hipGetLastError();
+}
+
+template <typename T, int NW, int UN>
+hipError_t stream(const LinearQ8Args& a, hipStream_t s) {
+  hipLaunchKernelGGL((k_linear_q8_stream<T, NW, UN>), dim3((unsigned)((a.N + 15) / 16)), dim3(64 * NW), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename T, int BN, int BM, int WN, int WM, int NS>
+hipError_t tile(const LinearQ8Args& a, hipStream_t s) {
+  const int32_t nt = (int32_t)((a.N + BN - 1) / BN), mt = (int32_t)((a.M + BM - 1) / BM);
+  hipLaunchKernelGGL((k_linear_q8_tile<T, BN, BM, WN, WM, NS>), dim3((unsigned)(nt * mt)),
+                     dim3(64 * WN * WM), 0, s, a, nt, mt);
+  return hipGetLastError();
+}
+
+// The kernel for M tokens, N outputs and K columns.  Up to 16 tokens the weights
+// stream (one tile of tokens: the matrix cores idle, and what counts is how
+// many bytes are in flight).  Beyond, the tile with the least modelled time:
+// rounds over the 256 compute units times (fixed + columns / 128 * step), in
+// units of 0.01 us fitted to measurements at 2560 x 5120 and 10576 x 2560 outputs
+// x columns, 16 to 4096 tokens (us):
+//   32 x 32, columns split 4 ways    64 x 2560 x 5120: 10.9   256 x 2560 x 5120: 26
+//   64 x 64                                            17.5                      16.3
+//   128 x 128                                          28.5                      30.4
+//   192 x 256 in turns   4096 x 2560 x 5120: 64  (one round)  4096 x 10576 x 2560: 141
+//   256 x 256 in turns                       68                                  127
+// A larger tile moves fewer bytes per product but fills the last round worse.
+enum Variant { kSplit, kTile64, kTile128, kTurns192, kTurns256 };
+Variant variant_of(int64_t M, int64_t N, int64_t K) {
+  const int64_t steps = K / 128;
+  auto tiles = [&](int64_t bn, int64_t bm) { return ((N + bn - 1) / bn) * ((M + bm - 1) / bm); };
+  auto rounds = [&](int64_t n) { return (n + 255) / 256; };
+  // two 64 x 64 tiles and more share a compute unit
+  const int64_t t64 = tiles(64, 64);
+  const int64_t cost[] = {
+      rounds(tiles(32, 32)) * (220 + 15 * steps),
+      t64 <= 256 ? 200 + 36 * steps : 200 + steps * (22 + 30 * t64 / 256),
+      rounds(tiles(128, 128)) * (200 + 70 * steps),
+      rounds(tiles(192, 256)) * (900 + 136 * steps),
+      rounds(tiles(256, 256)) * (1300 + 140 * steps),
+  };
+  int best = 0;
+  for (int v = 1; v < 5; ++v)
+    if (cost[v] < cost[best]) best = v;
+  return (Variant)best;
+}
+
+template <typename T>
+hipError_t linear_t(const LinearQ8Args& a, hipStream_t s) {
+  if (a.M <= 16) {
+    // a wavefront's share of the columns in one or two rounds of loads: 8
+    // wavefronts of 2 units for up to 2048 columns, 4 of 5 beyond (10576 x 2560:
+    // 8.2 against 8.9 us; 3352 x 768: 3.5 against 4.0 us)
+    return a.K <= 2048 ? stream<T, 8, 2>(a, s) : stream<T, 4, 5>(a, s);
+  }
+  switch (variant_of(a.M, a.N, a.K)) {
+    case kSplit: return split<T, 32, 32, 4, 4>(a, s);
+    case kTile64: return tile<T, 64, 64, 2, 2, 4>(a, s);
+    case kTile128: return tile<T, 128, 128, 4, 2, 4>(a, s);
+    case kTurns192: return turns<T, 3, 2>(a, s);
+    case kTurns256: return turns<T, 4, 2>(a, s);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
 hipError_t launch_linear_q8(const LinearQ8Args& a, bool out_bf16, hipStream_t s) {
-  const int64_t nt = (a.N + 15) / 16, mt = (a.M + 15) / 16;
-  const dim3 grid((unsigned)(nt * mt)), block(64);
-  if (out_bf16) hipLaunchKernelGGL(k_linear_q8<bf16>, grid, block, 0, s, a, nt);
-  else hipLaunchKernelGGL(k_linear_q8<float>, grid, block, 0, s, a, nt);
-  return hipGetLastError();
+  return out_bf16 ? linear_t<bf16>(a, s) : linear_t<float>(a, s);
 }
 
 }  // namespace ssd
