@@ -194,7 +194,7 @@ def _shape(t: Optional[torch.Tensor], name: str, shape) -> None:
     """Raise ValueError unless t is None or has exactly `shape`.  The C ABI
     receives bare pointers and cannot see a buffer's extent, so every tensor's
     shape is checked here, before any launch."""
-    if t is not None and tuple(t.shape) != tuple(int(v) for v in shape):
+    if t is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(int(v) for v in shape)}, "
                          f"got {tuple(t.shape)}")
 
@@ -203,8 +203,15 @@ def _nbytes(t: torch.Tensor) -> int:
     return t.numel() * t.element_size()
 
 
-def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+# The current stream's handle without a torch.cuda.Stream object around it,
+# which costs a one-token call 1.8 us of its 9.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(device) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _scan_shapes(x, dt, A, B, C, D=None, dt_bias=None, initial_state=None) -> None:
@@ -538,8 +545,8 @@ def ssd_conv1d_backward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[to
     K = weight.shape[1]
     io = x.dtype
     code = _io_code(io)
-    g = _grad_buffers(grads, {"dx": ((Bt, T, Dc), io), "dweight": ((Dc, K), torch.float32),
-                              "dbias": ((Dc,), torch.float32), "dstate": ((Bt, Dc, K - 1), io)})
+    g = _check_grads(grads, {"dx": x.shape, "dweight": weight.shape, "dbias": (Dc,),
+                             "dstate": (Bt, Dc, K - 1)})
     _shape(dy, "dy", (Bt, T, Dc))
     _shape(bias, "bias", (Dc,))
     _shape(state, "state", (Bt, Dc, K - 1))
@@ -549,43 +556,36 @@ def ssd_conv1d_backward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[to
                       (dy, "dy", torch.float32 if dy.dtype == torch.float32 else io),
                       (dstate_out, "dstate_out", io)):
         _check(t, n, dt_)
-    out = _allocate(g, x.device)
+    dev, f32 = x.device, torch.float32
+    dx = _output(g.get("dx"), "dx", x.shape, io, dev)
+    dweight = _output(g.get("dweight"), "dweight", weight.shape, f32, dev)
+    dbias = _output(g.get("dbias"), "dbias", (Dc,), f32, dev)
+    dstate = _output(g.get("dstate"), "dstate", (Bt, Dc, K - 1), io, dev)
     desc = ConvDesc(Bt, T, Dc, K, code, int(bool(silu)))
-    workspace = _workspace(workspace, lib.ssd_conv1d_backward_workspace_bytes, desc, x.device)
+    workspace = _workspace(workspace, lib.ssd_conv1d_backward_workspace_bytes, desc, dev)
     st = lib.ssd_conv1d_backward(
-        ctypes.byref(desc), _io_code(dy.dtype), _ptr(x), _ptr(weight), _ptr(bias), _ptr(state),
-        _ptr(dy), _ptr(dstate_out), _ptr(out["dx"]), _ptr(out["dweight"]), _ptr(out["dbias"]),
-        _ptr(out["dstate"]), _ptr(workspace), _nbytes(workspace), _stream(x.device))
+        ctypes.byref(desc), _io_code(dy.dtype), x.data_ptr(), weight.data_ptr(), _data(bias),
+        _data(state), dy.data_ptr(), _data(dstate_out), dx.data_ptr(), dweight.data_ptr(),
+        dbias.data_ptr(), dstate.data_ptr(), workspace.data_ptr(), _nbytes(workspace), _stream(dev))
     if st != SSD_OK:
         raise SSDError(st, "ssd_conv1d_backward")
-    return out
+    return {"dx": dx, "dweight": dweight, "dbias": dbias, "dstate": dstate}
 
 
 # ---------------------------------------------------------------------------
 # Norms, 8-bit rows and their product.  Tensors are [..., columns]: the leading
 # dimensions are rows.
 # ---------------------------------------------------------------------------
-def _grad_buffers(grads: Optional[dict], want: dict) -> dict:
-    """The caller's gradient buffers checked against {name: (shape, dtype)}, the
-    rest left to _allocate; shapes are checked here, before device placement."""
-    grads = grads or {}
-    unknown = set(grads) - set(want)
+def _check_grads(grads: Optional[dict], shapes: dict) -> dict:
+    """The caller's gradient buffers (by name) checked against their shapes."""
+    if not grads:
+        return {}
+    unknown = set(grads) - set(shapes)
     if unknown:
         raise ValueError(f"unknown gradient names {sorted(unknown)}")
     for k, v in grads.items():
-        _shape(v, k, want[k][0])
-    return {k: (grads.get(k), *want[k]) for k in want}
-
-
-def _allocate(buffers: dict, device) -> dict:
-    out = {}
-    for k, (v, shape, dtype) in buffers.items():
-        if v is None:
-            v = torch.empty(shape, device=device, dtype=dtype)
-        else:
-            _check(v, k, dtype)
-        out[k] = v
-    return out
+        _shape(v, k, shapes[k])
+    return grads
 
 
 def _workspace(workspace: Optional[torch.Tensor], query, desc, device) -> torch.Tensor:
@@ -599,6 +599,8 @@ def _workspace(workspace: Optional[torch.Tensor], query, desc, device) -> torch.
 def _row_stride(t: torch.Tensor, name: str) -> int:
     """Elements between the rows of t [..., D], whose rows must be dense and
     evenly spaced (a slice of a projection's columns is)."""
+    if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]:
+        return t.stride(0)
     if t.dim() < 2:
         return t.shape[-1]
     if t.numel() == 0:
@@ -635,33 +637,39 @@ def q8_cols(cols: int) -> int:
     return (cols + SSD_Q8_PAD - 1) // SSD_Q8_PAD * SSD_Q8_PAD
 
 
-def _add_norm_call(x, weight, residual, scale, eps, residual_out, **outs):
+def _add_norm_args(x, weight, residual, residual_out):
+    """Checks of the residual add and norm; (io code, D, residual_out)."""
     if x.dim() < 1 or weight.dim() != 1:
         raise ValueError("x [..., D], weight [D]")
-    D = x.shape[-1]
+    shape = x.shape
+    D = shape[-1]
     _shape(weight, "weight", (D,))
-    _shape(residual, "residual", x.shape)
-    _shape(residual_out, "residual_out", x.shape)
-    want = {"y": (x.shape, x.dtype), "q": ((*x.shape[:-1], q8_cols(D)), torch.int8),
-            "qscale": (x.shape[:-1], torch.float32)}
-    for k, v in outs.items():
-        _shape(v, k, want[k][0])
+    _shape(residual, "residual", shape)
+    _shape(residual_out, "residual_out", shape)
     code = _io_code(x.dtype)
-    for t, n, dt_ in ((x, "x", None), (weight, "weight", torch.float32),
-                      (residual, "residual", torch.float32),
-                      (residual_out, "residual_out", torch.float32)):
-        _check(t, n, dt_)
-    dev = x.device
-    outs = _allocate({k: (v, *want[k]) for k, v in outs.items()}, dev)
+    _check(x, "x")
+    _check(weight, "weight", torch.float32)
+    _check(residual, "residual", torch.float32)
     if residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=torch.float32, device=dev)
-    desc = AddNormDesc(x.numel() // max(D, 1), D, code, float(scale), float(eps))
-    head = (ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(weight))
-    call = lib.ssd_add_norm if "y" in outs else lib.ssd_add_norm_q8
-    st = call(*head, *[_ptr(v) for v in outs.values()], _ptr(residual_out), _stream(dev))
-    if st != SSD_OK:
-        raise SSDError(st, "ssd_add_norm" if "y" in outs else "ssd_add_norm_q8")
-    return (*outs.values(), residual_out)
+        if residual is not None:
+            residual_out = torch.empty_like(residual)
+        else:
+            residual_out = torch.empty(shape, dtype=torch.float32, device=x.device)
+    else:
+        _check(residual_out, "residual_out", torch.float32)
+    return code, D, residual_out
+
+
+def _output(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Tensor:
+    """The caller's output buffer, checked (its shape was), or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check(t, name, dtype)
+    return t
+
+
+def _data(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def ssd_add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
@@ -674,7 +682,18 @@ def ssd_add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
     x [..., D] float32 or bfloat16, residual [..., D] float32 or None (zeros),
     weight [D] float32.  Returns (y in x's dtype, residual_out float32).
     residual_out may be `residual` itself (updated in place)."""
-    return _add_norm_call(x, weight, residual, scale, eps, residual_out, y=y)
+    _shape(y, "y", x.shape)
+    code, D, residual_out = _add_norm_args(x, weight, residual, residual_out)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _check(y, "y", x.dtype)
+    desc = AddNormDesc(x.numel() // max(D, 1), D, code, scale, eps)
+    st = lib.ssd_add_norm(ctypes.byref(desc), x.data_ptr(), _data(residual), weight.data_ptr(),
+                          y.data_ptr(), residual_out.data_ptr(), _stream(x.device))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_add_norm")
+    return y, residual_out
 
 
 def ssd_add_norm_q8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -684,7 +703,20 @@ def ssd_add_norm_q8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[to
                     ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """ssd_add_norm with y quantised to 8-bit rows in the same pass: returns
     (q [..., q8_cols(D)] int8, qscale [...] float32, residual_out)."""
-    return _add_norm_call(x, weight, residual, scale, eps, residual_out, q=q, qscale=qscale)
+    rows = x.shape[:-1]
+    qshape = (*rows, q8_cols(x.shape[-1])) if x.dim() else ()
+    _shape(q, "q", qshape)
+    _shape(qscale, "qscale", rows)
+    code, D, residual_out = _add_norm_args(x, weight, residual, residual_out)
+    dev = x.device
+    q = _output(q, "q", qshape, torch.int8, dev)
+    qscale = _output(qscale, "qscale", rows, torch.float32, dev)
+    desc = AddNormDesc(x.numel() // max(D, 1), D, code, scale, eps)
+    st = lib.ssd_add_norm_q8(ctypes.byref(desc), x.data_ptr(), _data(residual), weight.data_ptr(),
+                             q.data_ptr(), qscale.data_ptr(), residual_out.data_ptr(), _stream(dev))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_add_norm_q8")
+    return q, qscale, residual_out
 
 
 def ssd_add_norm_backward(residual_out: torch.Tensor, weight: torch.Tensor, *, dy: torch.Tensor,
@@ -703,47 +735,38 @@ def ssd_add_norm_backward(residual_out: torch.Tensor, weight: torch.Tensor, *, d
     _shape(dy, "dy", shape)
     _shape(dresidual_out, "dresidual_out", shape)
     code = _io_code(dy.dtype)
-    g = _grad_buffers(grads, {"dx": (shape, dy.dtype), "dresidual": (shape, f32),
-                              "dweight": ((D,), f32)})
-    for t, n, dt_ in ((residual_out, "residual_out", f32), (weight, "weight", f32),
-                      (dy, "dy", None), (dresidual_out, "dresidual_out", f32)):
-        _check(t, n, dt_)
+    g = _check_grads(grads, {"dx": shape, "dresidual": shape, "dweight": (D,)})
+    _check(residual_out, "residual_out", f32)
+    _check(weight, "weight", f32)
+    _check(dy, "dy")
+    _check(dresidual_out, "dresidual_out", f32)
     dev = dy.device
-    out = _allocate(g, dev)
-    desc = AddNormDesc(dy.numel() // max(D, 1), D, code, float(scale), float(eps))
+    dx = _output(g.get("dx"), "dx", shape, dy.dtype, dev)
+    dresidual = _output(g.get("dresidual"), "dresidual", shape, f32, dev)
+    dweight = _output(g.get("dweight"), "dweight", (D,), f32, dev)
+    desc = AddNormDesc(dy.numel() // max(D, 1), D, code, scale, eps)
     workspace = _workspace(workspace, lib.ssd_add_norm_backward_workspace_bytes, desc, dev)
     st = lib.ssd_add_norm_backward(
-        ctypes.byref(desc), _ptr(residual_out), _ptr(weight), _ptr(dy), _ptr(dresidual_out),
-        _ptr(out["dx"]), _ptr(out["dresidual"]), _ptr(out["dweight"]), _ptr(workspace),
-        _nbytes(workspace), _stream(dev))
+        ctypes.byref(desc), residual_out.data_ptr(), weight.data_ptr(), dy.data_ptr(),
+        _data(dresidual_out), dx.data_ptr(), dresidual.data_ptr(), dweight.data_ptr(),
+        workspace.data_ptr(), _nbytes(workspace), _stream(dev))
     if st != SSD_OK:
         raise SSDError(st, "ssd_add_norm_backward")
-    return out
+    return {"dx": dx, "dresidual": dresidual, "dweight": dweight}
 
 
-def _gated_norm_call(y, z, weight, groups, eps, **outs):
+def _gated_norm_desc(y, z, weight, groups, eps) -> GatedNormDesc:
+    """Checks of the gated norm; its descriptor."""
     if y.dim() < 1 or weight.dim() != 1:
         raise ValueError("y [..., D], z [..., D], weight [D]")
     D = y.shape[-1]
     _shape(z, "z", y.shape)
     _shape(weight, "weight", (D,))
-    want = {"out": (y.shape, y.dtype), "q": ((*y.shape[:-1], q8_cols(D)), torch.int8),
-            "qscale": (y.shape[:-1], torch.float32)}
-    for k, v in outs.items():
-        _shape(v, k, want[k][0])
     code = _io_code(y.dtype)
     _check(y, "y")
     _check(weight, "weight", torch.float32)
     stride = _check_rows(z, "z", y.dtype)
-    dev = y.device
-    outs = _allocate({k: (v, *want[k]) for k, v in outs.items()}, dev)
-    desc = GatedNormDesc(y.numel() // max(D, 1), D, int(groups), stride, 0, code, float(eps))
-    call = lib.ssd_gated_norm if "out" in outs else lib.ssd_gated_norm_q8
-    st = call(ctypes.byref(desc), _ptr(y), _ptr(z), _ptr(weight),
-              *[_ptr(v) for v in outs.values()], _stream(dev))
-    if st != SSD_OK:
-        raise SSDError(st, "ssd_gated_norm" if "out" in outs else "ssd_gated_norm_q8")
-    return tuple(outs.values())
+    return GatedNormDesc(y.numel() // max(D, 1), D, groups, stride, 0, code, eps)
 
 
 def ssd_gated_norm(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *, groups: int = 1,
@@ -753,7 +776,17 @@ def ssd_gated_norm(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *, gr
 
     y [..., D] float32 or bfloat16, z [..., D] in y's dtype with evenly spaced
     rows (a slice of the projection's columns), weight [D] float32."""
-    return _gated_norm_call(y, z, weight, groups, eps, out=out)[0]
+    _shape(out, "out", y.shape)
+    desc = _gated_norm_desc(y, z, weight, groups, eps)
+    if out is None:
+        out = torch.empty_like(y)
+    else:
+        _check(out, "out", y.dtype)
+    st = lib.ssd_gated_norm(ctypes.byref(desc), y.data_ptr(), z.data_ptr(), weight.data_ptr(),
+                            out.data_ptr(), _stream(y.device))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_gated_norm")
+    return out
 
 
 def ssd_gated_norm_q8(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *, groups: int = 1,
@@ -761,7 +794,19 @@ def ssd_gated_norm_q8(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *,
                       qscale: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """ssd_gated_norm with its output quantised to 8-bit rows in the same pass:
     returns (q [..., q8_cols(D)] int8, qscale [...] float32)."""
-    return _gated_norm_call(y, z, weight, groups, eps, q=q, qscale=qscale)
+    rows = y.shape[:-1]
+    qshape = (*rows, q8_cols(y.shape[-1])) if y.dim() else ()
+    _shape(q, "q", qshape)
+    _shape(qscale, "qscale", rows)
+    desc = _gated_norm_desc(y, z, weight, groups, eps)
+    dev = y.device
+    q = _output(q, "q", qshape, torch.int8, dev)
+    qscale = _output(qscale, "qscale", rows, torch.float32, dev)
+    st = lib.ssd_gated_norm_q8(ctypes.byref(desc), y.data_ptr(), z.data_ptr(), weight.data_ptr(),
+                               q.data_ptr(), qscale.data_ptr(), _stream(dev))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_gated_norm_q8")
+    return q, qscale
 
 
 def ssd_gated_norm_backward(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *,
@@ -778,30 +823,28 @@ def ssd_gated_norm_backward(y: torch.Tensor, z: torch.Tensor, weight: torch.Tens
     _shape(weight, "weight", (D,))
     _shape(dout, "dout", shape)
     code = _io_code(io)
-    g = _grad_buffers(grads, {"dy": (shape, io), "dz": (shape, io),
-                              "dweight": ((D,), torch.float32)})
+    g = _check_grads(grads, {"dy": shape, "dz": shape, "dweight": (D,)})
     _check(y, "y")
     _check(weight, "weight", torch.float32)
     _check(dout, "dout", io)
     z_stride = _check_rows(z, "z", io)
     dev = y.device
-    dz = g["dz"][0]
+    dz = g.get("dz")
     if dz is not None:
         dz_stride = _check_rows(dz, "dz", io)
     else:
         dz, dz_stride = torch.empty(shape, dtype=io, device=dev), D
-    del g["dz"]
-    out = _allocate(g, dev)
-    out["dz"] = dz
-    desc = GatedNormDesc(y.numel() // max(D, 1), D, int(groups), z_stride, dz_stride, code,
-                         float(eps))
+    dy = _output(g.get("dy"), "dy", shape, io, dev)
+    dweight = _output(g.get("dweight"), "dweight", (D,), torch.float32, dev)
+    desc = GatedNormDesc(y.numel() // max(D, 1), D, groups, z_stride, dz_stride, code, eps)
     workspace = _workspace(workspace, lib.ssd_gated_norm_backward_workspace_bytes, desc, dev)
     st = lib.ssd_gated_norm_backward(
-        ctypes.byref(desc), _ptr(y), _ptr(z), _ptr(weight), _ptr(dout), _ptr(out["dy"]), _ptr(dz),
-        _ptr(out["dweight"]), _ptr(workspace), _nbytes(workspace), _stream(dev))
+        ctypes.byref(desc), y.data_ptr(), z.data_ptr(), weight.data_ptr(), dout.data_ptr(),
+        dy.data_ptr(), dz.data_ptr(), dweight.data_ptr(), workspace.data_ptr(),
+        _nbytes(workspace), _stream(dev))
     if st != SSD_OK:
         raise SSDError(st, "ssd_gated_norm_backward")
-    return out
+    return {"dy": dy, "dz": dz, "dweight": dweight}
 
 
 def ssd_quantize_q8(v: torch.Tensor, *, q: Optional[torch.Tensor] = None,
@@ -811,18 +854,20 @@ def ssd_quantize_q8(v: torch.Tensor, *, q: Optional[torch.Tensor] = None,
     q8_cols(K)] int8, zero-padded, and qscale [...] float32)."""
     if v.dim() < 1:
         raise ValueError("v [..., K]")
-    K = v.shape[-1]
-    want = {"q": ((*v.shape[:-1], q8_cols(K)), torch.int8), "qscale": (v.shape[:-1], torch.float32)}
-    _shape(q, "q", want["q"][0])
-    _shape(qscale, "qscale", want["qscale"][0])
+    K, rows = v.shape[-1], v.shape[:-1]
+    qshape = (*rows, q8_cols(K))
+    _shape(q, "q", qshape)
+    _shape(qscale, "qscale", rows)
     code = _io_code(v.dtype)
     _check(v, "v")
-    out = _allocate({"q": (q, *want["q"]), "qscale": (qscale, *want["qscale"])}, v.device)
-    st = lib.ssd_quantize_q8(v.numel() // max(K, 1), K, code, _ptr(v), _ptr(out["q"]),
-                             _ptr(out["qscale"]), _stream(v.device))
+    dev = v.device
+    q = _output(q, "q", qshape, torch.int8, dev)
+    qscale = _output(qscale, "qscale", rows, torch.float32, dev)
+    st = lib.ssd_quantize_q8(v.numel() // max(K, 1), K, code, v.data_ptr(), q.data_ptr(),
+                             qscale.data_ptr(), _stream(dev))
     if st != SSD_OK:
         raise SSDError(st, "ssd_quantize_q8")
-    return out["q"], out["qscale"]
+    return q, qscale
 
 
 def ssd_linear_q8(q: torch.Tensor, qscale: torch.Tensor, wq: torch.Tensor, wscale: torch.Tensor, *,
@@ -845,14 +890,15 @@ def ssd_linear_q8(q: torch.Tensor, qscale: torch.Tensor, wq: torch.Tensor, wscal
     _shape(wscale, "wscale", (N,))
     _shape(out, "out", shape)
     code = _io_code(out_dtype)
-    for t, n, dt_ in ((q, "q", torch.int8), (qscale, "qscale", torch.float32),
-                      (wq, "wq", torch.int8), (wscale, "wscale", torch.float32), (out, "out", None)):
-        _check(t, n, dt_)
-    if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=q.device)
+    _check(q, "q", torch.int8)
+    _check(qscale, "qscale", torch.float32)
+    _check(wq, "wq", torch.int8)
+    _check(wscale, "wscale", torch.float32)
+    dev = q.device
+    out = _output(out, "out", shape, out_dtype, dev)
     desc = LinearQ8Desc(q.numel() // max(Kp, 1), Kp, N, code)
-    st = lib.ssd_linear_q8(ctypes.byref(desc), _ptr(q), _ptr(qscale), _ptr(wq), _ptr(wscale),
-                           _ptr(out), _stream(q.device))
+    st = lib.ssd_linear_q8(ctypes.byref(desc), q.data_ptr(), qscale.data_ptr(), wq.data_ptr(),
+                           wscale.data_ptr(), out.data_ptr(), _stream(dev))
     if st != SSD_OK:
         raise SSDError(st, "ssd_linear_q8")
     return out
