@@ -556,10 +556,10 @@ def ssd_conv1d_backward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[to
                       (dy, "dy", torch.float32 if dy.dtype == torch.float32 else io),
                       (dstate_out, "dstate_out", io)):
         _check(t, n, dt_)
-    dev, f32 = x.device, torch.float32
-    dx = _output(g.get("dx"), "dx", x.shape, io, dev)
-    dweight = _output(g.get("dweight"), "dweight", weight.shape, f32, dev)
-    dbias = _output(g.get("dbias"), "dbias", (Dc,), f32, dev)
+    dev = x.device
+    dx = _like(g.get("dx"), "dx", x)
+    dweight = _like(g.get("dweight"), "dweight", weight)
+    dbias = _output(g.get("dbias"), "dbias", (Dc,), torch.float32, dev)
     dstate = _output(g.get("dstate"), "dstate", (Bt, Dc, K - 1), io, dev)
     desc = ConvDesc(Bt, T, Dc, K, code, int(bool(silu)))
     workspace = _workspace(workspace, lib.ssd_conv1d_backward_workspace_bytes, desc, dev)
@@ -668,6 +668,14 @@ def _output(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch
     return t
 
 
+def _like(t: Optional[torch.Tensor], name: str, like: torch.Tensor) -> torch.Tensor:
+    """_output with the shape, type and device of a dense tensor."""
+    if t is None:
+        return torch.empty_like(like)
+    _check(t, name, like.dtype)
+    return t
+
+
 def _data(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -684,10 +692,7 @@ def ssd_add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
     residual_out may be `residual` itself (updated in place)."""
     _shape(y, "y", x.shape)
     code, D, residual_out = _add_norm_args(x, weight, residual, residual_out)
-    if y is None:
-        y = torch.empty_like(x)
-    else:
-        _check(y, "y", x.dtype)
+    y = _like(y, "y", x)
     desc = AddNormDesc(x.numel() // max(D, 1), D, code, scale, eps)
     st = lib.ssd_add_norm(ctypes.byref(desc), x.data_ptr(), _data(residual), weight.data_ptr(),
                           y.data_ptr(), residual_out.data_ptr(), _stream(x.device))
@@ -741,9 +746,9 @@ def ssd_add_norm_backward(residual_out: torch.Tensor, weight: torch.Tensor, *, d
     _check(dy, "dy")
     _check(dresidual_out, "dresidual_out", f32)
     dev = dy.device
-    dx = _output(g.get("dx"), "dx", shape, dy.dtype, dev)
-    dresidual = _output(g.get("dresidual"), "dresidual", shape, f32, dev)
-    dweight = _output(g.get("dweight"), "dweight", (D,), f32, dev)
+    dx = _like(g.get("dx"), "dx", dy)
+    dresidual = _like(g.get("dresidual"), "dresidual", residual_out)
+    dweight = _like(g.get("dweight"), "dweight", weight)
     desc = AddNormDesc(dy.numel() // max(D, 1), D, code, scale, eps)
     workspace = _workspace(workspace, lib.ssd_add_norm_backward_workspace_bytes, desc, dev)
     st = lib.ssd_add_norm_backward(
@@ -778,10 +783,7 @@ def ssd_gated_norm(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *, gr
     rows (a slice of the projection's columns), weight [D] float32."""
     _shape(out, "out", y.shape)
     desc = _gated_norm_desc(y, z, weight, groups, eps)
-    if out is None:
-        out = torch.empty_like(y)
-    else:
-        _check(out, "out", y.dtype)
+    out = _like(out, "out", y)
     st = lib.ssd_gated_norm(ctypes.byref(desc), y.data_ptr(), z.data_ptr(), weight.data_ptr(),
                             out.data_ptr(), _stream(y.device))
     if st != SSD_OK:
@@ -833,9 +835,9 @@ def ssd_gated_norm_backward(y: torch.Tensor, z: torch.Tensor, weight: torch.Tens
     if dz is not None:
         dz_stride = _check_rows(dz, "dz", io)
     else:
-        dz, dz_stride = torch.empty(shape, dtype=io, device=dev), D
-    dy = _output(g.get("dy"), "dy", shape, io, dev)
-    dweight = _output(g.get("dweight"), "dweight", (D,), torch.float32, dev)
+        dz, dz_stride = torch.empty_like(y), D
+    dy = _like(g.get("dy"), "dy", y)
+    dweight = _like(g.get("dweight"), "dweight", weight)
     desc = GatedNormDesc(y.numel() // max(D, 1), D, groups, z_stride, dz_stride, code, eps)
     workspace = _workspace(workspace, lib.ssd_gated_norm_backward_workspace_bytes, desc, dev)
     st = lib.ssd_gated_norm_backward(

@@ -79,14 +79,14 @@ __global__ __launch_bounds__(64 * NW) void k_linear_q8_stream(LinearQ8Args a) {
                (int)(a.N - nn < 4 ? a.N - nn : 4));
 }
 
-// The tile of a workgroup, of nt x mt: consecutive tiles run on one XCD, in
+// The k-th tile in launch order, of nt x mt: those of one XCD are consecutive, in
 // groups of 8 tile rows, so that the tiles it holds at a time share both
 // operands' panels in its L2.
 struct TileOf {
   int32_t n, m;
-  __device__ __forceinline__ TileOf(int32_t nt, int32_t mt) {
+  __device__ __forceinline__ TileOf(int32_t nt, int32_t mt, int32_t k) {
     constexpr int32_t kRows = 8;
-    const uint32_t id = (uint32_t)xcd_remap(blockIdx.x, (int64_t)nt * mt);
+    const uint32_t id = (uint32_t)xcd_remap(k, (int64_t)nt * mt);
     const uint32_t per = kRows * nt, group = id / per, in = id % per, first = group * kRows;
     const uint32_t size = min((uint32_t)mt - first, (uint32_t)kRows);
     // divisions are done on the vector unit; the results are the same in every lane
@@ -152,103 +152,99 @@ __device__ __forceinline__ void store_tile(const LinearQ8Args& a, const i32x16 (
 
 // ---------------------------------------------------------------------------
 // Many tokens: BN outputs x BM tokens per workgroup, WN x WM wavefronts, the
-// operands staged through LDS 128 columns at a time in two buffers.
+// operands staged through LDS 128 columns at a time in a ring of NS buffers.
 //
 // Global loads write LDS directly, 16 bytes per lane: a wavefront's load fills
 // 8 rows of 128 bytes.  The 16-byte chunk c of row r is kept at position
 // c ^ (r / 2 % 8) of its row, so that the 16 lanes of a read phase, which take
 // one chunk of 16 adjacent rows, meet 16 different quarter-banks; the swizzle
 // is applied to the global address, as the LDS side of such a load is linear.
+// (Columns go 128 at a time because a cache line holds them: with 64, every
+// line is requested twice, 8192 x 8192 x 8192: 515 -> 555 us.)
 // ---------------------------------------------------------------------------
 template <typename T, int BN, int BM, int WN, int WM, int NS>
 __global__ __launch_bounds__(64 * WN * WM) void k_linear_q8_tile(LinearQ8Args a, int32_t nt,
                                                                   int32_t mt) {
-  constexpr int NW = WN * WM, BK = 128;
+  constexpr int NW = WN * WM, BK = 128, KK = BK / 32;
   constexpr int TN = BN / WN / 32, TM = BM / WM / 32;   // 32 x 32 tiles of a wavefront
-  constexpr int ROWS = BN + BM, CPR = BK / 16, RPL = 64 / CPR;   // chunks per row, rows per load
-  constexpr int LOADS = ROWS / RPL / NW;
-  static_assert(BM % (RPL * NW) == 0 && BN % (RPL * NW) == 0);
-  static_assert((NS - 2) * LOADS < 64);
-  constexpr int STAGE = ROWS * BK, BYTES = NS * STAGE > NW * kOutBytes ? NS * STAGE : NW * kOutBytes;
-  __shared__ __align__(1024) int8_t sm[BYTES];
+  constexpr int STAGE = (BN + BM) * BK, LOADS = (BN + BM) / 8 / NW;
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && (NS - 2) * LOADS < 64);
+  // (the outputs pass through the same memory afterwards)
+  __shared__ __align__(1024) int8_t sm[NS * STAGE > NW * kOutBytes ? NS * STAGE : NW * kOutBytes];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const TileOf at(nt, mt);
+  const TileOf at(nt, mt, blockIdx.x);
   const int64_t m0 = (int64_t)at.m * BM, n0 = (int64_t)at.n * BN;
 
+  // rows past the end repeat the last one (their outputs are not stored)
   const int8_t* wp = a.wq + n0 * a.K;
   const int8_t* xp = a.q + m0 * a.K;
-  const int nlast = (int)(a.N - n0 < BN ? a.N - n0 : BN) - 1, mlast = (int)(a.M - m0 < BM ? a.M - m0 : BM) - 1;
+  const int nlast = (int)(a.N - n0 < BN ? a.N - n0 : BN) - 1;
+  const int mlast = (int)(a.M - m0 < BM ? a.M - m0 : BM) - 1;
   uint32_t off[LOADS];
 #pragma unroll
   for (int j = 0; j < LOADS; ++j) {
-    const int r = (j * NW + wave) * RPL + lane / CPR;
-    const int chunk = (lane % CPR) ^ (r / (16 / CPR) % CPR);
-    const int row = j * NW * RPL < BN ? min(r, nlast) : min(r - BN, mlast);
+    const int r = (j * NW + wave) * 8 + lane / 8, chunk = (lane % 8) ^ (r / 2 % 8);
+    const int row = j * NW * 8 < BN ? min(r, nlast) : min(r - BN, mlast);
     off[j] = (uint32_t)row * (uint32_t)a.K + chunk * 16;
   }
-  auto stage_part = [&](int buf, int j0, int j1) {
+  // part of the loads of the step wp and xp point at
+  auto stage = [&](int buf, int j0, int j1) {
 #pragma unroll
-    for (int j = j0; j < j1; ++j) {
-      const int8_t* base = j * NW * RPL < BN ? wp : xp;
+    for (int j = j0; j < j1; ++j)
       __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void*)(base + off[j]),
+          (const __attribute__((address_space(1))) void*)((j * NW * 8 < BN ? wp : xp) + off[j]),
           (__attribute__((address_space(3))) void*)(sm + buf * STAGE + (j * NW + wave) * 1024), 16, 0, 0);
-    }
   };
-  auto stage = [&](int buf) {
-    stage_part(buf, 0, LOADS);
-    wp += BK;
-    xp += BK;
-  };
-  const int wn = wave % WN, wm = wave / WN;
-  const int rw = wn * (BN / WN) + (lane & 31), rx = BN + wm * (BM / WM) + (lane & 31);
-  const int half = lane >> 5;
-  i32x16 acc[TN][TM] = {};
   const int steps = a.K / BK;
+  // past the end the last step is loaded again, into a buffer that no one reads
+  auto advance = [&](int s) {
+    wp += s < steps ? BK : 0;
+    xp += s < steps ? BK : 0;
+  };
+  const int wn = wave % WN, wm = wave / WN, half = lane >> 5;
+  const int rw = wn * (BN / WN) + (lane & 31), rx = BN + wm * (BM / WM) + (lane & 31);
+  i32x16 acc[TN][TM] = {};
 #pragma unroll
   for (int p = 0; p < NS - 1; ++p) {
-    stage_part(p, 0, LOADS);
-    wp += p + 1 < steps ? BK : 0;
-    xp += p + 1 < steps ? BK : 0;
+    stage(p, 0, LOADS);
+    advance(p + 1);
   }
-  int cur = 0, nxt = NS - 1;
+  int cur = 0;
   for (int s = 0; s < steps; ++s) {
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * LOADS) : "memory");
+    // step s has landed everywhere, and step s - 1 has been read
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * LOADS)
+                 : "memory");
     const int8_t* b = sm + cur * STAGE;
-    i32x4 wf[BK / 32][TN], xf[BK / 32][TM];
+    i32x4 wf[KK][TN], xf[KK][TM];
     auto frags = [&](int kk) {
 #pragma unroll
       for (int t = 0; t < TN; ++t)
-        wf[kk][t] = load16(b + (rw + 32 * t) * BK + (((2 * kk + half) ^ (rw / (16 / CPR) % CPR)) << 4));
+        wf[kk][t] = load16(b + (rw + 32 * t) * BK + (((2 * kk + half) ^ (rw / 2 % 8)) << 4));
 #pragma unroll
       for (int t = 0; t < TM; ++t)
-        xf[kk][t] = load16(b + (rx + 32 * t) * BK + (((2 * kk + half) ^ (rx / (16 / CPR) % CPR)) << 4));
+        xf[kk][t] = load16(b + (rx + 32 * t) * BK + (((2 * kk + half) ^ (rx / 2 % 8)) << 4));
     };
+    const int free = cur == 0 ? NS - 1 : cur - 1;
     frags(0);
-    // (the last steps load the final columns again into a buffer that no one reads)
-    constexpr int KK = BK / 32, SP = NS == 2 ? (KK + 1) / 2 : KK;
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
       auto product = [&](int i0, int i1) {
 #pragma unroll
-        for (int i = i0; i < i1; ++i) {
-          const int tn = i / TM, tm = i % TM;
-          acc[tn][tm] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[kk][tn], xf[kk][tm], acc[tn][tm], 0, 0, 0);
-        }
+        for (int i = i0; i < i1; ++i)
+          acc[i / TM][i % TM] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
+              wf[kk][i / TM], xf[kk][i % TM], acc[i / TM][i % TM], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
       };
-      constexpr int HEAD = 1;
-      product(0, HEAD);
+      // the next operands and a share of the loads behind the first product
+      product(0, 1);
       if (kk + 1 < KK) frags(kk + 1);
-      if (kk < SP) stage_part(nxt, LOADS * kk / SP, LOADS * (kk + 1) / SP);
+      stage(free, LOADS * kk / KK, LOADS * (kk + 1) / KK);
       __builtin_amdgcn_sched_barrier(0);
-      product(HEAD, TN * TM);
+      product(1, TN * TM);
     }
-    wp += s + NS < steps ? BK : 0;
-    xp += s + NS < steps ? BK : 0;
+    advance(s + NS);
     cur = cur + 1 == NS ? 0 : cur + 1;
-    nxt = nxt + 1 == NS ? 0 : nxt + 1;
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load may reach LDS after this
   __syncthreads();
@@ -267,7 +263,7 @@ __global__ __launch_bounds__(64 * KS) void k_linear_q8_split(LinearQ8Args a, int
   __shared__ __align__(1024) int8_t sm[RING > OUT ? RING : OUT];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const TileOf at(nt, mt);
+  const TileOf at(nt, mt, blockIdx.x);
   const int64_t m0 = (int64_t)at.m * BM, n0 = (int64_t)at.n * BN;
   const int nlast = (int)(a.N - n0 < BN ? a.N - n0 : BN) - 1;
   const int mlast = (int)(a.M - m0 < BM ? a.M - m0 : BM) - 1;
@@ -343,117 +339,279 @@ hipError_t split(const LinearQ8Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Two groups of four wavefronts, one of each group per SIMD, take turns.
-template <typename T, int TN, int TM>
+// Many tiles: 32 TN outputs x 256 tokens, two groups of four wavefronts, one of
+// each group on every SIMD.  The groups take turns: while one multiplies, the
+// other fetches its operands of the next 128 columns from LDS into registers
+// and requests the columns after those.  A load's issue holds its wavefront
+// until the memory pipe takes it, which in the plain kernel above kept the
+// matrix cores waiting for about as long as they worked.  Phase 2g: group 0
+// reads step g from LDS, group 1 multiplies step g-1; phase 2g+1: group 0
+// multiplies step g, group 1 reads it.  A buffer is free for step g+2 once group
+// 1 has read step g, in the middle of phase 2g+1 (the second barrier there).
+//
+// A workgroup stays for several tiles: the loads run on into the next tile, so
+// that its first columns arrive while this one is stored, and the waits for
+// them leave the stores in flight.
+constexpr int64_t kTurnsMaxOuts = 1 << 24;
+constexpr int kTurnsOut = 16 * 256;   // bytes of LDS a wavefront's outputs pass through
+
+template <typename T, int TN>
 __global__ __launch_bounds__(512) void k_linear_q8_turns(LinearQ8Args a, int32_t nt, int32_t mt) {
-  constexpr int WN = 2, WM = 4, NW = 8, BK = 128, BN = WN * TN * 32, BM = WM * TM * 32;
-  constexpr int ROWS = BN + BM, LOADS = ROWS / 8 / NW;
-  static_assert(BN % 64 == 0 && BM % 64 == 0);
-  // two buffers of ROWS x BK bytes; the outputs pass through the same memory
-  constexpr int STAGE = ROWS * BK, BYTES = 2 * STAGE > NW * kOutBytes ? 2 * STAGE : NW * kOutBytes;
-  __shared__ __align__(1024) int8_t sm[BYTES];
+  constexpr int TM = 4, BK = 128, BN = 32 * TN, BM = 256, NW = 8;
+  constexpr int PIECES = (BN + BM) / 8, WPIECES = BN / 8, STAGE = (BN + BM) * BK;
+  constexpr int LOADS = (PIECES + NW - 1) / NW;
+  static_assert(WPIECES % 4 == 0 && PIECES % 4 == 0);   // a group's four loads share an operand
+  constexpr int SW = kTurnsOut / 16 / (int)sizeof(T), ST = SW / 16, CH = SW / 4;
+  // stores of a wavefront's whole tile, at least: every 64 columns and 4 tokens
+  constexpr int STORES = TM * 4 * ((16 * TN + 63) / 64);
+  static_assert(STORES < 64);
+  __shared__ __align__(1024) int8_t sm[2 * STAGE + NW * kTurnsOut];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const TileOf at(nt, mt);
-  const int64_t m0 = (int64_t)at.m * BM, n0 = (int64_t)at.n * BN;
-
-  const int nlast = (int)(a.N - n0 < BN ? a.N - n0 : BN) - 1;
-  const int mlast = (int)(a.M - m0 < BM ? a.M - m0 : BM) - 1;
-  uint32_t off[LOADS];
-#pragma unroll
-  for (int j = 0; j < LOADS; ++j) {
-    const int r = (j * NW + wave) * 8 + lane / 8;
-    const int chunk = (lane % 8) ^ (r / 2 % 8);
-    const int row = j * NW * 8 < BN ? min(r, nlast) : min(r - BN, mlast);
-    off[j] = (uint32_t)row * (uint32_t)a.K + chunk * 16;
-  }
-  const int8_t* wp = a.wq + n0 * a.K;
-  const int8_t* xp = a.q + m0 * a.K;
+  const int wn = wave & 1, wm = wave >> 1, l16 = lane & 15, q4 = lane >> 4;
+  const int32_t tiles = nt * mt;
   const int steps = a.K / BK;
-  // this wavefront's part of step s; past the last step it loads that step
-  // again, into a buffer that no one reads any more
-  auto stage = [&](int s) {
-    const int64_t k = (int64_t)(s < steps ? s : steps - 1) * BK;
+  const int mine = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int total = steps * mine;
+
+  // loader: runs ahead of the products, into the next tile
+  int32_t ltile = blockIdx.x;
+  int lstep = 0;
+  const int8_t *lw, *lx;
+  uint32_t off[LOADS];
+  auto aim = [&]() {
+    // (an opaque lane index here and in finish: what they derive from it is then
+    // formed there instead of being held in registers through the products)
+    const int lane = opaque_tid() & 63;
+    const TileOf at(nt, mt, ltile);
+    lw = a.wq + (int64_t)at.n * BN * a.K;
+    lx = a.q + (int64_t)at.m * BM * a.K;
+    const int64_t nl = a.N - (int64_t)at.n * BN, ml = a.M - (int64_t)at.m * BM;
+    const int nlast = (int)(nl < BN ? nl : BN) - 1, mlast = (int)(ml < BM ? ml : BM) - 1;
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j)
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void*)((j * NW * 8 < BN ? wp : xp) + k + off[j]),
-          (__attribute__((address_space(3))) void*)(sm + (s & 1) * STAGE + (j * NW + wave) * 1024), 16, 0, 0);
-  };
-  const int wn = wave % WN, wm = wave / WN;
-  const int rw = wn * (BN / WN) + (lane & 31), rx = BN + wm * (BM / WM) + (lane & 31);
-  const int half = lane >> 5;
-  i32x16 acc[TN][TM] = {};
-  i32x4 wf[4][TN], xf[4][TM];
-  auto frags = [&](int s) {
-    const int8_t* b = sm + (s & 1) * STAGE;
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-#pragma unroll
-      for (int t = 0; t < TN; ++t)
-        wf[kk][t] = load16(b + (rw + 32 * t) * BK + (((2 * kk + half) ^ (rw / 2 % 8)) << 4));
-#pragma unroll
-      for (int t = 0; t < TM; ++t)
-        xf[kk][t] = load16(b + (rx + 32 * t) * BK + (((2 * kk + half) ^ (rx / 2 % 8)) << 4));
+    for (int j = 0; j < LOADS; ++j) {
+      const int piece = j * NW + wave, r = piece * 8 + lane / 8;
+      const int row = piece < WPIECES ? min(r, nlast) : min(r - BN, mlast);
+      off[j] = (uint32_t)row * (uint32_t)a.K + (((lane % 8) ^ (r / 2 % 8)) << 4);
     }
   };
-  auto product = [&](int k0) {
+  // requests this wavefront's part of the loader's step into buffer g % 2
+  auto stage = [&](auto group, int g) {
+    constexpr int first = 4 * decltype(group)::value;
+    int8_t* dst = sm + (g & 1) * STAGE + wave * 1024;
 #pragma unroll
-    for (int kk = k0; kk < k0 + 2; ++kk)
-#pragma unroll
-      for (int tn = 0; tn < TN; ++tn)
-#pragma unroll
-        for (int tm = 0; tm < TM; ++tm)
-          acc[tn][tm] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[kk][tn], xf[kk][tm], acc[tn][tm], 0, 0, 0);
+    for (int j = 0; j < LOADS; ++j)
+      if (j * NW + first < PIECES)
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void*)(
+                (j * NW + first < WPIECES ? lw : lx) + off[j]),
+            (__attribute__((address_space(3))) void*)(dst + j * NW * 1024), 16, 0, 0);
   };
+  // past the last tile the loader repeats the last step, into a buffer no one
+  // reads any more
+  auto advance = [&]() {
+    if (lstep + 1 < steps) {
+      ++lstep;
+      lw += BK;
+      lx += BK;
+    } else if (ltile + (int)gridDim.x < tiles) {
+      ltile += gridDim.x;
+      lstep = 0;
+      aim();
+    }
+  };
+
+  i32x4 acc[TN][TM] = {};
+  i32x4 wf[2][TN], xf[2][TM];
+  const int rw = wn * (BN / 2) + l16, rx = BN + wm * (BM / 4) + l16;
+  auto frags = [&](int g) {
+    const int8_t* b = sm + (g & 1) * STAGE;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      // (rows 16 apart share the swizzle of their first)
+      const int pos = ((4 * kk + q4) ^ (l16 / 2 % 8)) << 4;
+#pragma unroll
+      for (int t = 0; t < TN; ++t) wf[kk][t] = load16(b + (rw + 16 * t) * BK + pos);
+#pragma unroll
+      for (int t = 0; t < TM; ++t) xf[kk][t] = load16(b + (rx + 16 * t) * BK + pos);
+    }
+  };
+  auto product = [&](int kk) {
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+      for (int tm = 0; tm < TM; ++tm)
+        acc[tn][tm] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[kk][tn], xf[kk][tm], acc[tn][tm], 0, 0, 0);
+  };
+
+  int32_t tile = blockIdx.x;
+  // Stores the finished tile and clears the sums; true for a whole tile, which
+  // issues at least STORES stores.  16 tokens x SW columns at a time pass
+  // through LDS in the output type (four columns of a token at chunk c ^ 2
+  // token), to leave as 64 adjacent columns of four tokens per instruction.
+  // Where every such piece is whole lines of memory they go out non-temporal
+  // (4096 x 10752 outputs: 133 -> 108 us); elsewhere the cache has to join the
+  // pieces (10576 outputs non-temporal: no gain, at 128 columns 37 -> 57 us).
+  // Shifting a token's pieces to its lines took longer (three instead of two
+  // instructions; 115 -> 120 us).
+  auto finish = [&]() {
+    const int lane = opaque_tid() & 63, l16 = lane & 15, q4 = lane >> 4;
+    typedef typename Pack<T, 4>::V V4;
+    const TileOf at(nt, mt, tile);
+    tile += gridDim.x;
+    const int64_t n0 = (int64_t)at.n * BN + wn * (BN / 2), m0 = (int64_t)at.m * BM + wm * (BM / 4);
+    const bool whole = (int64_t)(at.n + 1) * BN <= a.N && (int64_t)(at.m + 1) * BM <= a.M;
+    const bool lines = ((a.N | n0 | (int64_t)(reinterpret_cast<uintptr_t>(a.out) / sizeof(T))) & 63) == 0;
+    int8_t* lds = sm + 2 * STAGE + wave * kTurnsOut;
+    float xs[TM];
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm) {
+      const int64_t m = m0 + 16 * tm + l16;
+      xs[tm] = a.qscale[m < a.M ? m : a.M - 1];
+    }
+#pragma unroll
+    for (int t0 = 0; t0 < TN; t0 += ST) {
+      constexpr int kFull = 16 * ST;
+      const int W = 16 * (TN - t0) < kFull ? 16 * (TN - t0) : kFull;
+      fvec<4> ws[ST];
+#pragma unroll
+      for (int t = 0; t < ST; ++t)
+        if (t0 + t < TN) {
+          const int64_t n = n0 + 16 * (t0 + t) + 4 * q4;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ws[t][e] = a.wscale[n + e < a.N ? n + e : a.N - 1];
+        }
+#pragma unroll
+      for (int tm = 0; tm < TM; ++tm) {
+#pragma unroll
+        for (int t = 0; t < ST; ++t)
+          if (t0 + t < TN) {
+            fvec<4> v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = (float)acc[t0 + t][tm][e] * xs[tm] * ws[t][e];
+            *reinterpret_cast<V4*>(lds + (l16 * CH + ((4 * t + q4) ^ (2 * l16 & (CH - 1)))) * sizeof(V4)) =
+                convert_pack<T, 4>(v);
+          }
+        // (LDS operations of one wavefront complete in order)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const int row = r + q4;
+          const int64_t m = m0 + 16 * tm + row;
+          // a uniform base and 32 bits per lane (15 rows of at most kTurnsMaxOuts)
+          T* base = reinterpret_cast<T*>(a.out) + (m0 + 16 * tm) * a.N + n0 + 16 * t0;
+          const uint32_t ro = (uint32_t)row * (uint32_t)a.N;
+#pragma unroll
+          for (int i = 0; i < (W + 63) / 64; ++i) {
+            const int e = 64 * i + 4 * l16;
+            if (e >= W) continue;
+            const V4 o = *reinterpret_cast<const V4*>(
+                lds + (row * CH + ((e / 4) ^ (2 * row & (CH - 1)))) * sizeof(V4));
+            T* out = off32(base, ro + e);
+            if (lines && whole) {
+              __builtin_nontemporal_store(o, reinterpret_cast<typename Pack<T, 4>::U*>(out));
+            } else if (whole) {
+              store_pack<4>(out, o);
+            } else if (m < a.M) {
+              const int64_t left = a.N - (n0 + 16 * t0 + e);
+              if (left >= 4) {
+                store_pack<4>(out, o);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                  if (k < left) out[k] = o[k];
+              }
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+      for (int tm = 0; tm < TM; ++tm) acc[tn][tm] = i32x4{0, 0, 0, 0};
+    return whole;
+  };
+
 #define SSD_FENCE(text)                     \
   __builtin_amdgcn_sched_barrier(0);        \
   asm volatile(text ::: "memory");          \
   __builtin_amdgcn_sched_barrier(0)
-  stage(0);
+// every load has landed; `stored`: behind them are a whole tile's stores, which may stay in flight
+#define SSD_LANDED(stored)                                                        \
+  __builtin_amdgcn_sched_barrier(0);                                              \
+  if (stored) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(STORES) : "memory");       \
+  else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");                           \
+  __builtin_amdgcn_sched_barrier(0)
+
+  std::integral_constant<int, 0> g0;
+  std::integral_constant<int, 1> g1;
+  aim();
+  int in = 0;   // steps of the current tile multiplied
   if (wave < 4) {
+    stage(g0, 0);
+    advance();
     SSD_FENCE("s_waitcnt vmcnt(0)\n\ts_barrier");
-    for (int s = 0; s < steps; ++s) {
-      frags(s);
-      stage(s + 1);
+    for (int g = 0; g < total; ++g) {
+      stage(g0, g + 1);
+      advance();
+      bool stored = false;
+      if (in == steps) {
+        __builtin_amdgcn_sched_barrier(0);
+        stored = finish();
+        in = 0;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      frags(g);
       SSD_FENCE("s_waitcnt lgkmcnt(0)\n\ts_barrier");
       product(0);
       SSD_FENCE("s_barrier");
-      product(2);
-      SSD_FENCE("s_waitcnt vmcnt(0)\n\ts_barrier");
+      product(1);
+      ++in;
+      SSD_LANDED(stored);
+      SSD_FENCE("s_barrier");
     }
   } else {
-    stage(1);
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LOADS) : "memory");
-    __builtin_amdgcn_sched_barrier(0);
+    stage(g1, 0);
+    advance();
+    SSD_FENCE("s_waitcnt vmcnt(0)\n\ts_barrier");
+    stage(g1, 1);
+    advance();
     SSD_FENCE("s_barrier");
     frags(0);
     SSD_FENCE("s_waitcnt vmcnt(0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier");
-    stage(2);
+    stage(g1, 2);
     SSD_FENCE("s_barrier");
-    for (int s = 1; s < steps; ++s) {
+    for (int g = 1; g < total; ++g) {
       product(0);
-      product(2);
+      product(1);
+      bool stored = false;
+      if (++in == steps) {
+        stored = finish();
+        in = 0;
+      }
+      advance();   // (while no operands are held)
       SSD_FENCE("s_barrier");
-      frags(s);
-      SSD_FENCE("s_waitcnt vmcnt(0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier");
-      stage(s + 2);
+      frags(g);
+      SSD_LANDED(stored);
+      SSD_FENCE("s_waitcnt lgkmcnt(0)\n\ts_barrier");
+      stage(g1, g + 2);
       SSD_FENCE("s_barrier");
     }
     product(0);
-    product(2);
+    product(1);
   }
+  finish();
   SSD_FENCE("s_waitcnt vmcnt(0)");   // no load may reach LDS after the end
-  SSD_FENCE("s_barrier");            // every wavefront has read its operands
-  store_tile<T, TN, TM>(a, acc, sm + wave * kOutBytes, n0 + wn * (BN / WN), m0 + wm * (BM / WM), lane);
+#undef SSD_LANDED
+#undef SSD_FENCE
 }
 
-template <typename T, int TN, int TM>
+template <typename T, int TN>
 hipError_t turns(const LinearQ8Args& a, hipStream_t s) {
-  constexpr int BN = 64 * TN, BM = 128 * TM;
-  const int32_t nt = (int32_t)((a.N + BN - 1) / BN), mt = (int32_t)((a.M + BM - 1) / BM);
-  hipLaunchKernelGGL((k_linear_q8_turns<T, TN, TM>), dim3((unsigned)(nt * mt)), dim3(512), 0, s, a, nt, mt);
+  const int32_t nt = (int32_t)((a.N + 32 * TN - 1) / (32 * TN)), mt = (int32_t)((a.M + 255) / 256);
+  const int32_t tiles = nt * mt;
+  hipLaunchKernelGGL((k_linear_q8_turns<T, TN>), dim3((unsigned)(tiles < 256 ? tiles : 256)), dim3(512),
+                     0, s, a, nt, mt);
   return hipGetLastError();
 }
 
@@ -475,15 +633,21 @@ hipError_t tile(const LinearQ8Args& a, hipStream_t s) {
 // stream (one tile of tokens: the matrix cores idle, and what counts is how
 // many bytes are in flight).  Beyond, the tile with the least modelled time:
 // rounds over the 256 compute units times (fixed + columns / 128 * step), in
-// units of 0.01 us fitted to measurements at 2560 x 5120 and 10576 x 2560 outputs
-// x columns, 16 to 4096 tokens (us):
-//   32 x 32, columns split 4 ways    64 x 2560 x 5120: 10.9   256 x 2560 x 5120: 26
-//   64 x 64                                            17.5                      16.3
-//   128 x 128                                          28.5                      30.4
-//   192 x 256 in turns   4096 x 2560 x 5120: 64  (one round)  4096 x 10576 x 2560: 141
-//   256 x 256 in turns                       68                                  127
-// A larger tile moves fewer bytes per product but fills the last round worse.
-enum Variant { kSplit, kTile64, kTile128, kTurns192, kTurns256 };
+// units of 0.01 us fitted to these measurements (us, kernel time):
+//                            64 x 2560   256 x 2560   1024 x 2560   4096 x 2560   4096 x 10576
+//                             x 5120       x 5120        x 5120        x 5120        x 2560
+//   32 x 32, split columns     10.9         26
+//   64 x 64                    17.5         16.3          36            108           237
+//   128 x 128                  28.5         30.4          30             86           193
+//   160 x 256 in turns                                                   61           144
+//   192 x 256 in turns                                                   62           127
+//   224 x 256 in turns                                                   61           106-115
+//   256 x 256 in turns                                                   77           118-132
+// A larger tile moves fewer bytes per product but fills the last round worse;
+// at 8192 x 8192 x 8192 the 256 x 256 tiles reach 2.7 Pop/s (405 us), where the
+// same instructions on operands that never change reach 4.0-4.5 (the clock
+// falls with the work: 1.8-2.0 GHz there).
+enum Variant { kSplit, kTile64, kTile128, kTurns160, kTurns192, kTurns224, kTurns256 };
 Variant variant_of(int64_t M, int64_t N, int64_t K) {
   const int64_t steps = K / 128;
   auto tiles = [&](int64_t bn, int64_t bm) { return ((N + bn - 1) / bn) * ((M + bm - 1) / bm); };
@@ -494,11 +658,13 @@ Variant variant_of(int64_t M, int64_t N, int64_t K) {
       rounds(tiles(32, 32)) * (220 + 15 * steps),
       t64 <= 256 ? 200 + 36 * steps : 200 + steps * (22 + 30 * t64 / 256),
       rounds(tiles(128, 128)) * (200 + 70 * steps),
-      rounds(tiles(192, 256)) * (900 + 136 * steps),
-      rounds(tiles(256, 256)) * (1300 + 140 * steps),
+      rounds(tiles(160, 256)) * (1000 + 113 * steps),
+      rounds(tiles(192, 256)) * (1000 + 124 * steps),
+      rounds(tiles(224, 256)) * (1000 + 140 * steps),
+      rounds(tiles(256, 256)) * ((N % 64 == 0 ? 450 : 1000) + 158 * steps),   // (whole lines)
   };
   int best = 0;
-  for (int v = 1; v < 5; ++v)
+  for (int v = 1; v < (N <= kTurnsMaxOuts ? 7 : 3); ++v)
     if (cost[v] < cost[best]) best = v;
   return (Variant)best;
 }
@@ -515,8 +681,10 @@ hipError_t linear_t(const LinearQ8Args& a, hipStream_t s) {
     case kSplit: return split<T, 32, 32, 4, 4>(a, s);
     case kTile64: return tile<T, 64, 64, 2, 2, 4>(a, s);
     case kTile128: return tile<T, 128, 128, 4, 2, 4>(a, s);
-    case kTurns192: return turns<T, 3, 2>(a, s);
-    case kTurns256: return turns<T, 4, 2>(a, s);
+    case kTurns160: return turns<T, 5>(a, s);
+    case kTurns192: return turns<T, 6>(a, s);
+    case kTurns224: return turns<T, 7>(a, s);
+    case kTurns256: return turns<T, 8>(a, s);
   }
   return hipErrorInvalidValue;
 }

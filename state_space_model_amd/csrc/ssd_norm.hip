@@ -415,6 +415,7 @@ __global__ __launch_bounds__(kSumCols * kSumSplit) void k_sum_parts(const float*
 }
 
 hipError_t sum_parts(const float* part, float* out, int64_t parts, int64_t D, hipStream_t s) {
+  if (parts == 1) return hipSuccess;   // the part was written to `out` itself
   hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)((D + kSumCols - 1) / kSumCols)),
                      dim3(kSumCols * kSumSplit), 0, s, part, out, (int32_t)parts, D);
   return hipGetLastError();
@@ -544,7 +545,9 @@ hipError_t quantize_t(const T* v, int64_t R, int32_t K, int32_t Kp, int8_t* q, f
 // 34.5 and 37.6 us against 32.3 us at 4096 x 2560).
 int64_t backward_parts(int64_t R, int64_t G, int64_t W, bool io_bf16) {
   const int64_t n = row_blocks(team_of(W, io_bf16 ? 8 : 4), R), cap = (2 * kCus + G - 1) / G;
-  return n < cap ? n : cap;
+  // a few rows: one workgroup takes them in turn and its part is the sum, which
+  // saves the second launch
+  return n <= 4 ? 1 : n < cap ? n : cap;
 }
 
 }  // namespace
@@ -585,8 +588,10 @@ hipError_t launch_gated_norm(const GatedNormArgs& all, bool io_bf16, hipStream_t
   });
 }
 
-hipError_t launch_add_norm_backward(const AddNormArgs& a, bool io_bf16, hipStream_t s) {
+hipError_t launch_add_norm_backward(const AddNormArgs& all, bool io_bf16, hipStream_t s) {
+  AddNormArgs a = all;
   const int64_t parts = add_norm_backward_parts(a.R, a.D, io_bf16);
+  if (parts == 1) a.part = a.dweight;
   auto go = [&](auto zero) {
     using T = decltype(zero);
     const RowTeam t = team_of(a.D, vec_of<T>());
@@ -600,8 +605,10 @@ hipError_t launch_add_norm_backward(const AddNormArgs& a, bool io_bf16, hipStrea
   return e != hipSuccess ? e : sum_parts(a.part, a.dweight, parts, a.D, s);
 }
 
-hipError_t launch_gated_norm_backward(const GatedNormArgs& a, bool io_bf16, hipStream_t s) {
+hipError_t launch_gated_norm_backward(const GatedNormArgs& all, bool io_bf16, hipStream_t s) {
+  GatedNormArgs a = all;
   const int64_t parts = gated_norm_backward_parts(a.R, a.G, a.W, io_bf16);
+  if (parts == 1) a.part = a.dweight;
   auto go = [&](auto zero) {
     using T = decltype(zero);
     const RowTeam t = team_of(a.W, vec_of<T>());

@@ -374,6 +374,31 @@ def test_linear_q8(m, n, k, io):
     close(out, ref, (4 * U + (io_u(io) * 1.01 if io == "bf16" else 0)) * np.abs(ref), "out")
 
 
+# tiles of 256 tokens and 160 to 256 outputs, more of them than compute units, with
+# whole and cut ones, whole and cut lines
+LINEAR_LARGE = [(4000, 2400, 2560), (2600, 4099, 640), (1500, 9000, 640), (4100, 10570, 512),
+                (4352, 5376, 384), (4097, 2560, 1280)]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k", LINEAR_LARGE)
+def test_linear_q8_large(m, n, k, io):
+    """As test_linear_q8, the exact sums formed in float64 on the GPU; a second
+    call gives the same bits."""
+    need_gpu()
+    import state_space_model_amd as ssd
+    g = gen(m + n + k)
+    q, wq = dev(ints(g, m, k)), dev(ints(g, n, k))
+    qs, ws = dev(torch.rand(m, generator=g) + 0.01), dev(torch.rand(n, generator=g) + 0.01)
+    announce(f"linear_q8 large {io} {m}x{n}x{k}")
+    out = ssd.ssd_linear_q8(q, qs, wq, ws, out_dtype=DT[io])
+    ref = (q.double() @ wq.double().t().contiguous()) * qs.double()[:, None] * ws.double()
+    bar = (4 * U + (io_u(io) * 1.01 if io == "bf16" else 0)) * ref.abs()
+    bad = (out.double() - ref).abs() > bar
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:4].tolist())
+    assert torch.equal(out, ssd.ssd_linear_q8(q, qs, wq, ws, out_dtype=DT[io]))
+
+
 def test_linear_q8_extreme_sum():
     """The widest rows of -128 reach 2^31 - 2^21 without overflow."""
     need_gpu()
