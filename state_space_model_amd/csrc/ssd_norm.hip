@@ -15,7 +15,7 @@
 // one MI355X (kernel time in a HIP graph, inputs rotated through HBM):
 //   add norm   131072 x 2048 bfloat16   555 us  5.8 TB/s
 //              4097 x 768 float32      10.7 us  4.7 TB/s
-//   gated norm 4096 x 5120 bfloat16    25.7 us  4.9 TB/s
+//   gated norm 4096 x 5120 bfloat16    24.1 us  5.2 TB/s
 //   gradients: add norm 4096 x 2560    32.3 us  5.2 TB/s (the sum of the parts 4 us of it)
 //              gated, 8 groups, 16384 x 4096   127 us  5.3 TB/s
 // against 4.8 TB/s for a plain copy of 4 GiB.  Tried and slower: non-temporal
@@ -32,14 +32,15 @@
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;        // four wavefronts, a row each
+constexpr int kBlockThreads = 512;   // at most, for a workgroup per row
 constexpr int kCus = 256;
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
 template <typename T, int VEC, int NV, bool BLOCK, bool Q8>
-__global__ __launch_bounds__(BLOCK ? 1024 : kThreads) void k_add_norm(AddNormArgs a) {
+__global__ __launch_bounds__(BLOCK ? kBlockThreads : kThreads) void k_add_norm(AddNormArgs a) {
   __shared__ float sm[kMaxWaves], smq[kMaxWaves];
   const int team = BLOCK ? blockDim.x : 64;
   const int lane = BLOCK ? threadIdx.x : threadIdx.x & 63;
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(BLOCK ? 1024 : kThreads) void k_add_norm(AddNormArg
 
 // grid (.., G): block y -> group of columns; Q8 with one group only
 template <typename T, int VEC, int NV, bool BLOCK, bool Q8>
-__global__ __launch_bounds__(BLOCK ? 1024 : kThreads) void k_gated_norm(GatedNormArgs a) {
+__global__ __launch_bounds__(BLOCK ? kBlockThreads : kThreads) void k_gated_norm(GatedNormArgs a) {
   __shared__ float sm[kMaxWaves], smq[kMaxWaves];
   const int team = BLOCK ? blockDim.x : 64;
   const int lane = BLOCK ? threadIdx.x : threadIdx.x & 63;
@@ -200,7 +201,7 @@ __global__ __launch_bounds__(1024) void k_gated_norm_groups_q8(GatedNormArgs a) 
 }
 
 template <typename T, int VEC, int NV, bool BLOCK>
-__global__ __launch_bounds__(BLOCK ? 1024 : kThreads) void k_quantize_q8(const T* v, int64_t R,
+__global__ __launch_bounds__(BLOCK ? kBlockThreads : kThreads) void k_quantize_q8(const T* v, int64_t R,
                                                                          int32_t K, int32_t Kp,
                                                                          int8_t* q, float* qscale) {
   __shared__ float smq[kMaxWaves];
@@ -275,7 +276,7 @@ __device__ __forceinline__ void store_part(const RowCols<VEC, NV>& cols, fvec<VE
 }
 
 template <typename T, int VEC, int NV, bool BLOCK>
-__global__ __launch_bounds__(BLOCK ? 1024 : kThreads) void k_add_norm_backward(AddNormArgs a) {
+__global__ __launch_bounds__(BLOCK ? kBlockThreads : kThreads) void k_add_norm_backward(AddNormArgs a) {
   __shared__ float sm[2][2 * kMaxWaves];
   const int team = BLOCK ? blockDim.x : 64;
   const int lane = BLOCK ? threadIdx.x : threadIdx.x & 63;
@@ -333,7 +334,7 @@ __global__ __launch_bounds__(BLOCK ? 1024 : kThreads) void k_add_norm_backward(A
 
 // grid (parts, G)
 template <typename T, int VEC, int NV, bool BLOCK>
-__global__ __launch_bounds__(BLOCK ? 1024 : kThreads) void k_gated_norm_backward(GatedNormArgs a) {
+__global__ __launch_bounds__(BLOCK ? kBlockThreads : kThreads) void k_gated_norm_backward(GatedNormArgs a) {
   __shared__ float sm[2][2 * kMaxWaves];
   const int team = BLOCK ? blockDim.x : 64;
   const int lane = BLOCK ? threadIdx.x : threadIdx.x & 63;
@@ -430,8 +431,9 @@ hipError_t sum_parts(const float* part, float* out, int64_t parts, int64_t D, hi
 // columns: 10.7 us against 10.6-11.1; 512 bfloat16: a workgroup per row pays a
 // barrier for each 1 KB); beyond, a workgroup with one vector per lane spreads
 // a row's latency (2048 bfloat16 columns: 555 us against 578 us with four
-// vectors in one wavefront).  A row wider than 1024 vectors takes more per
-// lane.  The choice depends on the width alone, so a row's bits do not depend
+// vectors in one wavefront).  A row wider than 512 vectors takes more per
+// lane (5120 bfloat16 columns as 5 wavefronts of two vectors: 24.1 us, as 10 of
+// one: 28.5 us, three workgroups to a compute unit instead of six).  The choice depends on the width alone, so a row's bits do not depend
 // on the batch.
 struct RowTeam {
   int nv;
@@ -442,7 +444,7 @@ RowTeam team_of(int64_t W, int vec) {
   const int64_t chunks = (W + vec - 1) / vec;
   if (chunks <= 3 * 64) return {(int)((chunks + 63) / 64), false, kThreads};
   int nv = 1;
-  while (chunks > 1024 * nv) nv *= 2;
+  while (chunks > kBlockThreads * nv) nv *= 2;
   return {nv, true, (int)((chunks + 64 * nv - 1) / (64 * nv)) * 64};
 }
 
@@ -458,8 +460,9 @@ hipError_t dispatch(int64_t W, F&& f) {
   if (t.block) {
     if (t.nv == 1) return f(ic<VEC>{}, ic<1>{}, std::true_type{});
     if (t.nv == 2) return f(ic<VEC>{}, ic<2>{}, std::true_type{});
-    if constexpr (VEC == 4) return f(ic<VEC>{}, ic<4>{}, std::true_type{});
-    return hipErrorInvalidValue;  // 16384 columns end at two vectors of eight
+    if (t.nv == 4) return f(ic<VEC>{}, ic<4>{}, std::true_type{});
+    if constexpr (VEC == 4) return f(ic<VEC>{}, ic<8>{}, std::true_type{});
+    return hipErrorInvalidValue;  // 16384 columns end at four vectors of eight
   }
   if (t.nv == 1) return f(ic<VEC>{}, ic<1>{}, std::false_type{});
   if (t.nv == 2) return f(ic<VEC>{}, ic<2>{}, std::false_type{});
