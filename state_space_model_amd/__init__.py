@@ -4,6 +4,8 @@ Argument marshalling only: every step of the scan and of the decode step runs
 in the HIP kernels behind the C ABI declared in include/ssd.h.  PyTorch is
 used for device memory and for the current HIP stream; there is no CPU or
 PyTorch fallback -- if libssd.so is missing, importing this package raises.
+The operators between two scans are marshalled in C++ (_ssd_torch.so, from
+csrc/ssd_torch.cpp): a token's calls are bound by the host.
 
   ssd_chunk_scan(x, dt, A, B, C, D=None, *, chunk=256, ...) -> (y, final_state)
   ssd_step(state, x_t, dt_t, A, B_t, C_t, D=None, ...)      -> y_t  (state updated in place)
@@ -30,6 +32,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libssd.so")
+CALLS_PATH = os.path.join(_HERE, "_ssd_torch.so")
 
 SSD_OK = 0
 SSD_F32 = 0
@@ -164,7 +167,17 @@ def _load() -> ctypes.CDLL:
     return L
 
 
+def _load_calls():
+    if not os.path.exists(CALLS_PATH):
+        raise ImportError(f"{CALLS_PATH} is missing: build it with libssd.so "
+                          "(python state_space_model_amd/build.py).")
+    from . import _ssd_torch
+    return _ssd_torch
+
+
 lib = _load()
+_calls = _load_calls()
+_row_stride = _calls.row_stride
 
 
 def _io_code(dtype: torch.dtype) -> int:
@@ -204,14 +217,14 @@ def _nbytes(t: torch.Tensor) -> int:
 
 
 # The current stream's handle without a torch.cuda.Stream object around it,
-# which costs a one-token call 1.8 us of its 9.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# which costs a one-token call 1.8 us more.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_calls.connect(SSDError, _raw_stream)
 
 
 def _stream(device) -> int:
-    if _raw_stream is not None:
-        return _raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
 
 
 def _scan_shapes(x, dt, A, B, C, D=None, dt_bias=None, initial_state=None) -> None:
@@ -539,145 +552,16 @@ def ssd_conv1d_backward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[to
     x's dtype; dstate_out [Bt,D,k-1] in x's dtype or None.  Returns a dict: dx
     [Bt,T,D] and dstate [Bt,D,k-1] in x's dtype, dweight [D,k] and dbias [D]
     float32 (all four always computed)."""
-    if x.dim() != 3 or weight.dim() != 2 or weight.shape[0] != x.shape[2]:
-        raise ValueError("x [Bt,T,D], weight [D,k]")
-    Bt, T, Dc = x.shape
-    K = weight.shape[1]
-    io = x.dtype
-    code = _io_code(io)
-    g = _check_grads(grads, {"dx": x.shape, "dweight": weight.shape, "dbias": (Dc,),
-                             "dstate": (Bt, Dc, K - 1)})
-    _shape(dy, "dy", (Bt, T, Dc))
-    _shape(bias, "bias", (Dc,))
-    _shape(state, "state", (Bt, Dc, K - 1))
-    _shape(dstate_out, "dstate_out", (Bt, Dc, K - 1))
-    for t, n, dt_ in ((x, "x", None), (weight, "weight", torch.float32),
-                      (bias, "bias", torch.float32), (state, "state", io),
-                      (dy, "dy", torch.float32 if dy.dtype == torch.float32 else io),
-                      (dstate_out, "dstate_out", io)):
-        _check(t, n, dt_)
-    dev = x.device
-    dx = _like(g.get("dx"), "dx", x)
-    dweight = _like(g.get("dweight"), "dweight", weight)
-    dbias = _output(g.get("dbias"), "dbias", (Dc,), torch.float32, dev)
-    dstate = _output(g.get("dstate"), "dstate", (Bt, Dc, K - 1), io, dev)
-    desc = ConvDesc(Bt, T, Dc, K, code, int(bool(silu)))
-    workspace = _workspace(workspace, lib.ssd_conv1d_backward_workspace_bytes, desc, dev)
-    st = lib.ssd_conv1d_backward(
-        ctypes.byref(desc), _io_code(dy.dtype), x.data_ptr(), weight.data_ptr(), _data(bias),
-        _data(state), dy.data_ptr(), _data(dstate_out), dx.data_ptr(), dweight.data_ptr(),
-        dbias.data_ptr(), dstate.data_ptr(), workspace.data_ptr(), _nbytes(workspace), _stream(dev))
-    if st != SSD_OK:
-        raise SSDError(st, "ssd_conv1d_backward")
-    return {"dx": dx, "dweight": dweight, "dbias": dbias, "dstate": dstate}
+    return _calls.conv1d_backward(x, weight, bias, dy, state, dstate_out, silu, workspace, grads)
 
 
 # ---------------------------------------------------------------------------
 # Norms, 8-bit rows and their product.  Tensors are [..., columns]: the leading
 # dimensions are rows.
 # ---------------------------------------------------------------------------
-def _check_grads(grads: Optional[dict], shapes: dict) -> dict:
-    """The caller's gradient buffers (by name) checked against their shapes."""
-    if not grads:
-        return {}
-    unknown = set(grads) - set(shapes)
-    if unknown:
-        raise ValueError(f"unknown gradient names {sorted(unknown)}")
-    for k, v in grads.items():
-        _shape(v, k, shapes[k])
-    return grads
-
-
-def _workspace(workspace: Optional[torch.Tensor], query, desc, device) -> torch.Tensor:
-    if workspace is None:
-        workspace = torch.empty(max(int(query(ctypes.byref(desc))), 1), dtype=torch.uint8,
-                                device=device)
-    _check(workspace, "workspace")
-    return workspace
-
-
-def _row_stride(t: torch.Tensor, name: str) -> int:
-    """Elements between the rows of t [..., D], whose rows must be dense and
-    evenly spaced (a slice of a projection's columns is)."""
-    if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]:
-        return t.stride(0)
-    if t.dim() < 2:
-        return t.shape[-1]
-    if t.numel() == 0:
-        return max(t.stride(-2), t.shape[-1])
-    ok = t.stride(-1) == 1 or t.shape[-1] == 1
-    rows, step = 1, None
-    for d in range(t.dim() - 2, -1, -1):
-        if t.shape[d] == 1:
-            continue
-        if step is None:
-            step = t.stride(d)
-        ok = ok and t.stride(d) == step * rows
-        rows *= t.shape[d]
-    step = t.shape[-1] if step is None else step
-    if not ok or step < t.shape[-1]:
-        raise ValueError(f"{name} must have dense, evenly spaced rows (shape {tuple(t.shape)}, "
-                         f"strides {tuple(t.stride())})")
-    return step
-
-
-def _check_rows(t: Optional[torch.Tensor], name: str, dtype) -> int:
-    """_check for a tensor that may be a slice of columns; its row stride."""
-    if t is None:
-        return 0
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor (got {t.device}); there is no CPU path")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return _row_stride(t, name)
-
-
 def q8_cols(cols: int) -> int:
     """Columns of an 8-bit row that holds `cols` values (padded with zeros)."""
     return (cols + SSD_Q8_PAD - 1) // SSD_Q8_PAD * SSD_Q8_PAD
-
-
-def _add_norm_args(x, weight, residual, residual_out):
-    """Checks of the residual add and norm; (io code, D, residual_out)."""
-    if x.dim() < 1 or weight.dim() != 1:
-        raise ValueError("x [..., D], weight [D]")
-    shape = x.shape
-    D = shape[-1]
-    _shape(weight, "weight", (D,))
-    _shape(residual, "residual", shape)
-    _shape(residual_out, "residual_out", shape)
-    code = _io_code(x.dtype)
-    _check(x, "x")
-    _check(weight, "weight", torch.float32)
-    _check(residual, "residual", torch.float32)
-    if residual_out is None:
-        if residual is not None:
-            residual_out = torch.empty_like(residual)
-        else:
-            residual_out = torch.empty(shape, dtype=torch.float32, device=x.device)
-    else:
-        _check(residual_out, "residual_out", torch.float32)
-    return code, D, residual_out
-
-
-def _output(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Tensor:
-    """The caller's output buffer, checked (its shape was), or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _check(t, name, dtype)
-    return t
-
-
-def _like(t: Optional[torch.Tensor], name: str, like: torch.Tensor) -> torch.Tensor:
-    """_output with the shape, type and device of a dense tensor."""
-    if t is None:
-        return torch.empty_like(like)
-    _check(t, name, like.dtype)
-    return t
-
-
-def _data(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
 
 
 def ssd_add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
@@ -690,15 +574,7 @@ def ssd_add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
     x [..., D] float32 or bfloat16, residual [..., D] float32 or None (zeros),
     weight [D] float32.  Returns (y in x's dtype, residual_out float32).
     residual_out may be `residual` itself (updated in place)."""
-    _shape(y, "y", x.shape)
-    code, D, residual_out = _add_norm_args(x, weight, residual, residual_out)
-    y = _like(y, "y", x)
-    desc = AddNormDesc(x.numel() // max(D, 1), D, code, scale, eps)
-    st = lib.ssd_add_norm(ctypes.byref(desc), x.data_ptr(), _data(residual), weight.data_ptr(),
-                          y.data_ptr(), residual_out.data_ptr(), _stream(x.device))
-    if st != SSD_OK:
-        raise SSDError(st, "ssd_add_norm")
-    return y, residual_out
+    return _calls.add_norm(x, weight, residual, scale, eps, y, residual_out)
 
 
 def ssd_add_norm_q8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -708,20 +584,7 @@ def ssd_add_norm_q8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[to
                     ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """ssd_add_norm with y quantised to 8-bit rows in the same pass: returns
     (q [..., q8_cols(D)] int8, qscale [...] float32, residual_out)."""
-    rows = x.shape[:-1]
-    qshape = (*rows, q8_cols(x.shape[-1])) if x.dim() else ()
-    _shape(q, "q", qshape)
-    _shape(qscale, "qscale", rows)
-    code, D, residual_out = _add_norm_args(x, weight, residual, residual_out)
-    dev = x.device
-    q = _output(q, "q", qshape, torch.int8, dev)
-    qscale = _output(qscale, "qscale", rows, torch.float32, dev)
-    desc = AddNormDesc(x.numel() // max(D, 1), D, code, scale, eps)
-    st = lib.ssd_add_norm_q8(ctypes.byref(desc), x.data_ptr(), _data(residual), weight.data_ptr(),
-                             q.data_ptr(), qscale.data_ptr(), residual_out.data_ptr(), _stream(dev))
-    if st != SSD_OK:
-        raise SSDError(st, "ssd_add_norm_q8")
-    return q, qscale, residual_out
+    return _calls.add_norm_q8(x, weight, residual, scale, eps, q, qscale, residual_out)
 
 
 def ssd_add_norm_backward(residual_out: torch.Tensor, weight: torch.Tensor, *, dy: torch.Tensor,
@@ -732,46 +595,8 @@ def ssd_add_norm_backward(residual_out: torch.Tensor, weight: torch.Tensor, *, d
     residual_out), on the current stream, from the residual_out it returned.
     Returns a dict: dx [..., D] in dy's dtype, dresidual [..., D] and dweight
     [D] float32.  grads["dresidual"] may be dresidual_out itself."""
-    if residual_out.dim() < 1 or weight.dim() != 1:
-        raise ValueError("residual_out [..., D], weight [D]")
-    shape, D = residual_out.shape, residual_out.shape[-1]
-    f32 = torch.float32
-    _shape(weight, "weight", (D,))
-    _shape(dy, "dy", shape)
-    _shape(dresidual_out, "dresidual_out", shape)
-    code = _io_code(dy.dtype)
-    g = _check_grads(grads, {"dx": shape, "dresidual": shape, "dweight": (D,)})
-    _check(residual_out, "residual_out", f32)
-    _check(weight, "weight", f32)
-    _check(dy, "dy")
-    _check(dresidual_out, "dresidual_out", f32)
-    dev = dy.device
-    dx = _like(g.get("dx"), "dx", dy)
-    dresidual = _like(g.get("dresidual"), "dresidual", residual_out)
-    dweight = _like(g.get("dweight"), "dweight", weight)
-    desc = AddNormDesc(dy.numel() // max(D, 1), D, code, scale, eps)
-    workspace = _workspace(workspace, lib.ssd_add_norm_backward_workspace_bytes, desc, dev)
-    st = lib.ssd_add_norm_backward(
-        ctypes.byref(desc), residual_out.data_ptr(), weight.data_ptr(), dy.data_ptr(),
-        _data(dresidual_out), dx.data_ptr(), dresidual.data_ptr(), dweight.data_ptr(),
-        workspace.data_ptr(), _nbytes(workspace), _stream(dev))
-    if st != SSD_OK:
-        raise SSDError(st, "ssd_add_norm_backward")
-    return {"dx": dx, "dresidual": dresidual, "dweight": dweight}
-
-
-def _gated_norm_desc(y, z, weight, groups, eps) -> GatedNormDesc:
-    """Checks of the gated norm; its descriptor."""
-    if y.dim() < 1 or weight.dim() != 1:
-        raise ValueError("y [..., D], z [..., D], weight [D]")
-    D = y.shape[-1]
-    _shape(z, "z", y.shape)
-    _shape(weight, "weight", (D,))
-    code = _io_code(y.dtype)
-    _check(y, "y")
-    _check(weight, "weight", torch.float32)
-    stride = _check_rows(z, "z", y.dtype)
-    return GatedNormDesc(y.numel() // max(D, 1), D, groups, stride, 0, code, eps)
+    return _calls.add_norm_backward(residual_out, weight, dy, dresidual_out, scale, eps,
+                                    workspace, grads)
 
 
 def ssd_gated_norm(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *, groups: int = 1,
@@ -781,14 +606,7 @@ def ssd_gated_norm(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *, gr
 
     y [..., D] float32 or bfloat16, z [..., D] in y's dtype with evenly spaced
     rows (a slice of the projection's columns), weight [D] float32."""
-    _shape(out, "out", y.shape)
-    desc = _gated_norm_desc(y, z, weight, groups, eps)
-    out = _like(out, "out", y)
-    st = lib.ssd_gated_norm(ctypes.byref(desc), y.data_ptr(), z.data_ptr(), weight.data_ptr(),
-                            out.data_ptr(), _stream(y.device))
-    if st != SSD_OK:
-        raise SSDError(st, "ssd_gated_norm")
-    return out
+    return _calls.gated_norm(y, z, weight, groups, eps, out)
 
 
 def ssd_gated_norm_q8(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *, groups: int = 1,
@@ -796,19 +614,7 @@ def ssd_gated_norm_q8(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *,
                       qscale: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """ssd_gated_norm with its output quantised to 8-bit rows in the same pass:
     returns (q [..., q8_cols(D)] int8, qscale [...] float32)."""
-    rows = y.shape[:-1]
-    qshape = (*rows, q8_cols(y.shape[-1])) if y.dim() else ()
-    _shape(q, "q", qshape)
-    _shape(qscale, "qscale", rows)
-    desc = _gated_norm_desc(y, z, weight, groups, eps)
-    dev = y.device
-    q = _output(q, "q", qshape, torch.int8, dev)
-    qscale = _output(qscale, "qscale", rows, torch.float32, dev)
-    st = lib.ssd_gated_norm_q8(ctypes.byref(desc), y.data_ptr(), z.data_ptr(), weight.data_ptr(),
-                               q.data_ptr(), qscale.data_ptr(), _stream(dev))
-    if st != SSD_OK:
-        raise SSDError(st, "ssd_gated_norm_q8")
-    return q, qscale
+    return _calls.gated_norm_q8(y, z, weight, groups, eps, q, qscale)
 
 
 def ssd_gated_norm_backward(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *,
@@ -818,35 +624,7 @@ def ssd_gated_norm_backward(y: torch.Tensor, z: torch.Tensor, weight: torch.Tens
     """Gradients of ssd_gated_norm for L = sum(dout * out), on the current
     stream.  Returns a dict: dy, dz [..., D] in y's dtype, dweight [D] float32.
     grads["dz"] may be a slice of a larger tensor's columns, like z."""
-    if y.dim() < 1 or weight.dim() != 1:
-        raise ValueError("y [..., D], z [..., D], weight [D]")
-    shape, D, io = y.shape, y.shape[-1], y.dtype
-    _shape(z, "z", shape)
-    _shape(weight, "weight", (D,))
-    _shape(dout, "dout", shape)
-    code = _io_code(io)
-    g = _check_grads(grads, {"dy": shape, "dz": shape, "dweight": (D,)})
-    _check(y, "y")
-    _check(weight, "weight", torch.float32)
-    _check(dout, "dout", io)
-    z_stride = _check_rows(z, "z", io)
-    dev = y.device
-    dz = g.get("dz")
-    if dz is not None:
-        dz_stride = _check_rows(dz, "dz", io)
-    else:
-        dz, dz_stride = torch.empty_like(y), D
-    dy = _like(g.get("dy"), "dy", y)
-    dweight = _like(g.get("dweight"), "dweight", weight)
-    desc = GatedNormDesc(y.numel() // max(D, 1), D, groups, z_stride, dz_stride, code, eps)
-    workspace = _workspace(workspace, lib.ssd_gated_norm_backward_workspace_bytes, desc, dev)
-    st = lib.ssd_gated_norm_backward(
-        ctypes.byref(desc), y.data_ptr(), z.data_ptr(), weight.data_ptr(), dout.data_ptr(),
-        dy.data_ptr(), dz.data_ptr(), dweight.data_ptr(), workspace.data_ptr(),
-        _nbytes(workspace), _stream(dev))
-    if st != SSD_OK:
-        raise SSDError(st, "ssd_gated_norm_backward")
-    return {"dy": dy, "dz": dz, "dweight": dweight}
+    return _calls.gated_norm_backward(y, z, weight, dout, groups, eps, workspace, grads)
 
 
 def ssd_quantize_q8(v: torch.Tensor, *, q: Optional[torch.Tensor] = None,
@@ -854,22 +632,7 @@ def ssd_quantize_q8(v: torch.Tensor, *, q: Optional[torch.Tensor] = None,
     """Rows of v [..., K] (float32 or bfloat16) in 8 bits, on the current stream:
     a weight's output channels (laid out once) or tokens.  Returns (q [...,
     q8_cols(K)] int8, zero-padded, and qscale [...] float32)."""
-    if v.dim() < 1:
-        raise ValueError("v [..., K]")
-    K, rows = v.shape[-1], v.shape[:-1]
-    qshape = (*rows, q8_cols(K))
-    _shape(q, "q", qshape)
-    _shape(qscale, "qscale", rows)
-    code = _io_code(v.dtype)
-    _check(v, "v")
-    dev = v.device
-    q = _output(q, "q", qshape, torch.int8, dev)
-    qscale = _output(qscale, "qscale", rows, torch.float32, dev)
-    st = lib.ssd_quantize_q8(v.numel() // max(K, 1), K, code, v.data_ptr(), q.data_ptr(),
-                             qscale.data_ptr(), _stream(dev))
-    if st != SSD_OK:
-        raise SSDError(st, "ssd_quantize_q8")
-    return q, qscale
+    return _calls.quantize_q8(v, q, qscale)
 
 
 def ssd_linear_q8(q: torch.Tensor, qscale: torch.Tensor, wq: torch.Tensor, wscale: torch.Tensor, *,
@@ -881,29 +644,7 @@ def ssd_linear_q8(q: torch.Tensor, qscale: torch.Tensor, wq: torch.Tensor, wscal
     q [..., Kp] int8 and qscale [...] float32 (tokens), wq [N, Kp] int8 and
     wscale [N] float32 (output channels), Kp a multiple of SSD_Q8_PAD, as
     ssd_quantize_q8 and the norms' _q8 forms return them."""
-    if q.dim() < 1 or wq.dim() != 2:
-        raise ValueError("q [..., Kp], wq [N, Kp]")
-    Kp, N = q.shape[-1], wq.shape[0]
-    if out is not None:
-        out_dtype = out.dtype
-    shape = (*q.shape[:-1], N)
-    _shape(wq, "wq", (N, Kp))
-    _shape(qscale, "qscale", q.shape[:-1])
-    _shape(wscale, "wscale", (N,))
-    _shape(out, "out", shape)
-    code = _io_code(out_dtype)
-    _check(q, "q", torch.int8)
-    _check(qscale, "qscale", torch.float32)
-    _check(wq, "wq", torch.int8)
-    _check(wscale, "wscale", torch.float32)
-    dev = q.device
-    out = _output(out, "out", shape, out_dtype, dev)
-    desc = LinearQ8Desc(q.numel() // max(Kp, 1), Kp, N, code)
-    st = lib.ssd_linear_q8(ctypes.byref(desc), q.data_ptr(), qscale.data_ptr(), wq.data_ptr(),
-                           wscale.data_ptr(), out.data_ptr(), _stream(dev))
-    if st != SSD_OK:
-        raise SSDError(st, "ssd_linear_q8")
-    return out
+    return _calls.linear_q8(q, qscale, wq, wscale, _io_code(out_dtype) == SSD_BF16, out)
 
 
 def abi_version() -> int:

@@ -201,3 +201,19 @@ def test_row_strides_of_a_sliced_gate():
                 torch.zeros(1, 20).expand(5, 20)):
         with pytest.raises(ValueError, match="evenly spaced"):
             ssd._row_stride(bad, "z")
+
+
+@pytest.mark.parametrize("exc,fn", [
+    (TypeError, lambda: ssd.ssd_add_norm([1.0], Z(8))),
+    (TypeError, lambda: ssd.ssd_add_norm_backward(Z(2, 8), Z(8), dy=Z(2, 8), grads=[Z(8)])),
+    (TypeError, lambda: ssd.ssd_linear_q8(Z(2, 128), Z(2), Z(5, 128), Z(5), out_dtype=torch.float16)),
+    (TypeError, lambda: ssd.ssd_add_norm(Z(2, 8), Z(8), eps="small")),
+    (ValueError, lambda: ssd.ssd_add_norm(Z(()), Z(8))),
+    (ValueError, lambda: ssd.ssd_gated_norm_q8(Z(()), Z(()), Z(8))),
+    (ValueError, lambda: ssd.ssd_quantize_q8(Z(()))),
+    (ValueError, lambda: ssd.ssd_conv1d_backward(Z(2, 6, 8), Z(8, 0), dy=Z(2, 6, 8))),
+    (ValueError, lambda: ssd.ssd_conv1d_backward(Z(2, 6, 8), Z(8, 4), dy=Z(2, 6, 8),
+                                                 grads={3: Z(8)}))])
+def test_binding_refuses_what_is_no_tensor_or_has_no_columns(exc, fn):
+    with pytest.raises(exc):
+        fn()
