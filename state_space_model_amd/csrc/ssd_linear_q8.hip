@@ -37,9 +37,9 @@ __device__ __forceinline__ void store_quad(T* p, i32x4 acc, const float* ws, flo
 
 // ---------------------------------------------------------------------------
 // Few tokens: the weights stream once from memory.  A workgroup of NW
-// wavefronts owns 16 outputs and all tokens (MT tiles of 16); the wavefronts
-// split the columns, 128 bytes (a line of each weight row) at a time, load
-// straight into registers and add up through LDS.
+// wavefronts owns 16 outputs and all (up to 16) tokens; the wavefronts split
+// the columns, 128 bytes (a line of each weight row) at a time, load straight
+// into registers and add up through LDS.
 // ---------------------------------------------------------------------------
 template <typename T, int NW, int UN>
 __global__ __launch_bounds__(64 * NW) void k_linear_q8_stream(LinearQ8Args a) {
@@ -253,13 +253,16 @@ __global__ __launch_bounds__(64 * WN * WM) void k_linear_q8_tile(LinearQ8Args a,
 
 // Few tiles: the KS wavefronts of a workgroup share one BN x BM tile and split
 // its columns; each stages its part through a ring of its own, without
-// barriers, and the sums meet in LDS.
+// barriers, and the sums meet in LDS.  Workgroups next to each other on an XCD
+// start their columns three steps apart: all of them read the same tokens, and
+// in step they would ask the same channels of the L2 for the same lines
+// (64 x 2560 x 5120: 10.0 -> 9.0 us, 33 x 2560 x 5120: 8.6 -> 7.6 us).
 template <typename T, int BN, int BM, int KS, int NS>
 __global__ __launch_bounds__(64 * KS) void k_linear_q8_split(LinearQ8Args a, int32_t nt, int32_t mt) {
   constexpr int BK = 128, TN = BN / 32, TM = BM / 32, LOADS = (BN + BM) / 8;
   constexpr int STAGE = (BN + BM) * BK, RING = KS * NS * STAGE;
-  constexpr int SUMS = KS * TN * TM * 4096, OUT = SUMS + KS * kOutBytes;
-  static_assert((NS - 1) * LOADS < 64);
+  constexpr int OUT = KS * TN * TM * 4096;
+  static_assert((NS - 1) * LOADS < 64 && 4 * TN * TM % KS == 0);
   __shared__ __align__(1024) int8_t sm[RING > OUT ? RING : OUT];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -277,9 +280,11 @@ __global__ __launch_bounds__(64 * KS) void k_linear_q8_split(LinearQ8Args a, int
   const int8_t* wp = a.wq + n0 * a.K;
   const int8_t* xp = a.q + m0 * a.K;
   const int steps = a.K / BK, s0 = steps * wave / KS, s1 = steps * (wave + 1) / KS;
+  const int share = s1 - s0, turn = share > 0 ? (int)(blockIdx.x / 8 * 3 % share) : 0;
   int8_t* ring = sm + wave * NS * STAGE;
   auto stage = [&](int s, int buf) {   // past the end: the last step again, read by no one
-    const int64_t k = (int64_t)(s < s1 ? s : steps - 1) * BK;
+    const int at = s + turn < s1 ? s + turn : s + turn - share;
+    const int64_t k = (int64_t)(s < s1 ? at : steps - 1) * BK;
 #pragma unroll
     for (int j = 0; j < LOADS; ++j)
       __builtin_amdgcn_global_load_lds(
@@ -318,17 +323,29 @@ __global__ __launch_bounds__(64 * KS) void k_linear_q8_split(LinearQ8Args a, int
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load may reach LDS after this
   __syncthreads();
-  i32x16* sums = reinterpret_cast<i32x16*>(sm);
+  // registers 4 p .. 4 p + 3 of all the sums meet in one wavefront, p % KS; a
+  // lane holds four outputs of a token there and stores them as they are (by
+  // way of LDS as whole lines, and by one wavefront, 64 x 768 x 1536: 5.6
+  // against 4.2 us)
+  i32x4* sums = reinterpret_cast<i32x4*>(sm);
 #pragma unroll
-  for (int tn = 0; tn < TN; ++tn)
+  for (int t = 0; t < TN * TM; ++t)
 #pragma unroll
-    for (int tm = 0; tm < TM; ++tm) sums[((wave * TN + tn) * TM + tm) * 64 + lane] = acc[tn][tm];
+    for (int p = 0; p < 4; ++p) {
+      const i32x16& v = acc[t / TM][t % TM];
+      sums[((t * 4 + p) * KS + wave) * 64 + lane] = i32x4{v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]};
+    }
   __syncthreads();
-  for (int t = wave; t < TN * TM; t += KS) {
-    i32x16 sum[1][1] = {{sums[t * 64 + lane]}};
 #pragma unroll
-    for (int o = 1; o < KS; ++o) sum[0][0] += sums[(o * TN * TM + t) * 64 + lane];
-    store_tile<T, 1, 1>(a, sum, sm + SUMS + wave * kOutBytes, n0 + t / TM * 32, m0 + t % TM * 32, lane);
+  for (int o = 0; o < 4 * TN * TM / KS; ++o) {
+    const int q = o * KS + wave, t = q / 4, p = q % 4;
+    i32x4 sum = sums[q * KS * 64 + lane];
+#pragma unroll
+    for (int k = 1; k < KS; ++k) sum += sums[(q * KS + k) * 64 + lane];
+    const int64_t n = n0 + t / TM * 32 + 8 * p + 4 * half, m = m0 + t % TM * 32 + r32;
+    if (m < a.M && n < a.N)
+      store_quad(reinterpret_cast<T*>(a.out) + m * a.N + n, sum, a.wscale + n, a.qscale[m],
+                 (int)(a.N - n < 4 ? a.N - n : 4));
   }
 }
 
@@ -634,20 +651,21 @@ hipError_t tile(const LinearQ8Args& a, hipStream_t s) {
 // many bytes are in flight).  Beyond, the tile with the least modelled time:
 // rounds over the 256 compute units times (fixed + columns / 128 * step), in
 // units of 0.01 us fitted to these measurements (us, kernel time):
-//                            64 x 2560   256 x 2560   1024 x 2560   4096 x 2560   4096 x 10576
-//                             x 5120       x 5120        x 5120        x 5120        x 2560
-//   32 x 32, split columns     10.9         26
-//   64 x 64                    17.5         16.3          36            108           237
-//   128 x 128                  28.5         30.4          30             86           193
-//   160 x 256 in turns                                                   61           144
-//   192 x 256 in turns                                                   62           127
-//   224 x 256 in turns                                                   61           106-115
-//   256 x 256 in turns                                                   77           118-132
+//                          64 x 2560  128 x 2560  256 x 2560  1024 x 2560  4096 x 2560  4096 x 10576
+//                           x 5120      x 5120      x 5120      x 5120       x 5120       x 2560
+//   32 x 32, split columns    9.0        13.2        17.6
+//   the same, two to a CU     9.6        11.4        18.3
+//   64 x 64                  17.5                    16.3         36           108          237
+//   128 x 128                28.5                    30.4         30            86          193
+//   160 x 256 in turns                                                          61          144
+//   192 x 256 in turns                                                          62          127
+//   224 x 256 in turns                                                          61          106-115
+//   256 x 256 in turns                                                          77          118-132
 // A larger tile moves fewer bytes per product but fills the last round worse;
 // at 8192 x 8192 x 8192 the 256 x 256 tiles reach 2.7 Pop/s (405 us), where the
 // same instructions on operands that never change reach 4.0-4.5 (the clock
 // falls with the work: 1.8-2.0 GHz there).
-enum Variant { kSplit, kTile64, kTile128, kTurns160, kTurns192, kTurns224, kTurns256 };
+enum Variant { kSplit, kSplitPair, kTile64, kTile128, kTurns160, kTurns192, kTurns224, kTurns256 };
 Variant variant_of(int64_t M, int64_t N, int64_t K) {
   const int64_t steps = K / 128;
   auto tiles = [&](int64_t bn, int64_t bm) { return ((N + bn - 1) / bn) * ((M + bm - 1) / bm); };
@@ -655,7 +673,8 @@ Variant variant_of(int64_t M, int64_t N, int64_t K) {
   // two 64 x 64 tiles and more share a compute unit
   const int64_t t64 = tiles(64, 64);
   const int64_t cost[] = {
-      rounds(tiles(32, 32)) * (220 + 15 * steps),
+      rounds(tiles(32, 32)) * (210 + 17 * steps),
+      rounds((tiles(32, 32) + 1) / 2) * (315 + 21 * steps),   // two to a compute unit
       t64 <= 256 ? 200 + 36 * steps : 200 + steps * (22 + 30 * t64 / 256),
       rounds(tiles(128, 128)) * (200 + 70 * steps),
       rounds(tiles(160, 256)) * (1000 + 113 * steps),
@@ -664,7 +683,7 @@ Variant variant_of(int64_t M, int64_t N, int64_t K) {
       rounds(tiles(256, 256)) * ((N % 64 == 0 ? 450 : 1000) + 158 * steps),   // (whole lines)
   };
   int best = 0;
-  for (int v = 1; v < (N <= kTurnsMaxOuts ? 7 : 3); ++v)
+  for (int v = 1; v < (N <= kTurnsMaxOuts ? 8 : 4); ++v)
     if (cost[v] < cost[best]) best = v;
   return (Variant)best;
 }
@@ -678,7 +697,8 @@ hipError_t linear_t(const LinearQ8Args& a, hipStream_t s) {
     return a.K <= 2048 ? stream<T, 8, 2>(a, s) : stream<T, 4, 5>(a, s);
   }
   switch (variant_of(a.M, a.N, a.K)) {
-    case kSplit: return split<T, 32, 32, 4, 4>(a, s);
+    case kSplit: return split<T, 32, 32, 4, 3>(a, s);
+    case kSplitPair: return split<T, 32, 32, 4, 2>(a, s);
     case kTile64: return tile<T, 64, 64, 2, 2, 4>(a, s);
     case kTile128: return tile<T, 128, 128, 4, 2, 4>(a, s);
     case kTurns160: return turns<T, 5>(a, s);
