@@ -36,13 +36,19 @@ __device__ __forceinline__ void store_quad(T* p, i32x4 acc, const float* ws, flo
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: the weights stream once from memory.  A workgroup of NW
+// Few tokens: the weights stream once from memory.  A workgroup of eight
 // wavefronts owns 16 outputs and all (up to 16) tokens; the wavefronts split
 // the columns, 128 bytes (a line of each weight row) at a time, load straight
-// into registers and add up through LDS.
+// into registers and add up through LDS.  What counts is how many bytes are in
+// flight: many wavefronts with few loads each.  Two, three and five times 128
+// bytes at a time took the same or more (one token: 10576 x 2560 8.3-8.7 us,
+// 2560 x 5120 6.4-6.8, against 8.5 and 6.5), and so did 4 and 16 wavefronts
+// (2048 x 4096: 7.4 and 5.2 against 5.4 us; 16 x 10576 x 2560: 11.0 and 12.1
+// against 11.2).
 // ---------------------------------------------------------------------------
-template <typename T, int NW, int UN>
-__global__ __launch_bounds__(64 * NW) void k_linear_q8_stream(LinearQ8Args a) {
+template <typename T>
+__global__ __launch_bounds__(512) void k_linear_q8_stream(LinearQ8Args a) {
+  constexpr int NW = 8;
   __shared__ i32x4 part[NW - 1][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
@@ -52,21 +58,11 @@ __global__ __launch_bounds__(64 * NW) void k_linear_q8_stream(LinearQ8Args a) {
   const int8_t* w = a.wq + n * a.K + g * 16;
   const int8_t* x = a.q + m * a.K + g * 16;
   i32x4 acc = {};
-  // UN units at a time; past the end of the share the last one is loaded again
-  // and its activations are taken as zeros
-  for (int u = u0; u < u1; u += UN) {
-    i32x4 wr[2 * UN], xr[2 * UN];
-#pragma unroll
-    for (int j = 0; j < 2 * UN; ++j) {
-      const int k = min(u + j / 2, u1 - 1) * 128 + j % 2 * 64;
-      wr[j] = load16(w + k);
-      xr[j] = load16(x + k);
-    }
-#pragma unroll
-    for (int j = 0; j < 2 * UN; ++j) {
-      const i32x4 xv = u + j / 2 < u1 ? xr[j] : i32x4{0, 0, 0, 0};
-      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wr[j], xv, acc, 0, 0, 0);
-    }
+  for (int u = u0; u < u1; ++u) {
+    const i32x4 w0 = load16(w + u * 128), w1 = load16(w + u * 128 + 64);
+    const i32x4 x0 = load16(x + u * 128), x1 = load16(x + u * 128 + 64);
+    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0, x0, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w1, x1, acc, 0, 0, 0);
   }
   if (wave > 0) part[wave - 1][lane] = acc;
   __syncthreads();
@@ -632,9 +628,9 @@ hipError_t turns(const LinearQ8Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int NW, int UN>
+template <typename T>
 hipError_t stream(const LinearQ8Args& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_linear_q8_stream<T, NW, UN>), dim3((unsigned)((a.N + 15) / 16)), dim3(64 * NW), 0, s, a);
+  hipLaunchKernelGGL(k_linear_q8_stream<T>, dim3((unsigned)((a.N + 15) / 16)), dim3(512), 0, s, a);
   return hipGetLastError();
 }
 
@@ -690,12 +686,7 @@ Variant variant_of(int64_t M, int64_t N, int64_t K) {
 
 template <typename T>
 hipError_t linear_t(const LinearQ8Args& a, hipStream_t s) {
-  if (a.M <= 16) {
-    // a wavefront's share of the columns in one or two rounds of loads: 8
-    // wavefronts of 2 units for up to 2048 columns, 4 of 5 beyond (10576 x 2560:
-    // 8.2 against 8.9 us; 3352 x 768: 3.5 against 4.0 us)
-    return a.K <= 2048 ? stream<T, 8, 2>(a, s) : stream<T, 4, 5>(a, s);
-  }
+  if (a.M <= 16) return stream<T>(a, s);
   switch (variant_of(a.M, a.N, a.K)) {
     case kSplit: return split<T, 32, 32, 4, 3>(a, s);
     case kSplitPair: return split<T, 32, 32, 4, 2>(a, s);
