@@ -653,3 +653,26 @@ def test_side_stream_and_graph_replay():
             assert torch.equal(a, b), replay
         work()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [2, 63, 64, 65, 66, 127, 128, 129, 131, 192, 255, 256, 257])
+def test_narrow_rows(d, io):
+    """Rows of up to one wavefront's lanes, where a lane holds one, two or four
+    columns: on both sides of each change, even and odd."""
+    test_add_norm(d, io)
+    test_add_norm_backward(37, d, io)
+    test_add_norm_q8(9, d, io)
+    test_gated_norm(33, 3 * d, 3, 5, io)
+    test_gated_norm_backward(41, 2 * d, 2, 3, io)
+    test_gated_norm_q8(9, d, 1, io)
+    test_quantize_q8(9, d, io)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(33, 2560, 640), (40, 129, 128), (100, 3352, 768), (129, 2111, 384),
+                                   (17, 1001, 4992), (150, 2533, 1024)])
+def test_linear_q8_few_tiles(m, n, k, io):
+    """Columns split over wavefronts and turned from workgroup to workgroup: up
+    to one tile per compute unit and up to two, shares of none to ten steps."""
+    test_linear_q8(m, n, k, io)
