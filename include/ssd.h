@@ -561,6 +561,9 @@ typedef struct {
  *   q [M,Kp] int8, qscale [M] f32      wq [N,Kp] int8, wscale [N] f32
  *   out [M,N] out_dtype (written; element alignment)
  *   q and wq 16-byte aligned
+ *
+ * M <= 2^30, N <= 2^27 - 16 and (M/64 + 1) (N/64 + 1) < 2^24; larger problems
+ * return SSD_ERR_UNSUPPORTED.
  */
 ssd_status ssd_linear_q8(const ssd_linear_q8_desc* desc, const int8_t* q, const float* qscale,
                          const int8_t* wq, const float* wscale, void* out, hipStream_t stream);

@@ -261,8 +261,8 @@ ssd_status ssd_linear_q8(const ssd_linear_q8_desc* d, const int8_t* q, const flo
     return SSD_ERR_SHAPE;
   int64_t nq = 0, nw = 0, no = 0;
   // 2^14 * SSD_Q8_MAX_COLS < 2^31 bounds the integer sum for any 8-bit operands;
-  // a grid's threads (256 per 64 x 64 tile or per 16 outputs) count in 32 bits
-  if (d->cols > SSD_Q8_MAX_COLS || d->rows > (1 << 30) || d->outs > (1 << 27) ||
+  // a grid's threads (256 per 64 x 64 tile, 512 per 16 outputs) count in 32 bits
+  if (d->cols > SSD_Q8_MAX_COLS || d->rows > (1 << 30) || d->outs > (1 << 27) - 16 ||
       !elems_ok(d->rows, d->cols, &nq) || !elems_ok(d->outs, d->cols, &nw) ||
       !elems_ok(d->rows, d->outs, &no) || (d->rows / 64 + 1) * (d->outs / 64 + 1) >= (1 << 24))
     return SSD_ERR_UNSUPPORTED;

@@ -217,3 +217,12 @@ def test_row_strides_of_a_sliced_gate():
 def test_binding_refuses_what_is_no_tensor_or_has_no_columns(exc, fn):
     with pytest.raises(exc):
         fn()
+
+
+def test_linear_refuses_more_than_a_grid_counts():
+    """512 threads per 16 outputs, 256 per 64 x 64 tile, below 2^32 in all."""
+    lin = lambda r, o: call(lib.ssd_linear_q8, LinearQ8Desc(r, 128, o, 1), 5)
+    assert lin(1, (1 << 27) - 15) == UNSUP and lin(1, 1 << 27) == UNSUP
+    assert lin((1 << 30) + 1, 1) == UNSUP and lin(1 << 18, 1 << 18) == UNSUP
+    # the largest that one token has: its pointers are looked at
+    assert call(lib.ssd_linear_q8, LinearQ8Desc(1, 128, (1 << 27) - 16, 1), 5, p0=0) == INVALID
