@@ -676,3 +676,57 @@ def test_linear_q8_few_tiles(m, n, k, io):
     """Columns split over wavefronts and turned from workgroup to workgroup: up
     to one tile per compute unit and up to two, shares of none to ten steps."""
     test_linear_q8(m, n, k, io)
+
+
+def test_calls_check_what_they_are_given():
+    """Wrong types, layouts and buffers on the device are refused before any
+    launch; a caller's buffers come back as they are; nothing is leaked."""
+    need_gpu()
+    import sys
+
+    import state_space_model_amd as ssd
+    announce("checks of the calls")
+    c = dict(device="cuda")
+    x, r, w = torch.randn(6, 40, **c), torch.randn(6, 40, **c), torch.ones(40, **c)
+    for exc, f in (
+            (TypeError, lambda: ssd.ssd_add_norm(x, w.bfloat16())),
+            (TypeError, lambda: ssd.ssd_add_norm(x, w, r.bfloat16())),
+            (ValueError, lambda: ssd.ssd_add_norm(x, w.cpu())),
+            (ValueError, lambda: ssd.ssd_add_norm(torch.randn(40, 6, **c).t(), w)),
+            (TypeError, lambda: ssd.ssd_gated_norm(x, r.bfloat16(), w)),
+            (ValueError, lambda: ssd.ssd_gated_norm(x, torch.randn(40, 6, **c).t(), w)),
+            (TypeError, lambda: ssd.ssd_add_norm_q8(x, w, q=torch.empty(6, 128, **c))),
+            (TypeError, lambda: ssd.ssd_linear_q8(torch.empty(6, 128, **c), w[:6],
+                                                  torch.empty(5, 128, **c, dtype=torch.int8), w[:5]))):
+        with pytest.raises(exc):
+            f()
+    for status, f in (
+            (5, lambda: ssd.ssd_add_norm(torch.zeros(2, 16385, **c), torch.ones(16385, **c))),
+            (1, lambda: ssd.ssd_add_norm(x, w, r, y=x)),
+            (1, lambda: ssd.ssd_add_norm(x, w, r, eps=-1.0)),
+            (2, lambda: ssd.ssd_gated_norm(x, r, w, groups=3)),
+            (6, lambda: ssd.ssd_add_norm_backward(
+                torch.zeros(40, 40, **c), w, dy=torch.zeros(40, 40, **c),
+                workspace=torch.empty(16, **c, dtype=torch.uint8)))):
+        with pytest.raises(ssd.SSDError) as e:
+            f()
+        assert e.value.status == status
+    dw = torch.empty(40, **c)
+    out = torch.empty_like(x)
+    assert ssd.ssd_gated_norm(x, r, w, out=out) is out
+    assert ssd.ssd_gated_norm_backward(x, r, w, dout=x, grads={"dweight": dw})["dweight"] is dw
+
+    def work():
+        ssd.ssd_add_norm(x, w, r)
+        ssd.ssd_linear_q8(*ssd.ssd_gated_norm_q8(x, r, w), *ssd.ssd_quantize_q8(x))
+        ssd.ssd_gated_norm_backward(x, r, w, dout=x, grads={"dweight": dw})
+        with pytest.raises(ssd.SSDError):
+            ssd.ssd_add_norm(x, w, r, y=x)
+    work()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated(), [sys.getrefcount(t) for t in (x, r, w, dw, ssd.SSDError)]
+    for _ in range(50):
+        work()
+    torch.cuda.synchronize()
+    assert before == (torch.cuda.memory_allocated(),
+                      [sys.getrefcount(t) for t in (x, r, w, dw, ssd.SSDError)])
