@@ -92,13 +92,12 @@ void dense(const Tensor* t, const char* name, ScalarType want, const Tensor& fir
 }
 
 // Elements between the rows of t [..., D], whose rows must be dense and evenly
-// spaced (a slice of a projection's columns is).
+// spaced (a slice of a projection's columns is).  One dimension is one row.
 int64_t row_stride(const Tensor& t, const char* name) {
   const int64_t n = t.dim();
   const int64_t D = n ? t.size(n - 1) : 1;
-  if (n < 2) return D;
-  if (t.numel() == 0) return std::max(t.stride(n - 2), D);
-  bool ok = t.stride(n - 1) == 1 || D == 1;
+  if (t.numel() == 0) return n < 2 ? D : std::max(t.stride(n - 2), D);
+  bool ok = n == 0 || t.stride(n - 1) == 1 || D == 1;
   int64_t rows = 1, step = -1;
   for (int64_t d = n - 2; d >= 0; --d) {
     if (t.size(d) == 1) continue;
