@@ -245,7 +245,9 @@ __global__ __launch_bounds__(1024) void k_quantize_q8_wide(const T* v, int32_t K
 
 // ---------------------------------------------------------------------------
 // backward: a workgroup takes rows in turn and keeps its columns' part of
-// dweight in registers; the parts are summed by a second launch
+// dweight in registers; the parts are summed by a second launch.  The slope is
+// c (p - n mean(p n)) with the normalised row n formed first: the equal -c^3 r
+// mean(p r) leaves float32 at rows of 10^13 and 10^-13, where c itself does not
 // ---------------------------------------------------------------------------
 
 // The partial sums of the wavefronts that shared no row, added in the order of
@@ -315,12 +317,13 @@ __global__ __launch_bounds__(BLOCK ? kBlockThreads : kThreads) void k_add_norm_b
     }
     team_sum2<BLOCK>(ss, pr, sm[par]);
     const float c = rsqrtf(ss / (float)a.D + a.eps);
-    const float kr = c * c * c * (pr / (float)a.D);
+    const float m = c * (pr / (float)a.D);   // mean(p r c)
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const fvec<VEC> d = convert_pack<float, VEC>(dyr[k]);
-      acc[k] += d * (r[k] * c);
-      dr[k] += c * (d * w[k]) - kr * r[k];
+      const fvec<VEC> n = r[k] * c;
+      acc[k] += d * n;
+      dr[k] += c * (d * w[k] - n * m);
       if (cols.kept(k)) {
         if (a.dres) store_pack<VEC>(a.dres + o + cols.base[k], dr[k]);
         if (a.dx)
@@ -373,7 +376,7 @@ __global__ __launch_bounds__(BLOCK ? kBlockThreads : kThreads) void k_gated_norm
     }
     team_sum2<BLOCK>(ss, pg, sm[par]);
     const float c = rsqrtf(ss / (float)a.W + a.eps);
-    const float kg = c * c * c * (pg / (float)a.W);
+    const float m = c * (pg / (float)a.W);   // mean(p g c)
     T* dy = reinterpret_cast<T*>(a.dy) + o;
     T* dz = reinterpret_cast<T*>(a.dz) + row * a.dz_stride + c0;
 #pragma unroll
@@ -381,8 +384,9 @@ __global__ __launch_bounds__(BLOCK ? kBlockThreads : kThreads) void k_gated_norm
       const fvec<VEC> yf = convert_pack<float, VEC>(yr[k]), zf = convert_pack<float, VEC>(zr[k]);
       const fvec<VEC> d = convert_pack<float, VEC>(dr[k]);
       const fvec<VEC> act = zf * s[k], g = yf * act;
-      acc[k] += d * (g * c);
-      const fvec<VEC> dg = c * (d * w[k]) - kg * g;
+      const fvec<VEC> n = g * c;
+      acc[k] += d * n;
+      const fvec<VEC> dg = c * (d * w[k] - n * m);
       if (cols.kept(k)) {
         store_pack<VEC>(dy + cols.base[k], convert_pack<T, VEC>(dg * act));
         // silu'(z) = s (1 + z (1 - s)) = s + act (1 - s)
