@@ -217,14 +217,26 @@ def _nbytes(t: torch.Tensor) -> int:
 
 
 # The current stream's handle without a torch.cuda.Stream object around it,
-# which costs a one-token call 1.8 us more.
+# which costs a one-token call 1.8 us more, and the current device's index.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
-_calls.connect(SSDError, _raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_set_device = torch.cuda.set_device
+_calls.connect(SSDError, _raw_stream, _current_device, _set_device)
 
 
-def _stream(device) -> int:
-    return _raw_stream(device.index)
+def _launch(fn, device, *args) -> int:
+    """fn(*args, stream) on `device`'s current stream, with `device` current:
+    the handle of the default stream is the same for every device and means
+    the current one's."""
+    index, previous = device.index, _current_device()
+    if index == previous:
+        return fn(*args, _raw_stream(index))
+    _set_device(index)
+    try:
+        return fn(*args, _raw_stream(index))
+    finally:
+        _set_device(previous)
 
 
 def _scan_shapes(x, dt, A, B, C, D=None, dt_bias=None, initial_state=None) -> None:
@@ -311,20 +323,20 @@ def ssd_chunk_scan(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     wbytes = _nbytes(workspace)
     args = (ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(B), _ptr(C),
             _ptr(D), _ptr(initial_state), _ptr(y), _ptr(final_state), _ptr(workspace),
-            ctypes.c_size_t(wbytes), _stream(dev))
+            ctypes.c_size_t(wbytes))
     if variant != SSD_VARIANT_DEFAULT:
         if phase_events is not None:
             raise ValueError("phase_events time the default variant only")
-        st = lib.ssd_chunk_scan_ablation(args[0], int(variant), *args[1:])
+        st = _launch(lib.ssd_chunk_scan_ablation, dev, args[0], int(variant), *args[1:])
     elif phase_events is None:
-        st = lib.ssd_chunk_scan(*args)
+        st = _launch(lib.ssd_chunk_scan, dev, *args)
     else:
         for e in phase_events:  # torch creates the HIP event at its first record
             if not e.cuda_event:
-                e.record()
+                e.record(torch.cuda.current_stream(dev))
         evs = (ctypes.c_void_p * len(phase_events))(*[ctypes.c_void_p(e.cuda_event)
                                                       for e in phase_events])
-        st = lib.ssd_chunk_scan_timed(*args, evs, len(phase_events))
+        st = _launch(lambda *a: lib.ssd_chunk_scan_timed(*a, evs, len(phase_events)), dev, *args)
     if st != SSD_OK:
         raise SSDError(st, "ssd_chunk_scan")
     return y, final_state
@@ -356,9 +368,9 @@ def ssd_chunk_scan_noalloc(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B
     desc = scan_desc(x, B, chunk, dt_softplus, dt_limit)
     if y is None:
         y = torch.empty_like(x)
-    st = lib.ssd_chunk_scan_noalloc(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A),
-                                    _ptr(B), _ptr(C), _ptr(D), _ptr(initial_state), _ptr(y),
-                                    _ptr(final_state), _stream(x.device))
+    st = _launch(lib.ssd_chunk_scan_noalloc, x.device, ctypes.byref(desc), _ptr(x), _ptr(dt),
+                 _ptr(dt_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(initial_state), _ptr(y),
+                 _ptr(final_state))
     if st != SSD_OK:
         raise SSDError(st, "ssd_chunk_scan_noalloc")
     return y, final_state
@@ -399,8 +411,8 @@ def ssd_step(state: torch.Tensor, x_t: torch.Tensor, dt_t: torch.Tensor, A: torc
     if y_t is None:
         y_t = torch.empty_like(x_t)
     _check(y_t, "y_t", x_t.dtype)
-    st = lib.ssd_step(ctypes.byref(desc), _ptr(state), _ptr(x_t), _ptr(dt_t), _ptr(dt_bias),
-                      _ptr(A), _ptr(B_t), _ptr(C_t), _ptr(D), _ptr(y_t), _stream(state.device))
+    st = _launch(lib.ssd_step, state.device, ctypes.byref(desc), _ptr(state), _ptr(x_t), _ptr(dt_t),
+                 _ptr(dt_bias), _ptr(A), _ptr(B_t), _ptr(C_t), _ptr(D), _ptr(y_t))
     if st != SSD_OK:
         raise SSDError(st, "ssd_step")
     return y_t
@@ -467,12 +479,11 @@ def ssd_chunk_scan_backward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, 
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
     _check(workspace, "workspace")
-    st = lib.ssd_chunk_scan_backward(
-        ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+    st = _launch(
+        lib.ssd_chunk_scan_backward, dev, ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
         _ptr(initial_state), _ptr(dy), _ptr(dfinal_state), _ptr(out["dx"]), _ptr(out["ddt"]),
         _ptr(out["dA"]), _ptr(out["dB"]), _ptr(out["dC"]), _ptr(out["dD"]), _ptr(out["ddt_bias"]),
-        _ptr(out["dinitial_state"]), _ptr(workspace), ctypes.c_size_t(_nbytes(workspace)),
-        _stream(dev))
+        _ptr(out["dinitial_state"]), _ptr(workspace), ctypes.c_size_t(_nbytes(workspace)))
     if st != SSD_OK:
         raise SSDError(st, "ssd_chunk_scan_backward")
     return out
@@ -508,8 +519,8 @@ def ssd_conv1d(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     _check(y, "y", x.dtype)
     _check(state_out, "state_out", x.dtype)
     desc = ConvDesc(Bt, T, Dc, K, _io_code(x.dtype), int(bool(silu)))
-    st = lib.ssd_conv1d(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(state),
-                        _ptr(y), _ptr(state_out), _stream(x.device))
+    st = _launch(lib.ssd_conv1d, x.device, ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias),
+                 _ptr(state), _ptr(y), _ptr(state_out))
     if st != SSD_OK:
         raise SSDError(st, "ssd_conv1d")
     return y, state_out
@@ -535,8 +546,8 @@ def ssd_conv1d_step(state: torch.Tensor, x_t: torch.Tensor, weight: torch.Tensor
         y_t = torch.empty_like(x_t)
     _check(y_t, "y_t", x_t.dtype)
     desc = ConvDesc(Bt, 1, Dc, K, _io_code(x_t.dtype), int(bool(silu)))
-    st = lib.ssd_conv1d_step(ctypes.byref(desc), _ptr(state), _ptr(x_t), _ptr(weight),
-                             _ptr(bias), _ptr(y_t), _stream(x_t.device))
+    st = _launch(lib.ssd_conv1d_step, x_t.device, ctypes.byref(desc), _ptr(state), _ptr(x_t),
+                 _ptr(weight), _ptr(bias), _ptr(y_t))
     if st != SSD_OK:
         raise SSDError(st, "ssd_conv1d_step")
     return y_t

@@ -26,8 +26,10 @@ using at::ScalarType;
 using at::Tensor;
 using Shape = c10::SmallVector<int64_t, 6>;
 
-PyObject* g_error = nullptr;   // SSDError(status, where)
-PyObject* g_stream = nullptr;  // device index -> the current stream's handle
+PyObject* g_error = nullptr;           // SSDError(status, where)
+PyObject* g_stream = nullptr;          // device index -> the current stream's handle
+PyObject* g_current_device = nullptr;  // () -> the current device's index
+PyObject* g_set_device = nullptr;      // device index -> None: made current
 
 // ---------------------------------------------------------------------------
 // arguments
@@ -177,18 +179,58 @@ float* f32(const Tensor& t) { return static_cast<float*>(t.data_ptr()); }
 float* f32(const Tensor* t) { return t ? f32(*t) : nullptr; }
 int8_t* i8(const Tensor& t) { return static_cast<int8_t*>(t.data_ptr()); }
 
-hipStream_t stream(const Tensor& first) {
-  PyObject* index = PyLong_FromLong(first.get_device());
-  PyObject* handle = index ? PyObject_CallFunctionObjArgs(g_stream, index, nullptr) : nullptr;
-  Py_XDECREF(index);
-  if (!handle) throw python_error();
-  const uintptr_t s = (uintptr_t)PyLong_AsSize_t(handle);
-  Py_DECREF(handle);
+// a call's result as a number (None: 0)
+int64_t number_of(PyObject* r) {
+  if (!r) throw python_error();
+  const int64_t v = r == Py_None ? 0 : (int64_t)PyLong_AsUnsignedLongLong(r);
+  Py_DECREF(r);
   if (PyErr_Occurred()) throw python_error();
-  return reinterpret_cast<hipStream_t>(s);
+  return v;
+}
+int64_t ask(PyObject* f) { return number_of(PyObject_CallNoArgs(f)); }
+int64_t ask(PyObject* f, int64_t index) {
+  PyObject* i = PyLong_FromLongLong(index);
+  if (!i) throw python_error();
+  PyObject* r = PyObject_CallOneArg(f, i);
+  Py_DECREF(i);
+  return number_of(r);
 }
 
-void ok(ssd_status st, const char* where) {
+// The device of a call's tensors, current while the call launches: the handle
+// of the default stream is the same for every device and means the current
+// one's.
+class OnDevice {
+ public:
+  explicit OnDevice(int64_t index)
+      : previous_(ask(g_current_device)), moved_(index != previous_) {
+    if (moved_) ask(g_set_device, index);
+  }
+  ~OnDevice() {
+    if (!moved_) return;
+    try {
+      ask(g_set_device, previous_);
+    } catch (python_error&) {
+      PyErr_WriteUnraisable(g_set_device);
+    }
+  }
+  OnDevice(const OnDevice&) = delete;
+  OnDevice& operator=(const OnDevice&) = delete;
+
+ private:
+  int64_t previous_;
+  bool moved_;
+};
+
+// f(stream) -> status on the current stream of the first argument's device
+template <typename F>
+void launch(const Tensor& first, const char* where, F&& f) {
+  const int64_t index = first.get_device();
+  ssd_status st;
+  {
+    const auto s = reinterpret_cast<hipStream_t>((uintptr_t)ask(g_stream, index));
+    const OnDevice on(index);
+    st = f(s);
+  }
   if (st == SSD_OK) return;
   PyObject* e = PyObject_CallFunction(g_error, "is", (int)st, where);
   if (e) PyErr_SetObject(g_error, e);
@@ -261,8 +303,9 @@ PyObject* add_norm(PyObject* const* a) {
   dense(residual, "residual", at::kFloat, x);
   const Tensor r = output(r_, "residual_out", x.sizes(), at::kFloat, x);
   const Tensor y = output(y_, "y", x.sizes(), io, x);
-  ok(ssd_add_norm(&desc, ptr(x), f32(residual), f32(weight), ptr(y), f32(r), stream(x)),
-     "ssd_add_norm");
+  launch(x, "ssd_add_norm", [&](hipStream_t stream) {
+    return ssd_add_norm(&desc, ptr(x), f32(residual), f32(weight), ptr(y), f32(r), stream);
+  });
   return tuple({&y, &r});
 }
 
@@ -288,8 +331,10 @@ PyObject* add_norm_q8(PyObject* const* a) {
   const Tensor r = output(r_, "residual_out", x.sizes(), at::kFloat, x);
   const Tensor q = output(q_, "q", qshape, at::kChar, x);
   const Tensor s = output(s_, "qscale", lead, at::kFloat, x);
-  ok(ssd_add_norm_q8(&desc, ptr(x), f32(residual), f32(weight), i8(q), f32(s), f32(r), stream(x)),
-     "ssd_add_norm_q8");
+  launch(x, "ssd_add_norm_q8", [&](hipStream_t stream) {
+    return ssd_add_norm_q8(&desc, ptr(x), f32(residual), f32(weight), i8(q), f32(s), f32(r),
+                           stream);
+  });
   return tuple({&q, &s, &r});
 }
 
@@ -317,9 +362,10 @@ PyObject* add_norm_backward(PyObject* const* a) {
   const Tensor dresidual = output(dr_, "dresidual", r.sizes(), at::kFloat, r);
   const Tensor dweight = output(dw_, "dweight", D, at::kFloat, r);
   const Tensor ws = workspace(w_, ssd_add_norm_backward_workspace_bytes(&desc), r);
-  ok(ssd_add_norm_backward(&desc, f32(r), f32(weight), ptr(dy), f32(dr), ptr(dx), f32(dresidual),
-                           f32(dweight), ptr(ws), ws.nbytes(), stream(r)),
-     "ssd_add_norm_backward");
+  launch(r, "ssd_add_norm_backward", [&](hipStream_t stream) {
+    return ssd_add_norm_backward(&desc, f32(r), f32(weight), ptr(dy), f32(dr), ptr(dx),
+                                 f32(dresidual), f32(dweight), ptr(ws), ws.nbytes(), stream);
+  });
   return dict({{"dx", &dx}, {"dresidual", &dresidual}, {"dweight", &dweight}});
 }
 
@@ -343,7 +389,9 @@ PyObject* gated_norm(PyObject* const* a) {
   shape(&weight, "weight", y.size(-1));
   const ssd_gated_norm_desc desc = gated_desc(y, z, weight, a[3], a[4]);
   const Tensor out = output(o_, "out", y.sizes(), y.scalar_type(), y);
-  ok(ssd_gated_norm(&desc, ptr(y), ptr(z), f32(weight), ptr(out), stream(y)), "ssd_gated_norm");
+  launch(y, "ssd_gated_norm", [&](hipStream_t stream) {
+    return ssd_gated_norm(&desc, ptr(y), ptr(z), f32(weight), ptr(out), stream);
+  });
   return wrap(out);
 }
 
@@ -360,8 +408,9 @@ PyObject* gated_norm_q8(PyObject* const* a) {
   const ssd_gated_norm_desc desc = gated_desc(y, z, weight, a[3], a[4]);
   const Tensor q = output(q_, "q", qshape, at::kChar, y);
   const Tensor s = output(s_, "qscale", lead, at::kFloat, y);
-  ok(ssd_gated_norm_q8(&desc, ptr(y), ptr(z), f32(weight), i8(q), f32(s), stream(y)),
-     "ssd_gated_norm_q8");
+  launch(y, "ssd_gated_norm_q8", [&](hipStream_t stream) {
+    return ssd_gated_norm_q8(&desc, ptr(y), ptr(z), f32(weight), i8(q), f32(s), stream);
+  });
   return tuple({&q, &s});
 }
 
@@ -386,9 +435,10 @@ PyObject* gated_norm_backward(PyObject* const* a) {
   const Tensor dy = output(dy_, "dy", y.sizes(), io, y);
   const Tensor dweight = output(dw_, "dweight", D, at::kFloat, y);
   const Tensor ws = workspace(w_, ssd_gated_norm_backward_workspace_bytes(&desc), y);
-  ok(ssd_gated_norm_backward(&desc, ptr(y), ptr(z), f32(weight), ptr(dout), ptr(dy), ptr(dz),
-                             f32(dweight), ptr(ws), ws.nbytes(), stream(y)),
-     "ssd_gated_norm_backward");
+  launch(y, "ssd_gated_norm_backward", [&](hipStream_t stream) {
+    return ssd_gated_norm_backward(&desc, ptr(y), ptr(z), f32(weight), ptr(dout), ptr(dy), ptr(dz),
+                                   f32(dweight), ptr(ws), ws.nbytes(), stream);
+  });
   return dict({{"dy", &dy}, {"dz", &dz}, {"dweight", &dweight}});
 }
 
@@ -405,7 +455,9 @@ PyObject* quantize_q8(PyObject* const* a) {
   dense(&v, "v", v.scalar_type(), v);
   const Tensor q = output(q_, "q", qshape, at::kChar, v);
   const Tensor s = output(s_, "qscale", lead, at::kFloat, v);
-  ok(ssd_quantize_q8(rows(v), K, code, ptr(v), i8(q), f32(s), stream(v)), "ssd_quantize_q8");
+  launch(v, "ssd_quantize_q8", [&](hipStream_t stream) {
+    return ssd_quantize_q8(rows(v), K, code, ptr(v), i8(q), f32(s), stream);
+  });
   return tuple({&q, &s});
 }
 
@@ -428,8 +480,9 @@ PyObject* linear_q8(PyObject* const* a) {
   dense(&wq, "wq", at::kChar, q);
   dense(&wscale, "wscale", at::kFloat, q);
   const Tensor out = output(o_, "out", oshape, io, q);
-  ok(ssd_linear_q8(&desc, i8(q), f32(qscale), i8(wq), f32(wscale), ptr(out), stream(q)),
-     "ssd_linear_q8");
+  launch(q, "ssd_linear_q8", [&](hipStream_t stream) {
+    return ssd_linear_q8(&desc, i8(q), f32(qscale), i8(wq), f32(wscale), ptr(out), stream);
+  });
   return wrap(out);
 }
 
@@ -467,10 +520,11 @@ PyObject* conv1d_backward(PyObject* const* a) {
   if (silu < 0) throw python_error();
   const ssd_conv_desc desc{Bt, T, D, K, code, silu};
   const Tensor ws = workspace(w_, ssd_conv1d_backward_workspace_bytes(&desc), x);
-  ok(ssd_conv1d_backward(&desc, io_code(cot, "dy"), ptr(x), f32(weight), f32(bias), ptr(state),
-                         ptr(dy), ptr(ds), ptr(dx), f32(dweight), f32(dbias), ptr(dstate), ptr(ws),
-                         ws.nbytes(), stream(x)),
-     "ssd_conv1d_backward");
+  launch(x, "ssd_conv1d_backward", [&](hipStream_t stream) {
+    return ssd_conv1d_backward(&desc, io_code(cot, "dy"), ptr(x), f32(weight), f32(bias),
+                               ptr(state), ptr(dy), ptr(ds), ptr(dx), f32(dweight), f32(dbias),
+                               ptr(dstate), ptr(ws), ws.nbytes(), stream);
+  });
   return dict({{"dx", &dx}, {"dweight", &dweight}, {"dbias", &dbias}, {"dstate", &dstate}});
 }
 
@@ -486,15 +540,16 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// SSDError, the lookup of the current stream
+// SSDError, the current stream of a device, the current device, setting it
 PyObject* connect(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  TORCH_CHECK_TYPE(n == 2, "expected 2 arguments, got ", n);
-  for (int i = 0; i < 2; ++i) Py_INCREF(args[i]);
-  Py_XDECREF(g_error);
-  Py_XDECREF(g_stream);
-  g_error = args[0];
-  g_stream = args[1];
+  PyObject** const kept[] = {&g_error, &g_stream, &g_current_device, &g_set_device};
+  TORCH_CHECK_TYPE(n == 4, "expected 4 arguments, got ", n);
+  for (int i = 0; i < 4; ++i) {
+    Py_INCREF(args[i]);
+    Py_XDECREF(*kept[i]);
+    *kept[i] = args[i];
+  }
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
