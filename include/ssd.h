@@ -397,8 +397,9 @@ ssd_status ssd_conv1d_step(const ssd_conv_desc* desc, void* state, const void* x
  *   aligned
  *
  * All sums are float32 in an order that depends on the shape alone (no
- * atomics).  Shapes and grid limits as ssd_conv1d.  Outputs may not overlap
- * any input, the workspace or each other.  batch == 0 or seqlen == 0 writes
+ * atomics).  Shapes and grid limits as ssd_conv1d, and D <= 2^29 - 64, with
+ * seqlen == 0 also Bt * D * (k-1) <= 2^32 - 256.  Outputs may not overlap any
+ * input, the workspace or each other.  batch == 0 or seqlen == 0 writes
  * zeros to dw and dbias; with seqlen == 0 dstate is dstate_out (or zeros).
  */
 size_t ssd_conv1d_backward_workspace_bytes(const ssd_conv_desc* desc);

@@ -296,7 +296,7 @@ ssd_status check_conv_backward(const ssd_conv_desc* d, ConvBwdSizes* s) {
   if (!conv_width_supported(d->width) || !mul_ok(d->batch, d->seqlen, &bt) ||
       !elems_ok(bt, d->channels, &s->n) || !mul_ok(d->batch, d->channels, &bd) ||
       !elems_ok(bd, d->width - 1, &s->n_state) ||
-      !conv_shape_supported(d->batch, d->seqlen, d->channels))
+      !conv_backward_shape_supported(d->batch, d->seqlen, d->channels, d->width))
     return SSD_ERR_UNSUPPORTED;
   return SSD_OK;
 }

@@ -272,6 +272,14 @@ hipError_t launch_t(const ConvBwdArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// A grid's threads are counted in 32 bits: those of the sum of the parts and,
+// for an empty sequence, of the window's gradient.
+bool conv_backward_shape_supported(int64_t Bt, int64_t T, int64_t D, int64_t K) {
+  const int64_t windows = Bt * D * (K - 1);
+  return conv_shape_supported(Bt, T, D) && (D + 63) / 64 * (64 * SPLIT) <= UINT32_MAX &&
+         (T > 0 || (windows + kThreads - 1) / kThreads * kThreads <= UINT32_MAX);
+}
+
 int64_t conv_backward_parts(int64_t Bt, int64_t T, int64_t D) {
   return Bt > 0 && T > 0 ? Bt * runs_of(Bt, T, D).groups : 0;
 }

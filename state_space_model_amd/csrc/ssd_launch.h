@@ -234,6 +234,7 @@ hipError_t launch_step_bf16(const StepArgs& a, hipStream_t stream);
 // one-token kernel (step == true, window in state_out, updated in place).
 bool conv_width_supported(int64_t K);
 bool conv_shape_supported(int64_t Bt, int64_t T, int64_t D);
+bool conv_backward_shape_supported(int64_t Bt, int64_t T, int64_t D, int64_t K);
 hipError_t launch_conv(const ConvArgs& a, bool io_bf16, bool step, hipStream_t stream);
 
 // Rows of partial sums of dweight / (dw, dbias) the gradients leave in their
