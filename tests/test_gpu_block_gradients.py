@@ -1,5 +1,6 @@
 """The norms' gradients against their float64 definitions (oracle.block) over
-the range of sizes that their forwards take.  Bars as in test_gpu_block, whose terms scale with the inputs."""
+the range of sizes that their forwards take, and where a workgroup takes
+several rows.  Bars as in test_gpu_block, whose terms scale with the inputs."""
 import numpy as np
 import pytest
 import torch
@@ -80,3 +81,26 @@ def test_gated_norm_gradients_of_large_and_small_rows(d, groups, size, eps, io):
     announce(f"gated_norm_backward {io} 9x{d} groups {groups} of size {size}, eps {eps}")
     g, y, w, z = gated_case(9, d, io, d, 0)
     check_gated_norm(y * size, z, w, randn(g, 9, d, io=io), groups, eps, io)
+
+
+# Rows beyond one per workgroup (512 workgroups over all groups; four wavefronts
+# with a row each, or a workgroup per row), so that every workgroup takes
+# several, some one more than others, and the second launch adds all the parts.
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,d", [(1300, 2048), (1100, 4099), (700, 8200), (2600, 130), (5003, 768)])
+def test_add_norm_gradients_of_many_rows(rows, d, io):
+    need_gpu()
+    announce(f"add_norm_backward {io} {rows}x{d}")
+    g = gen(rows + d)
+    check_add_norm(2 * randn(g, rows, d), 1 + 0.1 * randn(g, d), randn(g, rows, d, io=io),
+                   randn(g, rows, d), EPS, io)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,d,groups", [(700, 4096, 1), (1100, 8192, 2), (1541, 5120, 1),
+                                           (9001, 96, 3), (3001, 1536, 4)])
+def test_gated_norm_gradients_of_many_rows(rows, d, groups, io):
+    need_gpu()
+    announce(f"gated_norm_backward {io} {rows}x{d} groups {groups}")
+    g, y, w, z = gated_case(rows, d, io, rows + d, 0)
+    check_gated_norm(y, z, w, randn(g, rows, d, io=io), groups, EPS, io)
