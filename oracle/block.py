@@ -1,9 +1,8 @@
 """The operators between two scans in float64 (numpy): test infrastructure.
 
-Norms, 8-bit rows and their product, and the gradients of the norms and of the
-depthwise convolution, written from their definitions.  Gradients come from
-the chain rule term by term (Jacobian products formed directly), not from the
-fused expressions the library uses.
+The norms, their gradients and those of the depthwise convolution, written from
+their definitions.  Gradients come from the chain rule term by term (Jacobian
+products formed directly), not from the fused expressions the library uses.
 """
 from __future__ import annotations
 
@@ -72,12 +71,6 @@ def gated_norm(y, z, weight, eps, groups=1):
 def gated_norm_backward(y, z, weight, dout, eps, groups=1):
     dg, dw = norm_backward(y * silu(z), weight, eps, dout, groups)
     return {"dy": dg * silu(z), "dz": dg * y * silu_slope(z), "dweight": dw}
-
-
-def linear_q8(q, qscale, wq, wscale):
-    """Exact integer product, scales applied in float64."""
-    acc = q.astype(np.int64) @ wq.astype(np.int64).T
-    return acc.astype(np.float64) * qscale[..., None] * wscale
 
 
 def conv1d_backward(x, weight, bias, dy, state=None, dstate_out=None, silu_on=True):
