@@ -53,8 +53,8 @@
  *    even).
  *  - The caller owns every buffer, including the workspace.  The library never
  *    allocates, frees or synchronises; calls are asynchronous on `stream`
- *    (0 = the null stream) and results are valid once the stream has reached
- *    them.  The library keeps no mutable global state other than the
+ *    (0 = the null stream of the current device, which must be the buffers')
+ *    and results are valid once the stream has reached them.  The library keeps no mutable global state other than the
  *    per-device address of ssd_chunk_scan_noalloc's static scratch.
  *  - Errors: arguments are validated before anything is launched; on any error
  *    other than SSD_ERR_HIP nothing has been written.  SSD_ERR_HIP means a

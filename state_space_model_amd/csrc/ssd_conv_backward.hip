@@ -14,13 +14,13 @@
 // added by a second launch.
 //
 // Measured (kernel time in a HIP graph, inputs rotated through HBM): 4096 x 5376
-// bfloat16 with float32 dy 42 us, 36 of them the first launch (4.9 TB/s); 3 x
-// 1001 x 1793 float32 with a window 23.5 us.  Four channels per lane (164 registers,
-// three wavefronts per SIMD, 1.9 resident on average) took 46-49 us however
-// the runs were split, eight tokens per batch 46-65 us, and runs shared out
-// over the wavefronts of a workgroup (their rows apart) 46 us: what counts is
-// that neighbouring wavefronts read neighbouring columns of the same rows and
-// that all of them are resident at once.
+// bfloat16 with float32 dy 42 us, 38 to 40 of them the first launch (4.9 TB/s
+// with the tokens read twice); 3 x 1001 x 1793 float32 with a window 22-23 us.
+// Four channels per lane (164 registers, three wavefronts per SIMD, 1.9
+// resident on average) took 46-49 us however the runs were split, eight tokens
+// per batch 46-65 us, and runs shared out over the wavefronts of a workgroup
+// (their rows apart) 46 us: what counts is that neighbouring wavefronts read
+// neighbouring columns of the same rows and that enough of them are resident.
 #include <type_traits>
 
 #include "ssd_launch.h"
@@ -226,10 +226,15 @@ __global__ __launch_bounds__(kThreads) void k_conv_hand_on(const T* src, T* dst,
   if (i < n) dst[i] = src ? src[i] : to_io<T>(0.0f);
 }
 
-// How the tokens are split: `groups` runs of R tokens along time, so that the
-// workgroups are all resident at once (three per compute unit: each holds its
-// registers for a whole run, and a second round would run half empty) and a
-// run is long against the k-1 tokens it reads twice.
+// How the tokens are split: `groups` runs of R tokens along time, the fewest
+// that give three workgroups to a compute unit (five fit, at up to 92
+// registers), each long against the k-1 tokens it reads twice.  All workgroups
+// are resident at once up to 640 blocks of columns over the batch; between
+// 641 and 767 the two runs of each are up to 1534 workgroups, a part of which
+// waits.  With the quotient rounded down, at most three to a unit, 11 x 3000 x
+// 1500 took 99 us against 109, 64 x 256 x 5376 153 against 164 and 4096 x 5376
+// the same, but 26 x 512 x 5120 (two runs instead of three) 130 against 126 and
+// 260 x 512 x 512 134 against 129.
 struct Runs {
   int64_t R, groups;
 };

@@ -642,9 +642,16 @@ hipError_t tile(const LinearQ8Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The kernel for M tokens, N outputs and K columns.  Up to 16 tokens the weights
-// stream (one tile of tokens: the matrix cores idle, and what counts is how
-// many bytes are in flight).  Beyond, the tile with the least modelled time:
+// The kernel for M tokens, N outputs and K columns.  Up to 16 tokens, as many
+// as one instruction of the stream holds, the weights stream.  Against the
+// better of the two split tiles (us, in a HIP graph):
+//   N x K         1 token      8 tokens     16 tokens     17 tokens
+//   768 x 1536   3.2 / 3.7    3.5 / 3.8    3.8 / 4.1        - / 4.1
+//   3352 x 768   3.2 / 3.8    3.4 / 3.9    3.6 / 3.9        - / 4.0
+//   2048 x 4096  4.9 / 5.5    5.6 / 5.6    6.2 / 5.7        - / 5.7
+//   2560 x 5120  6.3 / 7.8    6.8 / 8.4    7.7 / 9.0        - / 9.1
+//   10576 x 2560 8.8 / 9.7    9.5 / 9.5   10.9 / 10.1       - / 10.2
+// (16 tokens of two of these shapes would gain 7 to 8% on split tiles.)  Beyond, the tile with the least modelled time:
 // rounds over the 256 compute units times (fixed + columns / 128 * step), in
 // units of 0.01 us fitted to these measurements (us, kernel time):
 //                          64 x 2560  128 x 2560  256 x 2560  1024 x 2560  4096 x 2560  4096 x 10576
@@ -657,6 +664,8 @@ hipError_t tile(const LinearQ8Args& a, hipStream_t s) {
 //   192 x 256 in turns                                                          62          127
 //   224 x 256 in turns                                                          61          106-115
 //   256 x 256 in turns                                                          77          118-132
+// (The model overstates the split tiles past their first round, 23 to 27 us for
+// 256 x 2560 x 5120, where 64 x 64 tiles are the fastest and taken.)
 // A larger tile moves fewer bytes per product but fills the last round worse;
 // at 8192 x 8192 x 8192 the 256 x 256 tiles reach 2.7 Pop/s (405 us), where the
 // same instructions on operands that never change reach 4.0-4.5 (the clock

@@ -9,21 +9,27 @@
 //   gated norm  g  = y z / (1+e^-z);   out = g c w,   c per group of columns
 //   8-bit rows  a = max|v|;  q = rint(v 127/a), scale a/127
 //
-// Every kernel reads its row once, keeps it in registers through the
-// reduction, and writes once: they are bound by memory.  A row (or one group
+// A kernel reads its row once, keeps it in registers through the reduction, and
+// writes once (two kernels of 8-bit rows, for several groups and for the widest
+// rows, read it twice): they are bound by memory.  A row (or one group
 // of it) is shared by one wavefront or by a workgroup (RowTeam).  Measured on
 // one MI355X (kernel time in a HIP graph, inputs rotated through HBM):
-//   add norm   131072 x 2048 bfloat16   555 us  5.8 TB/s
-//              4097 x 768 float32      10.7 us  4.7 TB/s
+//   add norm   131072 x 2048 bfloat16   567 us  5.7 TB/s
+//              4097 x 768 float32      10.5 us  4.8 TB/s
 //   gated norm 4096 x 5120 bfloat16    24.1 us  5.2 TB/s
-//   gradients: add norm 4096 x 2560    32.3 us  5.2 TB/s (the sum of the parts 4 us of it)
-//              gated, 8 groups, 16384 x 4096   127 us  5.3 TB/s
-// against 4.8 TB/s for a plain copy of 4 GiB.  Tried and slower: non-temporal
-// stores (555 -> 572 us, gradients 32.3 -> 38.6 us: the next kernel's reads
-// and the partial lines of two instructions meet in the cache), forward
-// wavefronts that take rows in turn with the weight kept in registers (555 ->
-// 605 us), the gradients' next row requested before the current one's
-// reduction (32.3 -> 33.8 us).
+//   gradients: add norm 4096 x 2560    32.6 us  5.1 TB/s (the sum of the parts 4 us of it)
+//              gated, 8 groups, 16384 x 4096   129 us  5.2 TB/s (145 us on another card)
+//   8-bit rows 10576 x 2560 float32    25.0 us  5.4 TB/s
+//              4096 x 2560 bfloat16     9.1 us  3.5 TB/s
+// against 4.8 TB/s for a plain copy of 4 GiB.  Just past a change of variant,
+// where 33 to 42 of 64 lanes have a vector, less of it is reached: 65536 rows of
+// 264 and 333 bfloat16 columns, gradients of the gated norm 3.3 and 3.9 TB/s,
+// its forward 4.3 and 4.4, 8-bit rows 3.0 and 3.6 (512 columns: 5.1, 5.8, 5.1).
+// Tried and slower: non-temporal stores (555 -> 572 us, gradients 32.3 -> 38.6
+// us: the next kernel's reads and the partial lines of two instructions meet in
+// the cache), forward wavefronts that take rows in turn with the weight kept in
+// registers (555 -> 605 us), the gradients' next row requested before the
+// current one's reduction (32.3 -> 33.8 us).
 #include <type_traits>
 
 #include "ssd_launch.h"
@@ -158,7 +164,8 @@ __global__ __launch_bounds__(BLOCK ? kBlockThreads : kThreads) void k_gated_norm
 // The gated norm of several groups as one 8-bit row: a workgroup per row.  The
 // scale needs every group's norm first, so wavefronts take the groups in turn
 // for the mean squares and the largest |g w|, and the second pass reads the
-// row again (from the cache).
+// row again (from the cache) and forms every gate again: 4096 x 5120 bfloat16
+// in 4 groups 48 us, against 23.5 us for one group in registers.
 template <typename T, int VEC>
 __global__ __launch_bounds__(1024) void k_gated_norm_groups_q8(GatedNormArgs a) {
   __shared__ float rms[1024];      // 1/rms of each group (SSD_NORM_MAX_GROUPS_Q8)
@@ -229,7 +236,8 @@ __global__ __launch_bounds__(BLOCK ? kBlockThreads : kThreads) void k_quantize_q
   if (lane == 0) qscale[row] = q8.scale;
 }
 
-// rows wider than the register kernels hold: two passes over the row
+// rows wider than the register kernels hold: two passes over the row, a column
+// per lane (64 x 130944 float32: 104 us, 0.4 TB/s; 256 x 20000 bfloat16: 12.5)
 template <typename T>
 __global__ __launch_bounds__(1024) void k_quantize_q8_wide(const T* v, int32_t K, int32_t Kp,
                                                            int8_t* q, float* qscale) {
@@ -247,7 +255,7 @@ __global__ __launch_bounds__(1024) void k_quantize_q8_wide(const T* v, int32_t K
 // backward: a workgroup takes rows in turn and keeps its columns' part of
 // dweight in registers; the parts are summed by a second launch.  The slope is
 // c (p - n mean(p n)) with the normalised row n formed first: the equal -c^3 r
-// mean(p r) leaves float32 at rows of 10^13 and 10^-13, where c itself does not
+// mean(p r) leaves float32 at rows of 10^14 and 10^-13, where c itself does not
 // ---------------------------------------------------------------------------
 
 // The partial sums of the wavefronts that shared no row, added in the order of

@@ -5,8 +5,8 @@
 // It exists for the calls that a token makes one at a time, which the host
 // bounds: a norm of one token needs the GPU for 2 us and 3.1 us of the host for
 // its launch.  Per call, against the same checks and allocations made from
-// Python: one-token add norm 4.8 us (8.2), add norm and 8-bit product 10.4 us
-// (19.7), gradients of the gated norm 9.3 us (15.8).
+// Python: one-token add norm 4.7-5.6 us (8.2), add norm and 8-bit product 11.0 us
+// (19.7), gradients of the gated norm 10.4 us (15.8).
 #include <Python.h>
 
 #include <ATen/ATen.h>
