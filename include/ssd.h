@@ -23,6 +23,9 @@
  *                   residual add with the norm before a block, the gated norm
  *                   after its scan, the block's projections in 8-bit
  *                   integers, and the gradients of its convolution.
+ *   ssd_delta_scan, ssd_delta_step
+ *                   the gated delta rule, a mixer with the scan's decay and
+ *                   fixed-size state: over a sequence and for one token.
  *
  * The scan and the step compute, for every batch row b and head h (g = h / (H/G) is the B/C
  * group of head h), the selective diagonal SSM
@@ -568,6 +571,85 @@ typedef struct {
  */
 ssd_status ssd_linear_q8(const ssd_linear_q8_desc* desc, const int8_t* q, const float* qscale,
                          const int8_t* wq, const float* wscale, void* out, hipStream_t stream);
+
+/* Problem description of the gated delta rule (the scan, its step, its gradients). */
+typedef struct {
+  int64_t batch;      /* Bt >= 0 */
+  int64_t seqlen;     /* T >= 0; not used by ssd_delta_step */
+  int64_t nheads;     /* H: heads of v and y */
+  int64_t headdim;    /* P: a head's values, a multiple of 8 up to SSD_DELTA_MAX_P */
+  int64_t dstate;     /* N: a head's keys, a multiple of 8 up to SSD_DELTA_MAX_N */
+  int64_t ngroups;    /* G divides H: heads of q and k, each serving H/G adjacent heads */
+  int64_t q_stride;   /* elements between tokens of q, >= G*N; of k, the same; of v, >= H*P */
+  int64_t k_stride;
+  int64_t v_stride;
+  int64_t dq_stride;  /* the same for dq, dk, dv (the gradients only) */
+  int64_t dk_stride;
+  int64_t dv_stride;
+  int32_t io_dtype;   /* ssd_dtype of q, k, v, y and of the gradients of q, k, v */
+  int32_t dt_softplus;  /* 1: Delta = clip(softplus(dt + dt_bias)); 0: clip(dt + dt_bias) */
+  int32_t beta_sigmoid; /* 1: b = logistic(beta); 0: b = beta */
+  int32_t qk_norm;      /* 1: every key and query is divided by its length */
+  float dt_min, dt_max; /* clip bounds, dt_min <= dt_max (infinities allowed) */
+  float norm_eps;       /* added to the squared length, >= 0 */
+  float scale;          /* multiplies q (finite) */
+} ssd_delta_desc;
+
+#define SSD_DELTA_MAX_N 128
+#define SSD_DELTA_MAX_P 256
+
+/*
+ * The gated delta rule over a whole sequence: the linear-time mixer whose
+ * fixed-size state decays like the scan's, but where a token's write is the
+ * difference between its value and what the state already holds for its key.
+ * Per batch row b and head h (g = h / (H/G) its group of keys and queries):
+ *
+ *   Delta_t = clip(softplus(dt + dt_bias[h]), dt_min, dt_max);  a_t = exp(Delta_t A[h])
+ *   b_t = logistic(beta);  k^ = k / sqrt(|k|^2 + norm_eps);  q^ = scale q / sqrt(|q|^2 + norm_eps)
+ *   S_t[p,n] = a_t S_{t-1}[p,n] + b_t (v_t[p] - a_t sum_m S_{t-1}[p,m] k^_t[m]) k^_t[n]
+ *   y_t[p]   = sum_n S_t[p,n] q^_t[n]
+ *
+ *   q, k [Bt,T,G,N] io_dtype, v [Bt,T,H,P] io_dtype: a token's heads are dense,
+ *        tokens a stride apart (slices of the convolution's output are), token
+ *        (b, t) at row b T + t; pointers and strides in bytes multiples of 16
+ *   dt, beta [Bt,T,H] f32      A [H] f32 (<= 0)      dt_bias [H] f32 or NULL
+ *   initial_state [Bt,H,P,N] f32 or NULL (zeros)
+ *   y [Bt,T,H,P] io_dtype (written)
+ *   final_state [Bt,H,P,N] f32 (written) or NULL; it may be initial_state itself
+ *   workspace: at least ssd_delta_scan_workspace_bytes(desc), 256-byte aligned;
+ *        its contents need not survive, calls that may overlap need their own
+ *
+ * A caller that has the logarithm of a_t passes it as dt with A = 1,
+ * dt_softplus = 0 and clip bounds -inf, inf (it must not be positive).  A
+ * token with Delta = 0 and b = 0 (with dt_min = 0: dt = beta = -inf) leaves the
+ * state as it is: batches of unequal lengths are padded with such tokens.
+ *
+ * Computed in chunks of 64 tokens.  States, writes and decays are float32 for
+ * both io types; a bfloat16 y is rounded once.  A NaN or an infinity in a token
+ * of q, k, v, dt or beta reaches the outputs of its chunk, earlier tokens of
+ * the chunk included, and of later ones; no other head that does not share it
+ * and no other batch row.  The bits of a sequence do not depend on the batch.
+ * Bt H ceil(T/64) and Bt H ceil(P/16) below 2^24, else SSD_ERR_UNSUPPORTED.
+ */
+size_t ssd_delta_scan_workspace_bytes(const ssd_delta_desc* desc);
+ssd_status ssd_delta_scan(const ssd_delta_desc* desc, const void* q, const void* k, const void* v,
+                          const float* dt, const float* dt_bias, const float* A, const float* beta,
+                          const float* initial_state, void* y, float* final_state, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token of the gated delta rule, the state updated in place:
+ *
+ *   state [Bt,H,P,N] f32, read and overwritten with the new state
+ *   q_t, k_t [Bt,G,N], v_t [Bt,H,P] io_dtype, batch rows a stride apart
+ *   dt_t, beta_t [Bt,H] f32      y_t [Bt,H,P] io_dtype (written)
+ *
+ * The rest as ssd_delta_scan; each state element is read once and written once.
+ */
+ssd_status ssd_delta_step(const ssd_delta_desc* desc, float* state, const void* q_t,
+                          const void* k_t, const void* v_t, const float* dt_t,
+                          const float* dt_bias, const float* A, const float* beta_t, void* y_t,
+                          hipStream_t stream);
 
 /* Static description of a status code (never NULL). */
 const char* ssd_status_string(ssd_status status);

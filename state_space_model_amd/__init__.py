@@ -19,12 +19,18 @@ and, for the rest of a block between two scans,
   ssd_linear_q8(q, qscale, wq, wscale)          -> out                 product of 8-bit rows
   ssd_add_norm_backward, ssd_gated_norm_backward, ssd_conv1d_backward -> dict of gradients
 
+and the gated delta rule, a mixer with the scan's decay and fixed-size state,
+
+  ssd_delta_scan(q, k, v, dt, A, beta, ...)          -> (y, final_state)
+  ssd_delta_step(state, q_t, k_t, v_t, dt_t, A, beta_t, ...) -> y_t  (state updated in place)
+
 Source: "Compiler-First State Space Duality and Portable O(1) Autoregressive
 Caching" (Background, Eq. 2-3; O(1) cache).
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Sequence, Tuple
 
@@ -57,6 +63,7 @@ EXPORTED = ("ssd_chunk_scan", "ssd_chunk_scan_timed", "ssd_chunk_scan_workspace_
             "ssd_add_norm_backward_workspace_bytes", "ssd_gated_norm", "ssd_gated_norm_q8",
             "ssd_gated_norm_backward", "ssd_gated_norm_backward_workspace_bytes",
             "ssd_quantize_q8", "ssd_linear_q8",
+            "ssd_delta_scan", "ssd_delta_scan_workspace_bytes", "ssd_delta_step",
             "ssd_status_string", "ssd_abi_version")
 
 
@@ -97,6 +104,15 @@ class GatedNormDesc(ctypes.Structure):
 class LinearQ8Desc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("outs", ctypes.c_int64),
                 ("out_dtype", ctypes.c_int32)]
+
+
+class DeltaDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in
+                 ("batch", "seqlen", "nheads", "headdim", "dstate", "ngroups", "q_stride",
+                  "k_stride", "v_stride", "dq_stride", "dk_stride", "dv_stride")]
+                + [(n, ctypes.c_int32) for n in
+                   ("io_dtype", "dt_softplus", "beta_sigmoid", "qk_norm")]
+                + [(n, ctypes.c_float) for n in ("dt_min", "dt_max", "norm_eps", "scale")])
 
 
 class SSDError(RuntimeError):
@@ -160,6 +176,12 @@ def _load() -> ctypes.CDLL:
     L.ssd_quantize_q8.argtypes = [ctypes.c_int64, ctypes.c_int64, i32] + [vp] * 3 + [vp]
     L.ssd_linear_q8.restype = i32
     L.ssd_linear_q8.argtypes = [ctypes.POINTER(LinearQ8Desc)] + [vp] * 5 + [vp]
+    L.ssd_delta_scan_workspace_bytes.restype = sz
+    L.ssd_delta_scan_workspace_bytes.argtypes = [ctypes.POINTER(DeltaDesc)]
+    L.ssd_delta_scan.restype = i32
+    L.ssd_delta_scan.argtypes = [ctypes.POINTER(DeltaDesc)] + [vp] * 11 + [sz, vp]
+    L.ssd_delta_step.restype = i32
+    L.ssd_delta_step.argtypes = [ctypes.POINTER(DeltaDesc)] + [vp] * 9 + [vp]
     L.ssd_status_string.restype = ctypes.c_char_p
     L.ssd_status_string.argtypes = [i32]
     L.ssd_abi_version.restype = i32
@@ -656,6 +678,52 @@ def ssd_linear_q8(q: torch.Tensor, qscale: torch.Tensor, wq: torch.Tensor, wscal
     wscale [N] float32 (output channels), Kp a multiple of SSD_Q8_PAD, as
     ssd_quantize_q8 and the norms' _q8 forms return them."""
     return _calls.linear_q8(q, qscale, wq, wscale, _io_code(out_dtype) == SSD_BF16, out)
+
+
+# ---------------------------------------------------------------------------
+# The gated delta rule.
+# ---------------------------------------------------------------------------
+def ssd_delta_scan(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dt: torch.Tensor,
+                   A: torch.Tensor, beta: torch.Tensor, *, dt_bias: Optional[torch.Tensor] = None,
+                   dt_softplus: bool = True, dt_limit: Sequence[float] = (0.0, math.inf),
+                   beta_sigmoid: bool = True, qk_norm: bool = True, norm_eps: float = 1e-6,
+                   scale: Optional[float] = None, initial_state: Optional[torch.Tensor] = None,
+                   return_final_state: bool = True, y: Optional[torch.Tensor] = None,
+                   final_state: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None
+                   ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The gated delta rule over a sequence, on the current stream: with a =
+    exp(clip(softplus(dt + dt_bias)) A), b = logistic(beta), k and q of length 1
+    (q times scale, 1/sqrt(N) if None),
+
+      S_t = a_t S_{t-1} + b_t (v_t - a_t S_{t-1} k_t) k_t^T,   y_t = S_t q_t
+
+    q, k [Bt,T,G,N], v [Bt,T,H,P] float32 or bfloat16 (H a multiple of G; N up
+    to 128, P up to 256, multiples of 8; slices of a wider tensor's columns are
+    taken as they are); dt, beta [Bt,T,H], A, dt_bias [H], initial_state
+    [Bt,H,P,N] float32.  Returns (y [Bt,T,H,P] in v's dtype, final_state
+    [Bt,H,P,N] float32 or None).  final_state may be initial_state itself.
+
+    A logarithm of a goes in as dt with A = 1, dt_softplus=False and
+    dt_limit=(-inf, inf).  Tokens with dt = beta = -inf change nothing: pad
+    shorter sequences of a batch with them."""
+    return _calls.delta_scan(q, k, v, dt, A, beta, dt_bias, dt_softplus, dt_limit[0], dt_limit[1],
+                             beta_sigmoid, qk_norm, norm_eps, scale, initial_state,
+                             return_final_state, y, final_state, workspace)
+
+
+def ssd_delta_step(state: torch.Tensor, q_t: torch.Tensor, k_t: torch.Tensor, v_t: torch.Tensor,
+                   dt_t: torch.Tensor, A: torch.Tensor, beta_t: torch.Tensor, *,
+                   dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = True,
+                   dt_limit: Sequence[float] = (0.0, math.inf), beta_sigmoid: bool = True,
+                   qk_norm: bool = True, norm_eps: float = 1e-6, scale: Optional[float] = None,
+                   y_t: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of the gated delta rule on the current stream; `state`
+    [Bt,H,P,N] float32 is updated in place.  q_t, k_t [Bt,G,N], v_t [Bt,H,P]
+    (float32 or bfloat16), dt_t, beta_t [Bt,H] float32; the options as
+    ssd_delta_scan's.  Returns y_t [Bt,H,P] in v_t's dtype."""
+    return _calls.delta_step(q_t, k_t, v_t, dt_t, A, beta_t, dt_bias, dt_softplus, dt_limit[0],
+                             dt_limit[1], beta_sigmoid, qk_norm, norm_eps, scale, state, y_t)
 
 
 def abi_version() -> int:

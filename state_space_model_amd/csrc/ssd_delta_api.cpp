@@ -1,0 +1,184 @@
+// C ABI of the gated delta rule: argument validation and dispatch to the gfx950
+// kernels.  Declarations and the contract are in include/ssd.h.  As in
+// ssd_api.cpp everything here runs on the host, validation is complete before
+// the first launch, and nothing is allocated, synchronised or kept.
+#include "ssd.h"
+
+#include <math.h>
+#include <stdint.h>
+
+#include "ssd_check.h"
+#include "ssd_launch.h"
+
+namespace {
+
+using namespace ssd;
+
+inline bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+inline ssd_status status_of(hipError_t e) { return e == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
+
+// workgroups of 256 threads: a grid's threads count in 32 bits
+constexpr int64_t kMaxGroups = (1 << 24) - 1;
+
+// bytes that tensors and the spans of strided ones take
+struct Sizes {
+  int64_t q, k, v, y, gates, heads, state;
+  int64_t dq = 0, dk = 0, dv = 0;
+};
+
+// elements from the first to the last of `rows` rows of `width`, `stride` apart
+bool span_of(int64_t rows, int64_t width, int64_t stride, int64_t es, int64_t* bytes) {
+  int64_t n = 0;
+  if (rows == 0) { *bytes = 0; return true; }
+  if (!mul_ok(rows, stride, &n) || n > INT64_MAX / 16) return false;
+  *bytes = (n - stride + width) * es;
+  return true;
+}
+
+ssd_status check(const ssd_delta_desc* d, bool step, bool grads, Sizes* s) {
+  if (!d) return SSD_ERR_INVALID_ARG;
+  if (d->io_dtype != SSD_F32 && d->io_dtype != SSD_BF16) return SSD_ERR_DTYPE;
+  if (d->batch < 0 || (!step && d->seqlen < 0) || d->nheads <= 0 || d->headdim <= 0 ||
+      d->dstate <= 0 || d->ngroups <= 0 || d->nheads % d->ngroups != 0)
+    return SSD_ERR_SHAPE;
+  if (!limits_ok(d->dt_min, d->dt_max) || !(d->norm_eps >= 0.0f) || !isfinite(d->norm_eps) ||
+      !isfinite(d->scale))
+    return SSD_ERR_INVALID_ARG;
+  if (d->headdim % 8 != 0 || d->headdim > SSD_DELTA_MAX_P || d->dstate % 8 != 0 ||
+      d->dstate > SSD_DELTA_MAX_N || d->nheads > kMaxGroups)
+    return SSD_ERR_UNSUPPORTED;
+  const int64_t es = (int64_t)io_size(d->io_dtype);
+  const int64_t gn = d->ngroups * d->dstate, hp = d->nheads * d->headdim;
+  if (d->q_stride < gn || d->k_stride < gn || d->v_stride < hp) return SSD_ERR_SHAPE;
+  if (grads && (d->dq_stride < gn || d->dk_stride < gn || d->dv_stride < hp)) return SSD_ERR_SHAPE;
+  const int64_t chunks = step ? 1 : (d->seqlen / kDeltaChunk + (d->seqlen % kDeltaChunk != 0));
+  int64_t bh = 0, groups = 0, tokens = 0, state = 0, y = 0, gates = 0;
+  if (!mul_ok(d->batch, d->nheads, &bh) || !mul_ok(bh, chunks, &groups) || groups > kMaxGroups ||
+      !mul_ok(bh, (d->headdim + 15) / 16, &groups) || groups > kMaxGroups ||
+      !mul_ok(d->batch, step ? 1 : d->seqlen, &tokens) ||
+      !span_of(tokens, gn, d->q_stride, es, &s->q) || !span_of(tokens, gn, d->k_stride, es, &s->k) ||
+      !span_of(tokens, hp, d->v_stride, es, &s->v) || !mul_ok(tokens, hp, &y) || y > INT64_MAX / 16 ||
+      !mul_ok(tokens, d->nheads, &gates) || gates > INT64_MAX / 16)
+    return SSD_ERR_UNSUPPORTED;
+  if (grads && (!span_of(tokens, gn, d->dq_stride, es, &s->dq) ||
+                !span_of(tokens, gn, d->dk_stride, es, &s->dk) ||
+                !span_of(tokens, hp, d->dv_stride, es, &s->dv)))
+    return SSD_ERR_UNSUPPORTED;
+  state = bh * d->headdim * d->dstate;
+  s->y = y * es;
+  s->gates = gates * 4;
+  s->heads = d->nheads * 4;
+  s->state = state * 4;
+  return SSD_OK;
+}
+
+// rows that are read or written 16 bytes at a time
+bool rows_aligned(const void* p, int64_t stride, int32_t dtype) {
+  return aligned16(p) && stride * (int64_t)io_size(dtype) % 16 == 0;
+}
+
+// every output against every input and every other output
+template <size_t NO, size_t NI>
+bool outputs_clear(const Range (&outs)[NO], const Range (&ins)[NI]) {
+  for (size_t i = 0; i < NO; ++i) {
+    for (const Range& r : ins)
+      if (overlap(outs[i], r)) return false;
+    for (size_t j = i + 1; j < NO; ++j)
+      if (overlap(outs[i], outs[j])) return false;
+  }
+  return true;
+}
+
+DeltaArgs args_of(const ssd_delta_desc* d, const void* q, const void* k, const void* v,
+                  const float* dt, const float* dt_bias, const float* A, const float* beta) {
+  DeltaArgs a = {};
+  a.q = q; a.k = k; a.v = v;
+  a.q_stride = d->q_stride; a.k_stride = d->k_stride; a.v_stride = d->v_stride;
+  a.dt = dt; a.dt_bias = dt_bias; a.A = A; a.beta = beta;
+  a.Bt = d->batch; a.T = d->seqlen; a.H = d->nheads; a.G = d->ngroups;
+  a.Nc = (d->seqlen + kDeltaChunk - 1) / kDeltaChunk;
+  a.P = (int32_t)d->headdim; a.N = (int32_t)d->dstate;
+  a.softplus = d->dt_softplus ? 1 : 0; a.sigmoid = d->beta_sigmoid ? 1 : 0;
+  a.unit = d->qk_norm ? 1 : 0;
+  a.dt_min = d->dt_min; a.dt_max = d->dt_max; a.norm_eps = d->norm_eps; a.scale = d->scale;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssd_delta_scan_workspace_bytes(const ssd_delta_desc* d) {
+  Sizes s;
+  if (check(d, false, false, &s) != SSD_OK) return 0;
+  return delta_workspace(d->batch, d->seqlen, d->nheads, d->io_dtype == SSD_BF16).bytes;
+}
+
+ssd_status ssd_delta_scan(const ssd_delta_desc* d, const void* q, const void* k, const void* v,
+                          const float* dt, const float* dt_bias, const float* A, const float* beta,
+                          const float* initial_state, void* y, float* final_state, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream) {
+  Sizes s;
+  const ssd_status st = check(d, false, false, &s);
+  if (st != SSD_OK) return st;
+  const bool tokens = d->batch > 0 && d->seqlen > 0;
+  if (tokens && (!q || !k || !v || !dt || !A || !beta || !y)) return SSD_ERR_INVALID_ARG;
+  if (!rows_aligned(q, d->q_stride, d->io_dtype) || !rows_aligned(k, d->k_stride, d->io_dtype) ||
+      !rows_aligned(v, d->v_stride, d->io_dtype) || !aligned16(y) || !aligned16(initial_state) ||
+      !aligned16(final_state) || !aligned4(dt) || !aligned4(dt_bias) || !aligned4(A) ||
+      !aligned4(beta) || !aligned256(workspace))
+    return SSD_ERR_ALIGNMENT;
+  const size_t need = ssd_delta_scan_workspace_bytes(d);
+  if (tokens && (!workspace || workspace_bytes < need)) return SSD_ERR_WORKSPACE;
+  const bool in_place = final_state && final_state == initial_state;
+  const Range outs[] = {range_of(y, s.y), range_of(final_state, s.state),
+                        range_of(workspace, tokens ? (int64_t)need : 0)};
+  const Range ins[] = {range_of(q, s.q), range_of(k, s.k), range_of(v, s.v), range_of(dt, s.gates),
+                       range_of(beta, s.gates), range_of(A, s.heads), range_of(dt_bias, s.heads),
+                       in_place ? Range{0, 0} : range_of(initial_state, s.state)};
+  if (!outputs_clear(outs, ins)) return SSD_ERR_INVALID_ARG;
+  if (!tokens) {
+    if (!final_state || in_place) return SSD_OK;
+    // a launch's threads, one for 4 floats, count in 32 bits
+    constexpr int64_t kPart = int64_t{1} << 30;
+    for (int64_t at = 0, n = s.state / 4; at < n; at += kPart) {
+      const hipError_t e = launch_copy_or_zero(final_state + at, initial_state ? initial_state + at : nullptr,
+                                               n - at < kPart ? n - at : kPart, stream);
+      if (e != hipSuccess) return SSD_ERR_HIP;
+    }
+    return SSD_OK;
+  }
+  const bool io_bf16 = d->io_dtype == SSD_BF16;
+  DeltaArgs a = args_of(d, q, k, v, dt, dt_bias, A, beta);
+  a.h0 = initial_state; a.y = y; a.state = final_state;
+  const DeltaWorkspace w = delta_workspace(a.Bt, a.T, a.H, io_bf16);
+  char* ws = static_cast<char*>(workspace);
+  a.gate = reinterpret_cast<float4*>(ws + w.gate);
+  a.whole = reinterpret_cast<float*>(ws + w.whole);
+  a.inv = reinterpret_cast<__bf16*>(ws + w.inv);
+  a.qk = reinterpret_cast<__bf16*>(ws + w.qk);
+  return status_of(launch_delta_scan(a, io_bf16, stream));
+}
+
+ssd_status ssd_delta_step(const ssd_delta_desc* d, float* state, const void* q, const void* k,
+                          const void* v, const float* dt, const float* dt_bias, const float* A,
+                          const float* beta, void* y, hipStream_t stream) {
+  Sizes s;
+  const ssd_status st = check(d, true, false, &s);
+  if (st != SSD_OK) return st;
+  if (d->batch == 0) return SSD_OK;
+  if (!state || !q || !k || !v || !dt || !A || !beta || !y) return SSD_ERR_INVALID_ARG;
+  if (!rows_aligned(q, d->q_stride, d->io_dtype) || !rows_aligned(k, d->k_stride, d->io_dtype) ||
+      !rows_aligned(v, d->v_stride, d->io_dtype) || !aligned16(y) || !aligned16(state) ||
+      !aligned4(dt) || !aligned4(dt_bias) || !aligned4(A) || !aligned4(beta))
+    return SSD_ERR_ALIGNMENT;
+  const Range outs[] = {range_of(y, s.y), range_of(state, s.state)};
+  const Range ins[] = {range_of(q, s.q), range_of(k, s.k), range_of(v, s.v), range_of(dt, s.gates),
+                       range_of(beta, s.gates), range_of(A, s.heads), range_of(dt_bias, s.heads)};
+  if (!outputs_clear(outs, ins)) return SSD_ERR_INVALID_ARG;
+  DeltaArgs a = args_of(d, q, k, v, dt, dt_bias, A, beta);
+  a.y = y; a.state = state;
+  return status_of(launch_delta_step(a, d->io_dtype == SSD_BF16, stream));
+}
+
+}  // extern "C"

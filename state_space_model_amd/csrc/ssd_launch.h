@@ -192,6 +192,43 @@ struct ConvBwdArgs {
   int32_t silu;
 };
 
+// The gated delta rule (ssd_delta.hip, ssd_delta_backward.hip), after
+// validation.  Device pointers.  Rows of q, k, v and of their gradients are a
+// token's [heads, size], dense, and a stride apart; token b T + t is row b T + t.
+struct DeltaArgs {
+  const void* q;            // [Bt,T,G,N] io
+  const void* k;            // [Bt,T,G,N] io
+  const void* v;            // [Bt,T,H,P] io
+  int64_t q_stride, k_stride, v_stride;
+  const float* dt;          // [Bt,T,H]
+  const float* dt_bias;     // [H] or null
+  const float* A;           // [H]
+  const float* beta;        // [Bt,T,H]
+  const float* h0;          // [Bt,H,P,N] or null
+  void* y;                  // [Bt,T,H,P] io
+  float* state;             // the scan's final state [Bt,H,P,N] or null; the step's, in place
+  // workspace, per (b, h, chunk)
+  float4* gate;             // [C] factors of a token's rows (ssd_delta.hip)
+  float* whole;             // decay over the chunk
+  __bf16* inv;              // (1 + A)^-1, fragments of three planes
+  __bf16* qk;               // decayed q k^T, fragments of Planes<IO>::y planes
+  int64_t Bt, T, H, G, Nc;
+  int32_t P, N;
+  int32_t softplus, sigmoid, unit;  // dt through softplus, beta through the logistic, q, k to unit length
+  float dt_min, dt_max, norm_eps, scale;
+};
+
+constexpr int kDeltaChunk = 64;
+constexpr int kDeltaMaxN = 128;   // key sizes: multiples of 8 up to here
+constexpr int kDeltaMaxP = 256;   // value sizes: multiples of 8 up to here
+
+struct DeltaWorkspace {
+  size_t gate, whole, inv, qk, bytes;  // offsets, and the whole size
+};
+DeltaWorkspace delta_workspace(int64_t Bt, int64_t T, int64_t H, bool io_bf16);
+hipError_t launch_delta_scan(const DeltaArgs& a, bool io_bf16, hipStream_t stream);
+hipError_t launch_delta_step(const DeltaArgs& a, bool io_bf16, hipStream_t stream);
+
 // Compiled shape variants.
 bool scan_shape_supported(int64_t P, int64_t N, int64_t L, bool bf16);
 

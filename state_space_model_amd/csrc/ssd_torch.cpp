@@ -1,6 +1,7 @@
-// The operators between two scans as Python calls on torch tensors: checks of
-// the arguments, outputs and workspace from torch's allocator, the C ABI on the
-// current stream.  Host code only; _ssd_torch.so, next to libssd.so.
+// The operators between two scans, and the gated delta rule, as Python calls on
+// torch tensors: checks of the arguments, outputs and workspace from torch's
+// allocator, the C ABI on the current stream.  Host code only; _ssd_torch.so,
+// next to libssd.so.
 //
 // It exists for the calls that a token makes one at a time, which the host
 // bounds: a norm of one token needs the GPU for 2 us and 3.1 us of the host for
@@ -14,6 +15,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 #include <string>
 
@@ -528,6 +530,132 @@ PyObject* conv1d_backward(PyObject* const* a) {
   return dict({{"dx", &dx}, {"dweight", &dweight}, {"dbias", &dbias}, {"dstate", &dstate}});
 }
 
+// Elements between the tokens of t [..., heads, size], whose heads must be
+// dense and whose tokens evenly spaced (a slice of the convolution's output is).
+int64_t token_stride(const Tensor& t, const char* name, ScalarType want, const Tensor& first) {
+  device(t, name, first);
+  dtype(t, name, want);
+  const int64_t n = t.dim(), size = t.size(n - 1), heads = t.size(n - 2), D = heads * size;
+  if (t.numel() == 0) return D;
+  bool ok = (t.stride(n - 1) == 1 || size == 1) && (t.stride(n - 2) == size || heads == 1);
+  int64_t rows = 1, step = -1;
+  for (int64_t d = n - 3; d >= 0; --d) {
+    if (t.size(d) == 1) continue;
+    if (step < 0) step = t.stride(d);
+    ok = ok && t.stride(d) == step * rows;
+    rows *= t.size(d);
+  }
+  if (step < 0) step = D;
+  TORCH_CHECK_VALUE(ok && step >= D, name, " must have dense heads and evenly spaced tokens (shape ",
+                    text(t.sizes()), ", strides ", text(t.strides()), ")");
+  return step;
+}
+
+bool flag(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v;
+}
+
+// The inputs of the gated delta rule: q, k, v, dt, A, beta, dt_bias, then
+// dt_softplus, dt_min, dt_max, beta_sigmoid, qk_norm, norm_eps, scale (None:
+// 1/sqrt(N)).  q and k [.., G, N], v [.., H, P], with one leading dimension for
+// a token and two for a sequence.
+constexpr int kDeltaInputs = 14;
+struct Delta {
+  const Tensor &q, &k, &v, &dt, &A, &beta;
+  const Tensor* bias;
+  ssd_delta_desc d;
+  Shape yshape, state;
+  ScalarType io;
+  Delta(PyObject* const* a, bool step)
+      : q(tensor(a[0], "q")), k(tensor(a[1], "k")), v(tensor(a[2], "v")), dt(tensor(a[3], "dt")),
+        A(tensor(a[4], "A")), beta(tensor(a[5], "beta")), bias(maybe(a[6], "dt_bias")), d() {
+    const int64_t lead = step ? 1 : 2;
+    TORCH_CHECK_VALUE(v.dim() == lead + 2 && q.dim() == lead + 2,
+                      step ? "q_t, k_t [Bt,G,N], v_t [Bt,H,P]" : "q, k [Bt,T,G,N], v [Bt,T,H,P]");
+    d.batch = v.size(0);
+    d.seqlen = step ? 1 : v.size(1);
+    d.nheads = v.size(lead);
+    d.headdim = v.size(lead + 1);
+    d.ngroups = q.size(lead);
+    d.dstate = q.size(lead + 1);
+    Shape qk(v.sizes().begin(), v.sizes().begin() + lead), gate(qk);
+    qk.push_back(d.ngroups);
+    qk.push_back(d.dstate);
+    gate.push_back(d.nheads);
+    shape(&q, "q", qk);
+    shape(&k, "k", qk);
+    shape(&dt, "dt", gate);
+    shape(&beta, "beta", gate);
+    shape(&A, "A", d.nheads);
+    shape(bias, "dt_bias", d.nheads);
+    yshape = Shape(v.sizes().begin(), v.sizes().end());
+    state = Shape{d.batch, d.nheads, d.headdim, d.dstate};
+    io = v.scalar_type();
+    d.io_dtype = io_code(io, "v");
+    d.v_stride = token_stride(v, "v", io, v);
+    d.q_stride = token_stride(q, "q", io, v);
+    d.k_stride = token_stride(k, "k", io, v);
+    dense(&dt, "dt", at::kFloat, v);
+    dense(&A, "A", at::kFloat, v);
+    dense(&beta, "beta", at::kFloat, v);
+    dense(bias, "dt_bias", at::kFloat, v);
+    d.dt_softplus = flag(a[7]);
+    d.dt_min = (float)number(a[8]);
+    d.dt_max = (float)number(a[9]);
+    d.beta_sigmoid = flag(a[10]);
+    d.qk_norm = flag(a[11]);
+    d.norm_eps = (float)number(a[12]);
+    d.scale = a[13] == Py_None ? (float)(1.0 / std::sqrt((double)std::max<int64_t>(d.dstate, 1)))
+                               : (float)number(a[13]);
+  }
+};
+
+// the inputs, initial_state, return_final_state, y, final_state, workspace
+PyObject* delta_scan(PyObject* const* a) {
+  const Delta in(a, false);
+  const Tensor *h0 = maybe(a[kDeltaInputs], "initial_state"),
+               *y_ = maybe(a[kDeltaInputs + 2], "y"),
+               *f_ = maybe(a[kDeltaInputs + 3], "final_state"),
+               *w_ = maybe(a[kDeltaInputs + 4], "workspace");
+  shape(h0, "initial_state", in.state);
+  shape(y_, "y", in.yshape);
+  shape(f_, "final_state", in.state);
+  dense(h0, "initial_state", at::kFloat, in.v);
+  const bool keep = f_ || flag(a[kDeltaInputs + 1]);
+  const Tensor y = output(y_, "y", in.yshape, in.io, in.v);
+  const Tensor f = keep ? output(f_, "final_state", in.state, at::kFloat, in.v) : Tensor();
+  const Tensor ws = workspace(w_, ssd_delta_scan_workspace_bytes(&in.d), in.v);
+  launch(in.v, "ssd_delta_scan", [&](hipStream_t stream) {
+    return ssd_delta_scan(&in.d, ptr(in.q), ptr(in.k), ptr(in.v), f32(in.dt), f32(in.bias),
+                          f32(in.A), f32(in.beta), f32(h0), ptr(y), keep ? f32(f) : nullptr, ptr(ws),
+                          ws.nbytes(), stream);
+  });
+  PyObject* r = tuple({&y, keep ? &f : &y});
+  if (!keep) {
+    Py_INCREF(Py_None);
+    PyTuple_SetItem(r, 1, Py_None);
+  }
+  return r;
+}
+
+// the inputs, state, y_t
+PyObject* delta_step(PyObject* const* a) {
+  const Delta in(a, true);
+  const Tensor &state = tensor(a[kDeltaInputs], "state");
+  const Tensor* y_ = maybe(a[kDeltaInputs + 1], "y_t");
+  shape(&state, "state", in.state);
+  shape(y_, "y_t", in.yshape);
+  dense(&state, "state", at::kFloat, in.v);
+  const Tensor y = output(y_, "y_t", in.yshape, in.io, in.v);
+  launch(in.v, "ssd_delta_step", [&](hipStream_t stream) {
+    return ssd_delta_step(&in.d, f32(state), ptr(in.q), ptr(in.k), ptr(in.v), f32(in.dt),
+                          f32(in.bias), f32(in.A), f32(in.beta), ptr(y), stream);
+  });
+  return wrap(y);
+}
+
 // ---------------------------------------------------------------------------
 // the module
 // ---------------------------------------------------------------------------
@@ -577,10 +705,12 @@ PyMethodDef methods[] = {
     {"quantize_q8", FAST((entry<quantize_q8, 3>)), nullptr},
     {"linear_q8", FAST((entry<linear_q8, 6>)), nullptr},
     {"conv1d_backward", FAST((entry<conv1d_backward, 9>)), nullptr},
+    {"delta_scan", FAST((entry<delta_scan, kDeltaInputs + 5>)), nullptr},
+    {"delta_step", FAST((entry<delta_step, kDeltaInputs + 2>)), nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ssd_torch",
-                      "The operators between two scans on torch tensors.", -1, methods};
+                      "The operators between two scans, and the gated delta rule, on torch tensors.", -1, methods};
 
 }  // namespace
 
