@@ -23,9 +23,10 @@
  *                   residual add with the norm before a block, the gated norm
  *                   after its scan, the block's projections in 8-bit
  *                   integers, and the gradients of its convolution.
- *   ssd_delta_scan, ssd_delta_step
+ *   ssd_delta_scan, ssd_delta_step, ssd_delta_scan_backward
  *                   the gated delta rule, a mixer with the scan's decay and
- *                   fixed-size state: over a sequence and for one token.
+ *                   fixed-size state: over a sequence, for one token, and the
+ *                   gradients of the scan.
  *
  * The scan and the step compute, for every batch row b and head h (g = h / (H/G) is the B/C
  * group of head h), the selective diagonal SSM
@@ -650,6 +651,36 @@ ssd_status ssd_delta_step(const ssd_delta_desc* desc, float* state, const void* 
                           const void* k_t, const void* v_t, const float* dt_t,
                           const float* dt_bias, const float* A, const float* beta_t, void* y_t,
                           hipStream_t stream);
+
+/*
+ * Gradients of ssd_delta_scan (same descriptor and inputs) for the loss
+ * sum(dy * y) + sum(dfinal_state * final_state); states are formed again here.
+ *
+ *   dy [Bt,T,H,P] io_dtype      dfinal_state [Bt,H,P,N] f32 or NULL (zero)
+ *   dq, dk [Bt,T,G,N], dv [Bt,T,H,P] io_dtype (written): dense heads, tokens
+ *        a stride apart, pointers and strides in bytes multiples of 16; they may
+ *        be disjoint columns of one tensor with one stride.  dq and dk are
+ *        summed over the heads of a group and include the normalisation.
+ *   ddt, dbeta [Bt,T,H], dA [H] f32 (written); ddt is zero where Delta was clipped
+ *   ddt_bias [H] f32, dinitial_state [Bt,H,P,N] f32 (written) or NULL
+ *   workspace: at least ssd_delta_scan_backward_workspace_bytes(desc),
+ *        256-byte aligned; it holds the states and their gradients at every
+ *        chunk: about 8 Bt H T (P N / 64 + P + N + 80) bytes
+ *
+ * All sums are float32 or wider in an order that depends on the shape alone
+ * (no atomics).  Outputs may not overlap any input, the workspace or each
+ * other.  batch == 0 or seqlen == 0 writes zeros to dA and ddt_bias, and
+ * dfinal_state (or zeros) to dinitial_state.  Sizes as ssd_delta_scan, and
+ * 2 Bt T G below 2^27.
+ */
+size_t ssd_delta_scan_backward_workspace_bytes(const ssd_delta_desc* desc);
+ssd_status ssd_delta_scan_backward(const ssd_delta_desc* desc, const void* q, const void* k,
+                                   const void* v, const float* dt, const float* dt_bias,
+                                   const float* A, const float* beta, const float* initial_state,
+                                   const void* dy, const float* dfinal_state, void* dq, void* dk,
+                                   void* dv, float* ddt, float* dbeta, float* dA, float* ddt_bias,
+                                   float* dinitial_state, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
 
 /* Static description of a status code (never NULL). */
 const char* ssd_status_string(ssd_status status);

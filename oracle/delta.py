@@ -50,12 +50,15 @@ def scan(q, k, v, dt, A, beta, dt_bias=None, *, softplus=True, limit=(0.0, math.
 
 def gradients(inputs, dy, dfinal=None, **options):
     """Gradients of sum(dy y) + sum(dfinal final) with respect to every float64
-    input of the dict `inputs` (q, k, v, dt, A, beta, and dt_bias, h0 if there)."""
+    input of the dict `inputs` (q, k, v, dt, A, beta, and dt_bias, h0 if there),
+    and the states and their gradients."""
     leaves = {n: t.clone().requires_grad_(True) for n, t in inputs.items() if t is not None}
     y, states = scan(**leaves, **options)
     loss = (y * dy).sum()
     if dfinal is not None:
         loss = loss + (states[-1] * dfinal).sum()
-    got = torch.autograd.grad(loss, list(leaves.values()), allow_unused=True)
-    return {"d" + n: torch.zeros_like(x) if g is None else g
-            for (n, x), g in zip(leaves.items(), got)}
+    kept = [s for s in states if s.requires_grad]
+    got = torch.autograd.grad(loss, list(leaves.values()) + kept, allow_unused=True)
+    grads = {"d" + n: torch.zeros_like(x) if g is None else g
+             for (n, x), g in zip(leaves.items(), got)}
+    return grads, [s.detach() for s in states], [g for g in got[len(leaves):] if g is not None]

@@ -23,6 +23,7 @@ and the gated delta rule, a mixer with the scan's decay and fixed-size state,
 
   ssd_delta_scan(q, k, v, dt, A, beta, ...)          -> (y, final_state)
   ssd_delta_step(state, q_t, k_t, v_t, dt_t, A, beta_t, ...) -> y_t  (state updated in place)
+  ssd_delta_scan_backward(q, k, v, dt, A, beta, dy=...) -> dict of gradients
 
 Source: "Compiler-First State Space Duality and Portable O(1) Autoregressive
 Caching" (Background, Eq. 2-3; O(1) cache).
@@ -64,6 +65,7 @@ EXPORTED = ("ssd_chunk_scan", "ssd_chunk_scan_timed", "ssd_chunk_scan_workspace_
             "ssd_gated_norm_backward", "ssd_gated_norm_backward_workspace_bytes",
             "ssd_quantize_q8", "ssd_linear_q8",
             "ssd_delta_scan", "ssd_delta_scan_workspace_bytes", "ssd_delta_step",
+            "ssd_delta_scan_backward", "ssd_delta_scan_backward_workspace_bytes",
             "ssd_status_string", "ssd_abi_version")
 
 
@@ -180,6 +182,10 @@ def _load() -> ctypes.CDLL:
     L.ssd_delta_scan_workspace_bytes.argtypes = [ctypes.POINTER(DeltaDesc)]
     L.ssd_delta_scan.restype = i32
     L.ssd_delta_scan.argtypes = [ctypes.POINTER(DeltaDesc)] + [vp] * 11 + [sz, vp]
+    L.ssd_delta_scan_backward_workspace_bytes.restype = sz
+    L.ssd_delta_scan_backward_workspace_bytes.argtypes = [ctypes.POINTER(DeltaDesc)]
+    L.ssd_delta_scan_backward.restype = i32
+    L.ssd_delta_scan_backward.argtypes = [ctypes.POINTER(DeltaDesc)] + [vp] * 19 + [sz, vp]
     L.ssd_delta_step.restype = i32
     L.ssd_delta_step.argtypes = [ctypes.POINTER(DeltaDesc)] + [vp] * 9 + [vp]
     L.ssd_status_string.restype = ctypes.c_char_p
@@ -710,6 +716,27 @@ def ssd_delta_scan(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dt: torch.
     return _calls.delta_scan(q, k, v, dt, A, beta, dt_bias, dt_softplus, dt_limit[0], dt_limit[1],
                              beta_sigmoid, qk_norm, norm_eps, scale, initial_state,
                              return_final_state, y, final_state, workspace)
+
+
+def ssd_delta_scan_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dt: torch.Tensor,
+                            A: torch.Tensor, beta: torch.Tensor, *, dy: torch.Tensor,
+                            dfinal_state: Optional[torch.Tensor] = None,
+                            dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = True,
+                            dt_limit: Sequence[float] = (0.0, math.inf), beta_sigmoid: bool = True,
+                            qk_norm: bool = True, norm_eps: float = 1e-6,
+                            scale: Optional[float] = None,
+                            initial_state: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None,
+                            grads: Optional[dict] = None) -> dict:
+    """Gradients of ssd_delta_scan (the same inputs and options) for L =
+    sum(dy * y) + sum(dfinal_state * final_state), on the current stream.
+    Returns a dict: dq, dk [Bt,T,G,N], dv [Bt,T,H,P] in v's dtype, ddt, dbeta
+    [Bt,T,H], dA, ddt_bias [H], dinitial_state [Bt,H,P,N] float32 (all always
+    computed).  grads["dq"], ["dk"], ["dv"] may be column slices of one tensor,
+    like q, k and v."""
+    return _calls.delta_scan_backward(q, k, v, dt, A, beta, dt_bias, dt_softplus, dt_limit[0],
+                                      dt_limit[1], beta_sigmoid, qk_norm, norm_eps, scale, dy,
+                                      dfinal_state, initial_state, workspace, grads)
 
 
 def ssd_delta_step(state: torch.Tensor, q_t: torch.Tensor, k_t: torch.Tensor, v_t: torch.Tensor,

@@ -26,7 +26,7 @@ BINDING = os.path.join(PKG, "_ssd_torch.so")
 SOURCES = ["ssd_api.cpp", "ssd_step.hip", "ssd_state_pass.hip", "ssd_prefill_f32.hip",
            "ssd_prefill_bf16.hip", "ssd_conv.hip", "ssd_backward.hip", "ssd_block_api.cpp",
            "ssd_norm.hip", "ssd_linear_q8.hip", "ssd_conv_backward.hip", "ssd_delta_api.cpp",
-           "ssd_delta.hip"]
+           "ssd_delta.hip", "ssd_delta_backward.hip"]
 BINDING_SOURCE = "ssd_torch.cpp"
 ARCH = "gfx950"
 

@@ -2,16 +2,16 @@
 // the step; ssd_delta_backward.hip: the gradients): float32 matrix products on
 // the bfloat16 matrix cores, and the layout of the chunks' workspace.
 //
-// Products.  A float32 number is the exact sum of three bfloat16 numbers, its
-// significant bits cut 8 + 8 + 8 ("planes": h, m, l).  A product of two such
+// Products.  A float32 number is the exact sum of three bfloat16 numbers of 8
+// significant bits each ("planes": h, m, l).  A product of two such
 // operands is formed from the plane products whose indices add to at most 2
-// (hh, hm, mh, hl, mm, lh; the rest is below 2^-24 of it), each exact in the
+// (hh, hm, mh, hl, mm, lh; the rest is below 2^-26 of it), each exact in the
 // matrix core and accumulated in float32: six v_mfma_f32_16x16x32_bf16 (16
 // cycles each) where v_mfma_f32_16x16x4_f32 takes eight of 32 cycles.  An
 // operand that is bfloat16 already is one plane, and its product with a
 // float32 operand is exact up to the sum with three.  So states, writes and
 // their gradients keep float32 accuracy for both io types; only what ends in a
-// bfloat16 output is formed from two planes (2^-16 of it, against 2^-9 by the
+// bfloat16 output is formed from two planes (2^-17 of it, against 2^-8 by the
 // rounding of the output).
 #pragma once
 
@@ -53,47 +53,39 @@ __device__ __forceinline__ f32x4 mma(const Frag<NA>& a, const Frag<NB>& b, f32x4
   return acc;
 }
 
-// The planes of x, each in the upper half of a word (its lower half zero).
-// An infinity or a NaN leaves NaN behind.
-struct Split {
+// The planes of a pair, plane by plane in one word.  Each is rounded to nearest
+// (v_cvt_pk_bf16_f32), so what the dropped products leave out has no sign of its
+// own; the remainders are exact.  An infinity or a NaN leaves NaN behind.
+struct Split2 {
   uint32_t p[3];
-  __device__ __forceinline__ explicit Split(float x) {
-    p[0] = __float_as_uint(x) & 0xFFFF0000u;
-    const float r = x - __uint_as_float(p[0]);
-    p[1] = __float_as_uint(r) & 0xFFFF0000u;
-    p[2] = __float_as_uint(r - __uint_as_float(p[1]));
+  __device__ __forceinline__ Split2(float a, float b) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+      p[i] = __builtin_bit_cast(uint32_t, bf16x2{(bf16)a, (bf16)b});
+      a -= __uint_as_float(p[i] << 16);
+      b -= __uint_as_float(p[i] & 0xFFFF0000u);
+    }
   }
 };
-// bfloat16 pair from the upper halves of two words
-__device__ __forceinline__ uint32_t pair_hi(uint32_t lo, uint32_t hi) {
-  return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
-}
 
 // 8 float32 values as a fragment of NP planes
 template <int NP>
 __device__ __forceinline__ Frag<NP> split8(const float (&x)[8]) {
+  const Split2 a(x[0], x[1]), b(x[2], x[3]), c(x[4], x[5]), d(x[6], x[7]);
   Frag<NP> f;
-  uint32_t w[NP][4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const Split a(x[2 * e]), b(x[2 * e + 1]);
-#pragma unroll
-    for (int i = 0; i < NP; ++i) w[i][e] = pair_hi(a.p[i], b.p[i]);
-  }
 #pragma unroll
   for (int i = 0; i < NP; ++i)
-    f.p[i] = __builtin_bit_cast(bf16x8, make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]));
+    f.p[i] = __builtin_bit_cast(bf16x8, make_uint4(a.p[i], b.p[i], c.p[i], d.p[i]));
   return f;
 }
 
 // 4 consecutive values to NP planes `plane` elements apart (8-byte stores)
 template <int NP>
 __device__ __forceinline__ void store_split4(bf16* p, int plane, f32x4 v) {
-  const Split s0(v[0]), s1(v[1]), s2(v[2]), s3(v[3]);
+  const Split2 a(v[0], v[1]), b(v[2], v[3]);
 #pragma unroll
-  for (int i = 0; i < NP; ++i)
-    *reinterpret_cast<uint2*>(p + i * plane) =
-        make_uint2(pair_hi(s0.p[i], s1.p[i]), pair_hi(s2.p[i], s3.p[i]));
+  for (int i = 0; i < NP; ++i) *reinterpret_cast<uint2*>(p + i * plane) = make_uint2(a.p[i], b.p[i]);
 }
 
 __device__ __forceinline__ bf16x8 ld8(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
@@ -167,6 +159,58 @@ __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2
 // 1 / (1 + e^-z), also for -infinity (0)
 __device__ __forceinline__ float sigmoid_of(float z) {
   return 1.0f / (1.0f + exp2_of(-z * kLog2e));
+}
+
+// Wavefront w holds tokens 16 w .. + 15 of k and q as matrix operands: row
+// lane % 16, key columns 32 s + 8 (lane / 16) .. + 7 of step s.
+template <typename IO, int KP>
+__device__ __forceinline__ void load_rows(Frag<Planes<IO>::in> (&f)[KP / 32], const void* base,
+                                          int64_t stride, int64_t row0, int64_t left, int N, int r,
+                                          int q) {
+  const bool in = r < left;   // token r of the chunk that starts at row0
+  const IO* row = static_cast<const IO*>(base) + (row0 + (in ? r : 0)) * stride;
+#pragma unroll
+  for (int s = 0; s < KP / 32; ++s) {
+    const int col = 32 * s + 8 * q;
+    f[s] = load_io8<IO>(row + (col < N ? col : 0), in && col < N);
+  }
+}
+
+// Where the 32 columns from 32 s on of row tile w are among a triangular
+// operand's fragments, and these in the workspace
+__device__ __forceinline__ int lower_frag(int w, int s) { return w < 2 ? w : 2 * w - 2 + s; }
+__device__ __forceinline__ int upper_frag(int w, int s) { return w < 2 ? 2 * w + s : w + 2; }
+template <int NP>
+__device__ __forceinline__ void store_frag(bf16* base, int64_t at, int f, int lane, const Frag<NP>& v) {
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+    *reinterpret_cast<bf16x8*>(base + ((at * NP + i) * kTriFrags + f) * kFrag + lane * 8) = v.p[i];
+}
+template <int NP>
+__device__ __forceinline__ Frag<NP> load_frag(const bf16* base, int64_t at, int f, int lane) {
+  return load_planes<NP>(base + (at * NP * kTriFrags + f) * kFrag + lane * 8, kTriFrags * kFrag);
+}
+
+// State tiles of a chain's wavefront to [P, N]: keys 16 (KT w + t) + 4 q .. + 3
+// of value column col[n]
+template <int NT, int KT>
+__device__ __forceinline__ void store_state(float* to, const f32x4 (&st)[NT][KT], int N,
+                                            const int (&col)[NT], const bool (&col_in)[NT], int w,
+                                            int q) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const int key = 16 * (KT * w + t) + 4 * q;
+      if (col_in[n] && key < N)
+        *reinterpret_cast<f32x4*>(to + (int64_t)col[n] * N + key) = st[n][t];
+    }
+}
+
+// sum over a wavefront
+__device__ __forceinline__ float wave_sum64(float v) {
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
 }
 
 // Position of a (b, h, chunk)

@@ -13,29 +13,15 @@
 // its value columns in order, the state in matrix-core accumulators.
 #include "ssd_delta.h"
 
+#include <type_traits>
+
 namespace ssd {
 namespace delta {
 namespace {
 
 // ---------------------------------------------------------------------------
 // Chunk by chunk, before the states are known.
-//
-// Wavefront w holds tokens 16 w .. + 15 of k and q as matrix operands: row
-// lane % 16, key columns 32 s + 8 (lane / 16) .. + 7 of step s.
 // ---------------------------------------------------------------------------
-template <typename IO, int KP>
-__device__ __forceinline__ void load_rows(Frag<Planes<IO>::in> (&f)[KP / 32], const void* base,
-                                          int64_t stride, int64_t row0, int64_t left, int N, int r,
-                                          int q) {
-  const bool in = r < left;   // token r of the chunk that starts at row0
-  const IO* row = static_cast<const IO*>(base) + (row0 + (in ? r : 0)) * stride;
-#pragma unroll
-  for (int s = 0; s < KP / 32; ++s) {
-    const int col = 32 * s + 8 * q;
-    f[s] = load_io8<IO>(row + (col < N ? col : 0), in && col < N);
-  }
-}
-
 // sum of squares of the lane's row
 template <int PI, int KS>
 __device__ __forceinline__ float row_squares(const Frag<PI> (&f)[KS]) {
@@ -54,7 +40,9 @@ __device__ __forceinline__ float row_squares(const Frag<PI> (&f)[KS]) {
   return ss;
 }
 
-template <typename IO, int KP>
+// GRADS: for the gradients, whose chain from the last chunk needs both matrices
+// transposed and no output.
+template <typename IO, int KP, bool GRADS>
 __global__ __launch_bounds__(kThreads) void k_delta_prep(DeltaArgs a) {
   constexpr int PI = Planes<IO>::in, PY = Planes<IO>::y;
   constexpr int KS = KP / 32, KST = KP + 8;
@@ -186,21 +174,30 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(DeltaArgs a) {
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     if (s > (w >> 1)) continue;
-    const int f = w < 2 ? w : 2 * w - 2 + s;
+    const int f = lower_frag(w, s);
     float vx[8], vp[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       vx[e] = s_x[(16 * w + j) * kPairStride + 32 * s + 8 * q + e];
       vp[e] = s_a[(16 * w + j) * kPairStride + 32 * s + 8 * q + e];
     }
-    const auto fx = split8<3>(vx);
-    const auto fp = split8<PY>(vp);
+    store_frag(a.inv, at, f, lane, split8<3>(vx));
+    if constexpr (!GRADS) store_frag(a.qk, at, f, lane, split8<PY>(vp));
+  }
+  if constexpr (GRADS) {
+    // transposed: row tiles 0 and 1 reach over all columns, 2 and 3 over the last 32
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
-      *reinterpret_cast<bf16x8*>(a.inv + (at * 3 + i) * (kTriFrags * kFrag) + f * kFrag + lane * 8) = fx.p[i];
+    for (int s = 0; s < 2; ++s) {
+      if (s < (w >> 1)) continue;
+      float vx[8], vp[8];
 #pragma unroll
-    for (int i = 0; i < PY; ++i)
-      *reinterpret_cast<bf16x8*>(a.qk + (at * PY + i) * (kTriFrags * kFrag) + f * kFrag + lane * 8) = fp.p[i];
+      for (int e = 0; e < 8; ++e) {
+        vx[e] = s_x[(32 * s + 8 * q + e) * kPairStride + 16 * w + j];
+        vp[e] = s_a[(32 * s + 8 * q + e) * kPairStride + 16 * w + j];
+      }
+      store_frag(a.inv_t, at, upper_frag(w, s), lane, split8<3>(vx));
+      store_frag(a.qk, at, upper_frag(w, s), lane, split8<3>(vp));
+    }
   }
 
   // what multiplies a token's rows: v, K S^T, its write on the way to the end,
@@ -211,6 +208,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(DeltaArgs a) {
     a.gate[at * C + tid] = make_float4(beta, beta * gamma * s_rk[tid], end * s_rk[tid],
                                        gamma * s_rq[tid]);
     if (tid == C - 1) a.whole[at] = gamma;
+    if constexpr (GRADS) a.row[at * C + tid] = make_float4(s_rk[tid], s_rq[tid], s_hi[tid], s_lo[tid]);
   }
 }
 
@@ -223,7 +221,9 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(DeltaArgs a) {
 // goes to LDS value-major and token-contiguous, one 8-byte store per plane and
 // four tokens, since a result's lane holds four consecutive rows of a column.
 // ---------------------------------------------------------------------------
-template <typename IO, int KP, int NT>
+// KEEP: for the gradients, which need the state entering every chunk and its
+// writes, and no output.
+template <typename IO, int KP, int NT, bool KEEP>
 __global__ __launch_bounds__(kThreads) void k_delta_chain(DeltaArgs a) {
   constexpr int PI = Planes<IO>::in, PY = Planes<IO>::y;
   constexpr int KS = KP / 32, KST = KP + 8, KT = KP / 64, W = 16 * NT;
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_chain(DeltaArgs a) {
   const IO* kb = static_cast<const IO*>(a.k) + g * a.N;
   const IO* qb = static_cast<const IO*>(a.q) + g * a.N;
   const IO* vb = static_cast<const IO*>(a.v) + h * a.P;
-  IO* yb = static_cast<IO*>(a.y) + h * a.P;
+  IO* yb = KEEP ? nullptr : static_cast<IO*>(a.y) + h * a.P;
   bool col_in[NT];
   int col[NT];
 #pragma unroll
@@ -272,7 +272,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_chain(DeltaArgs a) {
   auto load_chunk = [&](int64_t c) {
     const int64_t t0 = c * C, row0 = b * a.T + t0, left = a.T - t0, at = chunk_at(a, bh, c);
     load_rows<IO, KP>(kf, kb, a.k_stride, row0, left, a.N, 16 * w + j, q);
-    load_rows<IO, KP>(qf, qb, a.q_stride, row0, left, a.N, 16 * w + j, q);
+    if constexpr (!KEEP) load_rows<IO, KP>(qf, qb, a.q_stride, row0, left, a.N, 16 * w + j, q);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int tok = 16 * w + 4 * q + r;
@@ -284,9 +284,8 @@ __global__ __launch_bounds__(kThreads) void k_delta_chain(DeltaArgs a) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       if (s > (w >> 1)) continue;
-      const int f = (w < 2 ? w : 2 * w - 2 + s) * kFrag + lane * 8;
-      xf[s] = load_planes<3>(a.inv + at * (3 * kTriFrags * kFrag) + f, kTriFrags * kFrag);
-      pf[s] = load_planes<PY>(a.qk + at * (PY * kTriFrags * kFrag) + f, kTriFrags * kFrag);
+      xf[s] = load_frag<3>(a.inv, at, lower_frag(w, s), lane);
+      if constexpr (!KEEP) pf[s] = load_frag<PY>(a.qk, at, lower_frag(w, s), lane);
     }
     whole = a.whole[at];
   };
@@ -304,6 +303,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_chain(DeltaArgs a) {
   for (int64_t c = 0; c < a.Nc; ++c) {
     const int64_t t0 = c * C, row0 = b * a.T + t0, left = a.T - t0;
     const bf16* sk = s_k[c & 1];
+    if constexpr (KEEP) store_state<NT, KT>(a.enter + chunk_at(a, bh, c) * a.P * a.N, st, a.N, col, col_in, w, q);
     // K S^T and Q S^T of the wavefront's tokens; the right sides b (v - gamma K S^T)
     f32x4 y[NT];
 #pragma unroll
@@ -313,10 +313,12 @@ __global__ __launch_bounds__(kThreads) void k_delta_chain(DeltaArgs a) {
       for (int s = 0; s < KS; ++s) {
         const auto sf = load_planes<3>(&s_s[(16 * n + j) * KST + 32 * s + 8 * q], W * KST);
         ks = mma(kf[s], sf, ks);
-        Frag<PY> sy;
+        if constexpr (!KEEP) {
+          Frag<PY> sy;
 #pragma unroll
-        for (int i = 0; i < PY; ++i) sy.p[i] = sf.p[i];
-        qs = mma(qf[s], sy, qs);
+          for (int i = 0; i < PY; ++i) sy.p[i] = sf.p[i];
+          qs = mma(qf[s], sy, qs);
+        }
       }
       f32x4 rs;
 #pragma unroll
@@ -342,12 +344,18 @@ __global__ __launch_bounds__(kThreads) void k_delta_chain(DeltaArgs a) {
       for (int r = 0; r < 4; ++r) es[r] = gate[r].z * ws[r];
       const int o = (16 * n + j) * kTokStride + 16 * w + 4 * q;
       store_split4<3>(&s_e[o], W * kTokStride, es);
-      store_split4<PY>(&s_w[o], W * kTokStride, ws);
+      if constexpr (!KEEP) {
+        store_split4<PY>(&s_w[o], W * kTokStride, ws);
+      } else {
+        if (col_in[n])
+          *reinterpret_cast<f32x4*>(a.write + (chunk_at(a, bh, c) * a.P + col[n]) * C + 16 * w + 4 * q) = ws;
+      }
     }
     __syncthreads();
     // outputs
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      if constexpr (KEEP) break;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (s > (w >> 1)) continue;
@@ -385,16 +393,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_chain(DeltaArgs a) {
     store_k(s_k[(c + 1) & 1]);
     __syncthreads();
   }
-  if (a.state) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int t = 0; t < KT; ++t) {
-        const int key = 16 * (KT * w + t) + 4 * q;
-        if (col_in[n] && key < a.N)
-          *reinterpret_cast<f32x4*>(a.state + (bh * a.P + col[n]) * a.N + key) = st[n][t];
-      }
-  }
+  if (!KEEP && a.state) store_state<NT, KT>(a.state + bh * a.P * a.N, st, a.N, col, col_in, w, q);
 }
 
 // ---------------------------------------------------------------------------
@@ -464,13 +463,21 @@ __global__ __launch_bounds__(kThreads) void k_delta_step(DeltaArgs a) {
   }
 }
 
-template <typename IO, int KP>
+// GRADS: the forward part of the gradients, which keeps states and writes
+template <typename IO, int KP, bool GRADS>
 hipError_t launch_scan(const DeltaArgs& a, hipStream_t stream) {
   const int64_t chunks = a.Bt * a.H * a.Nc;
-  hipLaunchKernelGGL((k_delta_prep<IO, KP>), dim3((unsigned)chunks), dim3(kThreads), 0, stream, a);
-  hipLaunchKernelGGL((k_delta_chain<IO, KP, 1>), dim3((unsigned)(a.Bt * a.H * ((a.P + 15) / 16))),
+  hipLaunchKernelGGL((k_delta_prep<IO, KP, GRADS>), dim3((unsigned)chunks), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((k_delta_chain<IO, KP, 1, GRADS>), dim3((unsigned)(a.Bt * a.H * ((a.P + 15) / 16))),
                      dim3(kThreads), 0, stream, a);
   return hipGetLastError();
+}
+
+template <bool GRADS>
+hipError_t launch_scan_of(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
+  if (a.N <= 64)
+    return io_bf16 ? launch_scan<bf16, 64, GRADS>(a, stream) : launch_scan<float, 64, GRADS>(a, stream);
+  return io_bf16 ? launch_scan<bf16, 128, GRADS>(a, stream) : launch_scan<float, 128, GRADS>(a, stream);
 }
 
 template <typename IO>
@@ -489,27 +496,40 @@ hipError_t launch_step(const DeltaArgs& a, hipStream_t stream) {
 }  // namespace
 }  // namespace delta
 
-DeltaWorkspace delta_workspace(int64_t Bt, int64_t T, int64_t H, bool io_bf16) {
-  const size_t n = (size_t)(Bt * H * ((T + kDeltaChunk - 1) / kDeltaChunk));
+size_t delta_workspace(DeltaArgs& a, bool io_bf16, bool grads, char* ws) {
+  const size_t n = (size_t)(a.Bt * a.H * a.Nc), C = kDeltaChunk;
   const size_t frags = delta::kTriFrags * delta::kFrag * sizeof(bf16);
-  DeltaWorkspace w;
-  auto take = [at = size_t{0}](size_t bytes) mutable {
-    const size_t here = at;
+  size_t at = 0;
+  auto take = [&](auto*& p, size_t bytes) {
+    if (ws) p = reinterpret_cast<std::remove_reference_t<decltype(p)>>(ws + at);
     at += (bytes + 255) / 256 * 256;
-    return here;
   };
-  w.gate = take(n * kDeltaChunk * sizeof(float4));
-  w.whole = take(n * sizeof(float));
-  w.inv = take(n * 3 * frags);
-  w.qk = take(n * (io_bf16 ? 2 : 3) * frags);
-  w.bytes = take(0);
-  return w;
+  take(a.gate, n * C * sizeof(float4));
+  take(a.whole, n * sizeof(float));
+  take(a.inv, n * 3 * frags);
+  take(a.qk, n * (io_bf16 && !grads ? 2 : 3) * frags);
+  if (grads) {
+    const size_t state = (size_t)a.P * a.N * sizeof(float), cols = (size_t)a.P * C * sizeof(float);
+    const size_t keys = (size_t)(a.Bt * a.T * a.H * a.N) * sizeof(float);
+    take(a.row, n * C * sizeof(float4));
+    take(a.inv_t, n * 3 * frags);
+    take(a.enter, n * state);
+    take(a.leave, n * state);
+    take(a.write, n * cols);
+    take(a.dright, n * cols);
+    take(a.part_q, keys);
+    take(a.part_k, keys);
+    take(a.part_h, n * 2 * sizeof(float));
+  }
+  return at;
 }
 
 hipError_t launch_delta_scan(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
-  if (a.N <= 64)
-    return io_bf16 ? delta::launch_scan<bf16, 64>(a, stream) : delta::launch_scan<float, 64>(a, stream);
-  return io_bf16 ? delta::launch_scan<bf16, 128>(a, stream) : delta::launch_scan<float, 128>(a, stream);
+  return delta::launch_scan_of<false>(a, io_bf16, stream);
+}
+
+hipError_t launch_delta_states(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
+  return delta::launch_scan_of<true>(a, io_bf16, stream);
 }
 
 hipError_t launch_delta_step(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {

@@ -64,6 +64,12 @@ ssd_status check(const ssd_delta_desc* d, bool step, bool grads, Sizes* s) {
                 !span_of(tokens, gn, d->dk_stride, es, &s->dk) ||
                 !span_of(tokens, hp, d->dv_stride, es, &s->dv)))
     return SSD_ERR_UNSUPPORTED;
+  // the gradients' workspace, in bytes (a bound), and a wavefront's half for each of 2 Bt T G rows
+  int64_t rows = 0, ws = 0;
+  if (grads && (!mul_ok(tokens, 2 * d->ngroups, &rows) || rows >= (int64_t{1} << 27) ||
+                !mul_ok(bh * chunks, 8 * (d->headdim * d->dstate + 64 * (d->headdim + d->dstate + 80)), &ws) ||
+                ws > INT64_MAX / 16))
+    return SSD_ERR_UNSUPPORTED;
   state = bh * d->headdim * d->dstate;
   s->y = y * es;
   s->gates = gates * 4;
@@ -89,6 +95,20 @@ bool outputs_clear(const Range (&outs)[NO], const Range (&ins)[NI]) {
   return true;
 }
 
+// Rows of two outputs that lie in one another's spans: disjoint columns of one
+// tensor are apart, everything else is not.
+struct Rows {
+  const void* p;
+  int64_t bytes, width, stride;  // of all rows, of a row's columns, between rows
+};
+bool rows_clear(const Rows& x, const Rows& y) {
+  const Range a = range_of(x.p, x.bytes), b = range_of(y.p, y.bytes);
+  if (!overlap(a, b)) return true;
+  if (a.lo > b.lo) return rows_clear(y, x);
+  const int64_t off = (int64_t)(b.lo - a.lo) % x.stride;
+  return x.stride == y.stride && off >= x.width && off + y.width <= x.stride;
+}
+
 DeltaArgs args_of(const ssd_delta_desc* d, const void* q, const void* k, const void* v,
                   const float* dt, const float* dt_bias, const float* A, const float* beta) {
   DeltaArgs a = {};
@@ -104,6 +124,17 @@ DeltaArgs args_of(const ssd_delta_desc* d, const void* q, const void* k, const v
   return a;
 }
 
+// dst = src, or zeros; a launch's threads, one for 4 floats, count in 32 bits
+ssd_status copy_state(float* dst, const float* src, int64_t n, hipStream_t stream) {
+  constexpr int64_t kPart = int64_t{1} << 30;
+  for (int64_t at = 0; at < n; at += kPart) {
+    const hipError_t e = launch_copy_or_zero(dst + at, src ? src + at : nullptr, n - at < kPart ? n - at : kPart,
+                                             stream);
+    if (e != hipSuccess) return SSD_ERR_HIP;
+  }
+  return SSD_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -111,7 +142,8 @@ extern "C" {
 size_t ssd_delta_scan_workspace_bytes(const ssd_delta_desc* d) {
   Sizes s;
   if (check(d, false, false, &s) != SSD_OK) return 0;
-  return delta_workspace(d->batch, d->seqlen, d->nheads, d->io_dtype == SSD_BF16).bytes;
+  DeltaArgs a = args_of(d, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
+  return delta_workspace(a, d->io_dtype == SSD_BF16, false, nullptr);
 }
 
 ssd_status ssd_delta_scan(const ssd_delta_desc* d, const void* q, const void* k, const void* v,
@@ -139,25 +171,79 @@ ssd_status ssd_delta_scan(const ssd_delta_desc* d, const void* q, const void* k,
   if (!outputs_clear(outs, ins)) return SSD_ERR_INVALID_ARG;
   if (!tokens) {
     if (!final_state || in_place) return SSD_OK;
-    // a launch's threads, one for 4 floats, count in 32 bits
-    constexpr int64_t kPart = int64_t{1} << 30;
-    for (int64_t at = 0, n = s.state / 4; at < n; at += kPart) {
-      const hipError_t e = launch_copy_or_zero(final_state + at, initial_state ? initial_state + at : nullptr,
-                                               n - at < kPart ? n - at : kPart, stream);
-      if (e != hipSuccess) return SSD_ERR_HIP;
-    }
-    return SSD_OK;
+    return copy_state(final_state, initial_state, s.state / 4, stream);
   }
   const bool io_bf16 = d->io_dtype == SSD_BF16;
   DeltaArgs a = args_of(d, q, k, v, dt, dt_bias, A, beta);
   a.h0 = initial_state; a.y = y; a.state = final_state;
-  const DeltaWorkspace w = delta_workspace(a.Bt, a.T, a.H, io_bf16);
-  char* ws = static_cast<char*>(workspace);
-  a.gate = reinterpret_cast<float4*>(ws + w.gate);
-  a.whole = reinterpret_cast<float*>(ws + w.whole);
-  a.inv = reinterpret_cast<__bf16*>(ws + w.inv);
-  a.qk = reinterpret_cast<__bf16*>(ws + w.qk);
+  delta_workspace(a, io_bf16, false, static_cast<char*>(workspace));
   return status_of(launch_delta_scan(a, io_bf16, stream));
+}
+
+size_t ssd_delta_scan_backward_workspace_bytes(const ssd_delta_desc* d) {
+  Sizes s;
+  if (check(d, false, true, &s) != SSD_OK) return 0;
+  DeltaArgs a = args_of(d, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
+  return delta_workspace(a, d->io_dtype == SSD_BF16, true, nullptr);
+}
+
+ssd_status ssd_delta_scan_backward(const ssd_delta_desc* d, const void* q, const void* k,
+                                   const void* v, const float* dt, const float* dt_bias,
+                                   const float* A, const float* beta, const float* initial_state,
+                                   const void* dy, const float* dfinal_state, void* dq, void* dk,
+                                   void* dv, float* ddt, float* dbeta, float* dA, float* ddt_bias,
+                                   float* dinitial_state, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream) {
+  Sizes s;
+  const ssd_status st = check(d, false, true, &s);
+  if (st != SSD_OK) return st;
+  const bool tokens = d->batch > 0 && d->seqlen > 0;
+  if (!dA || (tokens && (!q || !k || !v || !dt || !A || !beta || !dy || !dq || !dk || !dv || !ddt || !dbeta)))
+    return SSD_ERR_INVALID_ARG;
+  const int32_t io = d->io_dtype;
+  if (!rows_aligned(q, d->q_stride, io) || !rows_aligned(k, d->k_stride, io) ||
+      !rows_aligned(v, d->v_stride, io) || !rows_aligned(dq, d->dq_stride, io) ||
+      !rows_aligned(dk, d->dk_stride, io) || !rows_aligned(dv, d->dv_stride, io) || !aligned16(dy) ||
+      !aligned16(initial_state) || !aligned16(dfinal_state) || !aligned16(dinitial_state) ||
+      !aligned256(workspace))
+    return SSD_ERR_ALIGNMENT;
+  for (const float* p : {dt, dt_bias, A, beta, (const float*)ddt, (const float*)dbeta, (const float*)dA,
+                         (const float*)ddt_bias})
+    if (!aligned4(p)) return SSD_ERR_ALIGNMENT;
+  const size_t need = ssd_delta_scan_backward_workspace_bytes(d);
+  if (tokens && (!workspace || workspace_bytes < need)) return SSD_ERR_WORKSPACE;
+  const Range outs[] = {range_of(ddt, s.gates), range_of(dbeta, s.gates), range_of(dA, s.heads),
+                        range_of(ddt_bias, s.heads), range_of(dinitial_state, s.state),
+                        range_of(workspace, tokens ? (int64_t)need : 0)};
+  const Range ins[] = {range_of(q, s.q), range_of(k, s.k), range_of(v, s.v), range_of(dy, s.y),
+                       range_of(dt, s.gates), range_of(beta, s.gates), range_of(A, s.heads),
+                       range_of(dt_bias, s.heads), range_of(initial_state, s.state),
+                       range_of(dfinal_state, s.state)};
+  if (!outputs_clear(outs, ins)) return SSD_ERR_INVALID_ARG;
+  const int64_t es = (int64_t)io_size(io), gn = d->ngroups * d->dstate * es, hp = d->nheads * d->headdim * es;
+  const Rows rows[] = {{dq, s.dq, gn, d->dq_stride * es}, {dk, s.dk, gn, d->dk_stride * es},
+                       {dv, s.dv, hp, d->dv_stride * es}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& r : ins)
+      if (overlap(range_of(rows[i].p, rows[i].bytes), r)) return SSD_ERR_INVALID_ARG;
+    for (const Range& r : outs)
+      if (overlap(range_of(rows[i].p, rows[i].bytes), r)) return SSD_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 3; ++j)
+      if (!rows_clear(rows[i], rows[j])) return SSD_ERR_INVALID_ARG;
+  }
+  if (!tokens) {
+    const hipError_t e = launch_backward_zero_heads(dA, ddt_bias, nullptr, d->nheads, stream);
+    if (e != hipSuccess) return SSD_ERR_HIP;
+    return dinitial_state ? copy_state(dinitial_state, dfinal_state, s.state / 4, stream) : SSD_OK;
+  }
+  const bool io_bf16 = io == SSD_BF16;
+  DeltaArgs a = args_of(d, q, k, v, dt, dt_bias, A, beta);
+  a.h0 = initial_state; a.dy = dy; a.dfinal = dfinal_state;
+  a.dq = dq; a.dk = dk; a.dv = dv;
+  a.dq_stride = d->dq_stride; a.dk_stride = d->dk_stride; a.dv_stride = d->dv_stride;
+  a.ddt = ddt; a.dbeta = dbeta; a.dA = dA; a.ddt_bias = ddt_bias; a.dh0 = dinitial_state;
+  delta_workspace(a, io_bf16, true, static_cast<char*>(workspace));
+  return status_of(launch_delta_scan_backward(a, io_bf16, stream));
 }
 
 ssd_status ssd_delta_step(const ssd_delta_desc* d, float* state, const void* q, const void* k,

@@ -210,8 +210,22 @@ struct DeltaArgs {
   // workspace, per (b, h, chunk)
   float4* gate;             // [C] factors of a token's rows (ssd_delta.hip)
   float* whole;             // decay over the chunk
-  __bf16* inv;              // (1 + A)^-1, fragments of three planes
-  __bf16* qk;               // decayed q k^T, fragments of Planes<IO>::y planes
+  __bf16* inv;              // (1 + L)^-1, fragments of three planes
+  __bf16* qk;               // decayed q k^T, fragments (the gradients: of its transpose, three planes)
+  // the gradients
+  const void* dy;           // [Bt,T,H,P] io
+  const float* dfinal;      // [Bt,H,P,N] or null
+  float4* row;              // [C] 1/|k|, scale/|q| and the decay sum of a token, in two parts
+  __bf16* inv_t;            // transposed inverse, fragments of three planes
+  float* enter;             // [P,N] state entering the chunk
+  float* leave;             // [P,N] gradient of the state leaving it
+  float* write;             // [P,C] the chunk's writes, transposed
+  float* dright;            // [P,C] gradient of the right sides, transposed
+  float *part_q, *part_k;   // [Bt,T,H,N] gradients of unit q and k per head
+  float* part_h;            // [2] the chunk's parts of dA and ddt_bias
+  void *dq, *dk, *dv;       // io
+  int64_t dq_stride, dk_stride, dv_stride;
+  float *ddt, *dbeta, *dA, *ddt_bias, *dh0;
   int64_t Bt, T, H, G, Nc;
   int32_t P, N;
   int32_t softplus, sigmoid, unit;  // dt through softplus, beta through the logistic, q, k to unit length
@@ -222,10 +236,11 @@ constexpr int kDeltaChunk = 64;
 constexpr int kDeltaMaxN = 128;   // key sizes: multiples of 8 up to here
 constexpr int kDeltaMaxP = 256;   // value sizes: multiples of 8 up to here
 
-struct DeltaWorkspace {
-  size_t gate, whole, inv, qk, bytes;  // offsets, and the whole size
-};
-DeltaWorkspace delta_workspace(int64_t Bt, int64_t T, int64_t H, bool io_bf16);
+// Bytes of the scan's workspace and of its gradients'; with `ws` they are laid
+// out there.
+size_t delta_workspace(DeltaArgs& a, bool io_bf16, bool grads, char* ws);
+hipError_t launch_delta_states(const DeltaArgs& a, bool io_bf16, hipStream_t stream);  // the gradients' forward part
+hipError_t launch_delta_scan_backward(const DeltaArgs& a, bool io_bf16, hipStream_t stream);
 hipError_t launch_delta_scan(const DeltaArgs& a, bool io_bf16, hipStream_t stream);
 hipError_t launch_delta_step(const DeltaArgs& a, bool io_bf16, hipStream_t stream);
 

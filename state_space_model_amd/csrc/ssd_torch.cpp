@@ -640,6 +640,50 @@ PyObject* delta_scan(PyObject* const* a) {
   return r;
 }
 
+// the inputs, dy, dfinal_state, initial_state, workspace, grads
+PyObject* delta_scan_backward(PyObject* const* a) {
+  Delta in(a, false);
+  a += kDeltaInputs;
+  const Tensor& dy = tensor(a[0], "dy");
+  const Tensor *df = maybe(a[1], "dfinal_state"), *h0 = maybe(a[2], "initial_state"),
+               *w_ = maybe(a[3], "workspace");
+  const int64_t H = in.d.nheads;
+  const IntArrayRef qk = in.q.sizes(), gate = in.dt.sizes();
+  shape(&dy, "dy", in.yshape);
+  shape(df, "dfinal_state", in.state);
+  shape(h0, "initial_state", in.state);
+  const Grads g(a[4], {"dq", "dk", "dv", "ddt", "dbeta", "dA", "ddt_bias", "dinitial_state"});
+  const Tensor *dq_ = g.get("dq", qk), *dk_ = g.get("dk", qk), *dv_ = g.get("dv", in.yshape),
+               *dt_ = g.get("ddt", gate), *db_ = g.get("dbeta", gate), *dA_ = g.get("dA", H),
+               *dbias_ = g.get("ddt_bias", H), *dh_ = g.get("dinitial_state", in.state);
+  dense(&dy, "dy", in.io, in.v);
+  dense(df, "dfinal_state", at::kFloat, in.v);
+  dense(h0, "initial_state", at::kFloat, in.v);
+  // strided buffers, or new dense ones
+  auto rows = [&](const Tensor* t, const char* name, IntArrayRef sizes, int64_t* stride) {
+    const Tensor r = t ? *t : output(nullptr, name, sizes, in.io, in.v);
+    *stride = token_stride(r, name, in.io, in.v);
+    return r;
+  };
+  const Tensor dq = rows(dq_, "dq", qk, &in.d.dq_stride);
+  const Tensor dk = rows(dk_, "dk", qk, &in.d.dk_stride);
+  const Tensor dv = rows(dv_, "dv", in.yshape, &in.d.dv_stride);
+  const Tensor ddt = output(dt_, "ddt", gate, at::kFloat, in.v);
+  const Tensor dbeta = output(db_, "dbeta", gate, at::kFloat, in.v);
+  const Tensor dA = output(dA_, "dA", H, at::kFloat, in.v);
+  const Tensor dbias = output(dbias_, "ddt_bias", H, at::kFloat, in.v);
+  const Tensor dh = output(dh_, "dinitial_state", in.state, at::kFloat, in.v);
+  const Tensor ws = workspace(w_, ssd_delta_scan_backward_workspace_bytes(&in.d), in.v);
+  launch(in.v, "ssd_delta_scan_backward", [&](hipStream_t stream) {
+    return ssd_delta_scan_backward(&in.d, ptr(in.q), ptr(in.k), ptr(in.v), f32(in.dt), f32(in.bias),
+                                   f32(in.A), f32(in.beta), f32(h0), ptr(dy), f32(df), ptr(dq), ptr(dk),
+                                   ptr(dv), f32(ddt), f32(dbeta), f32(dA), f32(dbias), f32(dh), ptr(ws),
+                                   ws.nbytes(), stream);
+  });
+  return dict({{"dq", &dq}, {"dk", &dk}, {"dv", &dv}, {"ddt", &ddt}, {"dbeta", &dbeta}, {"dA", &dA},
+               {"ddt_bias", &dbias}, {"dinitial_state", &dh}});
+}
+
 // the inputs, state, y_t
 PyObject* delta_step(PyObject* const* a) {
   const Delta in(a, true);
@@ -706,6 +750,7 @@ PyMethodDef methods[] = {
     {"linear_q8", FAST((entry<linear_q8, 6>)), nullptr},
     {"conv1d_backward", FAST((entry<conv1d_backward, 9>)), nullptr},
     {"delta_scan", FAST((entry<delta_scan, kDeltaInputs + 5>)), nullptr},
+    {"delta_scan_backward", FAST((entry<delta_scan_backward, kDeltaInputs + 5>)), nullptr},
     {"delta_step", FAST((entry<delta_step, kDeltaInputs + 2>)), nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -54,6 +54,37 @@ def y_bar(y, states, T, N, io, scale):
     return bar + IO_U[io] * 1.01 * y.abs().numpy()
 
 
+def length(ts, dims):
+    """The greatest length of the vectors that `dims` dimensions make up."""
+    return max((float(t.double().flatten(-dims).square().sum(-1).max().sqrt()) for t in ts), default=0.0)
+
+
+def grad_bars(x, dy, ref, states, dstates, scale, norm=True):
+    """Bars of the gradients.  Each is a sum of products of states S, their gradients dS, values and
+    dy, and is formed from sums of n = T + N + P + 64 terms at most, whose roundings add as in
+    state_bar; the magnitudes are bounded by lengths (a write by |v| + |S|).  The gradient of a
+    decay sums 64 tokens' terms, those of A and dt_bias those of all tokens."""
+    io = x["v"].dtype
+    Bt, T, H, P = x["v"].shape
+    G, N = x["q"].shape[2:]
+    e = 8 * math.sqrt(T + N + P + 64) * U
+    S, dS, V, dY = length(states, 2), length(dstates, 2), length([x["v"]], 1), length([dy], 1)
+    least = lambda t: float(t.double().square().sum(-1).min().sqrt()) if norm else 1.0  # noqa: E731
+    most = lambda t: 1.0 if norm else length([t], 1)                                     # noqa: E731
+    kl, ql = most(x["k"]), most(x["q"]) * scale
+    write = V + S * kl
+    per, rate = H // G, float(ref["rates"].abs().max())
+    token = dS * write * kl + dY * S * ql + dS * S
+    dg = e * 8 * 3 * token
+    slope = float(x["A"].abs().max())
+    rounded = lambda n: IO_U[io] * 1.01 * ref[n].abs().numpy() if io != torch.float32 else 0.0  # noqa: E731
+    return {"dq": e * per * dY * S * scale / least(x["q"]) + rounded("dq"),
+            "dk": e * per * 3 * dS * (write + S) / least(x["k"]) + rounded("dk"),
+            "dv": e * dS * kl + rounded("dv"), "dbeta": e * 3 * dS * kl * (write + S),
+            "ddt": dg * slope, "dA": dg * rate * math.sqrt(Bt * T), "ddt_bias": dg * slope * math.sqrt(Bt * T),
+            "dinitial_state": e * dS}
+
+
 def oracle_of(x, **options):
     return delta.scan(**{n: delta.f64(t) for n, t in x.items()}, **options)
 
