@@ -665,7 +665,7 @@ ssd_status ssd_delta_step(const ssd_delta_desc* desc, float* state, const void* 
  *   ddt_bias [H] f32, dinitial_state [Bt,H,P,N] f32 (written) or NULL
  *   workspace: at least ssd_delta_scan_backward_workspace_bytes(desc),
  *        256-byte aligned; it holds the states and their gradients at every
- *        chunk: about 8 Bt H T (P N / 64 + P + N + 80) bytes
+ *        chunk: about 8 Bt H T (P N / 64 + P + N + 80) bytes (N rounded up to 64)
  *
  * All sums are float32 or wider in an order that depends on the shape alone
  * (no atomics).  Outputs may not overlap any input, the workspace or each

@@ -15,6 +15,8 @@
 // rounding of the output).
 #pragma once
 
+#include <type_traits>
+
 #include "ssd_device.h"
 #include "ssd_launch.h"
 
@@ -53,6 +55,21 @@ __device__ __forceinline__ f32x4 mma(const Frag<NA>& a, const Frag<NB>& b, f32x4
   return acc;
 }
 
+// acc[i] += A[i] B for independent tiles, plane product by plane product over
+// all of them: a tile's next product depends on its last one, whose result takes
+// longer than its issue
+template <int NT, int NA, int NB>
+__device__ __forceinline__ void mma_tiles(const Frag<NA> (&a)[NT], const Frag<NB>& b, f32x4* acc) {
+  constexpr int top = (NA > NB ? NA : NB) - 1;
+#pragma unroll
+  for (int s = top; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[t] = mma(a[t].p[i], b.p[s - i], acc[t]);
+}
+
 // The planes of a pair, plane by plane in one word.  Each is rounded to nearest
 // (v_cvt_pk_bf16_f32), so what the dropped products leave out has no sign of its
 // own; the remainders are exact.  An infinity or a NaN leaves NaN behind.
@@ -63,6 +80,7 @@ struct Split2 {
     for (int i = 0; i < 3; ++i) {
       typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
       p[i] = __builtin_bit_cast(uint32_t, bf16x2{(bf16)a, (bf16)b});
+      asm("" : "+v"(p[i]));   // one conversion: not a's again for the remainder
       a -= __uint_as_float(p[i] << 16);
       b -= __uint_as_float(p[i] & 0xFFFF0000u);
     }
@@ -98,23 +116,46 @@ __device__ __forceinline__ Frag<NP> load_planes(const bf16* p, int plane) {
   return f;
 }
 
-// 8 consecutive io elements of a row as a fragment (16-byte loads), zeros when
-// !ok; `p` is a valid address either way.
-template <typename IO>
-__device__ __forceinline__ Frag<Planes<IO>::in> load_io8(const IO* p, bool ok) {
-  if constexpr (sizeof(IO) == 2) {
-    uint4 v = *reinterpret_cast<const uint4*>(p);
-    v.x = ok ? v.x : 0u; v.y = ok ? v.y : 0u; v.z = ok ? v.z : 0u; v.w = ok ? v.w : 0u;
+// 8 consecutive io elements of a row as loaded (16-byte loads), and as a
+// fragment.
+template <typename IO> struct Raw8;
+template <> struct Raw8<bf16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const bf16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void keep(bool in) {
+    v.x = in ? v.x : 0u; v.y = in ? v.y : 0u; v.z = in ? v.z : 0u; v.w = in ? v.w : 0u;
+  }
+  __device__ __forceinline__ Frag<1> frag() const {
     Frag<1> f;
     f.p[0] = __builtin_bit_cast(bf16x8, v);
     return f;
-  } else {
-    const float4 lo = *reinterpret_cast<const float4*>(p);
-    const float4 hi = *reinterpret_cast<const float4*>(p + 4);
-    const float x[8] = {ok ? lo.x : 0.f, ok ? lo.y : 0.f, ok ? lo.z : 0.f, ok ? lo.w : 0.f,
-                        ok ? hi.x : 0.f, ok ? hi.y : 0.f, ok ? hi.z : 0.f, ok ? hi.w : 0.f};
+  }
+};
+template <> struct Raw8<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const f32x4*>(p);
+    b = *reinterpret_cast<const f32x4*>(p + 4);
+  }
+  __device__ __forceinline__ void keep(bool in) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      a[e] = in ? a[e] : 0.0f;
+      b[e] = in ? b[e] : 0.0f;
+    }
+  }
+  __device__ __forceinline__ Frag<3> frag() const {
+    const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     return split8<3>(x);
   }
+};
+// zeros when !in; `p` is a valid address either way
+template <typename IO>
+__device__ __forceinline__ Frag<Planes<IO>::in> load_io8(const IO* p, bool in) {
+  Raw8<IO> r;
+  r.load(p);
+  r.keep(in);
+  return r.frag();
 }
 
 // ds_read_b64_tr_b16: within each group of 16 lanes, lane j addresses 4
@@ -127,19 +168,24 @@ __device__ __forceinline__ bf16x4 lds_read_tr4(const bf16* p) {
   return __builtin_bit_cast(bf16x4, v);
 }
 // The operand that contracts over the rows of a row-major LDS tile: lane j of
-// group q gets m[r0 + 8 q .. + 7][c0 + j].
+// group q gets rows r0 + 8 q .. + 7 of column c0 + j, from its own address (row 8 q
+// + j / 4 past r0, column 4 (j % 4) past c0; `second` away for the other four
+// rows) or from the tile's.
+template <int NP>
+__device__ __forceinline__ Frag<NP> read_tr(const bf16* p, int plane, int second) {
+  Frag<NP> f;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const bf16x4 lo = lds_read_tr4(p + i * plane), hi = lds_read_tr4(p + i * plane + second);
+    f.p[i] = bf16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  }
+  return f;
+}
 template <int NP>
 __device__ __forceinline__ Frag<NP> load_planes_tr(const bf16* m, int plane, int stride, int r0,
                                                    int c0, int lane) {
   const int j = lane & 15, q = lane >> 4;
-  const bf16* p = m + (r0 + 8 * q + (j >> 2)) * stride + c0 + 4 * (j & 3);
-  Frag<NP> f;
-#pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const bf16x4 lo = lds_read_tr4(p + i * plane), hi = lds_read_tr4(p + i * plane + 4 * stride);
-    f.p[i] = bf16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-  }
-  return f;
+  return read_tr<NP>(m + (r0 + 8 * q + (j >> 2)) * stride + c0 + 4 * (j & 3), plane, 4 * stride);
 }
 
 // A 16 x 16 float32 product on the float32 matrix core, its right operand and
@@ -161,57 +207,229 @@ __device__ __forceinline__ float sigmoid_of(float z) {
   return 1.0f / (1.0f + exp2_of(-z * kLog2e));
 }
 
-// Wavefront w holds tokens 16 w .. + 15 of k and q as matrix operands: row
-// lane % 16, key columns 32 s + 8 (lane / 16) .. + 7 of step s.
-template <typename IO, int KP>
-__device__ __forceinline__ void load_rows(Frag<Planes<IO>::in> (&f)[KP / 32], const void* base,
-                                          int64_t stride, int64_t row0, int64_t left, int N, int r,
-                                          int q) {
-  const bool in = r < left;   // token r of the chunk that starts at row0
-  const IO* row = static_cast<const IO*>(base) + (row0 + (in ? r : 0)) * stride;
+// One row of k or q as a matrix operand: key columns 32 s + 8 (lane / 16) .. + 7
+// of step s, zeros from N on (FULL: N is KP).  `p` points at the lane's columns
+// of step 0.  Wavefront w holds rows 16 w + lane % 16 of a chunk; tokens past a
+// sequence's end are its last one again, which factors of zero keep out of
+// everything.
+template <typename IO, int KP, bool FULL> struct KeyRow {
+  Raw8<IO> f[KP / 32];
+  __device__ __forceinline__ void load(const IO* p, int N, int q) {
 #pragma unroll
-  for (int s = 0; s < KP / 32; ++s) {
-    const int col = 32 * s + 8 * q;
-    f[s] = load_io8<IO>(row + (col < N ? col : 0), in && col < N);
+    for (int s = 0; s < KP / 32; ++s) f[s].load(p + (FULL || 32 * s + 8 * q < N ? 32 * s : -8 * q));
   }
+  __device__ __forceinline__ Frag<Planes<IO>::in> frag(int s, int N, int q) const {
+    Raw8<IO> r = f[s];
+    if constexpr (!FULL) r.keep(32 * s + 8 * q < N);
+    return r.frag();
+  }
+};
+
+// f(io, KP, FULL) with the compiled variant of these keys as constants
+template <typename F>
+hipError_t with_keys(int N, bool io_bf16, F&& f) {
+  using std::integral_constant;
+  auto keys = [&](auto io) {
+    if (N == 128) return f(io, integral_constant<int, 128>{}, integral_constant<bool, true>{});
+    if (N > 64) return f(io, integral_constant<int, 128>{}, integral_constant<bool, false>{});
+    if (N == 64) return f(io, integral_constant<int, 64>{}, integral_constant<bool, true>{});
+    return f(io, integral_constant<int, 64>{}, integral_constant<bool, false>{});
+  };
+  return io_bf16 ? keys(bf16{}) : keys(float{});
 }
+
+// A gate component's 64 tokens
+enum Gate { kBeta = 0, kRight = C, kEnd = 2 * C, kOut = 3 * C, kGates = 4 * C };
 
 // Where the 32 columns from 32 s on of row tile w are among a triangular
 // operand's fragments, and these in the workspace
+// (a fragment's planes next to each other)
 __device__ __forceinline__ int lower_frag(int w, int s) { return w < 2 ? w : 2 * w - 2 + s; }
 __device__ __forceinline__ int upper_frag(int w, int s) { return w < 2 ? 2 * w + s : w + 2; }
 template <int NP>
 __device__ __forceinline__ void store_frag(bf16* base, int64_t at, int f, int lane, const Frag<NP>& v) {
 #pragma unroll
   for (int i = 0; i < NP; ++i)
-    *reinterpret_cast<bf16x8*>(base + ((at * NP + i) * kTriFrags + f) * kFrag + lane * 8) = v.p[i];
-}
-template <int NP>
-__device__ __forceinline__ Frag<NP> load_frag(const bf16* base, int64_t at, int f, int lane) {
-  return load_planes<NP>(base + (at * NP * kTriFrags + f) * kFrag + lane * 8, kTriFrags * kFrag);
+    *reinterpret_cast<bf16x8*>(base + ((at * kTriFrags + f) * NP + i) * kFrag + lane * 8) = v.p[i];
 }
 
-// State tiles of a chain's wavefront to [P, N]: keys 16 (KT w + t) + 4 q .. + 3
-// of value column col[n]
-template <int NT, int KT>
-__device__ __forceinline__ void store_state(float* to, const f32x4 (&st)[NT][KT], int N,
-                                            const int (&col)[NT], const bool (&col_in)[NT], int w,
-                                            int q) {
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int t = 0; t < KT; ++t) {
-      const int key = 16 * (KT * w + t) + 4 * q;
-      if (col_in[n] && key < N)
-        *reinterpret_cast<f32x4*>(to + (int64_t)col[n] * N + key) = st[n][t];
-    }
-}
+// The wavefront's index, in a scalar register
+__device__ __forceinline__ int wave_of(int tid) { return __builtin_amdgcn_readfirstlane(tid >> 6); }
 
 // sum over a wavefront
 __device__ __forceinline__ float wave_sum64(float v) {
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
   return v;
 }
+
+// ---------------------------------------------------------------------------
+// Chains of wavefronts that own whole value columns (bfloat16 io).
+//
+// A result of a matrix product becomes the right operand of the next one
+// without leaving the lane: the result of row tiles 2 s and 2 s + 1 gives lane
+// group q the rows 4 q .. + 3 of each, and a right operand of 32 contraction
+// indices wants 8 per lane group, in any order that the left operand shares.
+// Over tokens that order is as the tiles lie: 32 s + 4 q .. + 3, then 32 s + 16
+// + 4 q .. + 3; left operands come as such (the triangular fragments) or are read
+// so.  Over keys row i of tiles 2 u and 2 u + 1 stands for keys 32 u + 8 (i / 4) +
+// i % 4 and 4 more, so that the order is 32 u + 8 q .. + 7 and a left operand's
+// row one 16-byte vector: key_of(t, i).
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int key_of(int t, int i) {
+  return 32 * (t >> 1) + 8 * (i >> 2) + 4 * (t & 1) + (i & 3);
+}
+// where a token lies in that order, counted in the LDS rows of the chains
+__device__ __forceinline__ int token_slot(int t, int q) { return 32 * (t >> 1) + 8 * q + 4 * (t & 1); }
+
+// One plane of a transposed operand from the lane's two addresses
+__device__ __forceinline__ Frag<1> read_tr2(const bf16* p, int second) {
+  const bf16x4 lo = lds_read_tr4(p), hi = lds_read_tr4(p + second);
+  Frag<1> f;
+  f.p[0] = bf16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  return f;
+}
+
+// 16 bytes per lane from global memory (a uniform address and a lane's offset)
+// straight to LDS, 1 KB from byte address `to` + AT on in lane order.  The wait is
+// the caller's (landed()): for the builtin the compiler would put one for
+// everything requested before the next read of LDS.  s_nop: the base may come from
+// a vector instruction (v_readlane), five cycles before a load may use it.
+template <int AT = 0>
+__device__ __forceinline__ void request16(const void* from, uint32_t offset, uint32_t to) {
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(to), "v"(offset), "s"(from), "n"(AT) : "memory", "m0", "scc");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// The keys or queries of a chunk in LDS, row-major without padding (what lands
+// in lane order cannot be padded): the 16-byte vectors of a row are permuted by
+// its number instead, so that the 16 rows of an operand read and the 4 x 4
+// (row, vector) of a transposed one take different banks.
+template <int KP, int NW> struct KeyTile {
+  static constexpr int kVecs = KP / 8, kRows = 64 / kVecs;   // vectors of a row, rows of 1 KB
+  static constexpr int kElems = C * KP, kLoads = C / kRows / NW;
+  __device__ __forceinline__ static int swizzle(int row) {
+    return KP == 128 ? 4 * (row & 3) + (row >> 2 & 3) : 4 * (row >> 1 & 1) + (row >> 2 & 3);
+  }
+  // The lane's part of a wavefront's requests: byte offsets from the chunk's
+  // first row; past row `last` that row again.  64 rows count in 32 bits.
+  struct Offsets {
+    uint32_t at[kLoads];
+    bool in[kLoads];
+  };
+  __device__ __forceinline__ static void offsets(Offsets& o, int stride, int last, int N, int w, int lane) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = (i * NW + w) * kRows + lane / kVecs, vec = lane % kVecs ^ swizzle(row);
+      o.at[i] = (uint32_t)min(row, last) * (uint32_t)stride * 2u + 16u * vec;
+      o.in[i] = 8 * vec < N;
+    }
+  }
+  // `tile`: the LDS address plus w KB.  Columns from N on (FULL: there are none)
+  // are left as they are, zero.
+  template <bool FULL, int I = 0>
+  __device__ __forceinline__ static void request(const bf16* base, const Offsets& o, uint32_t tile) {
+    if constexpr (I < kLoads) {
+      if (FULL || o.in[I]) request16<I * NW * 1024>(base, o.at[I], tile);
+      request<FULL, I + 1>(base, o, tile);
+    }
+  }
+  // lane's address of row tile 0 of the left operand's step s (tile t: 16 t rows on)
+  __device__ __forceinline__ static int row_at(int s, int j, int q) { return j * KP + 8 * ((4 * s + q) ^ swizzle(j)); }
+  // lane's address of key tiles 2 u and 2 u + 1 (4 elements further) as left
+  // operand of the first 32 tokens, contracted over them (read transposed)
+  __device__ __forceinline__ static int col_at(int u, int j, int q) {
+    const int row = 4 * q + (j >> 2);
+    return row * KP + 8 * ((4 * u + (j & 3)) ^ swizzle(row));
+  }
+  // rows 16 further on have the same permutation
+  __device__ __forceinline__ static Frag<1> columns(const bf16* p) { return read_tr2(p, 16 * KP); }
+};
+
+// N KB, lane-linear, over NW wavefronts; `from` and `to` point w KB on
+template <int N, int NW, int I = 0>
+__device__ __forceinline__ void request_linear(const void* from, uint32_t to, int w, int lane) {
+  if constexpr (I * NW < N) {
+    if (I * NW + NW <= N || w < N - I * NW)
+      request16<I * NW * 1024>(static_cast<const char*>(from) + I * NW * 1024, 16 * lane, to);
+    request_linear<N, NW, I + 1>(from, to, w, lane);
+  }
+}
+
+// Value columns of a chunk in LDS: [C][16 NW], as KeyTile, not permuted
+template <int NW> struct ColumnTile {
+  static constexpr int kVecs = 2 * NW, kRows = 64 / kVecs, kLoads = C / kRows / NW;
+  struct Offsets {
+    uint32_t at[kLoads];
+    bool in;
+  };
+  __device__ __forceinline__ static void offsets(Offsets& o, int stride, int last, int left, int w, int lane) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      o.at[i] = (uint32_t)min((i * NW + w) * kRows + lane / kVecs, last) * (uint32_t)stride * 2u + 16u * (lane % kVecs);
+    o.in = 8 * (lane % kVecs) < left;
+  }
+  template <bool ALL, int I = 0>
+  __device__ __forceinline__ static void request(const bf16* base, const Offsets& o, uint32_t tile) {
+    if constexpr (I < kLoads) {
+      if (ALL || o.in) request16<I * NW * 1024>(base, o.at[I], tile);
+      request<ALL, I + 1>(base, o, tile);
+    }
+  }
+};
+
+// acc += A B for a triangular left operand, whose fragments lie from the lane's
+// address `a` on (lower: row tiles 0, 1 stop after the first 32 columns; upper:
+// tiles 2, 3 begin behind them)
+template <int NP, int NB>
+__device__ __forceinline__ void mma_lower(const bf16* a, const Frag<NB> (&b)[2], f32x4 (&acc)[4]) {
+  Frag<NP> f[4], g[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = load_planes<NP>(a + lower_frag(i, 0) * (NP * kFrag), kFrag);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) g[i] = load_planes<NP>(a + lower_frag(i + 2, 1) * (NP * kFrag), kFrag);
+  mma_tiles(f, b[0], acc);
+  mma_tiles(g, b[1], acc + 2);
+}
+template <int NP, int NB>
+__device__ __forceinline__ void mma_upper(const bf16* a, const Frag<NB> (&b)[2], f32x4 (&acc)[4]) {
+  Frag<NP> f[2], g[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) f[i] = load_planes<NP>(a + upper_frag(i, 0) * (NP * kFrag), kFrag);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) g[i] = load_planes<NP>(a + upper_frag(i, 1) * (NP * kFrag), kFrag);
+  mma_tiles(f, b[0], acc);
+  mma_tiles(g, b[1], acc);
+}
+
+// two result tiles as a right operand
+template <int NP>
+__device__ __forceinline__ Frag<NP> right_of(f32x4 a, f32x4 b) {
+  const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  return split8<NP>(x);
+}
+
+// Everything but the last STORES memory operations of the wavefront has landed,
+// its LDS reads are done, and every wavefront is here.
+template <int STORES>
+__device__ __forceinline__ void landed() {
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"(STORES) : "memory");
+}
+
+// f(wavefronts of a workgroup) for a chain of wavefronts that own 16 columns
+template <typename F>
+void columns_of(const DeltaArgs& a, F&& f) {
+  const int64_t waves = a.Bt * a.H * ((a.P + 15) / 16);
+  if (waves <= 256) f(std::integral_constant<int, 1>{});
+  else if (waves <= 512) f(std::integral_constant<int, 2>{});
+  else f(std::integral_constant<int, 4>{});
+}
+
+// Columns and keys that the chains keep of a head in the gradients' workspace:
+// whole tiles, so that no store is conditional
+__device__ __forceinline__ int padded_cols(int P) { return (P + 15) / 16 * 16; }
 
 // Position of a (b, h, chunk)
 __device__ __forceinline__ int64_t chunk_at(const DeltaArgs& a, int64_t bh, int64_t c) {

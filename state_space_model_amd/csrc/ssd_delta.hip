@@ -13,8 +13,6 @@
 // its value columns in order, the state in matrix-core accumulators.
 #include "ssd_delta.h"
 
-#include <type_traits>
-
 namespace ssd {
 namespace delta {
 namespace {
@@ -40,26 +38,49 @@ __device__ __forceinline__ float row_squares(const Frag<PI> (&f)[KS]) {
   return ss;
 }
 
+// Wavefront w owns tokens 16 w .. + 15 as rows of both matrices, and forms them
+// transposed: a result's lane then holds four consecutive columns of its row,
+// and two tiles of columns are a fragment of the matrix as it is (ssd_delta.h).
+//
+// The inverse X of 1 + L: the diagonal 16 x 16 blocks by back substitution, a
+// lane a row (X (1 + L) = 1: x_c = [c = row] - sum_{m > c} x_m L_mc); the blocks
+// left of them, nearest first, from X_ij = -(sum_{j < m <= i} X_im L_mj) X_jj on
+// the float32 matrix core, transposed.
+//
 // GRADS: for the gradients, whose chain from the last chunk needs both matrices
 // transposed and no output.
-template <typename IO, int KP, bool GRADS>
+template <typename IO, int KP, bool FULL, bool GRADS>
 __global__ __launch_bounds__(kThreads) void k_delta_prep(DeltaArgs a) {
   constexpr int PI = Planes<IO>::in, PY = Planes<IO>::y;
-  constexpr int KS = KP / 32, KST = KP + 8;
-  __shared__ __align__(16) bf16 s_k[PI * C * KST];
-  __shared__ __align__(16) float s_a[C * kPairStride], s_x[C * kPairStride];
-  __shared__ float s_hi[C], s_lo[C], s_beta[C], s_rk[C], s_rq[C];
+  constexpr int KS = KP / 32, KST = KP + 8, kDiag = 20;
+  constexpr int k_bytes = PI * C * KST * 2, p_bytes = GRADS ? C * kPairStride * 4 : 0;
+  __shared__ __align__(16) char lds_k[k_bytes > p_bytes ? k_bytes : p_bytes];
+  __shared__ __align__(16) float s_l[C * kPairStride];    // L transposed: [column][row]
+  __shared__ __align__(16) float s_d[4 * 16 * kDiag];     // inverse diagonal blocks, transposed
+  __shared__ __align__(16) float s_hi[C], s_lo[C], s_rk[C];
+  __shared__ float s_beta[C], s_rq[C];
+  bf16* const s_k = reinterpret_cast<bf16*>(lds_k);
 
   const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
   const int64_t h = id % a.H, c = id / a.H % a.Nc, b = id / a.H / a.Nc;
   const int64_t g = h / (a.H / a.G);
   const int64_t at = chunk_at(a, b * a.H + h, c);
   const int64_t t0 = c * C, row0 = b * a.T + t0, left = a.T - t0;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, j = lane & 15, q = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_of(tid), j = lane & 15, q = lane >> 4;
+  const int own = 16 * w + j;   // the lane's token
 
   Frag<PI> kf[KS], qf[KS];
-  load_rows<IO, KP>(kf, static_cast<const IO*>(a.k) + g * a.N, a.k_stride, row0, left, a.N, 16 * w + j, q);
-  load_rows<IO, KP>(qf, static_cast<const IO*>(a.q) + g * a.N, a.q_stride, row0, left, a.N, 16 * w + j, q);
+  {
+    const int64_t row = row0 + (own < left ? own : left - 1), at = g * a.N + 8 * q;
+    KeyRow<IO, KP, FULL> kr, qr;
+    kr.load(static_cast<const IO*>(a.k) + row * a.k_stride + at, a.N, q);
+    qr.load(static_cast<const IO*>(a.q) + row * a.q_stride + at, a.N, q);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      kf[s] = kr.frag(s, a.N, q);
+      qf[s] = qr.frag(s, a.N, q);
+    }
+  }
 
   // Decay sums in units of log 2, in float64: differences of them are
   // exponents, and float32 sums over a chunk of strong decays would be off by
@@ -82,121 +103,124 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(DeltaArgs a) {
     const float beta = a.beta[th];
     s_beta[lane] = in ? (a.sigmoid ? sigmoid_of(beta) : beta) : 0.0f;
   }
-  const bool row_in = 16 * w + j < left;
+  float rk_own, rq_own;
   {
+    const bool in = own < left;
     const float kk = row_squares<PI, KS>(kf), qq = row_squares<PI, KS>(qf);
+    rk_own = !in ? 0.0f : a.unit ? 1.0f / sqrtf(kk + a.norm_eps) : 1.0f;
+    rq_own = !in ? 0.0f : a.scale * (a.unit ? 1.0f / sqrtf(qq + a.norm_eps) : 1.0f);
     if (q == 0) {
-      s_rk[16 * w + j] = !row_in ? 0.0f : a.unit ? 1.0f / sqrtf(kk + a.norm_eps) : 1.0f;
-      s_rq[16 * w + j] = !row_in ? 0.0f : a.scale * (a.unit ? 1.0f / sqrtf(qq + a.norm_eps) : 1.0f);
+      s_rk[own] = rk_own;
+      s_rq[own] = rq_own;
     }
   }
 #pragma unroll
   for (int s = 0; s < KS; ++s)
 #pragma unroll
     for (int i = 0; i < PI; ++i)
-      *reinterpret_cast<bf16x8*>(&s_k[i * C * KST + (16 * w + j) * KST + 32 * s + 8 * q]) = kf[s].p[i];
+      *reinterpret_cast<bf16x8*>(&s_k[i * C * KST + own * KST + 32 * s + 8 * q]) = kf[s].p[i];
   __syncthreads();
 
-  // rows of wavefront w against key tokens up to them: L to LDS, D o Q K^T kept
+  // the rows against key tokens up to them: L to LDS, D o Q K^T kept, both
+  // transposed: lane (keys 16 jt + 4 q .. + 3, own token)
   f32x4 p[4];
+  {
+    const float hi_own = s_hi[own], lo_own = s_lo[own], l_own = s_beta[own] * rk_own;
 #pragma unroll
-  for (int jt = 0; jt < 4; ++jt) {
-    p[jt] = f32x4{0, 0, 0, 0};
-    if (jt > w) continue;
-    f32x4 kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0};
+    for (int jt = 0; jt < 4; ++jt) {
+      p[jt] = f32x4{0, 0, 0, 0};
+      if (jt > w) continue;
+      f32x4 kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0};
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const auto bf = load_planes<PI>(&s_k[(16 * jt + j) * KST + 32 * s + 8 * q], C * KST);
-      kk = mma(kf[s], bf, kk);
-      qk = mma(qf[s], bf, qk);
-    }
-    const int col = 16 * jt + j;
-    const float chi = s_hi[col], clo = s_lo[col], rk = s_rk[col];
+      for (int s = 0; s < KS; ++s) {
+        const auto ka = load_planes<PI>(&s_k[(16 * jt + j) * KST + 32 * s + 8 * q], C * KST);
+        kk = mma(ka, kf[s], kk);
+        qk = mma(ka, qf[s], qk);
+      }
+      const int key0 = 16 * jt + 4 * q;
+      const f32x4 hi = *reinterpret_cast<const f32x4*>(&s_hi[key0]), lo = *reinterpret_cast<const f32x4*>(&s_lo[key0]);
+      const f32x4 rk = *reinterpret_cast<const f32x4*>(&s_rk[key0]);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * w + 4 * q + r;
-      const float dec = exp2_of((s_hi[row] - chi) + (s_lo[row] - clo)) * rk;
-      s_a[row * kPairStride + col] = row > col ? s_beta[row] * s_rk[row] * dec * kk[r] : 0.0f;
-      p[jt][r] = row >= col ? s_rq[row] * dec * qk[r] : 0.0f;
+      for (int r = 0; r < 4; ++r) {
+        const float dec = exp2_of((hi_own - hi[r]) + (lo_own - lo[r])) * rk[r];
+        s_l[(key0 + r) * kPairStride + own] = own > key0 + r ? l_own * dec * kk[r] : 0.0f;
+        p[jt][r] = own >= key0 + r ? rq_own * dec * qk[r] : 0.0f;
+      }
     }
   }
+  if constexpr (!GRADS) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      if (s <= (w >> 1)) store_frag(a.qk, at, lower_frag(w, s), lane, right_of<PY>(p[2 * s], p[2 * s + 1]));
+  }
 
-  // The inverse of the diagonal 16 x 16 block by forward substitution, lane
-  // column j (each group of 16 lanes the same).  Only this wavefront wrote the block.
-  __builtin_amdgcn_wave_barrier();
-  f32x4 x[4];  // block (w + d, w) in the layout of a result
+  f32x4 x[4];   // block (w, w - d) of the inverse, transposed
   {
+    // only this wavefront wrote the block
+    __builtin_amdgcn_wave_barrier();
     float col[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float acc = i == j ? 1.0f : 0.0f;
-      const float* row = &s_a[(16 * w + i) * kPairStride + 16 * w];
+    for (int m = 15; m >= 0; --m) {
+      const float* l = &s_l[(16 * w + m) * kPairStride + 16 * w];   // column m of L
+      float acc = m == j ? 1.0f : 0.0f;
 #pragma unroll
-      for (int m = 0; m < i; ++m) acc = fmaf(-row[m], col[m], acc);
-      col[i] = acc;
+      for (int i = 15; i > m; --i) acc = fmaf(-l[i], col[i], acc);
+      col[m] = acc;
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       x[0][r] = q == 0 ? col[r] : q == 1 ? col[4 + r] : q == 2 ? col[8 + r] : col[12 + r];
-      s_x[(16 * w + 4 * q + r) * kPairStride + 16 * w + j] = x[0][r];
+      s_d[(16 * w + 4 * q + r) * kDiag + j] = x[0][r];
     }
   }
   __syncthreads();
-  // the blocks below it, X_iw = -X_ii sum_m L_im X_mw; zeros above it
 #pragma unroll
   for (int d = 1; d < 4; ++d) {
-    const int i = w + d;
-    if (i < 4) {
-      f32x4 acc = {0, 0, 0, 0};
+    x[d] = f32x4{0, 0, 0, 0};
+    const int jb = w - d;
+    if (jb < 0) continue;
+    f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-      for (int e = 0; e < d; ++e)
-        acc = mma16(*reinterpret_cast<const f32x4*>(&s_a[(16 * i + j) * kPairStride + 16 * (w + e) + 4 * q]),
-                    x[e], acc);
-      acc = mma16(*reinterpret_cast<const f32x4*>(&s_x[(16 * i + j) * kPairStride + 16 * i + 4 * q]), acc,
-                  f32x4{0, 0, 0, 0});
-      x[d] = -acc;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) s_x[(16 * i + 4 * q + r) * kPairStride + 16 * w + j] = x[d][r];
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)  // block (i - 4, w): above the diagonal
-        s_x[(16 * (i - 4) + 4 * q + r) * kPairStride + 16 * w + j] = 0.0f;
-    }
+    for (int e = 0; e < d; ++e)
+      acc = mma16(*reinterpret_cast<const f32x4*>(&s_l[(16 * jb + j) * kPairStride + 16 * (w - e) + 4 * q]), x[e], acc);
+    x[d] = -mma16(*reinterpret_cast<const f32x4*>(&s_d[(16 * jb + j) * kDiag + 4 * q]), acc, f32x4{0, 0, 0, 0});
   }
-  __syncthreads();
+  // by column tile: x[w - t], zeros right of the diagonal
+  f32x4 row[4];
 #pragma unroll
-  for (int jt = 0; jt < 4; ++jt)
+  for (int t = 0; t < 4; ++t)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) s_a[(16 * w + 4 * q + r) * kPairStride + 16 * jt + j] = p[jt][r];
-  __syncthreads();
+    for (int r = 0; r < 4; ++r)
+      row[t][r] = t == w ? x[0][r] : t == w - 1 ? x[1][r] : t == w - 2 ? x[2][r] : t == w - 3 ? x[3][r] : 0.0f;
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+    if (s <= (w >> 1)) store_frag(a.inv, at, lower_frag(w, s), lane, right_of<3>(row[2 * s], row[2 * s + 1]));
 
-  // fragments of row tile w: 32 columns for tiles 0 and 1, 64 for 2 and 3
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    if (s > (w >> 1)) continue;
-    const int f = lower_frag(w, s);
-    float vx[8], vp[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      vx[e] = s_x[(16 * w + j) * kPairStride + 32 * s + 8 * q + e];
-      vp[e] = s_a[(16 * w + j) * kPairStride + 32 * s + 8 * q + e];
-    }
-    store_frag(a.inv, at, f, lane, split8<3>(vx));
-    if constexpr (!GRADS) store_frag(a.qk, at, f, lane, split8<PY>(vp));
-  }
   if constexpr (GRADS) {
-    // transposed: row tiles 0 and 1 reach over all columns, 2 and 3 over the last 32
+    // both again, as rows in LDS and read by columns: row tiles 0 and 1 of the
+    // transposed reach over all of them, 2 and 3 over the last 32
+    float* const s_p = reinterpret_cast<float*>(lds_k);
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      *reinterpret_cast<f32x4*>(&s_l[own * kPairStride + 16 * t + 4 * q]) = row[t];
+      *reinterpret_cast<f32x4*>(&s_p[own * kPairStride + 16 * t + 4 * q]) = p[t];
+    }
+    __syncthreads();
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       if (s < (w >> 1)) continue;
-      float vx[8], vp[8];
+      f32x4 vx[2], vp[2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        vx[e] = s_x[(32 * s + 8 * q + e) * kPairStride + 16 * w + j];
-        vp[e] = s_a[(32 * s + 8 * q + e) * kPairStride + 16 * w + j];
-      }
-      store_frag(a.inv_t, at, upper_frag(w, s), lane, split8<3>(vx));
-      store_frag(a.qk, at, upper_frag(w, s), lane, split8<3>(vp));
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int o = (32 * s + 16 * t + 4 * q + r) * kPairStride + own;
+          vx[t][r] = s_l[o];
+          vp[t][r] = s_p[o];
+        }
+      store_frag(a.inv_t, at, upper_frag(w, s), lane, right_of<3>(vx[0], vx[1]));
+      store_frag(a.qk, at, upper_frag(w, s), lane, right_of<3>(vp[0], vp[1]));
     }
   }
 
@@ -205,8 +229,11 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(DeltaArgs a) {
   if (tid < C) {
     const float gamma = exp2_of(s_hi[tid] + s_lo[tid]), beta = s_beta[tid];
     const float end = exp2_of((s_hi[C - 1] - s_hi[tid]) + (s_lo[C - 1] - s_lo[tid]));
-    a.gate[at * C + tid] = make_float4(beta, beta * gamma * s_rk[tid], end * s_rk[tid],
-                                       gamma * s_rq[tid]);
+    float* gate = a.gate + at * kGates + tid;
+    gate[kBeta] = beta;
+    gate[kRight] = beta * gamma * s_rk[tid];
+    gate[kEnd] = end * s_rk[tid];
+    gate[kOut] = gamma * s_rq[tid];
     if (tid == C - 1) a.whole[at] = gamma;
     if constexpr (GRADS) a.row[at * C + tid] = make_float4(s_rk[tid], s_rq[tid], s_hi[tid], s_lo[tid]);
   }
@@ -223,25 +250,28 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(DeltaArgs a) {
 // ---------------------------------------------------------------------------
 // KEEP: for the gradients, which need the state entering every chunk and its
 // writes, and no output.
-template <typename IO, int KP, int NT, bool KEEP>
+//
+// A chunk's operands are requested as soon as the registers of the last one's
+// are free: k, q, v behind the first products, the inverse behind the second,
+// q k^T behind the third.  Every load and store of a step is issued on every
+// path (past the last chunk its own operands again; y of tokens past the end to
+// `park`; the workspace holds whole tiles), so that a wait covers what it is for
+// and no later request.
+template <typename IO, int KP, bool FULL, int NT, bool KEEP>
 __global__ __launch_bounds__(kThreads) void k_delta_chain(DeltaArgs a) {
   constexpr int PI = Planes<IO>::in, PY = Planes<IO>::y;
-  constexpr int KS = KP / 32, KST = KP + 8, KT = KP / 64, W = 16 * NT;
-  __shared__ __align__(16) bf16 s_k[2][PI * C * KST];
+  constexpr int KS = KP / 32, KST = KP + 8, KTR = KP + 16, KT = KP / 64, W = 16 * NT;
+  __shared__ __align__(16) bf16 s_k[2 * PI * C * KTR];
   __shared__ __align__(16) bf16 s_s[3 * W * KST];
   __shared__ __align__(16) bf16 s_r[3 * W * kTokStride];   // right sides
   __shared__ __align__(16) bf16 s_e[3 * W * kTokStride];   // writes, decayed to the chunk's end
-  __shared__ __align__(16) bf16 s_w[PY * W * kTokStride];  // writes
+  __shared__ __align__(16) bf16 s_w[KEEP ? 8 : PY * W * kTokStride];  // writes
 
-  const int64_t slices = (a.P + W - 1) / W;
+  const int slices = (a.P + W - 1) / W;
   const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
   const int64_t bh = id / slices, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
   const int col0 = (int)(id % slices) * W;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, j = lane & 15, q = lane >> 4;
-  const IO* kb = static_cast<const IO*>(a.k) + g * a.N;
-  const IO* qb = static_cast<const IO*>(a.q) + g * a.N;
-  const IO* vb = static_cast<const IO*>(a.v) + h * a.P;
-  IO* yb = KEEP ? nullptr : static_cast<IO*>(a.y) + h * a.P;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_of(tid), j = lane & 15, q = lane >> 4;
   bool col_in[NT];
   int col[NT];
 #pragma unroll
@@ -252,58 +282,102 @@ __global__ __launch_bounds__(kThreads) void k_delta_chain(DeltaArgs a) {
 
   // state tiles (keys 16 (KT w + t) + 4 q .. + 3, value column j of tile n)
   f32x4 st[NT][KT];
+  const int key0 = 16 * KT * w + 4 * q;
+  bf16* const put_s = &s_s[j * KST + key0];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
-      const int key = 16 * (KT * w + t) + 4 * q;
       st[n][t] = f32x4{0, 0, 0, 0};
-      if (a.h0 && col_in[n] && key < a.N)
-        st[n][t] = *reinterpret_cast<const f32x4*>(a.h0 + (bh * a.P + col[n]) * a.N + key);
-      store_split4<3>(&s_s[(16 * n + j) * KST + key], W * KST, st[n][t]);
+      if (a.h0 && col_in[n] && key0 + 16 * t < a.N)
+        st[n][t] = *reinterpret_cast<const f32x4*>(a.h0 + (bh * a.P + col[n]) * a.N + key0 + 16 * t);
+      store_split4<3>(put_s + 16 * n * KST + 16 * t, W * KST, st[n][t]);
     }
 
-  Frag<PI> kf[KS], qf[KS];
-  Frag<3> xf[2];
-  Frag<PY> pf[2];
-  float4 gate[4];
-  IO v[NT][4];
-  float whole;
-  auto load_chunk = [&](int64_t c) {
-    const int64_t t0 = c * C, row0 = b * a.T + t0, left = a.T - t0, at = chunk_at(a, bh, c);
-    load_rows<IO, KP>(kf, kb, a.k_stride, row0, left, a.N, 16 * w + j, q);
-    if constexpr (!KEEP) load_rows<IO, KP>(qf, qb, a.q_stride, row0, left, a.N, 16 * w + j, q);
+  // where the lane's rows are: row 16 w + j of k and q, rows 16 w + 4 q + r of v
+  const IO *kp, *qp, *vp[4];
+  auto rows_of = [&](int64_t c) {
+    const int64_t row0 = b * a.T + c * C, left = a.T - c * C;
+    const int64_t row = row0 + (16 * w + j < left ? 16 * w + j : left - 1), at = g * a.N + 8 * q;
+    kp = static_cast<const IO*>(a.k) + row * a.k_stride + at;
+    qp = static_cast<const IO*>(a.q) + row * a.q_stride + at;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int tok = 16 * w + 4 * q + r;
-      gate[r] = a.gate[at * C + tok];
-      const IO* row = vb + (row0 + (tok < left ? tok : 0)) * a.v_stride;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) v[n][r] = row[col[n]];
+      vp[r] = static_cast<const IO*>(a.v) + (row0 + (tok < left ? tok : left - 1)) * a.v_stride + h * a.P;
     }
+  };
+  const int64_t at0 = chunk_at(a, bh, 0);
+  const float* gp = a.gate + at0 * kGates + 16 * w + 4 * q;
+  // the second fragment of wavefronts 0 and 1 is their first one again, unused
+  const int second = w >= 2 ? 1 : 0;
+  const bf16* xp = a.inv + (at0 * kTriFrags + lower_frag(w, 0)) * (3 * kFrag) + lane * 8;
+  const bf16* pp = a.qk + (at0 * kTriFrags + lower_frag(w, 0)) * (PY * kFrag) + lane * 8;
+  const float* ep = a.whole + at0;
+  const int64_t y_row = a.H * a.P;
+  IO* yp = KEEP ? nullptr : static_cast<IO*>(a.y) + (b * a.T + 16 * w + 4 * q) * y_row + h * a.P;
+  IO* const park = static_cast<IO*>(a.park) + lane;
+  const int64_t cols = padded_cols(a.P);
+  float* state_at = KEEP ? a.enter + (at0 * cols + col0 + j) * KP + key0 : nullptr;
+  float* write_at = KEEP ? a.write + (at0 * cols + col0 + j) * C + 16 * w + 4 * q : nullptr;
+
+  KeyRow<IO, KP, FULL> kr, qr;
+  Frag<3> xf[2];
+  Frag<PY> pf[2];
+  f32x4 g_beta, g_right, g_end, g_out;
+  IO v[NT][4];
+  float whole = *ep;
+  auto load_rows = [&]() {
+    kr.load(kp, a.N, q);
+    if constexpr (!KEEP) qr.load(qp, a.N, q);
+    g_beta = *reinterpret_cast<const f32x4*>(gp + kBeta);
+    g_right = *reinterpret_cast<const f32x4*>(gp + kRight);
+    g_end = *reinterpret_cast<const f32x4*>(gp + kEnd);
+    if constexpr (!KEEP) g_out = *reinterpret_cast<const f32x4*>(gp + kOut);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (s > (w >> 1)) continue;
-      xf[s] = load_frag<3>(a.inv, at, lower_frag(w, s), lane);
-      if constexpr (!KEEP) pf[s] = load_frag<PY>(a.qk, at, lower_frag(w, s), lane);
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) v[n][r] = vp[r][col[n]];
+  };
+  auto load_x = [&]() {
+    xf[0] = load_planes<3>(xp, kFrag);
+    xf[1] = load_planes<3>(xp + second * (3 * kFrag), kFrag);
+  };
+  auto load_p = [&]() {
+    pf[0] = load_planes<PY>(pp, kFrag);
+    pf[1] = load_planes<PY>(pp + second * (PY * kFrag), kFrag);
+  };
+  bf16* const put_k = &s_k[(16 * w + j) * KTR + 8 * q];
+  int k_at = 0;   // which half of s_k holds the chunk
+  auto store_k = [&](int at) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const auto f = kr.frag(s, a.N, q);
+#pragma unroll
+      for (int i = 0; i < PI; ++i) *reinterpret_cast<bf16x8*>(put_k + at + i * C * KTR + 32 * s) = f.p[i];
     }
-    whole = a.whole[at];
   };
-  auto store_k = [&](bf16* to) {
-#pragma unroll
-    for (int s = 0; s < KS; ++s)
-#pragma unroll
-      for (int i = 0; i < PI; ++i)
-        *reinterpret_cast<bf16x8*>(&to[i * C * KST + (16 * w + j) * KST + 32 * s + 8 * q]) = kf[s].p[i];
-  };
-  load_chunk(0);
-  store_k(s_k[0]);
+  rows_of(0);
+  load_rows();
+  load_x();
+  if constexpr (!KEEP) load_p();
+  store_k(0);
   __syncthreads();
 
+  const bf16* const get_s = &s_s[j * KST + 8 * q];
+  const int put_t = j * kTokStride + token_slot(w, q), get_t = j * kTokStride + 8 * q;
+  const bf16* const get_k = &s_k[(4 * q + (j >> 2)) * KTR + 16 * KT * w + 4 * (j & 3)];
   for (int64_t c = 0; c < a.Nc; ++c) {
-    const int64_t t0 = c * C, row0 = b * a.T + t0, left = a.T - t0;
-    const bf16* sk = s_k[c & 1];
-    if constexpr (KEEP) store_state<NT, KT>(a.enter + chunk_at(a, bh, c) * a.P * a.N, st, a.N, col, col_in, w, q);
+    const int64_t left = a.T - c * C;
+    const int64_t next = c + 1 < a.Nc ? 1 : 0;
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+          *reinterpret_cast<f32x4*>(state_at + 16 * n * KP + 16 * t) = st[n][t];
+      state_at += cols * KP;
+    }
     // K S^T and Q S^T of the wavefront's tokens; the right sides b (v - gamma K S^T)
     f32x4 y[NT];
 #pragma unroll
@@ -311,89 +385,303 @@ __global__ __launch_bounds__(kThreads) void k_delta_chain(DeltaArgs a) {
       f32x4 ks = {0, 0, 0, 0}, qs = {0, 0, 0, 0};
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        const auto sf = load_planes<3>(&s_s[(16 * n + j) * KST + 32 * s + 8 * q], W * KST);
-        ks = mma(kf[s], sf, ks);
+        const auto sf = load_planes<3>(get_s + 16 * n * KST + 32 * s, W * KST);
+        ks = mma(kr.frag(s, a.N, q), sf, ks);
         if constexpr (!KEEP) {
           Frag<PY> sy;
 #pragma unroll
           for (int i = 0; i < PY; ++i) sy.p[i] = sf.p[i];
-          qs = mma(qf[s], sy, qs);
+          qs = mma(qr.frag(s, a.N, q), sy, qs);
         }
       }
       f32x4 rs;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float vv = 16 * w + 4 * q + r < left && col_in[n] ? to_f32(v[n][r]) : 0.0f;
-        rs[r] = gate[r].x * vv - gate[r].y * ks[r];
-        y[n][r] = gate[r].w * qs[r];
+        rs[r] = fmaf(-g_right[r], ks[r], g_beta[r] * to_f32(v[n][r]));
+        if constexpr (!KEEP) y[n][r] = g_out[r] * qs[r];
       }
-      store_split4<3>(&s_r[(16 * n + j) * kTokStride + 16 * w + 4 * q], W * kTokStride, rs);
+      store_split4<3>(s_r + put_t + 16 * n * kTokStride, W * kTokStride, rs);
     }
+    const f32x4 eta = g_end;
+    if (next && left < 2 * C) {
+      rows_of(c + 1);
+    } else {
+      kp += next * a.k_stride * C;
+      qp += next * a.q_stride * C;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) vp[r] += next * a.v_stride * C;
+    }
+    gp += next * kGates;
+    load_rows();
     __syncthreads();
     // the writes
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      f32x4 ws = {0, 0, 0, 0};
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (s > (w >> 1)) continue;
-        ws = mma(xf[s], load_planes<3>(&s_r[(16 * n + j) * kTokStride + 32 * s + 8 * q], W * kTokStride), ws);
-      }
+      f32x4 ws = mma(xf[0], load_planes<3>(s_r + get_t + 16 * n * kTokStride, W * kTokStride), f32x4{0, 0, 0, 0});
+      if (w >= 2) ws = mma(xf[1], load_planes<3>(s_r + get_t + 16 * n * kTokStride + 32, W * kTokStride), ws);
       f32x4 es;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) es[r] = gate[r].z * ws[r];
-      const int o = (16 * n + j) * kTokStride + 16 * w + 4 * q;
-      store_split4<3>(&s_e[o], W * kTokStride, es);
-      if constexpr (!KEEP) {
-        store_split4<PY>(&s_w[o], W * kTokStride, ws);
-      } else {
-        if (col_in[n])
-          *reinterpret_cast<f32x4*>(a.write + (chunk_at(a, bh, c) * a.P + col[n]) * C + 16 * w + 4 * q) = ws;
-      }
+      for (int r = 0; r < 4; ++r) es[r] = eta[r] * ws[r];
+      store_split4<3>(s_e + put_t + 16 * n * kTokStride, W * kTokStride, es);
+      if constexpr (!KEEP) store_split4<PY>(s_w + put_t + 16 * n * kTokStride, W * kTokStride, ws);
+      else *reinterpret_cast<f32x4*>(write_at + 16 * n * C) = ws;
     }
+    if constexpr (KEEP) write_at += cols * C;
+    xp += next * (kTriFrags * 3 * kFrag);
+    load_x();
     __syncthreads();
-    // outputs
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if constexpr (KEEP) break;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (s > (w >> 1)) continue;
-        y[n] = mma(pf[s], load_planes<PY>(&s_w[(16 * n + j) * kTokStride + 32 * s + 8 * q], W * kTokStride),
-                   y[n]);
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int tok = 16 * w + 4 * q + r;
-        if (tok < left && col_in[n])
-          yb[(row0 + tok) * (a.H * a.P) + col[n]] = to_io<IO>(y[n][r]);
-      }
-    }
     // the state at the chunk's end
     const float decay = whole;
-    if (c + 1 < a.Nc) load_chunk(c + 1);
+    ep += next;
+    whole = *ep;
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
       Frag<PI> ka[2];
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-        ka[s] = load_planes_tr<PI>(sk, C * KST, KST, 32 * s, 16 * (KT * w + t), lane);
+      for (int s = 0; s < 2; ++s) ka[s] = read_tr<PI>(get_k + k_at + 32 * s * KTR + 16 * t, C * KTR, 16 * KTR);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-          acc = mma(ka[s], load_planes<3>(&s_e[(16 * n + j) * kTokStride + 32 * s + 8 * q], W * kTokStride),
-                    acc);
+          acc = mma(ka[s], load_planes<3>(s_e + get_t + 16 * n * kTokStride + 32 * s, W * kTokStride), acc);
 #pragma unroll
         for (int r = 0; r < 4; ++r) st[n][t][r] = fmaf(decay, st[n][t][r], acc[r]);
-        store_split4<3>(&s_s[(16 * n + j) * KST + 16 * (KT * w + t) + 4 * q], W * KST, st[n][t]);
+        store_split4<3>(put_s + 16 * n * KST + 16 * t, W * KST, st[n][t]);
       }
     }
-    store_k(s_k[(c + 1) & 1]);
+    k_at = PI * C * KTR - k_at;
+    store_k(k_at);
+    // outputs
+    if constexpr (!KEEP) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        y[n] = mma(pf[0], load_planes<PY>(s_w + get_t + 16 * n * kTokStride, W * kTokStride), y[n]);
+        if (w >= 2) y[n] = mma(pf[1], load_planes<PY>(s_w + get_t + 16 * n * kTokStride + 32, W * kTokStride), y[n]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          IO* const to = 16 * w + 4 * q + r < left && col_in[n] ? yp + r * y_row + col[n] : park;
+          *to = to_io<IO>(y[n][r]);
+        }
+      }
+      yp += C * y_row;
+      pp += next * (kTriFrags * PY * kFrag);
+      load_p();
+    }
     __syncthreads();
   }
-  if (!KEEP && a.state) store_state<NT, KT>(a.state + bh * a.P * a.N, st, a.N, col, col_in, w, q);
+  if (!KEEP && a.state) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+        if (col_in[n] && key0 + 16 * t < a.N)
+          *reinterpret_cast<f32x4*>(a.state + (bh * a.P + col[n]) * a.N + key0 + 16 * t) = st[n][t];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The chunks of one (b, h) in order, bfloat16 io: every wavefront owns 16 value
+// columns alone.  The state, the right sides and the writes stay in its
+// registers (ssd_delta.h); what the wavefronts share, k, q and the two
+// matrices of a chunk, lands in LDS one chunk ahead, and one barrier a chunk is
+// all they need of each other.  A chunk takes a wavefront 182 matrix
+// instructions (keys of 128), 2912 cycles.
+// ---------------------------------------------------------------------------
+template <int KP, int NW, bool KEEP> struct ColumnsLds {
+  using Keys = KeyTile<KP, NW>;
+  static constexpr int k = 0, q = k + Keys::kElems, x = q + (KEEP ? 0 : Keys::kElems);
+  static constexpr int p = x + 3 * kTriFrags * kFrag, v = p + (KEEP ? 0 : 2 * kTriFrags * kFrag);
+  static constexpr int gate = v + C * 16 * NW, elems = gate + 2 * kGates;
+};
+
+template <int KP, bool FULL, int NW, bool KEEP>
+__global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
+  using L = ColumnsLds<KP, NW, KEEP>;
+  using Keys = KeyTile<KP, NW>;
+  using Cols = ColumnTile<NW>;
+  constexpr int KS = KP / 32, KT = KP / 16, W = 16 * NW;
+  __shared__ __align__(1024) bf16 lds[2 * L::elems];
+
+  const int slices = (a.P + W - 1) / W;
+  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
+  const int64_t bh = id / slices, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
+  const int col0 = (int)(id % slices) * W;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_of(tid), j = lane & 15, q = lane >> 4;
+  const int col = col0 + 16 * w + j;
+  const bool col_in = col < a.P;
+  const int64_t at0 = chunk_at(a, bh, 0), cols = padded_cols(a.P);
+
+  // columns that no request reaches stay zero
+  for (int i = tid; i < 2 * L::elems / 8; i += 64 * NW) reinterpret_cast<uint4*>(lds)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  // what the wavefront requests of a chunk: lane offsets, and where it starts
+  typename Keys::Offsets k_off, q_off;
+  typename Cols::Offsets v_off;
+  auto offsets = [&](int64_t c) {
+    const int last = (int)min((int64_t)C, a.T - c * C) - 1;
+    Keys::offsets(k_off, (int)a.k_stride, last, a.N, w, lane);
+    if constexpr (!KEEP) Keys::offsets(q_off, (int)a.q_stride, last, a.N, w, lane);
+    Cols::offsets(v_off, (int)a.v_stride, last, a.P - col0, w, lane);
+  };
+  const uint32_t lds0 = lds_address(lds) + w * 1024;
+  const bf16* kp = static_cast<const bf16*>(a.k) + b * a.T * a.k_stride + g * a.N;
+  const bf16* qp = static_cast<const bf16*>(a.q) + b * a.T * a.q_stride + g * a.N;
+  const bf16* vp = static_cast<const bf16*>(a.v) + b * a.T * a.v_stride + h * a.P + col0;
+  const bf16* xp = a.inv + at0 * (3 * kTriFrags * kFrag) + w * 512;
+  const bf16* pp = a.qk + at0 * (2 * kTriFrags * kFrag) + w * 512;
+  const float* gp = a.gate + at0 * kGates + w * 256;
+  const bool all_cols = a.P - col0 >= W;
+  auto request = [&](uint32_t to) {
+    Keys::template request<FULL>(kp, k_off, to + 2 * L::k);
+    if constexpr (!KEEP) Keys::template request<FULL>(qp, q_off, to + 2 * L::q);
+    request_linear<3 * kTriFrags, NW>(xp, to + 2 * L::x, w, lane);
+    if constexpr (!KEEP) request_linear<2 * kTriFrags, NW>(pp, to + 2 * L::p, w, lane);
+    if (all_cols) Cols::template request<true>(vp, v_off, to + 2 * L::v);
+    else Cols::template request<false>(vp, v_off, to + 2 * L::v);
+    request_linear<1, NW>(gp, to + 2 * L::gate, w, lane);
+  };
+  offsets(0);
+  request(lds0);
+
+  // state tiles: keys key_of(t, 4 q + r) of value column j
+  f32x4 st[KT];
+#pragma unroll
+  for (int t = 0; t < KT; ++t) {
+    const int key = key_of(t, 4 * q);
+    st[t] = f32x4{0, 0, 0, 0};
+    if (a.h0 && col_in && key < a.N) st[t] = *reinterpret_cast<const f32x4*>(a.h0 + (bh * a.P + col) * a.N + key);
+  }
+  const bool idle = col0 + 16 * w >= a.P;   // no column of this wavefront exists
+  float* state_at = KEEP ? a.enter + (at0 * cols + col) * KP + 8 * q : nullptr;
+  float* write_at = KEEP ? a.write + (at0 * cols + col) * C + 4 * q : nullptr;
+
+  int row_at[KS], col_at[KT / 2];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) row_at[s] = Keys::row_at(s, j, q);
+#pragma unroll
+  for (int u = 0; u < KT / 2; ++u) col_at[u] = Keys::col_at(u, j, q);
+  landed<0>();
+#pragma unroll
+  for (int t = 0; t < KT; ++t) asm("" : "+v"(st[t]));   // the state has landed too: no wait for it in the loop
+
+  for (int64_t c = 0; c < a.Nc; ++c) {
+    const bf16* const l = lds + (c & 1) * L::elems;
+    // past the last chunk that one again, into the half that no one reads any more
+    if (c + 1 < a.Nc) {
+      kp += C * a.k_stride;
+      qp += C * a.q_stride;
+      vp += C * a.v_stride;
+      xp += 3 * kTriFrags * kFrag;
+      pp += 2 * kTriFrags * kFrag;
+      gp += kGates;
+      if (c + 2 == a.Nc) offsets(c + 1);
+    }
+    request(lds0 + (uint32_t)(~c & 1) * (2 * L::elems));
+    const float whole = a.whole[at0 + c];
+    const float* const gate = reinterpret_cast<const float*>(l + L::gate) + 4 * q;
+    auto gates = [&](int which, int i) { return *reinterpret_cast<const f32x4*>(gate + which + 16 * i); };
+    if (KEEP && !idle) {
+#pragma unroll
+      for (int t = 0; t < KT; ++t) *reinterpret_cast<f32x4*>(state_at + key_of(t, 0)) = st[t];
+      state_at += cols * KP;
+    }
+
+    // K S^T and Q S^T
+    f32x4 ks[4], qs[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ks[i] = qs[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const auto sf = right_of<3>(st[2 * s], st[2 * s + 1]);
+      Frag<1> rows[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rows[i] = load_planes<1>(l + L::k + row_at[s] + 16 * i * KP, 0);
+      mma_tiles(rows, sf, ks);
+      if constexpr (!KEEP) {
+        const Frag<2> sy = {{sf.p[0], sf.p[1]}};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rows[i] = load_planes<1>(l + L::q + row_at[s] + 16 * i * KP, 0);
+        mma_tiles(rows, sy, qs);
+      }
+    }
+    // the right sides, and the writes
+    Frag<3> rf[2], ef[2];
+    f32x4 ws[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bf16x4 v = lds_read_tr4(l + L::v + (16 * i + 4 * q + (j >> 2)) * W + 16 * w + 4 * (j & 3));
+      const f32x4 gb = gates(kBeta, i), gr = gates(kRight, i);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) ks[i][r] = fmaf(-gr[r], ks[i][r], gb[r] * (float)v[r]);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) rf[s] = right_of<3>(ks[2 * s], ks[2 * s + 1]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ws[i] = f32x4{0, 0, 0, 0};
+    mma_lower<3>(l + L::x + lane * 8, rf, ws);
+    if (KEEP && !idle) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4*>(write_at + 16 * i) = ws[i];
+      write_at += cols * C;
+    }
+    // the state at the chunk's end
+#pragma unroll
+    for (int s = 0; s < 2; ++s) ef[s] = right_of<3>(gates(kEnd, 2 * s) * ws[2 * s], gates(kEnd, 2 * s + 1) * ws[2 * s + 1]);
+#pragma unroll
+    for (int t0 = 0; t0 < KT; t0 += 4) {
+      f32x4 acc[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        Frag<1> keys[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          keys[t] = Keys::columns(l + L::k + col_at[(t0 + t) / 2] + 4 * (t & 1) + 32 * s * KP);
+        mma_tiles(keys, ef[s], acc);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) st[t0 + t][r] = fmaf(whole, st[t0 + t][r], acc[t][r]);
+    }
+    // outputs, through the wavefront's own columns of v
+    if constexpr (!KEEP) {
+      Frag<2> wf[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) wf[s] = right_of<2>(ws[2 * s], ws[2 * s + 1]);
+      bf16* const out = lds + (c & 1) * L::elems + L::v + 16 * w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qs[i] *= gates(kOut, i);
+      mma_lower<2>(l + L::p + lane * 8, wf, qs);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) out[(16 * i + 4 * q + r) * W + j] = (bf16)qs[i][r];
+      const int64_t left = a.T - c * C;
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int row = 32 * n + (lane >> 1), part = 8 * (lane & 1);
+        const uint4 v = *reinterpret_cast<const uint4*>(out + row * W + part);
+        const bool in = row < left && col0 + 16 * w + part < a.P;
+        bf16* const to = static_cast<bf16*>(a.y) + (b * a.T + c * C + row) * (a.H * a.P) + h * a.P + col0 + 16 * w + part;
+        *reinterpret_cast<uint4*>(in ? to : static_cast<bf16*>(a.park) + lane * 8) = v;
+      }
+    }
+    // the writes, or y, may be on their way
+    if (KEEP && idle) landed<0>();
+    else landed<KEEP ? 4 : 2>();
+  }
+  if (!KEEP && a.state && col_in) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const int key = key_of(t, 4 * q);
+      if (key < a.N) *reinterpret_cast<f32x4*>(a.state + (bh * a.P + col) * a.N + key) = st[t];
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no request may reach LDS after this
 }
 
 // ---------------------------------------------------------------------------
@@ -464,20 +752,27 @@ __global__ __launch_bounds__(kThreads) void k_delta_step(DeltaArgs a) {
 }
 
 // GRADS: the forward part of the gradients, which keeps states and writes
-template <typename IO, int KP, bool GRADS>
-hipError_t launch_scan(const DeltaArgs& a, hipStream_t stream) {
-  const int64_t chunks = a.Bt * a.H * a.Nc;
-  hipLaunchKernelGGL((k_delta_prep<IO, KP, GRADS>), dim3((unsigned)chunks), dim3(kThreads), 0, stream, a);
-  hipLaunchKernelGGL((k_delta_chain<IO, KP, 1, GRADS>), dim3((unsigned)(a.Bt * a.H * ((a.P + 15) / 16))),
-                     dim3(kThreads), 0, stream, a);
-  return hipGetLastError();
-}
-
 template <bool GRADS>
-hipError_t launch_scan_of(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
-  if (a.N <= 64)
-    return io_bf16 ? launch_scan<bf16, 64, GRADS>(a, stream) : launch_scan<float, 64, GRADS>(a, stream);
-  return io_bf16 ? launch_scan<bf16, 128, GRADS>(a, stream) : launch_scan<float, 128, GRADS>(a, stream);
+hipError_t launch_scan(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
+  return with_keys(a.N, io_bf16, [&](auto io, auto kp, auto full) {
+    using IO = decltype(io);
+    constexpr int KP = decltype(kp)::value;
+    constexpr bool FULL = decltype(full)::value;
+    const unsigned chunks = (unsigned)(a.Bt * a.H * a.Nc);
+    const int64_t heads = a.Bt * a.H;
+    hipLaunchKernelGGL((k_delta_prep<IO, KP, FULL, GRADS>), dim3(chunks), dim3(kThreads), 0, stream, a);
+    if constexpr (sizeof(IO) == 2) {
+      columns_of(a, [&](auto nw) {
+        constexpr int NW = decltype(nw)::value;
+        hipLaunchKernelGGL((k_delta_columns<KP, FULL, NW, GRADS>), dim3((unsigned)(heads * ((a.P + 16 * NW - 1) / (16 * NW)))),
+                           dim3(64 * NW), 0, stream, a);
+      });
+    } else {
+      hipLaunchKernelGGL((k_delta_chain<IO, KP, FULL, 1, GRADS>), dim3((unsigned)(heads * ((a.P + 15) / 16))),
+                         dim3(kThreads), 0, stream, a);
+    }
+    return hipGetLastError();
+  });
 }
 
 template <typename IO>
@@ -504,12 +799,14 @@ size_t delta_workspace(DeltaArgs& a, bool io_bf16, bool grads, char* ws) {
     if (ws) p = reinterpret_cast<std::remove_reference_t<decltype(p)>>(ws + at);
     at += (bytes + 255) / 256 * 256;
   };
-  take(a.gate, n * C * sizeof(float4));
+  take(a.gate, n * 4 * C * sizeof(float));
   take(a.whole, n * sizeof(float));
   take(a.inv, n * 3 * frags);
   take(a.qk, n * (io_bf16 && !grads ? 2 : 3) * frags);
+  take(a.park, 64 * 16);
   if (grads) {
-    const size_t state = (size_t)a.P * a.N * sizeof(float), cols = (size_t)a.P * C * sizeof(float);
+    const size_t P16 = (a.P + 15) / 16 * 16, KP = a.N > 64 ? 128 : 64;
+    const size_t state = P16 * KP * sizeof(float), cols = P16 * C * sizeof(float);
     const size_t keys = (size_t)(a.Bt * a.T * a.H * a.N) * sizeof(float);
     take(a.row, n * C * sizeof(float4));
     take(a.inv_t, n * 3 * frags);
@@ -525,11 +822,11 @@ size_t delta_workspace(DeltaArgs& a, bool io_bf16, bool grads, char* ws) {
 }
 
 hipError_t launch_delta_scan(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
-  return delta::launch_scan_of<false>(a, io_bf16, stream);
+  return delta::launch_scan<false>(a, io_bf16, stream);
 }
 
 hipError_t launch_delta_states(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
-  return delta::launch_scan_of<true>(a, io_bf16, stream);
+  return delta::launch_scan<true>(a, io_bf16, stream);
 }
 
 hipError_t launch_delta_step(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {

@@ -44,7 +44,9 @@ ssd_status check(const ssd_delta_desc* d, bool step, bool grads, Sizes* s) {
   if (!limits_ok(d->dt_min, d->dt_max) || !(d->norm_eps >= 0.0f) || !isfinite(d->norm_eps) ||
       !isfinite(d->scale))
     return SSD_ERR_INVALID_ARG;
-  if (d->headdim % 8 != 0 || d->headdim > SSD_DELTA_MAX_P || d->dstate % 8 != 0 ||
+  // the 64 rows of a chunk count in 32 bits of bytes
+  constexpr int64_t kMaxStride = (1 << 25) - 512;
+  if (d->q_stride > kMaxStride || d->k_stride > kMaxStride || d->v_stride > kMaxStride || d->headdim % 8 != 0 || d->headdim > SSD_DELTA_MAX_P || d->dstate % 8 != 0 ||
       d->dstate > SSD_DELTA_MAX_N || d->nheads > kMaxGroups)
     return SSD_ERR_UNSUPPORTED;
   const int64_t es = (int64_t)io_size(d->io_dtype);
@@ -67,7 +69,7 @@ ssd_status check(const ssd_delta_desc* d, bool step, bool grads, Sizes* s) {
   // the gradients' workspace, in bytes (a bound), and a wavefront's half for each of 2 Bt T G rows
   int64_t rows = 0, ws = 0;
   if (grads && (!mul_ok(tokens, 2 * d->ngroups, &rows) || rows >= (int64_t{1} << 27) ||
-                !mul_ok(bh * chunks, 8 * (d->headdim * d->dstate + 64 * (d->headdim + d->dstate + 80)), &ws) ||
+                !mul_ok(bh * chunks, 8 * ((d->headdim + 8) * 128 + 64 * (d->headdim + d->dstate + 80)), &ws) ||
                 ws > INT64_MAX / 16))
     return SSD_ERR_UNSUPPORTED;
   state = bh * d->headdim * d->dstate;

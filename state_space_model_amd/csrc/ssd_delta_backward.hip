@@ -21,31 +21,27 @@
 // them and taken through the normalisation: du = r (dU - U (U.dU)), r = 1/|u|.
 #include "ssd_delta.h"
 
-#include <type_traits>
-
 namespace ssd {
 namespace delta {
 namespace {
 
-template <typename IO, int KP, int NT>
+// As k_delta_chain, from the last chunk to the first.
+template <typename IO, int KP, bool FULL, int NT>
 __global__ __launch_bounds__(kThreads) void k_delta_back_chain(DeltaArgs a) {
   constexpr int PI = Planes<IO>::in;
-  constexpr int KS = KP / 32, KST = KP + 8, KT = KP / 64, W = 16 * NT;
-  __shared__ __align__(16) bf16 s_k[PI * C * KST], s_q[PI * C * KST];
+  constexpr int KS = KP / 32, KST = KP + 8, KTR = KP + 16, KT = KP / 64, W = 16 * NT;
+  __shared__ __align__(16) bf16 s_k[PI * C * KTR], s_q[PI * C * KTR];
   __shared__ __align__(16) bf16 s_s[3 * W * KST];           // E, value-major
   __shared__ __align__(16) bf16 s_y[PI * W * kTokStride];   // dY
   __shared__ __align__(16) bf16 s_g[3 * W * kTokStride];    // diag(gamma / |q|) dY
   __shared__ __align__(16) bf16 s_r[3 * W * kTokStride];    // dW
   __shared__ __align__(16) bf16 s_e[3 * W * kTokStride];    // -diag(b gamma / |k|) dR
 
-  const int64_t slices = (a.P + W - 1) / W;
+  const int slices = (a.P + W - 1) / W;
   const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
   const int64_t bh = id / slices, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
   const int col0 = (int)(id % slices) * W;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, j = lane & 15, q = lane >> 4;
-  const IO* kb = static_cast<const IO*>(a.k) + g * a.N;
-  const IO* qb = static_cast<const IO*>(a.q) + g * a.N;
-  const IO* yb = static_cast<const IO*>(a.dy) + h * a.P;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_of(tid), j = lane & 15, q = lane >> 4;
   bool col_in[NT];
   int col[NT];
 #pragma unroll
@@ -55,133 +51,368 @@ __global__ __launch_bounds__(kThreads) void k_delta_back_chain(DeltaArgs a) {
   }
 
   f32x4 st[NT][KT];
+  const int key0 = 16 * KT * w + 4 * q;
+  bf16* const put_s = &s_s[j * KST + key0];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
-      const int key = 16 * (KT * w + t) + 4 * q;
       st[n][t] = f32x4{0, 0, 0, 0};
-      if (a.dfinal && col_in[n] && key < a.N)
-        st[n][t] = *reinterpret_cast<const f32x4*>(a.dfinal + (bh * a.P + col[n]) * a.N + key);
-      store_split4<3>(&s_s[(16 * n + j) * KST + key], W * KST, st[n][t]);
+      if (a.dfinal && col_in[n] && key0 + 16 * t < a.N)
+        st[n][t] = *reinterpret_cast<const f32x4*>(a.dfinal + (bh * a.P + col[n]) * a.N + key0 + 16 * t);
+      store_split4<3>(put_s + 16 * n * KST + 16 * t, W * KST, st[n][t]);
     }
 
-  Frag<PI> kf[KS], qf[KS];
-  Frag<3> xf[2], pf[2];
-  float4 gate[4];
-  IO dy[NT][4];
-  float whole;
-  auto load_chunk = [&](int64_t c) {
-    const int64_t t0 = c * C, row0 = b * a.T + t0, left = a.T - t0, at = chunk_at(a, bh, c);
-    load_rows<IO, KP>(kf, kb, a.k_stride, row0, left, a.N, 16 * w + j, q);
-    load_rows<IO, KP>(qf, qb, a.q_stride, row0, left, a.N, 16 * w + j, q);
+  // where the lane's rows are: row 16 w + j of k and q, rows 16 w + 4 q + r of dy
+  const IO *kp, *qp, *yp[4];
+  const int64_t y_row = a.H * a.P;
+  auto rows_of = [&](int64_t c) {
+    const int64_t row0 = b * a.T + c * C, left = a.T - c * C;
+    const int64_t row = row0 + (16 * w + j < left ? 16 * w + j : left - 1), at = g * a.N + 8 * q;
+    kp = static_cast<const IO*>(a.k) + row * a.k_stride + at;
+    qp = static_cast<const IO*>(a.q) + row * a.q_stride + at;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int tok = 16 * w + 4 * q + r;
-      gate[r] = a.gate[at * C + tok];
-      const IO* row = yb + (row0 + (tok < left ? tok : 0)) * (a.H * a.P);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) dy[n][r] = row[col[n]];
+      yp[r] = static_cast<const IO*>(a.dy) + (row0 + (tok < left ? tok : left - 1)) * y_row + h * a.P;
     }
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (s < (w >> 1)) continue;
-      xf[s] = load_frag<3>(a.inv_t, at, upper_frag(w, s), lane);
-      pf[s] = load_frag<3>(a.qk, at, upper_frag(w, s), lane);
-    }
-    whole = a.whole[at];
   };
-  auto store_chunk = [&](int64_t left) {
+  const int64_t at_last = chunk_at(a, bh, a.Nc - 1);
+  const float* gp = a.gate + at_last * kGates + 16 * w + 4 * q;
+  const bf16* xp = a.inv_t + (at_last * kTriFrags + upper_frag(w, w >> 1)) * (3 * kFrag) + lane * 8;
+  const bf16* pp = a.qk + (at_last * kTriFrags + upper_frag(w, w >> 1)) * (3 * kFrag) + lane * 8;
+  const float* ep = a.whole + at_last;
+  const int second = w < 2 ? 1 : 0;   // wavefronts 2 and 3: the first fragment again, unused
+  const int64_t cols = padded_cols(a.P);
+  float* state_at = a.leave + (at_last * cols + col0 + j) * KP + key0;
+  float* right_at = a.dright + (at_last * cols + col0 + j) * C + 16 * w + 4 * q;
+
+  KeyRow<IO, KP, FULL> kr, qr;
+  Frag<3> xf[2], pf[2];
+  f32x4 g_right, g_end, g_out;
+  IO dy[NT][4];
+  auto load_rows = [&]() {
+    kr.load(kp, a.N, q);
+    qr.load(qp, a.N, q);
+    g_right = *reinterpret_cast<const f32x4*>(gp + kRight);
+    g_end = *reinterpret_cast<const f32x4*>(gp + kEnd);
+    g_out = *reinterpret_cast<const f32x4*>(gp + kOut);
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) dy[n][r] = yp[r][col[n]];
+  };
+  // row tiles 0 and 1 reach over all columns, 2 and 3 over the last 32
+  auto load_upper = [&](Frag<3>(&f)[2], const bf16* from) {
+    f[0] = load_planes<3>(from, kFrag);
+    f[1] = load_planes<3>(from + second * (3 * kFrag), kFrag);
+  };
+  bf16 *const put_k = &s_k[(16 * w + j) * KTR + 8 * q], *const put_q = &s_q[(16 * w + j) * KTR + 8 * q];
+  const int put_t = j * kTokStride + token_slot(w, q), get_t = j * kTokStride + 8 * q;
+  auto store_chunk = [&]() {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const auto kf = kr.frag(s, a.N, q);
+      const auto qf = qr.frag(s, a.N, q);
 #pragma unroll
       for (int i = 0; i < PI; ++i) {
-        const int o = i * C * KST + (16 * w + j) * KST + 32 * s + 8 * q;
-        *reinterpret_cast<bf16x8*>(&s_k[o]) = kf[s].p[i];
-        *reinterpret_cast<bf16x8*>(&s_q[o]) = qf[s].p[i];
+        *reinterpret_cast<bf16x8*>(put_k + i * C * KTR + 32 * s) = kf.p[i];
+        *reinterpret_cast<bf16x8*>(put_q + i * C * KTR + 32 * s) = qf.p[i];
       }
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int o = (16 * n + j) * kTokStride + 16 * w + 4 * q;
       f32x4 v;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = 16 * w + 4 * q + r < left && col_in[n] ? to_f32(dy[n][r]) : 0.0f;
-      store_split4<PI>(&s_y[o], W * kTokStride, v);
+      for (int r = 0; r < 4; ++r) v[r] = to_f32(dy[n][r]);
+      store_split4<PI>(s_y + put_t + 16 * n * kTokStride, W * kTokStride, v);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] *= gate[r].w;
-      store_split4<3>(&s_g[o], W * kTokStride, v);
+      for (int r = 0; r < 4; ++r) v[r] *= g_out[r];
+      store_split4<3>(s_g + put_t + 16 * n * kTokStride, W * kTokStride, v);
     }
   };
-  load_chunk(a.Nc - 1);
-  store_chunk(a.T - (a.Nc - 1) * C);
+  rows_of(a.Nc - 1);
+  load_rows();
+  load_upper(xf, xp);
+  load_upper(pf, pp);
+  float whole = *ep;
+  store_chunk();
   __syncthreads();
 
+  const bf16* const get_s = &s_s[j * KST + 8 * q];
+  const int get_k = (4 * q + (j >> 2)) * KTR + 16 * KT * w + 4 * (j & 3);
+  const int t_first = w < 2 ? 0 : 32;
   for (int64_t c = a.Nc - 1; c >= 0; --c) {
-    const int64_t at = chunk_at(a, bh, c);
-    store_state<NT, KT>(a.leave + at * a.P * a.N, st, a.N, col, col_in, w, q);
+    const int64_t next = c > 0 ? 1 : 0;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+        *reinterpret_cast<f32x4*>(state_at + 16 * n * KP + 16 * t) = st[n][t];
+    state_at -= cols * KP;
     // dW
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      f32x4 ke = {0, 0, 0, 0}, dw = {0, 0, 0, 0};
+      f32x4 ke = {0, 0, 0, 0};
 #pragma unroll
       for (int s = 0; s < KS; ++s)
-        ke = mma(kf[s], load_planes<3>(&s_s[(16 * n + j) * KST + 32 * s + 8 * q], W * KST), ke);
+        ke = mma(kr.frag(s, a.N, q), load_planes<3>(get_s + 16 * n * KST + 32 * s, W * KST), ke);
+      f32x4 dw = mma(pf[0], load_planes<PI>(s_y + get_t + 16 * n * kTokStride + t_first, W * kTokStride),
+                     f32x4{0, 0, 0, 0});
+      if (w < 2) dw = mma(pf[1], load_planes<PI>(s_y + get_t + 16 * n * kTokStride + 32, W * kTokStride), dw);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (s < (w >> 1)) continue;
-        dw = mma(pf[s], load_planes<PI>(&s_y[(16 * n + j) * kTokStride + 32 * s + 8 * q], W * kTokStride), dw);
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) dw[r] = fmaf(gate[r].z, ke[r], dw[r]);
-      store_split4<3>(&s_r[(16 * n + j) * kTokStride + 16 * w + 4 * q], W * kTokStride, dw);
+      for (int r = 0; r < 4; ++r) dw[r] = fmaf(g_end[r], ke[r], dw[r]);
+      store_split4<3>(s_r + put_t + 16 * n * kTokStride, W * kTokStride, dw);
     }
+    const f32x4 gamma = -g_right;
+    if (next && c == a.Nc - 1) {
+      rows_of(c - 1);
+    } else {
+      kp -= next * a.k_stride * C;
+      qp -= next * a.q_stride * C;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) yp[r] -= next * y_row * C;
+    }
+    gp -= next * kGates;
+    load_rows();
+    pp -= next * (kTriFrags * 3 * kFrag);
+    load_upper(pf, pp);
     __syncthreads();
     // dR
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      f32x4 dr = {0, 0, 0, 0};
+      f32x4 dr = mma(xf[0], load_planes<3>(s_r + get_t + 16 * n * kTokStride + t_first, W * kTokStride),
+                     f32x4{0, 0, 0, 0});
+      if (w < 2) dr = mma(xf[1], load_planes<3>(s_r + get_t + 16 * n * kTokStride + 32, W * kTokStride), dr);
+      *reinterpret_cast<f32x4*>(right_at + 16 * n * C) = dr;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (s < (w >> 1)) continue;
-        dr = mma(xf[s], load_planes<3>(&s_r[(16 * n + j) * kTokStride + 32 * s + 8 * q], W * kTokStride), dr);
-      }
-      if (col_in[n])
-        *reinterpret_cast<f32x4*>(a.dright + (at * a.P + col[n]) * C + 16 * w + 4 * q) = dr;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) dr[r] *= -gate[r].y;
-      store_split4<3>(&s_e[(16 * n + j) * kTokStride + 16 * w + 4 * q], W * kTokStride, dr);
+      for (int r = 0; r < 4; ++r) dr[r] *= gamma[r];
+      store_split4<3>(s_e + put_t + 16 * n * kTokStride, W * kTokStride, dr);
     }
+    right_at -= cols * C;
+    xp -= next * (kTriFrags * 3 * kFrag);
+    load_upper(xf, xp);
     __syncthreads();
     // the gradient of the state that enters the chunk
     const float decay = whole;
-    if (c > 0) load_chunk(c - 1);
+    ep -= next;
+    whole = *ep;
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
       Frag<PI> ka[2], qa[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        ka[s] = load_planes_tr<PI>(s_k, C * KST, KST, 32 * s, 16 * (KT * w + t), lane);
-        qa[s] = load_planes_tr<PI>(s_q, C * KST, KST, 32 * s, 16 * (KT * w + t), lane);
+        ka[s] = read_tr<PI>(s_k + get_k + 32 * s * KTR + 16 * t, C * KTR, 16 * KTR);
+        qa[s] = read_tr<PI>(s_q + get_k + 32 * s * KTR + 16 * t, C * KTR, 16 * KTR);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const int o = (16 * n + j) * kTokStride + 32 * s + 8 * q;
-          acc = mma(qa[s], load_planes<3>(&s_g[o], W * kTokStride), acc);
-          acc = mma(ka[s], load_planes<3>(&s_e[o], W * kTokStride), acc);
+          const int o = get_t + 16 * n * kTokStride + 32 * s;
+          acc = mma(qa[s], load_planes<3>(s_g + o, W * kTokStride), acc);
+          acc = mma(ka[s], load_planes<3>(s_e + o, W * kTokStride), acc);
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) st[n][t][r] = fmaf(decay, st[n][t][r], acc[r]);
-        store_split4<3>(&s_s[(16 * n + j) * KST + 16 * (KT * w + t) + 4 * q], W * KST, st[n][t]);
+        store_split4<3>(put_s + 16 * n * KST + 16 * t, W * KST, st[n][t]);
       }
     }
     __syncthreads();
-    if (c > 0) store_chunk(C);
+    store_chunk();
     __syncthreads();
   }
-  if (a.dh0) store_state<NT, KT>(a.dh0 + bh * a.P * a.N, st, a.N, col, col_in, w, q);
+  if (a.dh0) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+        if (col_in[n] && key0 + 16 * t < a.N)
+          *reinterpret_cast<f32x4*>(a.dh0 + (bh * a.P + col[n]) * a.N + key0 + 16 * t) = st[n][t];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The same for bfloat16 io, as k_delta_columns: every wavefront owns 16 value
+// columns alone.
+// ---------------------------------------------------------------------------
+template <int KP, int NW> struct BackLds {
+  using Keys = KeyTile<KP, NW>;
+  static constexpr int k = 0, q = k + Keys::kElems, x = q + Keys::kElems, p = x + 3 * kTriFrags * kFrag;
+  static constexpr int y = p + 3 * kTriFrags * kFrag, gate = y + C * 16 * NW, elems = gate + 2 * kGates;
+};
+
+template <int KP, bool FULL, int NW>
+__global__ __launch_bounds__(64 * NW) void k_delta_back_columns(DeltaArgs a) {
+  using L = BackLds<KP, NW>;
+  using Keys = KeyTile<KP, NW>;
+  using Cols = ColumnTile<NW>;
+  constexpr int KS = KP / 32, KT = KP / 16, W = 16 * NW;
+  __shared__ __align__(1024) bf16 lds[2 * L::elems];
+
+  const int slices = (a.P + W - 1) / W;
+  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
+  const int64_t bh = id / slices, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
+  const int col0 = (int)(id % slices) * W;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_of(tid), j = lane & 15, q = lane >> 4;
+  const int col = col0 + 16 * w + j;
+  const bool col_in = col < a.P, idle = col0 + 16 * w >= a.P;
+  const int64_t c_last = a.Nc - 1, at = chunk_at(a, bh, c_last), cols = padded_cols(a.P);
+
+  for (int i = tid; i < 2 * L::elems / 8; i += 64 * NW) reinterpret_cast<uint4*>(lds)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  typename Keys::Offsets k_off, q_off;
+  typename Cols::Offsets y_off;
+  const int64_t y_row = a.H * a.P;
+  auto offsets = [&](int last) {
+    Keys::offsets(k_off, (int)a.k_stride, last, a.N, w, lane);
+    Keys::offsets(q_off, (int)a.q_stride, last, a.N, w, lane);
+    Cols::offsets(y_off, (int)y_row, last, a.P - col0, w, lane);
+  };
+  const uint32_t lds0 = lds_address(lds) + w * 1024;
+  const int64_t row0 = b * a.T + c_last * C;
+  const bf16* kp = static_cast<const bf16*>(a.k) + row0 * a.k_stride + g * a.N;
+  const bf16* qp = static_cast<const bf16*>(a.q) + row0 * a.q_stride + g * a.N;
+  const bf16* yp = static_cast<const bf16*>(a.dy) + row0 * y_row + h * a.P + col0;
+  const bf16* xp = a.inv_t + at * (3 * kTriFrags * kFrag) + w * 512;
+  const bf16* pp = a.qk + at * (3 * kTriFrags * kFrag) + w * 512;
+  const float* gp = a.gate + at * kGates + w * 256;
+  const bool all_cols = a.P - col0 >= W;
+  auto request = [&](uint32_t to) {
+    Keys::template request<FULL>(kp, k_off, to + 2 * L::k);
+    Keys::template request<FULL>(qp, q_off, to + 2 * L::q);
+    request_linear<3 * kTriFrags, NW>(xp, to + 2 * L::x, w, lane);
+    request_linear<3 * kTriFrags, NW>(pp, to + 2 * L::p, w, lane);
+    if (all_cols) Cols::template request<true>(yp, y_off, to + 2 * L::y);
+    else Cols::template request<false>(yp, y_off, to + 2 * L::y);
+    request_linear<1, NW>(gp, to + 2 * L::gate, w, lane);
+  };
+  offsets((int)(a.T - c_last * C) - 1);
+  request(lds0);
+
+  f32x4 st[KT];
+#pragma unroll
+  for (int t = 0; t < KT; ++t) {
+    const int key = key_of(t, 4 * q);
+    st[t] = f32x4{0, 0, 0, 0};
+    if (a.dfinal && col_in && key < a.N)
+      st[t] = *reinterpret_cast<const f32x4*>(a.dfinal + (bh * a.P + col) * a.N + key);
+  }
+  float* state_at = a.leave + (at * cols + col) * KP + 8 * q;
+  float* right_at = a.dright + (at * cols + col) * C + 4 * q;
+  int row_at[KS], col_at[KT / 2];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) row_at[s] = Keys::row_at(s, j, q);
+#pragma unroll
+  for (int u = 0; u < KT / 2; ++u) col_at[u] = Keys::col_at(u, j, q);
+  landed<0>();
+#pragma unroll
+  for (int t = 0; t < KT; ++t) asm("" : "+v"(st[t]));   // landed too: no wait for it in the loop
+  offsets(C - 1);
+
+  for (int64_t c = c_last; c >= 0; --c) {
+    const int half = (int)(c_last - c) & 1;
+    const bf16* const l = lds + half * L::elems;
+    if (c > 0) {
+      kp -= C * a.k_stride;
+      qp -= C * a.q_stride;
+      yp -= C * y_row;
+      xp -= 3 * kTriFrags * kFrag;
+      pp -= 3 * kTriFrags * kFrag;
+      gp -= kGates;
+    } else if (c == c_last) {
+      offsets((int)a.T - 1);   // the only chunk again
+    }
+    request(lds0 + (uint32_t)(half ^ 1) * (2 * L::elems));
+    const float whole = a.whole[at - c_last + c];
+    const float* const gate = reinterpret_cast<const float*>(l + L::gate) + 4 * q;
+    auto gates = [&](int which, int i) { return *reinterpret_cast<const f32x4*>(gate + which + 16 * i); };
+    if (!idle) {
+#pragma unroll
+      for (int t = 0; t < KT; ++t) *reinterpret_cast<f32x4*>(state_at + key_of(t, 0)) = st[t];
+      state_at -= cols * KP;
+    }
+    // dW
+    f32x4 ke[4], dw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ke[i] = dw[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      Frag<1> rows[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rows[i] = load_planes<1>(l + L::k + row_at[s] + 16 * i * KP, 0);
+      mma_tiles(rows, right_of<3>(st[2 * s], st[2 * s + 1]), ke);
+    }
+    Frag<1> dy[2];
+    Frag<3> rf[2], gf[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      dy[s] = read_tr2(l + L::y + (32 * s + 4 * q + (j >> 2)) * W + 16 * w + 4 * (j & 3), 16 * W);
+    mma_upper<3>(l + L::p + lane * 8, dy, dw);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 ge = gates(kEnd, i);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) dw[i][r] = fmaf(ge[r], ke[i][r], dw[i][r]);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) rf[s] = right_of<3>(dw[2 * s], dw[2 * s + 1]);
+    // dR
+    f32x4 dr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dr[i] = f32x4{0, 0, 0, 0};
+    mma_upper<3>(l + L::x + lane * 8, rf, dr);
+    if (!idle) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4*>(right_at + 16 * i) = dr[i];
+      right_at -= cols * C;
+    }
+    // the gradient of the state that enters the chunk
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      rf[s] = right_of<3>(-gates(kRight, 2 * s) * dr[2 * s], -gates(kRight, 2 * s + 1) * dr[2 * s + 1]);
+      f32x4 lo = gates(kOut, 2 * s), hi = gates(kOut, 2 * s + 1);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        lo[r] *= (float)dy[s].p[0][r];
+        hi[r] *= (float)dy[s].p[0][4 + r];
+      }
+      gf[s] = right_of<3>(lo, hi);
+    }
+#pragma unroll
+    for (int t0 = 0; t0 < KT; t0 += 4) {
+      f32x4 acc[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        Frag<1> cols4[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          cols4[t] = Keys::columns(l + L::q + col_at[(t0 + t) / 2] + 4 * (t & 1) + 32 * s * KP);
+        mma_tiles(cols4, gf[s], acc);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          cols4[t] = Keys::columns(l + L::k + col_at[(t0 + t) / 2] + 4 * (t & 1) + 32 * s * KP);
+        mma_tiles(cols4, rf[s], acc);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) st[t0 + t][r] = fmaf(whole, st[t0 + t][r], acc[t][r]);
+    }
+    if (idle) landed<0>();
+    else landed<4>();   // dR may be on its way
+  }
+  if (a.dh0 && col_in) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const int key = key_of(t, 4 * q);
+      if (key < a.N) *reinterpret_cast<f32x4*>(a.dh0 + (bh * a.P + col) * a.N + key) = st[t];
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no request may reach LDS after this
 }
 
 // ---------------------------------------------------------------------------
@@ -192,7 +423,10 @@ __global__ __launch_bounds__(kThreads) void k_delta_back_chain(DeltaArgs a) {
 constexpr int kSlice = 32;
 
 template <typename IO, int KP> struct GradsLds {
-  static constexpr int PI = Planes<IO>::in, KST = KP + 8;
+  static constexpr int PI = Planes<IO>::in;
+  // rows 8 words past a multiple of 64: the four rows of a transposed read take
+  // different banks (float32 keys of 128: 4 words, or the tiles would not fit)
+  static constexpr int KST = KP + (PI == 3 && KP == 128 ? 8 : 16);
   static constexpr int tok = 3 * kSlice * kTokStride, key = 3 * kSlice * KST;  // staged slices
   static constexpr int rows = PI * C * KST, pairs = 3 * C * kTokStride;        // k, q and the pairs
   static constexpr int first = 2 * tok + 2 * key, second = 2 * rows + 2 * pairs;
@@ -212,13 +446,13 @@ __device__ __forceinline__ float sum16(float v) {
   return v;
 }
 
-template <typename IO, int KP>
+template <typename IO, int KP, bool FULL>
 __global__ __launch_bounds__(kThreads) void k_delta_grads(DeltaArgs a) {
   using L = GradsLds<IO, KP>;
   constexpr int PI = L::PI, KST = L::KST, KT = KP / 16;
   __shared__ __align__(16) bf16 lds[L::elems];
-  __shared__ float4 s_gate[C], s_row[C];
-  __shared__ float s_cum[C], s_beta[C], s_sum[2 * kThreads / 64];
+  __shared__ float4 s_row[C];
+  __shared__ float s_b[C], s_cum[C], s_beta[C], s_sum[2 * kThreads / 64];
   bf16 *s_w = lds, *s_d = lds + L::tok, *s_s = lds + 2 * L::tok, *s_e = s_s + L::key;
   bf16 *s_k = lds, *s_q = lds + L::rows, *s_p = lds + 2 * L::rows, *s_l = s_p + L::pairs;
 
@@ -226,9 +460,9 @@ __global__ __launch_bounds__(kThreads) void k_delta_grads(DeltaArgs a) {
   const int64_t h = id % a.H, c = id / a.H % a.Nc, b = id / a.H / a.Nc;
   const int64_t g = h / (a.H / a.G), bh = b * a.H + h, at = chunk_at(a, bh, c);
   const int64_t t0 = c * C, row0 = b * a.T + t0, left = a.T - t0;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, j = lane & 15, q = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_of(tid), j = lane & 15, q = lane >> 4;
   if (tid < C) {
-    s_gate[tid] = a.gate[at * C + tid];
+    s_b[tid] = a.gate[at * kGates + kBeta + tid];
     s_row[tid] = a.row[at * C + tid];
   }
 
@@ -239,6 +473,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_grads(DeltaArgs a) {
   for (int i = 0; i < KT; ++i) dq[i] = z[i] = x[i] = f32x4{0, 0, 0, 0};
   const bool row_in = 16 * w + j < left;
   const int64_t my_row = row0 + (row_in ? 16 * w + j : 0);
+  const int64_t cols = padded_cols(a.P);
   float es = 0.0f, dr_v = 0.0f;
 
   for (int p0 = 0; p0 < a.P; p0 += kSlice) {
@@ -247,7 +482,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_grads(DeltaArgs a) {
     for (int i = 0; i < kSlice * C / 4 / kThreads; ++i) {
       const int at4 = tid + i * kThreads, p = at4 / (C / 4), t = at4 % (C / 4) * 4;
       const bool in = p0 + p < a.P;
-      const int64_t o = (at * a.P + (in ? p0 + p : 0)) * C + t;
+      const int64_t o = (at * cols + (in ? p0 + p : 0)) * C + t;
       f32x4 vw = *reinterpret_cast<const f32x4*>(a.write + o), vd = *reinterpret_cast<const f32x4*>(a.dright + o);
       if (!in) vw = vd = f32x4{0, 0, 0, 0};
       store_split4<3>(&s_w[p * kTokStride + t], kSlice * kTokStride, vw);
@@ -257,7 +492,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_grads(DeltaArgs a) {
     for (int i = 0; i < kSlice * KP / 4 / kThreads; ++i) {
       const int at4 = tid + i * kThreads, p = at4 / (KP / 4), key = at4 % (KP / 4) * 4;
       const bool in = p0 + p < a.P && key < a.N;
-      const int64_t o = (at * a.P + (in ? p0 + p : 0)) * a.N + (in ? key : 0);
+      const int64_t o = (at * cols + (in ? p0 + p : 0)) * KP + (in ? key : 0);
       f32x4 vs = *reinterpret_cast<const f32x4*>(a.enter + o), ve = *reinterpret_cast<const f32x4*>(a.leave + o);
       if (!in) vs = ve = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -273,7 +508,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_grads(DeltaArgs a) {
     const auto drf = load_planes_tr<3>(s_d, kSlice * kTokStride, kTokStride, 0, 16 * w, lane);
     const auto wf = load_planes_tr<3>(s_w, kSlice * kTokStride, kTokStride, 0, 16 * w, lane);
     {
-      const float beta = s_gate[16 * w + j].x;
+      const float beta = s_b[16 * w + j];
       IO out[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -312,17 +547,21 @@ __global__ __launch_bounds__(kThreads) void k_delta_grads(DeltaArgs a) {
   __syncthreads();
 
   {
-    Frag<PI> kf[KP / 32], qf[KP / 32];
-    load_rows<IO, KP>(kf, static_cast<const IO*>(a.k) + g * a.N, a.k_stride, row0, left, a.N, 16 * w + j, q);
-    load_rows<IO, KP>(qf, static_cast<const IO*>(a.q) + g * a.N, a.q_stride, row0, left, a.N, 16 * w + j, q);
+    const int64_t row = row0 + (row_in ? 16 * w + j : left - 1), at = g * a.N + 8 * q;
+    KeyRow<IO, KP, FULL> kr, qr;
+    kr.load(static_cast<const IO*>(a.k) + row * a.k_stride + at, a.N, q);
+    qr.load(static_cast<const IO*>(a.q) + row * a.q_stride + at, a.N, q);
 #pragma unroll
-    for (int s = 0; s < KP / 32; ++s)
+    for (int s = 0; s < KP / 32; ++s) {
+      const auto kf = kr.frag(s, a.N, q);
+      const auto qf = qr.frag(s, a.N, q);
 #pragma unroll
       for (int i = 0; i < PI; ++i) {
         const int o = i * C * KST + (16 * w + j) * KST + 32 * s + 8 * q;
-        *reinterpret_cast<bf16x8*>(&s_k[o]) = kf[s].p[i];
-        *reinterpret_cast<bf16x8*>(&s_q[o]) = qf[s].p[i];
+        *reinterpret_cast<bf16x8*>(&s_k[o]) = kf.p[i];
+        *reinterpret_cast<bf16x8*>(&s_q[o]) = qf.p[i];
       }
+    }
   }
   // the pairs (i, j) of this wavefront's tokens i, over their decay, stored
   // [j][i]; times 1/|k_j| for the sums over j
@@ -385,7 +624,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_grads(DeltaArgs a) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       vp[r] = dp[jt][r] * rec[r].y;
-      vl[r] = -dl[jt][r] * s_gate[16 * w + 4 * q + r].x * rec[r].x;
+      vl[r] = -dl[jt][r] * s_b[16 * w + 4 * q + r] * rec[r].x;
     }
     store_split4<3>(&s_p[cj * kTokStride + 16 * w + 4 * q], C * kTokStride, vp);
     store_split4<3>(&s_l[cj * kTokStride + 16 * w + 4 * q], C * kTokStride, vl);
@@ -408,7 +647,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_grads(DeltaArgs a) {
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int ri = 16 * w + 4 * q + r;
-    const float beta = s_gate[ri].x;
+    const float beta = s_b[ri];
     float kz = 0.0f, kx = 0.0f, qd = 0.0f;
     float* pq = a.part_q + ((row0 + ri) * a.H + h) * a.N;
     float* pk = a.part_k + ((row0 + ri) * a.H + h) * a.N;
@@ -463,7 +702,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_grads(DeltaArgs a) {
   const float ddt = in ? dg * slope : 0.0f;
   const float sum_a = wave_sum64(in ? dg * rate : 0.0f), sum_b = wave_sum64(ddt);
   if (in) {
-    const float beta = s_gate[lane].x;
+    const float beta = s_b[lane];
     a.ddt[th] = ddt;
     a.dbeta[th] = s_beta[lane] * (a.sigmoid ? beta * (1.0f - beta) : 1.0f);
   }
@@ -546,17 +785,31 @@ __global__ __launch_bounds__(kThreads) void k_delta_head_grads(DeltaArgs a) {
   }
 }
 
-template <typename IO, int KP>
-hipError_t launch_grads(const DeltaArgs& a, hipStream_t stream) {
-  const unsigned chunks = (unsigned)(a.Bt * a.H * a.Nc), chains = (unsigned)(a.Bt * a.H * ((a.P + 15) / 16));
-  hipLaunchKernelGGL((k_delta_back_chain<IO, KP, 1>), dim3(chains), dim3(kThreads), 0, stream, a);
-  hipLaunchKernelGGL((k_delta_grads<IO, KP>), dim3(chunks), dim3(kThreads), 0, stream, a);
-  constexpr int per = kThreads / (KP / 4);
-  const int64_t rows = 2 * a.Bt * a.T * a.G;
-  hipLaunchKernelGGL((k_delta_unit_grads<IO, KP / 4>), dim3((unsigned)((rows + per - 1) / per)), dim3(kThreads), 0,
-                     stream, a);
-  hipLaunchKernelGGL(k_delta_head_grads, dim3((unsigned)a.H), dim3(kThreads), 0, stream, a);
-  return hipGetLastError();
+hipError_t launch_grads(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
+  return with_keys(a.N, io_bf16, [&](auto io, auto kp, auto full) {
+    using IO = decltype(io);
+    constexpr int KP = decltype(kp)::value;
+    constexpr bool FULL = decltype(full)::value;
+    const unsigned chunks = (unsigned)(a.Bt * a.H * a.Nc);
+    const int64_t heads = a.Bt * a.H;
+    if constexpr (sizeof(IO) == 2) {
+      columns_of(a, [&](auto nw) {
+        constexpr int NW = decltype(nw)::value;
+        hipLaunchKernelGGL((k_delta_back_columns<KP, FULL, NW>),
+                           dim3((unsigned)(heads * ((a.P + 16 * NW - 1) / (16 * NW)))), dim3(64 * NW), 0, stream, a);
+      });
+    } else {
+      hipLaunchKernelGGL((k_delta_back_chain<IO, KP, FULL, 1>), dim3((unsigned)(heads * ((a.P + 15) / 16))),
+                         dim3(kThreads), 0, stream, a);
+    }
+    hipLaunchKernelGGL((k_delta_grads<IO, KP, FULL>), dim3(chunks), dim3(kThreads), 0, stream, a);
+    constexpr int per = kThreads / (KP / 4);
+    const int64_t rows = 2 * a.Bt * a.T * a.G;
+    hipLaunchKernelGGL((k_delta_unit_grads<IO, KP / 4>), dim3((unsigned)((rows + per - 1) / per)), dim3(kThreads),
+                       0, stream, a);
+    hipLaunchKernelGGL(k_delta_head_grads, dim3((unsigned)a.H), dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace
@@ -564,11 +817,7 @@ hipError_t launch_grads(const DeltaArgs& a, hipStream_t stream) {
 
 hipError_t launch_delta_scan_backward(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
   const hipError_t e = launch_delta_states(a, io_bf16, stream);
-  if (e != hipSuccess) return e;
-  using namespace delta;
-  if (a.N <= 64)
-    return io_bf16 ? launch_grads<bf16, 64>(a, stream) : launch_grads<float, 64>(a, stream);
-  return io_bf16 ? launch_grads<bf16, 128>(a, stream) : launch_grads<float, 128>(a, stream);
+  return e != hipSuccess ? e : delta::launch_grads(a, io_bf16, stream);
 }
 
 }  // namespace ssd

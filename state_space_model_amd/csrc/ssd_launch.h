@@ -208,19 +208,20 @@ struct DeltaArgs {
   void* y;                  // [Bt,T,H,P] io
   float* state;             // the scan's final state [Bt,H,P,N] or null; the step's, in place
   // workspace, per (b, h, chunk)
-  float4* gate;             // [C] factors of a token's rows (ssd_delta.hip)
+  float* gate;              // [4,C] factors of the tokens' rows (ssd_delta.hip)
   float* whole;             // decay over the chunk
   __bf16* inv;              // (1 + L)^-1, fragments of three planes
   __bf16* qk;               // decayed q k^T, fragments (the gradients: of its transpose, three planes)
-  // the gradients
+  void* park;               // [64] float: stores of tokens past the end go here, nothing reads it
+  // the gradients (P16: P rounded up to 16; KP: N rounded up to 64)
   const void* dy;           // [Bt,T,H,P] io
   const float* dfinal;      // [Bt,H,P,N] or null
   float4* row;              // [C] 1/|k|, scale/|q| and the decay sum of a token, in two parts
   __bf16* inv_t;            // transposed inverse, fragments of three planes
-  float* enter;             // [P,N] state entering the chunk
-  float* leave;             // [P,N] gradient of the state leaving it
-  float* write;             // [P,C] the chunk's writes, transposed
-  float* dright;            // [P,C] gradient of the right sides, transposed
+  float* enter;             // [P16,KP] state entering the chunk
+  float* leave;             // [P16,KP] gradient of the state leaving it
+  float* write;             // [P16,C] the chunk's writes, transposed
+  float* dright;            // [P16,C] gradient of the right sides, transposed
   float *part_q, *part_k;   // [Bt,T,H,N] gradients of unit q and k per head
   float* part_h;            // [2] the chunk's parts of dA and ddt_bias
   void *dq, *dk, *dv;       // io

@@ -222,7 +222,7 @@ def test_far_offsets():
     need_gpu()
     import state_space_model_amd as ssd
     announce("delta far offsets")
-    T, stride = 70, 1 << 25          # 70 x 2^25 bfloat16 = 4.7 GB
+    T, stride = 140, 1 << 24         # 140 x 2^24 bfloat16 = 4.7 GB
     base = torch.empty((T - 1) * stride + 256, dtype=BF16, device="cuda")
     x, _ = make(15, 1, T, 1, 1, 16, 16, io=BF16, h0=False)
     d = {n: None if t is None else t.cuda() for n, t in x.items()}
