@@ -23,6 +23,8 @@
  *                   residual add with the norm before a block, the gated norm
  *                   after its scan, the block's projections in 8-bit
  *                   integers, and the gradients of its convolution.
+ *   ssd_dropout_add_norm (and its gradients)
+ *                   the residual add with dropout of the block's output.
  *   ssd_delta_scan, ssd_delta_step, ssd_delta_scan_backward
  *                   the gated delta rule, a mixer with the scan's decay and
  *                   fixed-size state: over a sequence, for one token, and the
@@ -481,6 +483,56 @@ ssd_status ssd_add_norm_backward(const ssd_add_norm_desc* desc, const float* res
                                  const float* weight, const void* dy, const float* dresidual_out,
                                  void* dx, float* dresidual, float* dweight, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream);
+
+/* Problem description of the residual add with dropout, and norm. */
+typedef struct {
+  int64_t rows;      /* as ssd_add_norm_desc */
+  int64_t cols;
+  int32_t io_dtype;
+  float scale;
+  float eps;
+  double p;          /* share of x that is dropped, 0 <= p < 1 */
+} ssd_dropout_add_norm_desc;
+
+/*
+ * ssd_add_norm with dropout of x, as a training step adds a block's output to
+ * the residual stream.  Per row:
+ *
+ *   r' = residual + s / (1 - p) * x  where element (row, c) is kept, residual elsewhere
+ *   y  = r' / sqrt(mean(r'^2) + eps) * weight
+ *
+ * The mask is never stored: element (row, c) is kept where word c % 4 of
+ * Philox4x32-10 (Salmon, Moraes, Dror and Shaw, 2011) with the counter words
+ * (c / 4, row, low and high half of offset) and the key (low and high half of
+ * seed) is at least p * 2^32, rounded.  It depends on the element's place
+ * alone, not on the tensor's layout or the launch.
+ *
+ *   rng [2] int64 in device memory, 8-byte aligned: seed and offset, read when
+ *   the kernel runs and not changed.  A program advances the offset between
+ *   calls (in a captured graph: by a kernel of its own) and hands the gradients
+ *   the values that the forward pass had.
+ *
+ * A dropped value reaches nothing, whatever it is.  The rest as ssd_add_norm;
+ * with p = 0 the bits are those of ssd_add_norm.
+ */
+ssd_status ssd_dropout_add_norm(const ssd_dropout_add_norm_desc* desc, const void* x,
+                                const float* residual, const float* weight, const int64_t* rng,
+                                void* y, float* residual_out, hipStream_t stream);
+
+/*
+ * Gradients of ssd_dropout_add_norm: those of ssd_add_norm, with
+ *
+ *   dx = s / (1 - p) * dresidual where (row, c) is kept, 0 elsewhere
+ *
+ * the mask formed again from the same rng.
+ */
+size_t ssd_dropout_add_norm_backward_workspace_bytes(const ssd_dropout_add_norm_desc* desc);
+ssd_status ssd_dropout_add_norm_backward(const ssd_dropout_add_norm_desc* desc,
+                                         const float* residual_out, const float* weight,
+                                         const void* dy, const float* dresidual_out,
+                                         const int64_t* rng, void* dx, float* dresidual,
+                                         float* dweight, void* workspace, size_t workspace_bytes,
+                                         hipStream_t stream);
 
 /* Problem description of the gated norm after the scan. */
 typedef struct {

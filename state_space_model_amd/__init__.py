@@ -14,10 +14,12 @@ csrc/ssd_torch.cpp): a token's calls are bound by the host.
 and, for the rest of a block between two scans,
 
   ssd_add_norm(x, weight, residual=None, ...)   -> (y, residual_out)   residual add + RMS norm
+  ssd_dropout_add_norm(x, weight, residual, p=, rng=, ...) -> (y, residual_out)   the same with dropout of x
   ssd_gated_norm(y, z, weight, ...)             -> out                 gated RMS norm
   ssd_add_norm_q8, ssd_gated_norm_q8, ssd_quantize_q8 -> (q, qscale, ...)  8-bit rows
   ssd_linear_q8(q, qscale, wq, wscale)          -> out                 product of 8-bit rows
-  ssd_add_norm_backward, ssd_gated_norm_backward, ssd_conv1d_backward -> dict of gradients
+  ssd_add_norm_backward, ssd_dropout_add_norm_backward, ssd_gated_norm_backward,
+  ssd_conv1d_backward                           -> dict of gradients
 
 and the gated delta rule, a mixer with the scan's decay and fixed-size state,
 
@@ -64,6 +66,8 @@ EXPORTED = ("ssd_chunk_scan", "ssd_chunk_scan_timed", "ssd_chunk_scan_workspace_
             "ssd_add_norm_backward_workspace_bytes", "ssd_gated_norm", "ssd_gated_norm_q8",
             "ssd_gated_norm_backward", "ssd_gated_norm_backward_workspace_bytes",
             "ssd_quantize_q8", "ssd_linear_q8",
+            "ssd_dropout_add_norm", "ssd_dropout_add_norm_backward",
+            "ssd_dropout_add_norm_backward_workspace_bytes",
             "ssd_delta_scan", "ssd_delta_scan_workspace_bytes", "ssd_delta_step",
             "ssd_delta_scan_backward", "ssd_delta_scan_backward_workspace_bytes",
             "ssd_status_string", "ssd_abi_version")
@@ -95,6 +99,10 @@ class ConvDesc(ctypes.Structure):
 class AddNormDesc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class DropoutAddNormDesc(ctypes.Structure):
+    _fields_ = AddNormDesc._fields_ + [("p", ctypes.c_double)]
 
 
 class GatedNormDesc(ctypes.Structure):
@@ -163,6 +171,11 @@ def _load() -> ctypes.CDLL:
     L.ssd_add_norm_q8.argtypes = [ctypes.POINTER(AddNormDesc)] + [vp] * 6 + [vp]
     L.ssd_add_norm_backward.restype = i32
     L.ssd_add_norm_backward.argtypes = [ctypes.POINTER(AddNormDesc)] + [vp] * 8 + [sz, vp]
+    L.ssd_dropout_add_norm.restype = i32
+    L.ssd_dropout_add_norm.argtypes = [ctypes.POINTER(DropoutAddNormDesc)] + [vp] * 6 + [vp]
+    L.ssd_dropout_add_norm_backward.restype = i32
+    L.ssd_dropout_add_norm_backward.argtypes = ([ctypes.POINTER(DropoutAddNormDesc)] + [vp] * 9
+                                                + [sz, vp])
     L.ssd_gated_norm.restype = i32
     L.ssd_gated_norm.argtypes = [ctypes.POINTER(GatedNormDesc)] + [vp] * 4 + [vp]
     L.ssd_gated_norm_q8.restype = i32
@@ -170,6 +183,7 @@ def _load() -> ctypes.CDLL:
     L.ssd_gated_norm_backward.restype = i32
     L.ssd_gated_norm_backward.argtypes = [ctypes.POINTER(GatedNormDesc)] + [vp] * 8 + [sz, vp]
     for name, desc in (("ssd_conv1d_backward", ConvDesc), ("ssd_add_norm_backward", AddNormDesc),
+                       ("ssd_dropout_add_norm_backward", DropoutAddNormDesc),
                        ("ssd_gated_norm_backward", GatedNormDesc)):
         query = getattr(L, name + "_workspace_bytes")
         query.restype = sz
@@ -636,6 +650,33 @@ def ssd_add_norm_backward(residual_out: torch.Tensor, weight: torch.Tensor, *, d
     [D] float32.  grads["dresidual"] may be dresidual_out itself."""
     return _calls.add_norm_backward(residual_out, weight, dy, dresidual_out, scale, eps,
                                     workspace, grads)
+
+
+def ssd_dropout_add_norm(x: torch.Tensor, weight: torch.Tensor,
+                         residual: Optional[torch.Tensor] = None, *, p: float, rng: torch.Tensor,
+                         scale: float = 1.0, eps: float = 1e-5, y: Optional[torch.Tensor] = None,
+                         residual_out: Optional[torch.Tensor] = None
+                         ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """ssd_add_norm with dropout of x: residual_out = residual + scale / (1 - p) * x
+    where an element is kept, residual elsewhere.
+
+    0 <= p < 1; rng [2] int64 on the device: seed and offset of a counter-based
+    generator (Philox4x32-10, see include/ssd.h), read and left as they are.  The
+    mask depends on them and on an element's row and column alone and is not
+    stored: advance the offset between calls, and give
+    ssd_dropout_add_norm_backward the values that this call had."""
+    return _calls.dropout_add_norm(x, weight, residual, p, rng, scale, eps, y, residual_out)
+
+
+def ssd_dropout_add_norm_backward(residual_out: torch.Tensor, weight: torch.Tensor, *,
+                                  dy: torch.Tensor, p: float, rng: torch.Tensor,
+                                  dresidual_out: Optional[torch.Tensor] = None, scale: float = 1.0,
+                                  eps: float = 1e-5, workspace: Optional[torch.Tensor] = None,
+                                  grads: Optional[dict] = None) -> dict:
+    """Gradients of ssd_dropout_add_norm, as ssd_add_norm_backward's, with dx =
+    scale / (1 - p) * dresidual where an element was kept, 0 elsewhere."""
+    return _calls.dropout_add_norm_backward(residual_out, weight, dy, dresidual_out, p, rng, scale,
+                                            eps, workspace, grads)
 
 
 def ssd_gated_norm(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *, groups: int = 1,

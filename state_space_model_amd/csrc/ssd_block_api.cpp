@@ -71,14 +71,34 @@ ssd_status check_gated_norm(const ssd_gated_norm_desc* d, bool backward, int64_t
   return SSD_OK;
 }
 
+// The dropout of an add norm: what multiplies a kept value, and the generator's
+// words that drop one.
+struct Dropout {
+  const int64_t* rng = nullptr;
+  float scale = 1.0f;
+  uint32_t drop = 0;
+};
+ssd_status check_dropout(const ssd_dropout_add_norm_desc* d, ssd_add_norm_desc* plain, Dropout* drop) {
+  if (!d) return SSD_ERR_INVALID_ARG;
+  *plain = {d->rows, d->cols, d->io_dtype, d->scale, d->eps};
+  if (!(d->p >= 0.0 && d->p < 1.0)) return SSD_ERR_INVALID_ARG;
+  drop->scale = (float)((double)d->scale / (1.0 - d->p));
+  // p in units of 2^-32, below 1
+  const double words = rint(d->p * 4294967296.0);
+  drop->drop = words < 4294967295.0 ? (uint32_t)words : 4294967295u;
+  return SSD_OK;
+}
+
 ssd_status add_norm(const ssd_add_norm_desc* d, const void* x, const float* residual,
                     const float* weight, void* y, int8_t* q, float* qscale, float* residual_out,
-                    bool q8, hipStream_t stream) {
+                    bool q8, hipStream_t stream, const Dropout* drop = nullptr) {
   int64_t n = 0;
   const ssd_status st = check_add_norm(d, &n);
   if (st != SSD_OK) return st;
   if (d->rows == 0) return SSD_OK;
-  if (!x || !weight || (q8 ? (!q || !qscale) : !y)) return SSD_ERR_INVALID_ARG;
+  if (!x || !weight || (q8 ? (!q || !qscale) : !y) || (drop && !drop->rng)) return SSD_ERR_INVALID_ARG;
+  if (drop && (!aligned_to(drop->rng, 8) || !isfinite(drop->scale)))
+    return isfinite(drop->scale) ? SSD_ERR_ALIGNMENT : SSD_ERR_INVALID_ARG;
   const size_t es = io_size(d->io_dtype);
   if (!aligned_to(x, es) || !aligned_to(y, es) || !aligned4(residual) || !aligned4(weight) ||
       !aligned4(residual_out) || !aligned4(qscale) || !aligned16(q))
@@ -89,7 +109,7 @@ ssd_status add_norm(const ssd_add_norm_desc* d, const void* x, const float* resi
   const Range outs[] = {range_of(y, n * (int64_t)es), range_of(q, q8 ? d->rows * Dp : 0),
                         range_of(qscale, d->rows * 4), range_of(residual_out, n * 4)};
   const Range ins[] = {range_of(x, n * (int64_t)es), range_of(weight, d->cols * 4),
-                       in_place ? Range{0, 0} : r_res};
+                       in_place ? Range{0, 0} : r_res, range_of(drop ? drop->rng : nullptr, 16)};
   if (!outputs_clear(outs, ins)) return SSD_ERR_INVALID_ARG;
 
   AddNormArgs a = {};
@@ -97,8 +117,14 @@ ssd_status add_norm(const ssd_add_norm_desc* d, const void* x, const float* resi
   a.residual_out = residual_out;
   a.R = d->rows; a.D = (int32_t)d->cols; a.Dp = (int32_t)Dp;
   a.scale = d->scale; a.eps = d->eps;
+  if (drop) { a.rng = drop->rng; a.scale = drop->scale; a.drop = drop->drop; }
   return status_of(launch_add_norm(a, d->io_dtype == SSD_BF16, stream));
 }
+
+ssd_status add_norm_backward(const ssd_add_norm_desc* d, const float* residual_out,
+                             const float* weight, const void* dy, const float* dresidual_out,
+                             void* dx, float* dresidual, float* dweight, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream, const Dropout* drop);
 
 ssd_status gated_norm(const ssd_gated_norm_desc* d, const void* y, const void* z,
                       const float* weight, void* out, int8_t* q, float* qscale, bool q8,
@@ -154,11 +180,57 @@ ssd_status ssd_add_norm_backward(const ssd_add_norm_desc* d, const float* residu
                                  const float* weight, const void* dy, const float* dresidual_out,
                                  void* dx, float* dresidual, float* dweight, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream) {
+  return add_norm_backward(d, residual_out, weight, dy, dresidual_out, dx, dresidual, dweight,
+                           workspace, workspace_bytes, stream, nullptr);
+}
+
+ssd_status ssd_dropout_add_norm(const ssd_dropout_add_norm_desc* d, const void* x,
+                                const float* residual, const float* weight, const int64_t* rng,
+                                void* y, float* residual_out, hipStream_t stream) {
+  ssd_add_norm_desc plain;
+  Dropout drop;
+  const ssd_status st = check_dropout(d, &plain, &drop);
+  if (st != SSD_OK) return st;
+  drop.rng = rng;
+  return add_norm(&plain, x, residual, weight, y, nullptr, nullptr, residual_out, false, stream, &drop);
+}
+
+size_t ssd_dropout_add_norm_backward_workspace_bytes(const ssd_dropout_add_norm_desc* d) {
+  ssd_add_norm_desc plain;
+  Dropout drop;
+  return check_dropout(d, &plain, &drop) == SSD_OK ? ssd_add_norm_backward_workspace_bytes(&plain) : 0;
+}
+
+ssd_status ssd_dropout_add_norm_backward(const ssd_dropout_add_norm_desc* d,
+                                         const float* residual_out, const float* weight,
+                                         const void* dy, const float* dresidual_out,
+                                         const int64_t* rng, void* dx, float* dresidual,
+                                         float* dweight, void* workspace, size_t workspace_bytes,
+                                         hipStream_t stream) {
+  ssd_add_norm_desc plain;
+  Dropout drop;
+  const ssd_status st = check_dropout(d, &plain, &drop);
+  if (st != SSD_OK) return st;
+  drop.rng = rng;
+  return add_norm_backward(&plain, residual_out, weight, dy, dresidual_out, dx, dresidual, dweight,
+                           workspace, workspace_bytes, stream, &drop);
+}
+
+}  // extern "C"
+
+namespace {
+
+ssd_status add_norm_backward(const ssd_add_norm_desc* d, const float* residual_out,
+                             const float* weight, const void* dy, const float* dresidual_out,
+                             void* dx, float* dresidual, float* dweight, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream, const Dropout* drop) {
   int64_t n = 0;
   const ssd_status st = check_add_norm(d, &n);
   if (st != SSD_OK) return st;
   if (!dweight) return SSD_ERR_INVALID_ARG;
-  if (d->rows > 0 && (!residual_out || !weight || !dy)) return SSD_ERR_INVALID_ARG;
+  if (d->rows > 0 && (!residual_out || !weight || !dy || (drop && !drop->rng))) return SSD_ERR_INVALID_ARG;
+  if (drop && !isfinite(drop->scale)) return SSD_ERR_INVALID_ARG;
+  if (drop && !aligned_to(drop->rng, 8)) return SSD_ERR_ALIGNMENT;
   const size_t es = io_size(d->io_dtype);
   if (!aligned4(residual_out) || !aligned4(weight) || !aligned_to(dy, es) ||
       !aligned4(dresidual_out) || !aligned_to(dx, es) || !aligned4(dresidual) ||
@@ -172,7 +244,8 @@ ssd_status ssd_add_norm_backward(const ssd_add_norm_desc* d, const float* residu
                         range_of(workspace, d->rows > 0 ? (int64_t)need : 0)};
   const Range ins[] = {range_of(residual_out, n * 4), range_of(weight, d->cols * 4),
                        range_of(dy, n * (int64_t)es),
-                       in_place ? Range{0, 0} : range_of(dresidual_out, n * 4)};
+                       in_place ? Range{0, 0} : range_of(dresidual_out, n * 4),
+                       range_of(drop ? drop->rng : nullptr, 16)};
   if (!outputs_clear(outs, ins)) return SSD_ERR_INVALID_ARG;
   if (d->rows == 0)
     return status_of(launch_backward_zero_heads(dweight, nullptr, nullptr, d->cols, stream));
@@ -182,8 +255,13 @@ ssd_status ssd_add_norm_backward(const ssd_add_norm_desc* d, const float* residu
   a.dres_out = dresidual_out; a.dx = dx; a.dres = dresidual; a.dweight = dweight;
   a.part = static_cast<float*>(workspace);
   a.R = d->rows; a.D = (int32_t)d->cols; a.scale = d->scale; a.eps = d->eps;
+  if (drop) { a.rng = drop->rng; a.scale = drop->scale; a.drop = drop->drop; }
   return status_of(launch_add_norm_backward(a, d->io_dtype == SSD_BF16, stream));
 }
+
+}  // namespace
+
+extern "C" {
 
 ssd_status ssd_gated_norm(const ssd_gated_norm_desc* d, const void* y, const void* z,
                           const float* weight, void* out, hipStream_t stream) {

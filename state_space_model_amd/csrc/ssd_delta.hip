@@ -50,16 +50,19 @@ __device__ __forceinline__ float row_squares(const Frag<PI> (&f)[KS]) {
 // GRADS: for the gradients, whose chain from the last chunk needs both matrices
 // transposed and no output.
 template <typename IO, int KP, bool FULL, bool GRADS>
-__global__ __launch_bounds__(kThreads) void k_delta_prep(DeltaArgs a) {
+__global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 4 : 2) void k_delta_prep(DeltaArgs a) {
   constexpr int PI = Planes<IO>::in, PY = Planes<IO>::y;
   constexpr int KS = KP / 32, KST = KP + 8, kDiag = 20;
-  constexpr int k_bytes = PI * C * KST * 2, p_bytes = GRADS ? C * kPairStride * 4 : 0;
-  __shared__ __align__(16) char lds_k[k_bytes > p_bytes ? k_bytes : p_bytes];
-  __shared__ __align__(16) float s_l[C * kPairStride];    // L transposed: [column][row]
+  constexpr int k_bytes = PI * C * KST * 2, l_bytes = (GRADS ? 2 : 1) * C * kPairStride * 4;
+  // the keys, then L transposed ([column][row]), then for GRADS both results: a
+  // workgroup in 24 KB (bfloat16), and six of them to a compute unit hide one
+  // another's chain of dependent steps
+  __shared__ __align__(16) char lds[k_bytes > l_bytes ? k_bytes : l_bytes];
   __shared__ __align__(16) float s_d[4 * 16 * kDiag];     // inverse diagonal blocks, transposed
   __shared__ __align__(16) float s_hi[C], s_lo[C], s_rk[C];
   __shared__ float s_beta[C], s_rq[C];
-  bf16* const s_k = reinterpret_cast<bf16*>(lds_k);
+  bf16* const s_k = reinterpret_cast<bf16*>(lds);
+  float* const s_l = reinterpret_cast<float*>(lds);
 
   const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
   const int64_t h = id % a.H, c = id / a.H % a.Nc, b = id / a.H / a.Nc;
@@ -123,12 +126,12 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(DeltaArgs a) {
 
   // the rows against key tokens up to them: L to LDS, D o Q K^T kept, both
   // transposed: lane (keys 16 jt + 4 q .. + 3, own token)
-  f32x4 p[4];
+  f32x4 p[4], l[4];
   {
     const float hi_own = s_hi[own], lo_own = s_lo[own], l_own = s_beta[own] * rk_own;
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt) {
-      p[jt] = f32x4{0, 0, 0, 0};
+      p[jt] = l[jt] = f32x4{0, 0, 0, 0};
       if (jt > w) continue;
       f32x4 kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0};
 #pragma unroll
@@ -143,7 +146,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(DeltaArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float dec = exp2_of((hi_own - hi[r]) + (lo_own - lo[r])) * rk[r];
-        s_l[(key0 + r) * kPairStride + own] = own > key0 + r ? l_own * dec * kk[r] : 0.0f;
+        l[jt][r] = own > key0 + r ? l_own * dec * kk[r] : 0.0f;
         p[jt][r] = own >= key0 + r ? rq_own * dec * qk[r] : 0.0f;
       }
     }
@@ -153,6 +156,13 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(DeltaArgs a) {
     for (int s = 0; s < 2; ++s)
       if (s <= (w >> 1)) store_frag(a.qk, at, lower_frag(w, s), lane, right_of<PY>(p[2 * s], p[2 * s + 1]));
   }
+
+  __syncthreads();
+#pragma unroll
+  for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (jt <= w) s_l[(16 * jt + 4 * q + r) * kPairStride + own] = l[jt][r];
 
   f32x4 x[4];   // block (w, w - d) of the inverse, transposed
   {
@@ -199,7 +209,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(DeltaArgs a) {
   if constexpr (GRADS) {
     // both again, as rows in LDS and read by columns: row tiles 0 and 1 of the
     // transposed reach over all of them, 2 and 3 over the last 32
-    float* const s_p = reinterpret_cast<float*>(lds_k);
+    float* const s_p = s_l + C * kPairStride;
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < 4; ++t) {

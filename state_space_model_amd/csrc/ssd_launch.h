@@ -140,9 +140,11 @@ struct AddNormArgs {
   float* dres;              // [R,D] or null
   float* dweight;           // [D]
   float* part;              // [parts,D] partial sums of dweight
-  int64_t R;
+  const int64_t* rng;       // [2] seed and offset of the dropout's generator, or null (no dropout)
+  int64_t R, row0;          // row0: number of the first row
   int32_t D, Dp;            // Dp: columns of q
-  float scale, eps;
+  uint32_t drop;            // words below it drop
+  float scale, eps;         // scale: with dropout, over the share that is kept
 };
 
 // The gated norm and its gradients (ssd_norm.hip).

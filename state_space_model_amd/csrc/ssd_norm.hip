@@ -6,6 +6,7 @@
 // residual stream and the norms in float32).
 //
 //   add norm    r' = r + s x;          y   = r' c w,  c = 1/sqrt(mean(r'^2) + eps)
+//               (with dropout: s x / (1 - p) where the generator keeps x, else r)
 //   gated norm  g  = y z / (1+e^-z);   out = g c w,   c per group of columns
 //   8-bit rows  a = max|v|;  q = rint(v 127/a), scale a/127
 //
@@ -45,7 +46,7 @@ constexpr int kCus = 256;
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-template <typename T, int VEC, int NV, bool BLOCK, bool Q8>
+template <typename T, int VEC, int NV, bool BLOCK, bool Q8, bool DROP>
 __global__ __launch_bounds__(BLOCK ? kBlockThreads : kThreads) void k_add_norm(AddNormArgs a) {
   __shared__ float sm[kMaxWaves], smq[kMaxWaves];
   const int team = BLOCK ? blockDim.x : 64;
@@ -73,8 +74,14 @@ __global__ __launch_bounds__(BLOCK ? kBlockThreads : kThreads) void k_add_norm(A
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const fvec<VEC> xf = convert_pack<float, VEC>(xr[k]);
+    if constexpr (DROP) {
+      const uint32_t keep = Philox(a.rng).kept_pack<VEC>(cols.base[k], cols.may_move(k), (uint32_t)(a.row0 + row), a.drop);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) r[k][e] = __fmaf_rn(a.scale, xf[e], r[k][e]);
+      for (int e = 0; e < VEC; ++e) r[k][e] = keep >> e & 1 ? __fmaf_rn(a.scale, xf[e], r[k][e]) : r[k][e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) r[k][e] = __fmaf_rn(a.scale, xf[e], r[k][e]);
+    }
     ss += sum_of<VEC>(cols.own(k, r[k] * r[k]));
   }
   const float c = rsqrtf(team_sum<BLOCK>(ss, sm) / (float)a.D + a.eps);
@@ -285,7 +292,7 @@ __device__ __forceinline__ void store_part(const RowCols<VEC, NV>& cols, fvec<VE
   }
 }
 
-template <typename T, int VEC, int NV, bool BLOCK>
+template <typename T, int VEC, int NV, bool BLOCK, bool DROP>
 __global__ __launch_bounds__(BLOCK ? kBlockThreads : kThreads) void k_add_norm_backward(AddNormArgs a) {
   __shared__ float sm[2][2 * kMaxWaves];
   const int team = BLOCK ? blockDim.x : 64;
@@ -334,9 +341,15 @@ __global__ __launch_bounds__(BLOCK ? kBlockThreads : kThreads) void k_add_norm_b
       dr[k] += c * (d * w[k] - n * m);
       if (cols.kept(k)) {
         if (a.dres) store_pack<VEC>(a.dres + o + cols.base[k], dr[k]);
-        if (a.dx)
-          store_pack<VEC>(reinterpret_cast<T*>(a.dx) + o + cols.base[k],
-                          convert_pack<T, VEC>(a.scale * dr[k]));
+        if (a.dx) {
+          fvec<VEC> dx = a.scale * dr[k];
+          if constexpr (DROP) {
+            const uint32_t keep = Philox(a.rng).kept_pack<VEC>(cols.base[k], cols.may_move(k), (uint32_t)row, a.drop);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) dx[e] = keep >> e & 1 ? dx[e] : 0.0f;
+          }
+          store_pack<VEC>(reinterpret_cast<T*>(a.dx) + o + cols.base[k], convert_pack<T, VEC>(dx));
+        }
       }
     }
   }
@@ -519,9 +532,11 @@ hipError_t add_norm_t(const AddNormArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)row_blocks(t, a.R)), block(t.threads);
   return dispatch<T>(a.D, [&](auto vec, auto nv, auto blk) {
     if (a.q)
-      hipLaunchKernelGGL((k_add_norm<T, vec, nv, blk, true>), grid, block, 0, s, a);
+      hipLaunchKernelGGL((k_add_norm<T, vec, nv, blk, true, false>), grid, block, 0, s, a);
+    else if (a.rng)
+      hipLaunchKernelGGL((k_add_norm<T, vec, nv, blk, false, true>), grid, block, 0, s, a);
     else
-      hipLaunchKernelGGL((k_add_norm<T, vec, nv, blk, false>), grid, block, 0, s, a);
+      hipLaunchKernelGGL((k_add_norm<T, vec, nv, blk, false, false>), grid, block, 0, s, a);
     return hipGetLastError();
   });
 }
@@ -595,6 +610,7 @@ hipError_t launch_add_norm(const AddNormArgs& all, bool io_bf16, hipStream_t s) 
     a.qscale = ahead(a.qscale, r0 * 4);
     a.residual_out = ahead(a.residual_out, e * 4);
     a.R = rows;
+    a.row0 = r0;
     return io_bf16 ? add_norm_t<bf16>(a, s) : add_norm_t<float>(a, s);
   });
 }
@@ -620,8 +636,12 @@ hipError_t launch_add_norm_backward(const AddNormArgs& all, bool io_bf16, hipStr
     using T = decltype(zero);
     const RowTeam t = team_of(a.D, vec_of<T>());
     return dispatch<T>(a.D, [&](auto vec, auto nv, auto blk) {
-      hipLaunchKernelGGL((k_add_norm_backward<T, vec, nv, blk>), dim3((unsigned)parts),
-                         dim3(t.threads), 0, s, a);
+      if (a.rng)
+        hipLaunchKernelGGL((k_add_norm_backward<T, vec, nv, blk, true>), dim3((unsigned)parts),
+                           dim3(t.threads), 0, s, a);
+      else
+        hipLaunchKernelGGL((k_add_norm_backward<T, vec, nv, blk, false>), dim3((unsigned)parts),
+                           dim3(t.threads), 0, s, a);
       return hipGetLastError();
     });
   };

@@ -371,6 +371,71 @@ PyObject* add_norm_backward(PyObject* const* a) {
   return dict({{"dx", &dx}, {"dresidual", &dresidual}, {"dweight", &dweight}});
 }
 
+// seed and offset of the dropout's generator
+const int64_t* generator(const Tensor& rng, const Tensor& first) {
+  shape(&rng, "rng", 2);
+  dense(&rng, "rng", at::kLong, first);
+  return static_cast<const int64_t*>(rng.data_ptr());
+}
+
+// x, weight, residual, p, rng, scale, eps, y, residual_out
+PyObject* dropout_add_norm(PyObject* const* a) {
+  const Tensor &x = tensor(a[0], "x"), &weight = tensor(a[1], "weight"), &rng = tensor(a[4], "rng");
+  const Tensor *residual = maybe(a[2], "residual"), *y_ = maybe(a[7], "y"),
+               *r_ = maybe(a[8], "residual_out");
+  vectors(x, weight, "x [..., D], weight [D]");
+  const int64_t D = x.size(-1);
+  shape(y_, "y", x.sizes());
+  shape(&weight, "weight", D);
+  shape(residual, "residual", x.sizes());
+  shape(r_, "residual_out", x.sizes());
+  const ScalarType io = x.scalar_type();
+  const ssd_dropout_add_norm_desc desc{rows(x), D, io_code(io, "x"), (float)number(a[5]),
+                                       (float)number(a[6]), number(a[3])};
+  dense(&x, "x", io, x);
+  dense(&weight, "weight", at::kFloat, x);
+  dense(residual, "residual", at::kFloat, x);
+  const int64_t* state = generator(rng, x);
+  const Tensor r = output(r_, "residual_out", x.sizes(), at::kFloat, x);
+  const Tensor y = output(y_, "y", x.sizes(), io, x);
+  launch(x, "ssd_dropout_add_norm", [&](hipStream_t stream) {
+    return ssd_dropout_add_norm(&desc, ptr(x), f32(residual), f32(weight), state, ptr(y), f32(r), stream);
+  });
+  return tuple({&y, &r});
+}
+
+// residual_out, weight, dy, dresidual_out, p, rng, scale, eps, workspace, grads
+PyObject* dropout_add_norm_backward(PyObject* const* a) {
+  const Tensor &r = tensor(a[0], "residual_out"), &weight = tensor(a[1], "weight"),
+               &dy = tensor(a[2], "dy"), &rng = tensor(a[5], "rng");
+  const Tensor *dr = maybe(a[3], "dresidual_out"), *w_ = maybe(a[8], "workspace");
+  vectors(r, weight, "residual_out [..., D], weight [D]");
+  const int64_t D = r.size(-1);
+  shape(&weight, "weight", D);
+  shape(&dy, "dy", r.sizes());
+  shape(dr, "dresidual_out", r.sizes());
+  const ScalarType io = dy.scalar_type();
+  const ssd_dropout_add_norm_desc desc{rows(r), D, io_code(io, "dy"), (float)number(a[6]),
+                                       (float)number(a[7]), number(a[4])};
+  const Grads g(a[9], {"dx", "dresidual", "dweight"});
+  const Tensor *dx_ = g.get("dx", r.sizes()), *dr_ = g.get("dresidual", r.sizes()),
+               *dw_ = g.get("dweight", D);
+  dense(&r, "residual_out", at::kFloat, r);
+  dense(&weight, "weight", at::kFloat, r);
+  dense(&dy, "dy", io, r);
+  dense(dr, "dresidual_out", at::kFloat, r);
+  const int64_t* state = generator(rng, r);
+  const Tensor dx = output(dx_, "dx", r.sizes(), io, r);
+  const Tensor dresidual = output(dr_, "dresidual", r.sizes(), at::kFloat, r);
+  const Tensor dweight = output(dw_, "dweight", D, at::kFloat, r);
+  const Tensor ws = workspace(w_, ssd_dropout_add_norm_backward_workspace_bytes(&desc), r);
+  launch(r, "ssd_dropout_add_norm_backward", [&](hipStream_t stream) {
+    return ssd_dropout_add_norm_backward(&desc, f32(r), f32(weight), ptr(dy), f32(dr), state, ptr(dx),
+                                         f32(dresidual), f32(dweight), ptr(ws), ws.nbytes(), stream);
+  });
+  return dict({{"dx", &dx}, {"dresidual", &dresidual}, {"dweight", &dweight}});
+}
+
 ssd_gated_norm_desc gated_desc(const Tensor& y, const Tensor& z, const Tensor& weight,
                                PyObject* groups, PyObject* eps) {
   const ScalarType io = y.scalar_type();
@@ -660,14 +725,12 @@ PyObject* delta_scan_backward(PyObject* const* a) {
   dense(df, "dfinal_state", at::kFloat, in.v);
   dense(h0, "initial_state", at::kFloat, in.v);
   // strided buffers, or new dense ones
-  auto rows = [&](const Tensor* t, const char* name, IntArrayRef sizes, int64_t* stride) {
-    const Tensor r = t ? *t : output(nullptr, name, sizes, in.io, in.v);
-    *stride = token_stride(r, name, in.io, in.v);
-    return r;
-  };
-  const Tensor dq = rows(dq_, "dq", qk, &in.d.dq_stride);
-  const Tensor dk = rows(dk_, "dk", qk, &in.d.dk_stride);
-  const Tensor dv = rows(dv_, "dv", in.yshape, &in.d.dv_stride);
+  in.d.dq_stride = dq_ ? token_stride(*dq_, "dq", in.io, in.v) : in.d.ngroups * in.d.dstate;
+  in.d.dk_stride = dk_ ? token_stride(*dk_, "dk", in.io, in.v) : in.d.ngroups * in.d.dstate;
+  in.d.dv_stride = dv_ ? token_stride(*dv_, "dv", in.io, in.v) : H * in.d.headdim;
+  const Tensor dq = dq_ ? *dq_ : output(nullptr, "dq", qk, in.io, in.v);
+  const Tensor dk = dk_ ? *dk_ : output(nullptr, "dk", qk, in.io, in.v);
+  const Tensor dv = dv_ ? *dv_ : output(nullptr, "dv", in.yshape, in.io, in.v);
   const Tensor ddt = output(dt_, "ddt", gate, at::kFloat, in.v);
   const Tensor dbeta = output(db_, "dbeta", gate, at::kFloat, in.v);
   const Tensor dA = output(dA_, "dA", H, at::kFloat, in.v);
@@ -743,6 +806,8 @@ PyMethodDef methods[] = {
     {"add_norm", FAST((entry<add_norm, 7>)), nullptr},
     {"add_norm_q8", FAST((entry<add_norm_q8, 8>)), nullptr},
     {"add_norm_backward", FAST((entry<add_norm_backward, 8>)), nullptr},
+    {"dropout_add_norm", FAST((entry<dropout_add_norm, 9>)), nullptr},
+    {"dropout_add_norm_backward", FAST((entry<dropout_add_norm_backward, 10>)), nullptr},
     {"gated_norm", FAST((entry<gated_norm, 6>)), nullptr},
     {"gated_norm_q8", FAST((entry<gated_norm_q8, 7>)), nullptr},
     {"gated_norm_backward", FAST((entry<gated_norm_backward, 8>)), nullptr},
