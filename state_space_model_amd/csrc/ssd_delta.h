@@ -70,6 +70,19 @@ __device__ __forceinline__ void mma_tiles(const Frag<NA> (&a)[NT], const Frag<NB
         for (int t = 0; t < NT; ++t) acc[t] = mma(a[t].p[i], b.p[s - i], acc[t]);
 }
 
+// acc[n] += A B[n], likewise
+template <int NT, int NA, int NB>
+__device__ __forceinline__ void mma_across(const Frag<NA>& a, const Frag<NB> (&b)[NT], f32x4 (&acc)[NT]) {
+  constexpr int top = (NA > NB ? NA : NB) - 1;
+#pragma unroll
+  for (int s = top; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[n] = mma(a.p[i], b[n].p[s - i], acc[n]);
+}
+
 // The planes of a pair, plane by plane in one word.  Each is rounded to nearest
 // (v_cvt_pk_bf16_f32), so what the dropped products leave out has no sign of its
 // own; the remainders are exact.  An infinity or a NaN leaves NaN behind.
@@ -358,6 +371,17 @@ __device__ __forceinline__ void request_linear(const void* from, uint32_t to, in
   }
 }
 
+// The same with as many requests from every wavefront: past the N-th KB the ones
+// from the start again, the same bytes to the same place
+template <int N, int NW, int I = 0>
+__device__ __forceinline__ void request_evenly(const void* from, uint32_t to, int w, int lane) {
+  if constexpr (I * NW < N) {
+    const int back = I * NW + NW <= N || w < N - I * NW ? 0 : N * 1024;
+    request16<I * NW * 1024>(static_cast<const char*>(from) + (I * NW * 1024 - back), 16 * lane, to - back);
+    request_evenly<N, NW, I + 1>(from, to, w, lane);
+  }
+}
+
 // Value columns of a chunk in LDS: [C][16 NW], as KeyTile, not permuted
 template <int NW> struct ColumnTile {
   static constexpr int kVecs = 2 * NW, kRows = 64 / kVecs, kLoads = C / kRows / NW;
@@ -411,20 +435,37 @@ __device__ __forceinline__ Frag<NP> right_of(f32x4 a, f32x4 b) {
   return split8<NP>(x);
 }
 
+// `x` has been waited for: the compiler does not see the waits of landed() and
+// would put one of its own before x's first use in a loop, for whatever is in
+// flight there
+__device__ __forceinline__ void pin(f32x4& x) { asm volatile("" : "+v"(x)); }
+
+// A value that the launch before left, the same for the whole wavefront, through
+// the scalar unit: a vector load's wait would be for every request before it too
+__device__ __forceinline__ float load_uniform(const float* p) {
+  return *(const __attribute__((address_space(4))) float*)p;
+}
+
 // Everything but the last STORES memory operations of the wavefront has landed,
 // its LDS reads are done, and every wavefront is here.
 template <int STORES>
 __device__ __forceinline__ void landed() {
+  static_assert(STORES < 64, "the counter's range");
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"(STORES) : "memory");
 }
 
-// f(wavefronts of a workgroup) for a chain of wavefronts that own 16 columns
-template <typename F>
-void columns_of(const DeltaArgs& a, F&& f) {
-  const int64_t waves = a.Bt * a.H * ((a.P + 15) / 16);
-  if (waves <= 256) f(std::integral_constant<int, 1>{});
-  else if (waves <= 512) f(std::integral_constant<int, 2>{});
-  else f(std::integral_constant<int, 4>{});
+// Value columns of a chain whose four wavefronts share them and split the tokens
+// (tokens(NT), 16 NT columns), or a chain of wavefronts that own 16 each
+// (columns()).  A chain fills a compute unit's LDS.  Sharing makes a step as short
+// as it gets and is taken while every chain has a unit to itself; owning needs
+// less than half the work of LDS and VALU for as many columns.
+template <typename F, typename G>
+hipError_t chain_of(const DeltaArgs& a, F&& tokens, G&& columns) {
+  const int64_t groups = a.Bt * a.H * ((a.P + 15) / 16), pairs = a.Bt * a.H * ((a.P + 31) / 32);
+  if (groups <= 256) tokens(std::integral_constant<int, 1>{}, (unsigned)groups);
+  else if (pairs <= 256) tokens(std::integral_constant<int, 2>{}, (unsigned)pairs);
+  else columns((unsigned)(a.Bt * a.H * ((a.P + 63) / 64)));
+  return hipGetLastError();
 }
 
 // Columns and keys that the chains keep of a head in the gradients' workspace:

@@ -573,7 +573,7 @@ __global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
   for (int u = 0; u < KT / 2; ++u) col_at[u] = Keys::col_at(u, j, q);
   landed<0>();
 #pragma unroll
-  for (int t = 0; t < KT; ++t) asm("" : "+v"(st[t]));   // the state has landed too: no wait for it in the loop
+  for (int t = 0; t < KT; ++t) pin(st[t]);
 
   for (int64_t c = 0; c < a.Nc; ++c) {
     const bf16* const l = lds + (c & 1) * L::elems;
@@ -588,7 +588,7 @@ __global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
       if (c + 2 == a.Nc) offsets(c + 1);
     }
     request(lds0 + (uint32_t)(~c & 1) * (2 * L::elems));
-    const float whole = a.whole[at0 + c];
+    const float whole = load_uniform(a.whole + at0 + c);
     const float* const gate = reinterpret_cast<const float*>(l + L::gate) + 4 * q;
     auto gates = [&](int which, int i) { return *reinterpret_cast<const f32x4*>(gate + which + 16 * i); };
     if (KEEP && !idle) {
@@ -695,6 +695,302 @@ __global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// The chunks of one (b, h) in order, bfloat16 io: the four wavefronts of a
+// workgroup share 16 NT value columns, wavefront w the rows of tokens 16 w .. + 15
+// and a quarter of the state's keys.  The state, the right sides and the writes
+// go through LDS as in k_delta_chain; what comes from memory lands in LDS as in
+// k_delta_columns, each operand requested when its last reader is done:
+//   top        q k^T of this chunk; k, gates of the next (two places for each)
+//   barrier 1  q, v of the next            (waits for the inverse)
+//   barrier 2  the next inverse            (waits for q k^T)
+//   barrier 3                              (waits for k, gates, q, v)
+// Every wavefront makes the same requests, so that the counts that the waits
+// leave outstanding are constants.
+// ---------------------------------------------------------------------------
+template <int KP, int NT, bool KEEP> struct TokensLds {
+  using Keys = KeyTile<KP, 4>;
+  static constexpr int KST = KP + 8, W = 16 * NT;
+  static constexpr int k = 0, q = k + 2 * Keys::kElems, x = q + (KEEP ? 0 : Keys::kElems);
+  static constexpr int p = x + 3 * kTriFrags * kFrag, v = p + (KEEP ? 0 : 2 * kTriFrags * kFrag);
+  static constexpr int gate = v + C * W, s = gate + 4 * kGates, r = s + 3 * W * KST;
+  static constexpr int e = r + 3 * W * kTokStride, wr = e + 3 * W * kTokStride;
+  static constexpr int y = wr + (KEEP ? 0 : 2 * W * kTokStride), elems = y + (KEEP ? 0 : C * W);
+};
+
+template <int KP, bool FULL, int NT, bool KEEP>
+__global__ __launch_bounds__(kThreads) void k_delta_tokens(DeltaArgs a) {
+  using L = TokensLds<KP, NT, KEEP>;
+  using Keys = typename L::Keys;
+  constexpr int KS = KP / 32, KST = L::KST, KT = KP / 64, W = L::W;
+  constexpr int kKeyLoads = Keys::kLoads, kXLoads = (3 * kTriFrags + 3) / 4, kPLoads = (2 * kTriFrags + 3) / 4;
+  __shared__ __align__(1024) bf16 lds[L::elems];
+
+  const int slices = (a.P + W - 1) / W;
+  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
+  const int64_t bh = id / slices, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
+  const int col0 = (int)(id % slices) * W;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_of(tid), j = lane & 15, q = lane >> 4;
+  const int64_t at0 = chunk_at(a, bh, 0), cols = padded_cols(a.P);
+
+  // columns that no request reaches stay zero
+  for (int i = tid; i < L::elems / 8; i += kThreads) reinterpret_cast<uint4*>(lds)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  typename Keys::Offsets k_off, q_off;
+  uint32_t v_off;
+  constexpr int v_vecs = 2 * NT, v_rows = 64 / v_vecs, v_kb = C / v_rows;   // 16-byte vectors of a row, KB in all
+  const int v_t = w % v_kb;
+  const bool v_in = col0 + 8 * (lane % v_vecs) < a.P;
+  auto offsets = [&](int64_t c) {
+    const int last = (int)min((int64_t)C, a.T - c * C) - 1;
+    Keys::offsets(k_off, (int)a.k_stride, last, a.N, w, lane);
+    if constexpr (!KEEP) Keys::offsets(q_off, (int)a.q_stride, last, a.N, w, lane);
+    v_off = (uint32_t)min(v_t * v_rows + lane / v_vecs, last) * (uint32_t)a.v_stride * 2u + 16u * (lane % v_vecs);
+  };
+  const uint32_t lds0 = lds_address(lds), mine = lds0 + w * 1024;
+  const bf16* kp = static_cast<const bf16*>(a.k) + b * a.T * a.k_stride + g * a.N;
+  const bf16* qp = static_cast<const bf16*>(a.q) + b * a.T * a.q_stride + g * a.N;
+  const bf16* vp = static_cast<const bf16*>(a.v) + b * a.T * a.v_stride + h * a.P + col0;
+  const bf16* xp = a.inv + at0 * (3 * kTriFrags * kFrag) + w * 512;
+  const bf16* pp = a.qk + at0 * (2 * kTriFrags * kFrag) + w * 512;
+  const float* gp = a.gate + at0 * kGates;
+  const bool all_cols = a.P - col0 >= W;
+  auto request_k = [&](int half) {
+    Keys::template request<FULL>(kp, k_off, mine + 2 * (L::k + half * Keys::kElems));
+    request16(gp, 16 * lane, lds0 + 2 * (L::gate + half * 2 * kGates));
+  };
+  auto request_qv = [&]() {
+    if constexpr (!KEEP) Keys::template request<FULL>(qp, q_off, mine + 2 * L::q);
+    if (all_cols || v_in) request16(vp, v_off, lds0 + 2 * L::v + v_t * 1024);
+  };
+  auto request_x = [&]() { request_evenly<3 * kTriFrags, 4>(xp, mine + 2 * L::x, w, lane); };
+  offsets(0);
+  request_k(0);
+  request_qv();
+  request_x();
+
+  // state tiles: keys key_of(KT w + t, 4 q + r) of value column j of tile n
+  f32x4 st[NT][KT];
+  bool col_in[NT];
+  int key[KT];
+#pragma unroll
+  for (int t = 0; t < KT; ++t) key[t] = key_of(KT * w + t, 4 * q);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    col_in[n] = col0 + 16 * n + j < a.P;
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      st[n][t] = f32x4{0, 0, 0, 0};
+      if (a.h0 && col_in[n] && key[t] < a.N)
+        st[n][t] = *reinterpret_cast<const f32x4*>(a.h0 + (bh * a.P + col0 + 16 * n + j) * a.N + key[t]);
+    }
+  }
+  bf16* const put_s = lds + L::s + j * KST;
+  auto store_s = [&]() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int t = 0; t < KT; ++t) store_split4<3>(put_s + 16 * n * KST + key[t], W * KST, st[n][t]);
+  };
+  store_s();
+  // the workspace has whole tiles of columns; a pair's second may lie past them
+  float *state_at[NT], *write_at[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const bool in = col0 + 16 * n < cols;
+    const int64_t col = at0 * cols + col0 + 16 * n + j;
+    state_at[n] = KEEP && in ? a.enter + col * KP : nullptr;
+    write_at[n] = KEEP && in ? a.write + col * C + 16 * w + 4 * q : nullptr;
+  }
+  float* const park = static_cast<float*>(a.park) + 4 * lane;
+
+  const bf16* const get_s = lds + L::s + j * KST + 8 * q;
+  const int put_t = j * kTokStride + token_slot(w, q), get_t = j * kTokStride + 8 * q;
+  int row_at[KS];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) row_at[s] = Keys::row_at(s, j, q) + 16 * w * KP;
+  int col_at[KT];
+#pragma unroll
+  for (int t = 0; t < KT; ++t) col_at[t] = Keys::col_at((KT * w + t) >> 1, j, q) + 4 * ((KT * w + t) & 1);
+  landed<0>();
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int t = 0; t < KT; ++t) pin(st[n][t]);
+
+  for (int64_t c = 0; c < a.Nc; ++c) {
+    const int half = (int)c & 1;
+    const int64_t left = a.T - c * C;
+    const bf16* const lk = lds + L::k + half * Keys::kElems;
+    const float* const gate = reinterpret_cast<const float*>(lds + L::gate + half * 2 * kGates) + 16 * w + 4 * q;
+    auto gates = [&](int which) { return *reinterpret_cast<const f32x4*>(gate + which); };
+    const float whole = load_uniform(a.whole + at0 + c);
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+          *reinterpret_cast<f32x4*>(state_at[n] ? state_at[n] + key[t] : park) = st[n][t];
+        if (state_at[n]) state_at[n] += cols * KP;
+      }
+    } else {
+      request_evenly<2 * kTriFrags, 4>(pp, mine + 2 * L::p, w, lane);
+      pp += 2 * kTriFrags * kFrag;
+    }
+    // past the last chunk that one again, to where no one reads any more
+    if (c + 1 < a.Nc) {
+      kp += C * a.k_stride;
+      qp += C * a.q_stride;
+      vp += C * a.v_stride;
+      xp += 3 * kTriFrags * kFrag;
+      gp += kGates;
+      if (c + 2 == a.Nc) offsets(c + 1);
+    }
+    request_k(half ^ 1);
+
+    // K S^T and Q S^T of the wavefront's tokens; the right sides
+    f32x4 ks[NT], y[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) ks[n] = y[n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const bf16x8 kf = ld8(lk + row_at[s]);
+      bf16x8 qf;
+      if constexpr (!KEEP) qf = ld8(lds + L::q + row_at[s]);
+      Frag<3> sf[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) sf[n] = load_planes<3>(get_s + 16 * n * KST + 32 * s, W * KST);
+#pragma unroll
+      for (int i = 2; i >= 0; --i) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) ks[n] = mma(kf, sf[n].p[i], ks[n]);
+        if constexpr (!KEEP)
+          if (i < 2)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) y[n] = mma(qf, sf[n].p[i], y[n]);
+      }
+    }
+    {
+      const f32x4 gb = gates(kBeta), gr = gates(kRight), go = gates(kOut);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const bf16x4 v = lds_read_tr4(lds + L::v + (16 * w + 4 * q + (j >> 2)) * W + 16 * n + 4 * (j & 3));
+        f32x4 rs;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) rs[r] = fmaf(-gr[r], ks[n][r], gb[r] * (float)v[r]);
+        y[n] *= go;
+        store_split4<3>(lds + L::r + put_t + 16 * n * kTokStride, W * kTokStride, rs);
+      }
+    }
+    landed<KEEP ? NT * KT + kKeyLoads + 1 : 1 + kPLoads + kKeyLoads + 1>();
+    request_qv();
+    // the writes
+    {
+      const f32x4 ge = gates(kEnd);
+      const bf16* const lx = lds + L::x + lower_frag(w, 0) * (3 * kFrag) + lane * 8;
+      Frag<3> xf[2];
+      xf[0] = load_planes<3>(lx, kFrag);
+      if (w >= 2) xf[1] = load_planes<3>(lx + 3 * kFrag, kFrag);
+      f32x4 ws[NT], ws2[NT];
+      Frag<3> rf[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        ws[n] = ws2[n] = f32x4{0, 0, 0, 0};
+        rf[n] = load_planes<3>(lds + L::r + get_t + 16 * n * kTokStride, W * kTokStride);
+      }
+      mma_across<NT>(xf[0], rf, ws);
+      if (w >= 2) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) rf[n] = load_planes<3>(lds + L::r + get_t + 16 * n * kTokStride + 32, W * kTokStride);
+        mma_across<NT>(xf[1], rf, ws2);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        ws[n] += ws2[n];
+        store_split4<3>(lds + L::e + put_t + 16 * n * kTokStride, W * kTokStride, ge * ws[n]);
+        if constexpr (!KEEP) {
+          store_split4<2>(lds + L::wr + put_t + 16 * n * kTokStride, W * kTokStride, ws[n]);
+        } else {
+          *reinterpret_cast<f32x4*>(write_at[n] ? write_at[n] : park) = ws[n];
+          if (write_at[n]) write_at[n] += cols * C;
+        }
+      }
+    }
+    landed<KEEP ? 63 : kKeyLoads + 1 + kKeyLoads + 1>();
+    request_x();
+    // the state at the chunk's end
+    {
+      f32x4 acc[NT][KT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int t = 0; t < KT; ++t) acc[n][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        Frag<1> ka[KT];
+        Frag<3> ef[NT];
+#pragma unroll
+        for (int t = 0; t < KT; ++t) ka[t] = Keys::columns(lk + col_at[t] + 32 * s * KP);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          ef[n] = load_planes<3>(lds + L::e + get_t + 16 * n * kTokStride + 32 * s, W * kTokStride);
+#pragma unroll
+        for (int i = 2; i >= 0; --i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int t = 0; t < KT; ++t) acc[n][t] = mma(ka[t].p[0], ef[n].p[i], acc[n][t]);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) st[n][t][r] = fmaf(whole, st[n][t][r], acc[n][t][r]);
+      store_s();
+    }
+    // outputs
+    if constexpr (!KEEP) {
+      const bf16* const lp = lds + L::p + lower_frag(w, 0) * (2 * kFrag) + lane * 8;
+      Frag<2> wf[NT];
+      f32x4 y2[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        y2[n] = f32x4{0, 0, 0, 0};
+        wf[n] = load_planes<2>(lds + L::wr + get_t + 16 * n * kTokStride, W * kTokStride);
+      }
+      mma_across<NT>(load_planes<2>(lp, kFrag), wf, y);
+      if (w >= 2) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) wf[n] = load_planes<2>(lds + L::wr + get_t + 16 * n * kTokStride + 32, W * kTokStride);
+        mma_across<NT>(load_planes<2>(lp + 2 * kFrag, kFrag), wf, y2);
+      }
+      // to rows of the output through LDS; only this wavefront touches them
+      bf16* const out = lds + L::y + 16 * w * W;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) out[(4 * q + r) * W + 16 * n + j] = (bf16)(y[n][r] + y2[n][r]);
+      __builtin_amdgcn_wave_barrier();
+      const int row = lane / v_vecs, part = 8 * (lane % v_vecs);
+      const bool in = row < 16 && 16 * w + row < left && col0 + part < a.P;
+      const uint4 val = *reinterpret_cast<const uint4*>(out + (in ? row * W + part : 0));
+      bf16* const to = static_cast<bf16*>(a.y) + (b * a.T + c * C + 16 * w + row) * (a.H * a.P) + h * a.P + col0 + part;
+      *reinterpret_cast<uint4*>(in ? to : reinterpret_cast<bf16*>(park)) = val;
+    }
+    landed<KEEP ? NT + kXLoads : kXLoads + 1>();
+  }
+  if (!KEEP && a.state) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+        if (col_in[n] && key[t] < a.N)
+          *reinterpret_cast<f32x4*>(a.state + (bh * a.P + col0 + 16 * n + j) * a.N + key[t]) = st[n][t];
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no request may reach LDS after this
+}
+
+// ---------------------------------------------------------------------------
 // One token.  A row p of the state needs two dot products, S k and S q; the
 // token's own part of y is its write times k.q.
 //   y = a S.q + u k.q,  S' = a S + u k,  u = b (v - a S.k)
@@ -772,11 +1068,14 @@ hipError_t launch_scan(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
     const int64_t heads = a.Bt * a.H;
     hipLaunchKernelGGL((k_delta_prep<IO, KP, FULL, GRADS>), dim3(chunks), dim3(kThreads), 0, stream, a);
     if constexpr (sizeof(IO) == 2) {
-      columns_of(a, [&](auto nw) {
-        constexpr int NW = decltype(nw)::value;
-        hipLaunchKernelGGL((k_delta_columns<KP, FULL, NW, GRADS>), dim3((unsigned)(heads * ((a.P + 16 * NW - 1) / (16 * NW)))),
-                           dim3(64 * NW), 0, stream, a);
-      });
+      return chain_of(
+          a,
+          [&](auto nt, unsigned groups) {
+            hipLaunchKernelGGL((k_delta_tokens<KP, FULL, nt.value, GRADS>), dim3(groups), dim3(kThreads), 0, stream, a);
+          },
+          [&](unsigned groups) {
+            hipLaunchKernelGGL((k_delta_columns<KP, FULL, 4, GRADS>), dim3(groups), dim3(256), 0, stream, a);
+          });
     } else {
       hipLaunchKernelGGL((k_delta_chain<IO, KP, FULL, 1, GRADS>), dim3((unsigned)(heads * ((a.P + 15) / 16))),
                          dim3(kThreads), 0, stream, a);
