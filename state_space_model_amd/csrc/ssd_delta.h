@@ -70,19 +70,6 @@ __device__ __forceinline__ void mma_tiles(const Frag<NA> (&a)[NT], const Frag<NB
         for (int t = 0; t < NT; ++t) acc[t] = mma(a[t].p[i], b.p[s - i], acc[t]);
 }
 
-// acc[n] += A B[n], likewise
-template <int NT, int NA, int NB>
-__device__ __forceinline__ void mma_across(const Frag<NA>& a, const Frag<NB> (&b)[NT], f32x4 (&acc)[NT]) {
-  constexpr int top = (NA > NB ? NA : NB) - 1;
-#pragma unroll
-  for (int s = top; s >= 0; --s)
-#pragma unroll
-    for (int i = 0; i < NA; ++i)
-      if (s - i >= 0 && s - i < NB)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n] = mma(a.p[i], b[n].p[s - i], acc[n]);
-}
-
 // The planes of a pair, plane by plane in one word.  Each is rounded to nearest
 // (v_cvt_pk_bf16_f32), so what the dropped products leave out has no sign of its
 // own; the remainders are exact.  An infinity or a NaN leaves NaN behind.
@@ -316,15 +303,28 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 
-// The keys or queries of a chunk in LDS, row-major without padding (what lands
-// in lane order cannot be padded): the 16-byte vectors of a row are permuted by
-// its number instead, so that the 16 rows of an operand read and the 4 x 4
-// (row, vector) of a transposed one take different banks.
+// LDS banks.  A 16-byte read takes lanes 0-3, 12-15, 20-23 and 24-27 at a time
+// (then the other half of 0-31, and 32-63 alike; found from the conflict counter
+// over row strides): rows j of one lane group with those of the next, whose
+// vector number differs in bit 0.  So rows are not padded; the 16-byte vectors
+// of a row are permuted by exclusive or with a function of its number that takes
+// {0-3, 12-15} and {4-11} each to a set closed under changing bit 0.
+//
+// Rows that are only written 8 bytes and read 16 bytes at a time, R elements
+// each: the row's number itself.
+template <int R>
+__device__ __forceinline__ int row_vec(int row, int vec) {
+  return row * R + 8 * (vec ^ (R == 128 ? row & 15 : row >> 1 & 7));
+}
+
+// The keys or queries of a chunk: read transposed, too, 4 x 4 (row 4 q + d, vector
+// 4 u + b) at a time, which wants different upper bits for each d.
 template <int KP, int NW> struct KeyTile {
   static constexpr int kVecs = KP / 8, kRows = 64 / kVecs;   // vectors of a row, rows of 1 KB
   static constexpr int kElems = C * KP, kLoads = C / kRows / NW;
   __device__ __forceinline__ static int swizzle(int row) {
-    return KP == 128 ? 4 * (row & 3) + (row >> 2 & 3) : 4 * (row >> 1 & 1) + (row >> 2 & 3);
+    const int q = row >> 2 & 3, low = (0x78 >> (2 * q) & 3);   // 0, 2, 3, 1
+    return (KP == 128 ? 4 * (row & 3) : 4 * (row >> 1 & 1)) + low;
   }
   // The lane's part of a wavefront's requests: byte offsets from the chunk's
   // first row; past row `last` that row again.  64 rows count in 32 bits.

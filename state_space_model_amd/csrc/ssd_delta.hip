@@ -695,11 +695,11 @@ __global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// The chunks of one (b, h) in order, bfloat16 io: the four wavefronts of a
-// workgroup share 16 NT value columns, wavefront w the rows of tokens 16 w .. + 15
-// and a quarter of the state's keys.  The state, the right sides and the writes
-// go through LDS as in k_delta_chain; what comes from memory lands in LDS as in
-// k_delta_columns, each operand requested when its last reader is done:
+// The chunks of one (b, h) in order, bfloat16 io: four wavefronts share 16 value
+// columns (NG such groups to a workgroup), wavefront w the rows of tokens 16 w
+// .. + 15 and a quarter of the state's keys.  The state, the right sides and the
+// writes go through LDS as in k_delta_chain; what comes from memory lands in LDS
+// as in k_delta_columns, each operand requested when its last reader is done:
 //   top        q k^T of this chunk; k, gates of the next (two places for each)
 //   barrier 1  q, v of the next            (waits for the inverse)
 //   barrier 2  the next inverse            (waits for q k^T)
@@ -707,51 +707,53 @@ __global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
 // Every wavefront makes the same requests, so that the counts that the waits
 // leave outstanding are constants.
 // ---------------------------------------------------------------------------
-template <int KP, int NT, bool KEEP> struct TokensLds {
-  using Keys = KeyTile<KP, 4>;
-  static constexpr int KST = KP + 8, W = 16 * NT;
+template <int KP, int NG, bool KEEP> struct TokensLds {
+  using Keys = KeyTile<KP, 4 * NG>;
+  static constexpr int W = 16 * NG;
   static constexpr int k = 0, q = k + 2 * Keys::kElems, x = q + (KEEP ? 0 : Keys::kElems);
   static constexpr int p = x + 3 * kTriFrags * kFrag, v = p + (KEEP ? 0 : 2 * kTriFrags * kFrag);
-  static constexpr int gate = v + C * W, s = gate + 4 * kGates, r = s + 3 * W * KST;
-  static constexpr int e = r + 3 * W * kTokStride, wr = e + 3 * W * kTokStride;
-  static constexpr int y = wr + (KEEP ? 0 : 2 * W * kTokStride), elems = y + (KEEP ? 0 : C * W);
+  static constexpr int gate = v + C * W, s = gate + 4 * kGates, r = s + 3 * W * KP;
+  static constexpr int e = r + 3 * W * C, wr = e + 3 * W * C;
+  static constexpr int y = wr + (KEEP ? 0 : 2 * W * C), elems = y + (KEEP ? 0 : C * W);
 };
 
-template <int KP, bool FULL, int NT, bool KEEP>
-__global__ __launch_bounds__(kThreads) void k_delta_tokens(DeltaArgs a) {
-  using L = TokensLds<KP, NT, KEEP>;
+template <int KP, bool FULL, int NG, bool KEEP>
+__global__ __launch_bounds__(256 * NG) void k_delta_tokens(DeltaArgs a) {
+  using L = TokensLds<KP, NG, KEEP>;
   using Keys = typename L::Keys;
-  constexpr int KS = KP / 32, KST = L::KST, KT = KP / 64, W = L::W;
-  constexpr int kKeyLoads = Keys::kLoads, kXLoads = (3 * kTriFrags + 3) / 4, kPLoads = (2 * kTriFrags + 3) / 4;
+  constexpr int KS = KP / 32, KT = KP / 64, W = L::W, NW = 4 * NG;
+  constexpr int kKeyLoads = Keys::kLoads, kXLoads = (3 * kTriFrags + NW - 1) / NW, kPLoads = (2 * kTriFrags + NW - 1) / NW;
   __shared__ __align__(1024) bf16 lds[L::elems];
 
   const int slices = (a.P + W - 1) / W;
   const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
   const int64_t bh = id / slices, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
   const int col0 = (int)(id % slices) * W;
-  const int tid = threadIdx.x, lane = tid & 63, w = wave_of(tid), j = lane & 15, q = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_of(tid), j = lane & 15, q = lane >> 4;
+  const int w = wave & 3, n = wave >> 2;   // row tile, column group
+  const int row = 16 * n + j;              // the lane's value column among the workgroup's
   const int64_t at0 = chunk_at(a, bh, 0), cols = padded_cols(a.P);
 
   // columns that no request reaches stay zero
-  for (int i = tid; i < L::elems / 8; i += kThreads) reinterpret_cast<uint4*>(lds)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < L::elems / 8; i += 64 * NW) reinterpret_cast<uint4*>(lds)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   typename Keys::Offsets k_off, q_off;
   uint32_t v_off;
-  constexpr int v_vecs = 2 * NT, v_rows = 64 / v_vecs, v_kb = C / v_rows;   // 16-byte vectors of a row, KB in all
-  const int v_t = w % v_kb;
+  constexpr int v_vecs = 2 * NG, v_rows = 64 / v_vecs, v_kb = C / v_rows;   // 16-byte vectors of a row, KB in all
+  const int v_t = wave % v_kb;
   const bool v_in = col0 + 8 * (lane % v_vecs) < a.P;
   auto offsets = [&](int64_t c) {
     const int last = (int)min((int64_t)C, a.T - c * C) - 1;
-    Keys::offsets(k_off, (int)a.k_stride, last, a.N, w, lane);
-    if constexpr (!KEEP) Keys::offsets(q_off, (int)a.q_stride, last, a.N, w, lane);
+    Keys::offsets(k_off, (int)a.k_stride, last, a.N, wave, lane);
+    if constexpr (!KEEP) Keys::offsets(q_off, (int)a.q_stride, last, a.N, wave, lane);
     v_off = (uint32_t)min(v_t * v_rows + lane / v_vecs, last) * (uint32_t)a.v_stride * 2u + 16u * (lane % v_vecs);
   };
-  const uint32_t lds0 = lds_address(lds), mine = lds0 + w * 1024;
+  const uint32_t lds0 = lds_address(lds), mine = lds0 + wave * 1024;
   const bf16* kp = static_cast<const bf16*>(a.k) + b * a.T * a.k_stride + g * a.N;
   const bf16* qp = static_cast<const bf16*>(a.q) + b * a.T * a.q_stride + g * a.N;
   const bf16* vp = static_cast<const bf16*>(a.v) + b * a.T * a.v_stride + h * a.P + col0;
-  const bf16* xp = a.inv + at0 * (3 * kTriFrags * kFrag) + w * 512;
-  const bf16* pp = a.qk + at0 * (2 * kTriFrags * kFrag) + w * 512;
+  const bf16* xp = a.inv + at0 * (3 * kTriFrags * kFrag) + wave * 512;
+  const bf16* pp = a.qk + at0 * (2 * kTriFrags * kFrag) + wave * 512;
   const float* gp = a.gate + at0 * kGates;
   const bool all_cols = a.P - col0 >= W;
   auto request_k = [&](int half) {
@@ -762,60 +764,50 @@ __global__ __launch_bounds__(kThreads) void k_delta_tokens(DeltaArgs a) {
     if constexpr (!KEEP) Keys::template request<FULL>(qp, q_off, mine + 2 * L::q);
     if (all_cols || v_in) request16(vp, v_off, lds0 + 2 * L::v + v_t * 1024);
   };
-  auto request_x = [&]() { request_evenly<3 * kTriFrags, 4>(xp, mine + 2 * L::x, w, lane); };
+  auto request_x = [&]() { request_evenly<3 * kTriFrags, NW>(xp, mine + 2 * L::x, wave, lane); };
   offsets(0);
   request_k(0);
   request_qv();
   request_x();
 
-  // state tiles: keys key_of(KT w + t, 4 q + r) of value column j of tile n
-  f32x4 st[NT][KT];
-  bool col_in[NT];
-  int key[KT];
+  // state tiles: keys key_of(KT w + t, 4 q + r) of the lane's value column
+  f32x4 st[KT];
+  const int col = col0 + row;
+  const bool col_in = col < a.P;
+  int key[KT], put_s[KT];
 #pragma unroll
-  for (int t = 0; t < KT; ++t) key[t] = key_of(KT * w + t, 4 * q);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    col_in[n] = col0 + 16 * n + j < a.P;
-#pragma unroll
-    for (int t = 0; t < KT; ++t) {
-      st[n][t] = f32x4{0, 0, 0, 0};
-      if (a.h0 && col_in[n] && key[t] < a.N)
-        st[n][t] = *reinterpret_cast<const f32x4*>(a.h0 + (bh * a.P + col0 + 16 * n + j) * a.N + key[t]);
-    }
+  for (int t = 0; t < KT; ++t) {
+    key[t] = key_of(KT * w + t, 4 * q);
+    put_s[t] = L::s + row_vec<KP>(row, key[t] / 8) + key[t] % 8;
+    st[t] = f32x4{0, 0, 0, 0};
+    if (a.h0 && col_in && key[t] < a.N) st[t] = *reinterpret_cast<const f32x4*>(a.h0 + (bh * a.P + col) * a.N + key[t]);
   }
-  bf16* const put_s = lds + L::s + j * KST;
   auto store_s = [&]() {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int t = 0; t < KT; ++t) store_split4<3>(put_s + 16 * n * KST + key[t], W * KST, st[n][t]);
+    for (int t = 0; t < KT; ++t) store_split4<3>(lds + put_s[t], W * KP, st[t]);
   };
   store_s();
-  // the workspace has whole tiles of columns; a pair's second may lie past them
-  float *state_at[NT], *write_at[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const bool in = col0 + 16 * n < cols;
-    const int64_t col = at0 * cols + col0 + 16 * n + j;
-    state_at[n] = KEEP && in ? a.enter + col * KP : nullptr;
-    write_at[n] = KEEP && in ? a.write + col * C + 16 * w + 4 * q : nullptr;
-  }
+  // the workspace has whole tiles of columns; the last groups may lie past them
+  const bool kept = KEEP && col0 + 16 * n < cols;
   float* const park = static_cast<float*>(a.park) + 4 * lane;
+  float* state_at = kept ? a.enter + (at0 * cols + col) * KP : park;
+  float* write_at = kept ? a.write + (at0 * cols + col) * C + 16 * w + 4 * q : park;
 
-  const bf16* const get_s = lds + L::s + j * KST + 8 * q;
-  const int put_t = j * kTokStride + token_slot(w, q), get_t = j * kTokStride + 8 * q;
-  int row_at[KS];
+  const int put_t = row_vec<C>(row, 4 * (w >> 1) + q) + 4 * (w & 1);   // token_slot(w, q)
+  int get_s[KS], get_t[2], row_at[KS], col_at[KT];
 #pragma unroll
-  for (int s = 0; s < KS; ++s) row_at[s] = Keys::row_at(s, j, q) + 16 * w * KP;
-  int col_at[KT];
+  for (int s = 0; s < KS; ++s) {
+    get_s[s] = L::s + row_vec<KP>(row, 4 * s + q);
+    row_at[s] = Keys::row_at(s, j, q) + 16 * w * KP;
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) get_t[s] = row_vec<C>(row, 4 * s + q);
 #pragma unroll
   for (int t = 0; t < KT; ++t) col_at[t] = Keys::col_at((KT * w + t) >> 1, j, q) + 4 * ((KT * w + t) & 1);
+  const int own_v = (16 * w + 4 * q + (j >> 2)) * W + 16 * n + 4 * (j & 3);
   landed<0>();
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int t = 0; t < KT; ++t) pin(st[n][t]);
+  for (int t = 0; t < KT; ++t) pin(st[t]);
 
   for (int64_t c = 0; c < a.Nc; ++c) {
     const int half = (int)c & 1;
@@ -826,14 +818,10 @@ __global__ __launch_bounds__(kThreads) void k_delta_tokens(DeltaArgs a) {
     const float whole = load_uniform(a.whole + at0 + c);
     if constexpr (KEEP) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int t = 0; t < KT; ++t)
-          *reinterpret_cast<f32x4*>(state_at[n] ? state_at[n] + key[t] : park) = st[n][t];
-        if (state_at[n]) state_at[n] += cols * KP;
-      }
+      for (int t = 0; t < KT; ++t) *reinterpret_cast<f32x4*>(kept ? state_at + key[t] : park) = st[t];
+      state_at += cols * KP;
     } else {
-      request_evenly<2 * kTriFrags, 4>(pp, mine + 2 * L::p, w, lane);
+      request_evenly<2 * kTriFrags, NW>(pp, mine + 2 * L::p, wave, lane);
       pp += 2 * kTriFrags * kFrag;
     }
     // past the last chunk that one again, to where no one reads any more
@@ -847,145 +835,101 @@ __global__ __launch_bounds__(kThreads) void k_delta_tokens(DeltaArgs a) {
     }
     request_k(half ^ 1);
 
-    // K S^T and Q S^T of the wavefront's tokens; the right sides
-    f32x4 ks[NT], y[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) ks[n] = y[n] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const bf16x8 kf = ld8(lk + row_at[s]);
-      bf16x8 qf;
-      if constexpr (!KEEP) qf = ld8(lds + L::q + row_at[s]);
-      Frag<3> sf[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) sf[n] = load_planes<3>(get_s + 16 * n * KST + 32 * s, W * KST);
-#pragma unroll
-      for (int i = 2; i >= 0; --i) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) ks[n] = mma(kf, sf[n].p[i], ks[n]);
-        if constexpr (!KEEP)
-          if (i < 2)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) y[n] = mma(qf, sf[n].p[i], y[n]);
-      }
-    }
+    // K S^T and Q S^T of the wavefront's tokens, in two sums each; the right sides
+    f32x4 y;
     {
-      const f32x4 gb = gates(kBeta), gr = gates(kRight), go = gates(kOut);
+      f32x4 ks[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}}, qs[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const bf16x4 v = lds_read_tr4(lds + L::v + (16 * w + 4 * q + (j >> 2)) * W + 16 * n + 4 * (j & 3));
-        f32x4 rs;
+      for (int s = 0; s < KS; s += 2) {
+        bf16x8 kf[2], qf[2];
+        Frag<3> sf[2];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) rs[r] = fmaf(-gr[r], ks[n][r], gb[r] * (float)v[r]);
-        y[n] *= go;
-        store_split4<3>(lds + L::r + put_t + 16 * n * kTokStride, W * kTokStride, rs);
+        for (int o = 0; o < 2; ++o) {
+          kf[o] = ld8(lk + row_at[s + o]);
+          if constexpr (!KEEP) qf[o] = ld8(lds + L::q + row_at[s + o]);
+          sf[o] = load_planes<3>(lds + get_s[s + o], W * KP);
+        }
+#pragma unroll
+        for (int i = 2; i >= 0; --i) {
+#pragma unroll
+          for (int o = 0; o < 2; ++o) ks[o] = mma(kf[o], sf[o].p[i], ks[o]);
+          if constexpr (!KEEP)
+            if (i < 2)
+#pragma unroll
+              for (int o = 0; o < 2; ++o) qs[o] = mma(qf[o], sf[o].p[i], qs[o]);
+        }
       }
+      const f32x4 gb = gates(kBeta), gr = gates(kRight);
+      const bf16x4 v = lds_read_tr4(lds + L::v + own_v);
+      f32x4 rs;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) rs[r] = fmaf(-gr[r], ks[0][r] + ks[1][r], gb[r] * (float)v[r]);
+      store_split4<3>(lds + L::r + put_t, W * C, rs);
+      if constexpr (!KEEP) y = gates(kOut) * (qs[0] + qs[1]);
     }
-    landed<KEEP ? NT * KT + kKeyLoads + 1 : 1 + kPLoads + kKeyLoads + 1>();
+    landed<KEEP ? KT + kKeyLoads + 1 : 1 + kPLoads + kKeyLoads + 1>();
     request_qv();
     // the writes
     {
       const f32x4 ge = gates(kEnd);
       const bf16* const lx = lds + L::x + lower_frag(w, 0) * (3 * kFrag) + lane * 8;
-      Frag<3> xf[2];
-      xf[0] = load_planes<3>(lx, kFrag);
-      if (w >= 2) xf[1] = load_planes<3>(lx + 3 * kFrag, kFrag);
-      f32x4 ws[NT], ws2[NT];
-      Frag<3> rf[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        ws[n] = ws2[n] = f32x4{0, 0, 0, 0};
-        rf[n] = load_planes<3>(lds + L::r + get_t + 16 * n * kTokStride, W * kTokStride);
-      }
-      mma_across<NT>(xf[0], rf, ws);
-      if (w >= 2) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) rf[n] = load_planes<3>(lds + L::r + get_t + 16 * n * kTokStride + 32, W * kTokStride);
-        mma_across<NT>(xf[1], rf, ws2);
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        ws[n] += ws2[n];
-        store_split4<3>(lds + L::e + put_t + 16 * n * kTokStride, W * kTokStride, ge * ws[n]);
-        if constexpr (!KEEP) {
-          store_split4<2>(lds + L::wr + put_t + 16 * n * kTokStride, W * kTokStride, ws[n]);
-        } else {
-          *reinterpret_cast<f32x4*>(write_at[n] ? write_at[n] : park) = ws[n];
-          if (write_at[n]) write_at[n] += cols * C;
-        }
+      f32x4 ws = {0, 0, 0, 0}, ws2 = {0, 0, 0, 0};
+      ws = mma(load_planes<3>(lx, kFrag), load_planes<3>(lds + L::r + get_t[0], W * C), ws);
+      if (w >= 2) ws2 = mma(load_planes<3>(lx + 3 * kFrag, kFrag), load_planes<3>(lds + L::r + get_t[1], W * C), ws2);
+      ws += ws2;
+      store_split4<3>(lds + L::e + put_t, W * C, ge * ws);
+      if constexpr (!KEEP) {
+        store_split4<2>(lds + L::wr + put_t, W * C, ws);
+      } else {
+        *reinterpret_cast<f32x4*>(write_at) = ws;
+        if (kept) write_at += cols * C;
       }
     }
     landed<KEEP ? 63 : kKeyLoads + 1 + kKeyLoads + 1>();
     request_x();
     // the state at the chunk's end
     {
-      f32x4 acc[NT][KT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int t = 0; t < KT; ++t) acc[n][t] = f32x4{0, 0, 0, 0};
+      f32x4 acc[2][KT];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
+        const auto ef = load_planes<3>(lds + L::e + get_t[s], W * C);
         Frag<1> ka[KT];
-        Frag<3> ef[NT];
 #pragma unroll
-        for (int t = 0; t < KT; ++t) ka[t] = Keys::columns(lk + col_at[t] + 32 * s * KP);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          ef[n] = load_planes<3>(lds + L::e + get_t + 16 * n * kTokStride + 32 * s, W * kTokStride);
-#pragma unroll
-        for (int i = 2; i >= 0; --i)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int t = 0; t < KT; ++t) acc[n][t] = mma(ka[t].p[0], ef[n].p[i], acc[n][t]);
+        for (int t = 0; t < KT; ++t) {
+          ka[t] = Keys::columns(lk + col_at[t] + 32 * s * KP);
+          acc[s][t] = f32x4{0, 0, 0, 0};
+        }
+        mma_tiles(ka, ef, acc[s]);
       }
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) st[n][t][r] = fmaf(whole, st[n][t][r], acc[n][t][r]);
+        for (int r = 0; r < 4; ++r) st[t][r] = fmaf(whole, st[t][r], acc[0][t][r] + acc[1][t][r]);
       store_s();
     }
     // outputs
     if constexpr (!KEEP) {
       const bf16* const lp = lds + L::p + lower_frag(w, 0) * (2 * kFrag) + lane * 8;
-      Frag<2> wf[NT];
-      f32x4 y2[NT];
+      f32x4 y2 = {0, 0, 0, 0};
+      y = mma(load_planes<2>(lp, kFrag), load_planes<2>(lds + L::wr + get_t[0], W * C), y);
+      if (w >= 2) y2 = mma(load_planes<2>(lp + 2 * kFrag, kFrag), load_planes<2>(lds + L::wr + get_t[1], W * C), y2);
+      // to rows of the output through LDS; only this wavefront touches these
+      bf16* const out = lds + L::y + wave * 256;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        y2[n] = f32x4{0, 0, 0, 0};
-        wf[n] = load_planes<2>(lds + L::wr + get_t + 16 * n * kTokStride, W * kTokStride);
-      }
-      mma_across<NT>(load_planes<2>(lp, kFrag), wf, y);
-      if (w >= 2) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) wf[n] = load_planes<2>(lds + L::wr + get_t + 16 * n * kTokStride + 32, W * kTokStride);
-        mma_across<NT>(load_planes<2>(lp + 2 * kFrag, kFrag), wf, y2);
-      }
-      // to rows of the output through LDS; only this wavefront touches them
-      bf16* const out = lds + L::y + 16 * w * W;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) out[(4 * q + r) * W + 16 * n + j] = (bf16)(y[n][r] + y2[n][r]);
+      for (int r = 0; r < 4; ++r) out[(4 * q + r) * 16 + j] = (bf16)(y[r] + y2[r]);
       __builtin_amdgcn_wave_barrier();
-      const int row = lane / v_vecs, part = 8 * (lane % v_vecs);
-      const bool in = row < 16 && 16 * w + row < left && col0 + part < a.P;
-      const uint4 val = *reinterpret_cast<const uint4*>(out + (in ? row * W + part : 0));
-      bf16* const to = static_cast<bf16*>(a.y) + (b * a.T + c * C + 16 * w + row) * (a.H * a.P) + h * a.P + col0 + part;
+      const int tok = lane >> 1 & 15, part = 8 * (lane & 1);
+      const bool in = lane < 32 && 16 * w + tok < left && col0 + 16 * n + part < a.P;
+      const uint4 val = *reinterpret_cast<const uint4*>(out + tok * 16 + part);
+      bf16* const to = static_cast<bf16*>(a.y) + (b * a.T + c * C + 16 * w + tok) * (a.H * a.P) + h * a.P + col0 + 16 * n + part;
       *reinterpret_cast<uint4*>(in ? to : reinterpret_cast<bf16*>(park)) = val;
     }
-    landed<KEEP ? NT + kXLoads : kXLoads + 1>();
+    landed<KEEP ? 1 + kXLoads : kXLoads + 1>();
   }
-  if (!KEEP && a.state) {
+  if (!KEEP && a.state && col_in) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-        if (col_in[n] && key[t] < a.N)
-          *reinterpret_cast<f32x4*>(a.state + (bh * a.P + col0 + 16 * n + j) * a.N + key[t]) = st[n][t];
+    for (int t = 0; t < KT; ++t)
+      if (key[t] < a.N) *reinterpret_cast<f32x4*>(a.state + (bh * a.P + col) * a.N + key[t]) = st[t];
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no request may reach LDS after this
 }
@@ -1070,8 +1014,9 @@ hipError_t launch_scan(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
     if constexpr (sizeof(IO) == 2) {
       return chain_of(
           a,
-          [&](auto nt, unsigned groups) {
-            hipLaunchKernelGGL((k_delta_tokens<KP, FULL, nt.value, GRADS>), dim3(groups), dim3(kThreads), 0, stream, a);
+          [&](auto ng, unsigned groups) {
+            hipLaunchKernelGGL((k_delta_tokens<KP, FULL, ng.value, GRADS>), dim3(groups), dim3(256 * ng.value), 0,
+                               stream, a);
           },
           [&](unsigned groups) {
             hipLaunchKernelGGL((k_delta_columns<KP, FULL, 4, GRADS>), dim3(groups), dim3(256), 0, stream, a);

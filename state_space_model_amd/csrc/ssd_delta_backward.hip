@@ -416,57 +416,57 @@ __global__ __launch_bounds__(64 * NW) void k_delta_back_columns(DeltaArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// The same for bfloat16 io, as k_delta_tokens: four wavefronts share 16 NT value
+// The same for bfloat16 io, as k_delta_tokens: four wavefronts share 16 value
 // columns.  Requests, and what they wait for:
 //   top        q of this chunk; k, gates of the one before it (two places for each)
 //   barrier 1  q k^T, dy of the one before   (waits for the inverse)
 //   barrier 2  its inverse                   (waits for q)
 //   barrier 3                                (waits for k, gates, q k^T, dy)
 // ---------------------------------------------------------------------------
-template <int KP, int NT> struct BackTokensLds {
-  using Keys = KeyTile<KP, 4>;
-  static constexpr int KST = KP + 8, W = 16 * NT;
+template <int KP, int NG> struct BackTokensLds {
+  using Keys = KeyTile<KP, 4 * NG>;
+  static constexpr int W = 16 * NG;
   static constexpr int k = 0, q = k + 2 * Keys::kElems, x = q + Keys::kElems, p = x + 3 * kTriFrags * kFrag;
   static constexpr int y = p + 3 * kTriFrags * kFrag, gate = y + C * W, s = gate + 4 * kGates;
-  static constexpr int r = s + 3 * W * KST, e = r + 3 * W * kTokStride, g = e + 3 * W * kTokStride;
-  static constexpr int elems = g + 3 * W * kTokStride;
+  static constexpr int r = s + 3 * W * KP, e = r + 3 * W * C, g = e + 3 * W * C, elems = g + 3 * W * C;
 };
 
-template <int KP, bool FULL, int NT>
-__global__ __launch_bounds__(kThreads) void k_delta_back_tokens(DeltaArgs a) {
-  using L = BackTokensLds<KP, NT>;
+template <int KP, bool FULL, int NG>
+__global__ __launch_bounds__(256 * NG) void k_delta_back_tokens(DeltaArgs a) {
+  using L = BackTokensLds<KP, NG>;
   using Keys = typename L::Keys;
-  constexpr int KS = KP / 32, KST = L::KST, KT = KP / 64, W = L::W;
-  constexpr int kKeyLoads = Keys::kLoads, kTriLoads = (3 * kTriFrags + 3) / 4;
+  constexpr int KS = KP / 32, KT = KP / 64, W = L::W, NW = 4 * NG;
+  constexpr int kKeyLoads = Keys::kLoads, kTriLoads = (3 * kTriFrags + NW - 1) / NW;
   __shared__ __align__(1024) bf16 lds[L::elems];
 
   const int slices = (a.P + W - 1) / W;
   const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
   const int64_t bh = id / slices, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
   const int col0 = (int)(id % slices) * W;
-  const int tid = threadIdx.x, lane = tid & 63, w = wave_of(tid), j = lane & 15, q = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_of(tid), j = lane & 15, q = lane >> 4;
+  const int w = wave & 3, n = wave >> 2, row = 16 * n + j;
   const int64_t c_last = a.Nc - 1, at0 = chunk_at(a, bh, 0), at = at0 + c_last, cols = padded_cols(a.P);
 
-  for (int i = tid; i < L::elems / 8; i += kThreads) reinterpret_cast<uint4*>(lds)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < L::elems / 8; i += 64 * NW) reinterpret_cast<uint4*>(lds)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   typename Keys::Offsets k_off, q_off;
   uint32_t y_off;
-  constexpr int v_vecs = 2 * NT, v_rows = 64 / v_vecs, v_kb = C / v_rows;
-  const int v_t = w % v_kb;
+  constexpr int v_vecs = 2 * NG, v_rows = 64 / v_vecs, v_kb = C / v_rows;
+  const int v_t = wave % v_kb;
   const bool v_in = col0 + 8 * (lane % v_vecs) < a.P;
   const int64_t y_row = a.H * a.P;
-  auto offsets_q = [&](int last) { Keys::offsets(q_off, (int)a.q_stride, last, a.N, w, lane); };
+  auto offsets_q = [&](int last) { Keys::offsets(q_off, (int)a.q_stride, last, a.N, wave, lane); };
   auto offsets_ky = [&](int last) {
-    Keys::offsets(k_off, (int)a.k_stride, last, a.N, w, lane);
+    Keys::offsets(k_off, (int)a.k_stride, last, a.N, wave, lane);
     y_off = (uint32_t)min(v_t * v_rows + lane / v_vecs, last) * (uint32_t)y_row * 2u + 16u * (lane % v_vecs);
   };
-  const uint32_t lds0 = lds_address(lds), mine = lds0 + w * 1024;
+  const uint32_t lds0 = lds_address(lds), mine = lds0 + wave * 1024;
   const int64_t row0 = b * a.T + c_last * C;
   const bf16* kp = static_cast<const bf16*>(a.k) + row0 * a.k_stride + g * a.N;
   const bf16* qp = static_cast<const bf16*>(a.q) + row0 * a.q_stride + g * a.N;
   const bf16* yp = static_cast<const bf16*>(a.dy) + row0 * y_row + h * a.P + col0;
-  const bf16* xp = a.inv_t + at * (3 * kTriFrags * kFrag) + w * 512;
-  const bf16* pp = a.qk + at * (3 * kTriFrags * kFrag) + w * 512;
+  const bf16* xp = a.inv_t + at * (3 * kTriFrags * kFrag) + wave * 512;
+  const bf16* pp = a.qk + at * (3 * kTriFrags * kFrag) + wave * 512;
   const float* gp = a.gate + at * kGates;
   const bool all_cols = a.P - col0 >= W;
   auto request_k = [&](int half) {
@@ -474,10 +474,10 @@ __global__ __launch_bounds__(kThreads) void k_delta_back_tokens(DeltaArgs a) {
     request16(gp, 16 * lane, lds0 + 2 * (L::gate + half * 2 * kGates));
   };
   auto request_py = [&]() {
-    request_evenly<3 * kTriFrags, 4>(pp, mine + 2 * L::p, w, lane);
+    request_evenly<3 * kTriFrags, NW>(pp, mine + 2 * L::p, wave, lane);
     if (all_cols || v_in) request16(yp, y_off, lds0 + 2 * L::y + v_t * 1024);
   };
-  auto request_x = [&]() { request_evenly<3 * kTriFrags, 4>(xp, mine + 2 * L::x, w, lane); };
+  auto request_x = [&]() { request_evenly<3 * kTriFrags, NW>(xp, mine + 2 * L::x, wave, lane); };
   const int tail = (int)(a.T - c_last * C) - 1;   // last row of the last chunk
   offsets_q(tail);
   offsets_ky(tail);
@@ -485,52 +485,45 @@ __global__ __launch_bounds__(kThreads) void k_delta_back_tokens(DeltaArgs a) {
   request_py();
   request_x();
 
-  f32x4 st[NT][KT];
-  bool col_in[NT];
-  int key[KT];
+  f32x4 st[KT];
+  const int col = col0 + row;
+  const bool col_in = col < a.P;
+  int key[KT], put_s[KT];
 #pragma unroll
-  for (int t = 0; t < KT; ++t) key[t] = key_of(KT * w + t, 4 * q);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    col_in[n] = col0 + 16 * n + j < a.P;
-#pragma unroll
-    for (int t = 0; t < KT; ++t) {
-      st[n][t] = f32x4{0, 0, 0, 0};
-      if (a.dfinal && col_in[n] && key[t] < a.N)
-        st[n][t] = *reinterpret_cast<const f32x4*>(a.dfinal + (bh * a.P + col0 + 16 * n + j) * a.N + key[t]);
-    }
+  for (int t = 0; t < KT; ++t) {
+    key[t] = key_of(KT * w + t, 4 * q);
+    put_s[t] = L::s + row_vec<KP>(row, key[t] / 8) + key[t] % 8;
+    st[t] = f32x4{0, 0, 0, 0};
+    if (a.dfinal && col_in && key[t] < a.N)
+      st[t] = *reinterpret_cast<const f32x4*>(a.dfinal + (bh * a.P + col) * a.N + key[t]);
   }
-  bf16* const put_s = lds + L::s + j * KST;
   auto store_s = [&]() {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int t = 0; t < KT; ++t) store_split4<3>(put_s + 16 * n * KST + key[t], W * KST, st[n][t]);
+    for (int t = 0; t < KT; ++t) store_split4<3>(lds + put_s[t], W * KP, st[t]);
   };
   store_s();
-  float *state_at[NT], *right_at[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const bool in = col0 + 16 * n < cols;
-    const int64_t col = at * cols + col0 + 16 * n + j;
-    state_at[n] = in ? a.leave + col * KP : nullptr;
-    right_at[n] = in ? a.dright + col * C + 16 * w + 4 * q : nullptr;
-  }
+  const bool kept = col0 + 16 * n < cols;
   float* const park = static_cast<float*>(a.park) + 4 * lane;
-  const bf16* const get_s = lds + L::s + j * KST + 8 * q;
-  const int put_t = j * kTokStride + token_slot(w, q), get_t = j * kTokStride + 8 * q;
-  int row_at[KS], col_at[KT];
+  float* state_at = kept ? a.leave + (at * cols + col) * KP : park;
+  float* right_at = kept ? a.dright + (at * cols + col) * C + 16 * w + 4 * q : park;
+  const int put_t = row_vec<C>(row, 4 * (w >> 1) + q) + 4 * (w & 1);   // token_slot(w, q)
+  int get_s[KS], get_t[2], row_at[KS], col_at[KT];
 #pragma unroll
-  for (int s = 0; s < KS; ++s) row_at[s] = Keys::row_at(s, j, q) + 16 * w * KP;
+  for (int s = 0; s < KS; ++s) {
+    get_s[s] = L::s + row_vec<KP>(row, 4 * s + q);
+    row_at[s] = Keys::row_at(s, j, q) + 16 * w * KP;
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) get_t[s] = row_vec<C>(row, 4 * s + q);
 #pragma unroll
   for (int t = 0; t < KT; ++t) col_at[t] = Keys::col_at((KT * w + t) >> 1, j, q) + 4 * ((KT * w + t) & 1);
+  // dy as right operand from token `tok` on, and as a result tile
+  const int dy_at = L::y + (4 * q + (j >> 2)) * W + 16 * n + 4 * (j & 3);
   // rows of tiles 0 and 1 of the triangles reach over all columns, 2 and 3 over the last 32
-  const int first = w < 2 ? 0 : 32;
+  const int first = w >> 1;
   landed<0>();
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int t = 0; t < KT; ++t) pin(st[n][t]);
+  for (int t = 0; t < KT; ++t) pin(st[t]);
   if (c_last > 0) offsets_ky(C - 1);
 
   for (int64_t c = c_last; c >= 0; --c) {
@@ -540,12 +533,8 @@ __global__ __launch_bounds__(kThreads) void k_delta_back_tokens(DeltaArgs a) {
     auto gates = [&](int which) { return *reinterpret_cast<const f32x4*>(gate + which); };
     const float whole = load_uniform(a.whole + at0 + c);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-        *reinterpret_cast<f32x4*>(state_at[n] ? state_at[n] + key[t] : park) = st[n][t];
-      if (state_at[n]) state_at[n] -= cols * KP;
-    }
+    for (int t = 0; t < KT; ++t) *reinterpret_cast<f32x4*>(kept ? state_at + key[t] : park) = st[t];
+    state_at -= cols * KP;
     Keys::template request<FULL>(qp, q_off, mine + 2 * L::q);
     if (c == c_last) offsets_q(C - 1);
     if (c > 0) {   // before the first chunk that one again, to where no one reads any more
@@ -560,116 +549,78 @@ __global__ __launch_bounds__(kThreads) void k_delta_back_tokens(DeltaArgs a) {
 
     // dW
     {
-      f32x4 ke[NT], dw[NT], dw2[NT];
+      f32x4 ke[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}}, dw[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-      for (int n = 0; n < NT; ++n) ke[n] = dw[n] = dw2[n] = f32x4{0, 0, 0, 0};
+      for (int s = 0; s < KS; s += 2) {
+        bf16x8 kf[2];
+        Frag<3> ef[2];
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        Frag<1> kf;
-        kf.p[0] = ld8(lk + row_at[s]);
-        Frag<3> ef[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) ef[n] = load_planes<3>(get_s + 16 * n * KST + 32 * s, W * KST);
-        mma_across<NT>(kf, ef, ke);
-      }
-      const bf16* const lp = lds + L::p + upper_frag(w, w >> 1) * (3 * kFrag) + lane * 8;
-      auto dy_of = [&](int tok, Frag<1>(&f)[NT]) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          f[n] = read_tr2(lds + L::y + (tok + 4 * q + (j >> 2)) * W + 16 * n + 4 * (j & 3), 16 * W);
-      };
-      Frag<1> dy[NT];
-      dy_of(first, dy);
-      mma_across<NT>(load_planes<3>(lp, kFrag), dy, dw);
-      if (w < 2) {
-        dy_of(32, dy);
-        mma_across<NT>(load_planes<3>(lp + 3 * kFrag, kFrag), dy, dw2);
-      }
-      const f32x4 ge = gates(kEnd), go = gates(kOut);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const bf16x4 own = lds_read_tr4(lds + L::y + (16 * w + 4 * q + (j >> 2)) * W + 16 * n + 4 * (j & 3));
-        f32x4 gy;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          dw[n][r] = fmaf(ge[r], ke[n][r], dw[n][r] + dw2[n][r]);
-          gy[r] = go[r] * (float)own[r];
+        for (int o = 0; o < 2; ++o) {
+          kf[o] = ld8(lk + row_at[s + o]);
+          ef[o] = load_planes<3>(lds + get_s[s + o], W * KP);
         }
-        store_split4<3>(lds + L::r + put_t + 16 * n * kTokStride, W * kTokStride, dw[n]);
-        store_split4<3>(lds + L::g + put_t + 16 * n * kTokStride, W * kTokStride, gy);
+#pragma unroll
+        for (int i = 2; i >= 0; --i)
+#pragma unroll
+          for (int o = 0; o < 2; ++o) ke[o] = mma(kf[o], ef[o].p[i], ke[o]);
       }
+      const bf16* const lp = lds + L::p + upper_frag(w, first) * (3 * kFrag) + lane * 8;
+      dw[0] = mma(load_planes<3>(lp, kFrag), read_tr2(lds + dy_at + 32 * first * W, 16 * W), dw[0]);
+      if (w < 2) dw[1] = mma(load_planes<3>(lp + 3 * kFrag, kFrag), read_tr2(lds + dy_at + 32 * W, 16 * W), dw[1]);
+      const f32x4 ge = gates(kEnd), go = gates(kOut);
+      const bf16x4 own = lds_read_tr4(lds + dy_at + 16 * w * W);
+      f32x4 gy;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        dw[0][r] = fmaf(ge[r], ke[0][r] + ke[1][r], dw[0][r] + dw[1][r]);
+        gy[r] = go[r] * (float)own[r];
+      }
+      store_split4<3>(lds + L::r + put_t, W * C, dw[0]);
+      store_split4<3>(lds + L::g + put_t, W * C, gy);
     }
-    landed<NT * KT + 2 * kKeyLoads + 1>();
+    landed<KT + 2 * kKeyLoads + 1>();
     request_py();
     // dR
     {
       const f32x4 gr = gates(kRight);
-      const bf16* const lx = lds + L::x + upper_frag(w, w >> 1) * (3 * kFrag) + lane * 8;
-      f32x4 dr[NT], dr2[NT];
-      Frag<3> rf[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        dr[n] = dr2[n] = f32x4{0, 0, 0, 0};
-        rf[n] = load_planes<3>(lds + L::r + get_t + 16 * n * kTokStride + first, W * kTokStride);
-      }
-      mma_across<NT>(load_planes<3>(lx, kFrag), rf, dr);
-      if (w < 2) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) rf[n] = load_planes<3>(lds + L::r + get_t + 16 * n * kTokStride + 32, W * kTokStride);
-        mma_across<NT>(load_planes<3>(lx + 3 * kFrag, kFrag), rf, dr2);
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        dr[n] += dr2[n];
-        *reinterpret_cast<f32x4*>(right_at[n] ? right_at[n] : park) = dr[n];
-        if (right_at[n]) right_at[n] -= cols * C;
-        store_split4<3>(lds + L::e + put_t + 16 * n * kTokStride, W * kTokStride, -gr * dr[n]);
-      }
+      const bf16* const lx = lds + L::x + upper_frag(w, first) * (3 * kFrag) + lane * 8;
+      f32x4 dr = {0, 0, 0, 0}, dr2 = {0, 0, 0, 0};
+      dr = mma(load_planes<3>(lx, kFrag), load_planes<3>(lds + L::r + (w < 2 ? get_t[0] : get_t[1]), W * C), dr);
+      if (w < 2) dr2 = mma(load_planes<3>(lx + 3 * kFrag, kFrag), load_planes<3>(lds + L::r + get_t[1], W * C), dr2);
+      dr += dr2;
+      *reinterpret_cast<f32x4*>(right_at) = dr;
+      if (kept) right_at -= cols * C;
+      store_split4<3>(lds + L::e + put_t, W * C, -gr * dr);
     }
-    landed<kKeyLoads + 1 + kTriLoads + 1 + NT>();
+    landed<kKeyLoads + 1 + kTriLoads + 1 + 1>();
     request_x();
     // the gradient of the state that enters the chunk
     {
-      f32x4 acc[NT][KT];
+      f32x4 acc[2][KT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int of = 0; of < 2; ++of) {   // Q^T of the outputs' gradients, K^T of the right sides'
 #pragma unroll
-        for (int t = 0; t < KT; ++t) acc[n][t] = f32x4{0, 0, 0, 0};
+        for (int t = 0; t < KT; ++t) acc[of][t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int of = 0; of < 2; ++of) {   // Q^T of the outputs' gradients, K^T of the right sides'
+        for (int s = 0; s < 2; ++s) {
           Frag<1> ka[KT];
-          Frag<3> ef[NT];
 #pragma unroll
           for (int t = 0; t < KT; ++t) ka[t] = Keys::columns((of == 0 ? lds + L::q : lk) + col_at[t] + 32 * s * KP);
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            ef[n] = load_planes<3>(lds + (of == 0 ? L::g : L::e) + get_t + 16 * n * kTokStride + 32 * s, W * kTokStride);
-#pragma unroll
-          for (int i = 2; i >= 0; --i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int t = 0; t < KT; ++t) acc[n][t] = mma(ka[t].p[0], ef[n].p[i], acc[n][t]);
+          mma_tiles(ka, load_planes<3>(lds + (of == 0 ? L::g : L::e) + get_t[s], W * C), acc[of]);
         }
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) st[n][t][r] = fmaf(whole, st[n][t][r], acc[n][t][r]);
-      store_s();
-    }
-    landed<NT + kTriLoads>();
-  }
-  if (a.dh0) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
+      }
 #pragma unroll
       for (int t = 0; t < KT; ++t)
-        if (col_in[n] && key[t] < a.N)
-          *reinterpret_cast<f32x4*>(a.dh0 + (bh * a.P + col0 + 16 * n + j) * a.N + key[t]) = st[n][t];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) st[t][r] = fmaf(whole, st[t][r], acc[0][t][r] + acc[1][t][r]);
+      store_s();
+    }
+    landed<1 + kTriLoads>();
+  }
+  if (a.dh0 && col_in) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+      if (key[t] < a.N) *reinterpret_cast<f32x4*>(a.dh0 + (bh * a.P + col) * a.N + key[t]) = st[t];
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no request may reach LDS after this
 }
@@ -1054,8 +1005,9 @@ hipError_t launch_grads(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
     if constexpr (sizeof(IO) == 2) {
       chain_of(
           a,
-          [&](auto nt, unsigned groups) {
-            hipLaunchKernelGGL((k_delta_back_tokens<KP, FULL, nt.value>), dim3(groups), dim3(kThreads), 0, stream, a);
+          [&](auto ng, unsigned groups) {
+            hipLaunchKernelGGL((k_delta_back_tokens<KP, FULL, ng.value>), dim3(groups), dim3(256 * ng.value), 0, stream,
+                               a);
           },
           [&](unsigned groups) {
             hipLaunchKernelGGL((k_delta_back_columns<KP, FULL, 4>), dim3(groups), dim3(256), 0, stream, a);
