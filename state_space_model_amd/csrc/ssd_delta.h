@@ -454,6 +454,9 @@ __device__ __forceinline__ void landed() {
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"(STORES) : "memory");
 }
 
+// Everyone has read what it will of LDS: requests may overwrite it
+__device__ __forceinline__ void lds_free() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // Value columns of a chain whose four wavefronts share them and split the tokens
 // (tokens(NT), 16 NT columns), or a chain of wavefronts that own 16 each
 // (columns()).  A chain fills a compute unit's LDS.  Sharing makes a step as short

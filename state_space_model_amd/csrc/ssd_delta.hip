@@ -494,9 +494,11 @@ __global__ __launch_bounds__(kThreads) void k_delta_chain(DeltaArgs a) {
 // The chunks of one (b, h) in order, bfloat16 io: every wavefront owns 16 value
 // columns alone.  The state, the right sides and the writes stay in its
 // registers (ssd_delta.h); what the wavefronts share, k, q and the two
-// matrices of a chunk, lands in LDS one chunk ahead, and one barrier a chunk is
-// all they need of each other.  A chunk takes a wavefront 182 matrix
-// instructions (keys of 128), 2912 cycles.
+// matrices of a chunk, lands in LDS, half of a compute unit's, so that one
+// workgroup computes while another waits for its chunk (8 x 16384 x 64 heads of
+// 64 x 128: 1780 us; one
+// workgroup a unit that requests a chunk ahead 2270).  A
+// chunk takes a wavefront 182 matrix instructions (keys of 128), 2912 cycles.
 // ---------------------------------------------------------------------------
 template <int KP, int NW, bool KEEP> struct ColumnsLds {
   using Keys = KeyTile<KP, NW>;
@@ -505,13 +507,13 @@ template <int KP, int NW, bool KEEP> struct ColumnsLds {
   static constexpr int gate = v + C * 16 * NW, elems = gate + 2 * kGates;
 };
 
-template <int KP, bool FULL, int NW, bool KEEP>
-__global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
+template <int KP, bool FULL, bool KEEP>
+__global__ __launch_bounds__(256, 2) void k_delta_columns(DeltaArgs a) {
+  constexpr int NW = 4, KS = KP / 32, KT = KP / 16, W = 16 * NW;
   using L = ColumnsLds<KP, NW, KEEP>;
   using Keys = KeyTile<KP, NW>;
   using Cols = ColumnTile<NW>;
-  constexpr int KS = KP / 32, KT = KP / 16, W = 16 * NW;
-  __shared__ __align__(1024) bf16 lds[2 * L::elems];
+  __shared__ __align__(1024) bf16 lds[L::elems];
 
   const int slices = (a.P + W - 1) / W;
   const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
@@ -523,7 +525,7 @@ __global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
   const int64_t at0 = chunk_at(a, bh, 0), cols = padded_cols(a.P);
 
   // columns that no request reaches stay zero
-  for (int i = tid; i < 2 * L::elems / 8; i += 64 * NW) reinterpret_cast<uint4*>(lds)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < L::elems / 8; i += 256) reinterpret_cast<uint4*>(lds)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   // what the wavefront requests of a chunk: lane offsets, and where it starts
   typename Keys::Offsets k_off, q_off;
@@ -542,17 +544,17 @@ __global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
   const bf16* pp = a.qk + at0 * (2 * kTriFrags * kFrag) + w * 512;
   const float* gp = a.gate + at0 * kGates + w * 256;
   const bool all_cols = a.P - col0 >= W;
-  auto request = [&](uint32_t to) {
-    Keys::template request<FULL>(kp, k_off, to + 2 * L::k);
-    if constexpr (!KEEP) Keys::template request<FULL>(qp, q_off, to + 2 * L::q);
-    request_linear<3 * kTriFrags, NW>(xp, to + 2 * L::x, w, lane);
-    if constexpr (!KEEP) request_linear<2 * kTriFrags, NW>(pp, to + 2 * L::p, w, lane);
-    if (all_cols) Cols::template request<true>(vp, v_off, to + 2 * L::v);
-    else Cols::template request<false>(vp, v_off, to + 2 * L::v);
-    request_linear<1, NW>(gp, to + 2 * L::gate, w, lane);
+  auto request = [&]() {
+    Keys::template request<FULL>(kp, k_off, lds0 + 2 * L::k);
+    if constexpr (!KEEP) Keys::template request<FULL>(qp, q_off, lds0 + 2 * L::q);
+    request_linear<3 * kTriFrags, NW>(xp, lds0 + 2 * L::x, w, lane);
+    if constexpr (!KEEP) request_linear<2 * kTriFrags, NW>(pp, lds0 + 2 * L::p, w, lane);
+    if (all_cols) Cols::template request<true>(vp, v_off, lds0 + 2 * L::v);
+    else Cols::template request<false>(vp, v_off, lds0 + 2 * L::v);
+    request_linear<1, NW>(gp, lds0 + 2 * L::gate, w, lane);
   };
   offsets(0);
-  request(lds0);
+  request();
 
   // state tiles: keys key_of(t, 4 q + r) of value column j
   f32x4 st[KT];
@@ -571,25 +573,14 @@ __global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
   for (int s = 0; s < KS; ++s) row_at[s] = Keys::row_at(s, j, q);
 #pragma unroll
   for (int u = 0; u < KT / 2; ++u) col_at[u] = Keys::col_at(u, j, q);
-  landed<0>();
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
   for (int t = 0; t < KT; ++t) pin(st[t]);
 
   for (int64_t c = 0; c < a.Nc; ++c) {
-    const bf16* const l = lds + (c & 1) * L::elems;
-    // past the last chunk that one again, into the half that no one reads any more
-    if (c + 1 < a.Nc) {
-      kp += C * a.k_stride;
-      qp += C * a.q_stride;
-      vp += C * a.v_stride;
-      xp += 3 * kTriFrags * kFrag;
-      pp += 2 * kTriFrags * kFrag;
-      gp += kGates;
-      if (c + 2 == a.Nc) offsets(c + 1);
-    }
-    request(lds0 + (uint32_t)(~c & 1) * (2 * L::elems));
+    landed<0>();
     const float whole = load_uniform(a.whole + at0 + c);
-    const float* const gate = reinterpret_cast<const float*>(l + L::gate) + 4 * q;
+    const float* const gate = reinterpret_cast<const float*>(lds + L::gate) + 4 * q;
     auto gates = [&](int which, int i) { return *reinterpret_cast<const f32x4*>(gate + which + 16 * i); };
     if (KEEP && !idle) {
 #pragma unroll
@@ -606,12 +597,12 @@ __global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
       const auto sf = right_of<3>(st[2 * s], st[2 * s + 1]);
       Frag<1> rows[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) rows[i] = load_planes<1>(l + L::k + row_at[s] + 16 * i * KP, 0);
+      for (int i = 0; i < 4; ++i) rows[i] = load_planes<1>(lds + L::k + row_at[s] + 16 * i * KP, 0);
       mma_tiles(rows, sf, ks);
       if constexpr (!KEEP) {
         const Frag<2> sy = {{sf.p[0], sf.p[1]}};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) rows[i] = load_planes<1>(l + L::q + row_at[s] + 16 * i * KP, 0);
+        for (int i = 0; i < 4; ++i) rows[i] = load_planes<1>(lds + L::q + row_at[s] + 16 * i * KP, 0);
         mma_tiles(rows, sy, qs);
       }
     }
@@ -620,7 +611,7 @@ __global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
     f32x4 ws[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bf16x4 v = lds_read_tr4(l + L::v + (16 * i + 4 * q + (j >> 2)) * W + 16 * w + 4 * (j & 3));
+      const bf16x4 v = lds_read_tr4(lds + L::v + (16 * i + 4 * q + (j >> 2)) * W + 16 * w + 4 * (j & 3));
       const f32x4 gb = gates(kBeta, i), gr = gates(kRight, i);
 #pragma unroll
       for (int r = 0; r < 4; ++r) ks[i][r] = fmaf(-gr[r], ks[i][r], gb[r] * (float)v[r]);
@@ -629,7 +620,7 @@ __global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
     for (int s = 0; s < 2; ++s) rf[s] = right_of<3>(ks[2 * s], ks[2 * s + 1]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) ws[i] = f32x4{0, 0, 0, 0};
-    mma_lower<3>(l + L::x + lane * 8, rf, ws);
+    mma_lower<3>(lds + L::x + lane * 8, rf, ws);
     if (KEEP && !idle) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4*>(write_at + 16 * i) = ws[i];
@@ -648,7 +639,7 @@ __global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
         Frag<1> keys[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-          keys[t] = Keys::columns(l + L::k + col_at[(t0 + t) / 2] + 4 * (t & 1) + 32 * s * KP);
+          keys[t] = Keys::columns(lds + L::k + col_at[(t0 + t) / 2] + 4 * (t & 1) + 32 * s * KP);
         mma_tiles(keys, ef[s], acc);
       }
 #pragma unroll
@@ -661,10 +652,10 @@ __global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
       Frag<2> wf[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) wf[s] = right_of<2>(ws[2 * s], ws[2 * s + 1]);
-      bf16* const out = lds + (c & 1) * L::elems + L::v + 16 * w;
+      bf16* const out = lds + L::v + 16 * w;
 #pragma unroll
       for (int i = 0; i < 4; ++i) qs[i] *= gates(kOut, i);
-      mma_lower<2>(l + L::p + lane * 8, wf, qs);
+      mma_lower<2>(lds + L::p + lane * 8, wf, qs);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -680,9 +671,17 @@ __global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
         *reinterpret_cast<uint4*>(in ? to : static_cast<bf16*>(a.park) + lane * 8) = v;
       }
     }
-    // the writes, or y, may be on their way
-    if (KEEP && idle) landed<0>();
-    else landed<KEEP ? 4 : 2>();
+    lds_free();
+    if (c + 1 < a.Nc) {
+      kp += C * a.k_stride;
+      qp += C * a.q_stride;
+      vp += C * a.v_stride;
+      xp += 3 * kTriFrags * kFrag;
+      pp += 2 * kTriFrags * kFrag;
+      gp += kGates;
+      if (c + 2 == a.Nc) offsets(c + 1);
+      request();
+    }
   }
   if (!KEEP && a.state && col_in) {
 #pragma unroll
@@ -691,7 +690,6 @@ __global__ __launch_bounds__(64 * NW) void k_delta_columns(DeltaArgs a) {
       if (key < a.N) *reinterpret_cast<f32x4*>(a.state + (bh * a.P + col) * a.N + key) = st[t];
     }
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no request may reach LDS after this
 }
 
 // ---------------------------------------------------------------------------
@@ -1019,7 +1017,7 @@ hipError_t launch_scan(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
                                stream, a);
           },
           [&](unsigned groups) {
-            hipLaunchKernelGGL((k_delta_columns<KP, FULL, 4, GRADS>), dim3(groups), dim3(256), 0, stream, a);
+            hipLaunchKernelGGL((k_delta_columns<KP, FULL, GRADS>), dim3(groups), dim3(256), 0, stream, a);
           });
     } else {
       hipLaunchKernelGGL((k_delta_chain<IO, KP, FULL, 1, GRADS>), dim3((unsigned)(heads * ((a.P + 15) / 16))),

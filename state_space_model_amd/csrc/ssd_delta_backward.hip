@@ -243,13 +243,13 @@ template <int KP, int NW> struct BackLds {
   static constexpr int y = p + 3 * kTriFrags * kFrag, gate = y + C * 16 * NW, elems = gate + 2 * kGates;
 };
 
-template <int KP, bool FULL, int NW>
-__global__ __launch_bounds__(64 * NW) void k_delta_back_columns(DeltaArgs a) {
+template <int KP, bool FULL>
+__global__ __launch_bounds__(256, 2) void k_delta_back_columns(DeltaArgs a) {
+  constexpr int NW = 4, KS = KP / 32, KT = KP / 16, W = 16 * NW;
   using L = BackLds<KP, NW>;
   using Keys = KeyTile<KP, NW>;
   using Cols = ColumnTile<NW>;
-  constexpr int KS = KP / 32, KT = KP / 16, W = 16 * NW;
-  __shared__ __align__(1024) bf16 lds[2 * L::elems];
+  __shared__ __align__(1024) bf16 lds[L::elems];
 
   const int slices = (a.P + W - 1) / W;
   const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(64 * NW) void k_delta_back_columns(DeltaArgs a) {
   const bool col_in = col < a.P, idle = col0 + 16 * w >= a.P;
   const int64_t c_last = a.Nc - 1, at = chunk_at(a, bh, c_last), cols = padded_cols(a.P);
 
-  for (int i = tid; i < 2 * L::elems / 8; i += 64 * NW) reinterpret_cast<uint4*>(lds)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < L::elems / 8; i += 256) reinterpret_cast<uint4*>(lds)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   typename Keys::Offsets k_off, q_off;
   typename Cols::Offsets y_off;
@@ -279,17 +279,17 @@ __global__ __launch_bounds__(64 * NW) void k_delta_back_columns(DeltaArgs a) {
   const bf16* pp = a.qk + at * (3 * kTriFrags * kFrag) + w * 512;
   const float* gp = a.gate + at * kGates + w * 256;
   const bool all_cols = a.P - col0 >= W;
-  auto request = [&](uint32_t to) {
-    Keys::template request<FULL>(kp, k_off, to + 2 * L::k);
-    Keys::template request<FULL>(qp, q_off, to + 2 * L::q);
-    request_linear<3 * kTriFrags, NW>(xp, to + 2 * L::x, w, lane);
-    request_linear<3 * kTriFrags, NW>(pp, to + 2 * L::p, w, lane);
-    if (all_cols) Cols::template request<true>(yp, y_off, to + 2 * L::y);
-    else Cols::template request<false>(yp, y_off, to + 2 * L::y);
-    request_linear<1, NW>(gp, to + 2 * L::gate, w, lane);
+  auto request = [&]() {
+    Keys::template request<FULL>(kp, k_off, lds0 + 2 * L::k);
+    Keys::template request<FULL>(qp, q_off, lds0 + 2 * L::q);
+    request_linear<3 * kTriFrags, NW>(xp, lds0 + 2 * L::x, w, lane);
+    request_linear<3 * kTriFrags, NW>(pp, lds0 + 2 * L::p, w, lane);
+    if (all_cols) Cols::template request<true>(yp, y_off, lds0 + 2 * L::y);
+    else Cols::template request<false>(yp, y_off, lds0 + 2 * L::y);
+    request_linear<1, NW>(gp, lds0 + 2 * L::gate, w, lane);
   };
   offsets((int)(a.T - c_last * C) - 1);
-  request(lds0);
+  request();
 
   f32x4 st[KT];
 #pragma unroll
@@ -306,27 +306,15 @@ __global__ __launch_bounds__(64 * NW) void k_delta_back_columns(DeltaArgs a) {
   for (int s = 0; s < KS; ++s) row_at[s] = Keys::row_at(s, j, q);
 #pragma unroll
   for (int u = 0; u < KT / 2; ++u) col_at[u] = Keys::col_at(u, j, q);
-  landed<0>();
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
   for (int t = 0; t < KT; ++t) pin(st[t]);
   offsets(C - 1);
 
   for (int64_t c = c_last; c >= 0; --c) {
-    const int half = (int)(c_last - c) & 1;
-    const bf16* const l = lds + half * L::elems;
-    if (c > 0) {
-      kp -= C * a.k_stride;
-      qp -= C * a.q_stride;
-      yp -= C * y_row;
-      xp -= 3 * kTriFrags * kFrag;
-      pp -= 3 * kTriFrags * kFrag;
-      gp -= kGates;
-    } else if (c == c_last) {
-      offsets((int)a.T - 1);   // the only chunk again
-    }
-    request(lds0 + (uint32_t)(half ^ 1) * (2 * L::elems));
+    landed<0>();
     const float whole = load_uniform(a.whole + at - c_last + c);
-    const float* const gate = reinterpret_cast<const float*>(l + L::gate) + 4 * q;
+    const float* const gate = reinterpret_cast<const float*>(lds + L::gate) + 4 * q;
     auto gates = [&](int which, int i) { return *reinterpret_cast<const f32x4*>(gate + which + 16 * i); };
     if (!idle) {
 #pragma unroll
@@ -341,15 +329,15 @@ __global__ __launch_bounds__(64 * NW) void k_delta_back_columns(DeltaArgs a) {
     for (int s = 0; s < KS; ++s) {
       Frag<1> rows[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) rows[i] = load_planes<1>(l + L::k + row_at[s] + 16 * i * KP, 0);
+      for (int i = 0; i < 4; ++i) rows[i] = load_planes<1>(lds + L::k + row_at[s] + 16 * i * KP, 0);
       mma_tiles(rows, right_of<3>(st[2 * s], st[2 * s + 1]), ke);
     }
     Frag<1> dy[2];
     Frag<3> rf[2], gf[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s)
-      dy[s] = read_tr2(l + L::y + (32 * s + 4 * q + (j >> 2)) * W + 16 * w + 4 * (j & 3), 16 * W);
-    mma_upper<3>(l + L::p + lane * 8, dy, dw);
+      dy[s] = read_tr2(lds + L::y + (32 * s + 4 * q + (j >> 2)) * W + 16 * w + 4 * (j & 3), 16 * W);
+    mma_upper<3>(lds + L::p + lane * 8, dy, dw);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f32x4 ge = gates(kEnd, i);
@@ -362,7 +350,7 @@ __global__ __launch_bounds__(64 * NW) void k_delta_back_columns(DeltaArgs a) {
     f32x4 dr[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) dr[i] = f32x4{0, 0, 0, 0};
-    mma_upper<3>(l + L::x + lane * 8, rf, dr);
+    mma_upper<3>(lds + L::x + lane * 8, rf, dr);
     if (!idle) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4*>(right_at + 16 * i) = dr[i];
@@ -390,11 +378,11 @@ __global__ __launch_bounds__(64 * NW) void k_delta_back_columns(DeltaArgs a) {
         Frag<1> cols4[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-          cols4[t] = Keys::columns(l + L::q + col_at[(t0 + t) / 2] + 4 * (t & 1) + 32 * s * KP);
+          cols4[t] = Keys::columns(lds + L::q + col_at[(t0 + t) / 2] + 4 * (t & 1) + 32 * s * KP);
         mma_tiles(cols4, gf[s], acc);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-          cols4[t] = Keys::columns(l + L::k + col_at[(t0 + t) / 2] + 4 * (t & 1) + 32 * s * KP);
+          cols4[t] = Keys::columns(lds + L::k + col_at[(t0 + t) / 2] + 4 * (t & 1) + 32 * s * KP);
         mma_tiles(cols4, rf[s], acc);
       }
 #pragma unroll
@@ -402,8 +390,16 @@ __global__ __launch_bounds__(64 * NW) void k_delta_back_columns(DeltaArgs a) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) st[t0 + t][r] = fmaf(whole, st[t0 + t][r], acc[t][r]);
     }
-    if (idle) landed<0>();
-    else landed<4>();   // dR may be on its way
+    lds_free();
+    if (c > 0) {
+      kp -= C * a.k_stride;
+      qp -= C * a.q_stride;
+      yp -= C * y_row;
+      xp -= 3 * kTriFrags * kFrag;
+      pp -= 3 * kTriFrags * kFrag;
+      gp -= kGates;
+      request();
+    }
   }
   if (a.dh0 && col_in) {
 #pragma unroll
@@ -412,7 +408,6 @@ __global__ __launch_bounds__(64 * NW) void k_delta_back_columns(DeltaArgs a) {
       if (key < a.N) *reinterpret_cast<f32x4*>(a.dh0 + (bh * a.P + col) * a.N + key) = st[t];
     }
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no request may reach LDS after this
 }
 
 // ---------------------------------------------------------------------------
@@ -1010,7 +1005,7 @@ hipError_t launch_grads(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
                                a);
           },
           [&](unsigned groups) {
-            hipLaunchKernelGGL((k_delta_back_columns<KP, FULL, 4>), dim3(groups), dim3(256), 0, stream, a);
+            hipLaunchKernelGGL((k_delta_back_columns<KP, FULL>), dim3(groups), dim3(256), 0, stream, a);
           });
     } else {
       hipLaunchKernelGGL((k_delta_back_chain<IO, KP, FULL, 1>), dim3((unsigned)(heads * ((a.P + 15) / 16))),

@@ -16,7 +16,9 @@ NAMES = {"dinitial_state": "dh0"}
 
 SHAPES = [(1, 1, 1, 1, 8, 8), (2, 63, 2, 1, 16, 16), (1, 64, 2, 2, 64, 128), (1, 65, 3, 3, 64, 128),
           (2, 130, 4, 2, 128, 64), (1, 140, 4, 1, 24, 72), (3, 129, 2, 2, 40, 40),
-          (1, 70, 2, 2, 256, 128), (2, 17, 5, 5, 136, 120), (1, 80, 2, 2, 72, 104)]
+          (1, 70, 2, 2, 256, 128), (2, 17, 5, 5, 136, 120), (1, 80, 2, 2, 72, 104),
+          (4, 66, 16, 4, 72, 40), (3, 130, 40, 8, 48, 128),             # chains in pairs
+          (9, 70, 16, 2, 72, 104), (5, 65, 60, 20, 16, 64), (2, 129, 70, 70, 128, 128)]  # chains that own columns
 
 
 def cotangents(seed, x, final=True):
