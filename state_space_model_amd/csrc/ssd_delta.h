@@ -256,6 +256,14 @@ __device__ __forceinline__ void store_frag(bf16* base, int64_t at, int f, int la
 // The wavefront's index, in a scalar register
 __device__ __forceinline__ int wave_of(int tid) { return __builtin_amdgcn_readfirstlane(tid >> 6); }
 
+// f with the wavefront's index as a constant
+template <typename F> __device__ __forceinline__ void by_wave(int w, F&& f) {
+  if (w == 0) f(std::integral_constant<int, 0>{});
+  else if (w == 1) f(std::integral_constant<int, 1>{});
+  else if (w == 2) f(std::integral_constant<int, 2>{});
+  else f(std::integral_constant<int, 3>{});
+}
+
 // sum over a wavefront
 __device__ __forceinline__ float wave_sum64(float v) {
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
@@ -474,6 +482,16 @@ hipError_t chain_of(const DeltaArgs& a, F&& tokens, G&& columns) {
 // Columns and keys that the chains keep of a head in the gradients' workspace:
 // whole tiles, so that no store is conditional
 __device__ __forceinline__ int padded_cols(int P) { return (P + 15) / 16 * 16; }
+
+// What a workgroup of one chunk and head works on.  Workgroups count below 2^24,
+// H and Nc no further: divisions of 32 bits (64-bit ones were a tenth of
+// k_delta_prep's instructions).
+struct ChunkHead { int64_t b, c, h, g; };
+__device__ __forceinline__ ChunkHead chunk_head(const DeltaArgs& a) {
+  const uint32_t id = (uint32_t)xcd_remap(blockIdx.x, gridDim.x), H = (uint32_t)a.H, Nc = (uint32_t)a.Nc;
+  const uint32_t h = id % H, rest = id / H;
+  return {rest / Nc, rest % Nc, h, h / (H / (uint32_t)a.G)};
+}
 
 // Position of a (b, h, chunk)
 __device__ __forceinline__ int64_t chunk_at(const DeltaArgs& a, int64_t bh, int64_t c) {

@@ -20,24 +20,6 @@ namespace {
 // ---------------------------------------------------------------------------
 // Chunk by chunk, before the states are known.
 // ---------------------------------------------------------------------------
-// sum of squares of the lane's row
-template <int PI, int KS>
-__device__ __forceinline__ float row_squares(const Frag<PI> (&f)[KS]) {
-  float ss = 0.0f;
-#pragma unroll
-  for (int s = 0; s < KS; ++s)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float x = (float)f[s].p[PI - 1][e];
-#pragma unroll
-      for (int i = PI - 2; i >= 0; --i) x += (float)f[s].p[i][e];
-      ss = fmaf(x, x, ss);
-    }
-  ss += __shfl_xor(ss, 16, 64);
-  ss += __shfl_xor(ss, 32, 64);
-  return ss;
-}
-
 // Wavefront w owns tokens 16 w .. + 15 as rows of both matrices, and forms them
 // transposed: a result's lane then holds four consecutive columns of its row,
 // and two tiles of columns are a fragment of the matrix as it is (ssd_delta.h).
@@ -64,9 +46,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 4 : 2) void k_delta_pre
   bf16* const s_k = reinterpret_cast<bf16*>(lds);
   float* const s_l = reinterpret_cast<float*>(lds);
 
-  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
-  const int64_t h = id % a.H, c = id / a.H % a.Nc, b = id / a.H / a.Nc;
-  const int64_t g = h / (a.H / a.G);
+  const auto [b, c, h, g] = chunk_head(a);
   const int64_t at = chunk_at(a, b * a.H + h, c);
   const int64_t t0 = c * C, row0 = b * a.T + t0, left = a.T - t0;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_of(tid), j = lane & 15, q = lane >> 4;
@@ -106,17 +86,6 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 4 : 2) void k_delta_pre
     const float beta = a.beta[th];
     s_beta[lane] = in ? (a.sigmoid ? sigmoid_of(beta) : beta) : 0.0f;
   }
-  float rk_own, rq_own;
-  {
-    const bool in = own < left;
-    const float kk = row_squares<PI, KS>(kf), qq = row_squares<PI, KS>(qf);
-    rk_own = !in ? 0.0f : a.unit ? 1.0f / sqrtf(kk + a.norm_eps) : 1.0f;
-    rq_own = !in ? 0.0f : a.scale * (a.unit ? 1.0f / sqrtf(qq + a.norm_eps) : 1.0f);
-    if (q == 0) {
-      s_rk[own] = rk_own;
-      s_rq[own] = rq_own;
-    }
-  }
 #pragma unroll
   for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -124,32 +93,55 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 4 : 2) void k_delta_pre
       *reinterpret_cast<bf16x8*>(&s_k[i * C * KST + own * KST + 32 * s + 8 * q]) = kf[s].p[i];
   __syncthreads();
 
-  // the rows against key tokens up to them: L to LDS, D o Q K^T kept, both
-  // transposed: lane (keys 16 jt + 4 q .. + 3, own token)
+  // The rows against key tokens up to them, transposed: lane (keys 16 jt + 4 q
+  // .. + 3, own token).  The diagonal of K K^T and one tile of Q Q^T are the
+  // squares of the lengths.
   f32x4 p[4], l[4];
-  {
-    const float hi_own = s_hi[own], lo_own = s_lo[own], l_own = s_beta[own] * rk_own;
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-      p[jt] = l[jt] = f32x4{0, 0, 0, 0};
-      if (jt > w) continue;
-      f32x4 kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0};
+  for (int jt = 0; jt < 4; ++jt) {
+    p[jt] = l[jt] = f32x4{0, 0, 0, 0};
+    if (jt > w) continue;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const auto ka = load_planes<PI>(&s_k[(16 * jt + j) * KST + 32 * s + 8 * q], C * KST);
-        kk = mma(ka, kf[s], kk);
-        qk = mma(ka, qf[s], qk);
+    for (int s = 0; s < KS; ++s) {
+      const auto ka = load_planes<PI>(&s_k[(16 * jt + j) * KST + 32 * s + 8 * q], C * KST);
+      l[jt] = mma(ka, kf[s], l[jt]);
+      p[jt] = mma(ka, qf[s], p[jt]);
+    }
+    if (jt == w) {
+      f32x4 qq = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) qq = mma(qf[s], qf[s], qq);
+      if (q == j >> 2) {
+        const int r = j & 3;
+        const float k2 = r == 0 ? l[jt][0] : r == 1 ? l[jt][1] : r == 2 ? l[jt][2] : l[jt][3];
+        const float q2 = r == 0 ? qq[0] : r == 1 ? qq[1] : r == 2 ? qq[2] : qq[3];
+        const bool in = own < left;
+        s_rk[own] = !in ? 0.0f : a.unit ? 1.0f / sqrtf(k2 + a.norm_eps) : 1.0f;
+        s_rq[own] = !in ? 0.0f : a.scale * (a.unit ? 1.0f / sqrtf(q2 + a.norm_eps) : 1.0f);
       }
+    }
+  }
+  __syncthreads();
+  {
+    const float hi_own = s_hi[own], lo_own = s_lo[own], l_own = s_beta[own] * s_rk[own], p_own = s_rq[own];
+    by_wave(w, [&](auto W) {
+#pragma unroll
+    for (int jt = 0; jt <= W; ++jt) {
       const int key0 = 16 * jt + 4 * q;
       const f32x4 hi = *reinterpret_cast<const f32x4*>(&s_hi[key0]), lo = *reinterpret_cast<const f32x4*>(&s_lo[key0]);
       const f32x4 rk = *reinterpret_cast<const f32x4*>(&s_rk[key0]);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float dec = exp2_of((hi_own - hi[r]) + (lo_own - lo[r])) * rk[r];
-        l[jt][r] = own > key0 + r ? l_own * dec * kk[r] : 0.0f;
-        p[jt][r] = own >= key0 + r ? rq_own * dec * qk[r] : 0.0f;
+        l[jt][r] *= l_own * dec;
+        p[jt][r] *= p_own * dec;
+        if (jt == W) {
+          l[jt][r] = own > key0 + r ? l[jt][r] : 0.0f;
+          p[jt][r] = own >= key0 + r ? p[jt][r] : 0.0f;
+        }
       }
     }
+    });
   }
   if constexpr (!GRADS) {
 #pragma unroll
@@ -168,43 +160,51 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 4 : 2) void k_delta_pre
   {
     // only this wavefront wrote the block
     __builtin_amdgcn_wave_barrier();
-    float col[16];
+    // halves of 8 by substitution, lane j solving for its half's column of the
+    // transposed inverse; then D - D U D for the block U between them
+    const int half = j & 8;
+    float col[8];
 #pragma unroll
-    for (int m = 15; m >= 0; --m) {
-      const float* l = &s_l[(16 * w + m) * kPairStride + 16 * w];   // column m of L
-      float acc = m == j ? 1.0f : 0.0f;
+    for (int m = 7; m >= 0; --m) {
+      const float* l = &s_l[(16 * w + half + m) * kPairStride + 16 * w + half];   // column m of L
+      float acc = m == (j & 7) ? 1.0f : 0.0f;
 #pragma unroll
-      for (int i = 15; i > m; --i) acc = fmaf(-l[i], col[i], acc);
+      for (int i = 7; i > m; --i) acc = fmaf(-l[i], col[i], acc);
       col[m] = acc;
     }
+    const bool same = (q >> 1) == (j >> 3);
+    const f32x4 zero = {0, 0, 0, 0};
+    f32x4 u = *reinterpret_cast<const f32x4*>(&s_l[(16 * w + j) * kPairStride + 16 * w + 4 * q]);
+    if (j >= 8 || q < 2) u = zero;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      x[0][r] = q == 0 ? col[r] : q == 1 ? col[4 + r] : q == 2 ? col[8 + r] : col[12 + r];
+      x[0][r] = !same ? 0.0f : q & 1 ? col[4 + r] : col[r];
       s_d[(16 * w + 4 * q + r) * kDiag + j] = x[0][r];
     }
+    __builtin_amdgcn_wave_barrier();
+    const f32x4 d = *reinterpret_cast<const f32x4*>(&s_d[(16 * w + j) * kDiag + 4 * q]);
+    x[0] -= mma16(d, mma16(u, x[0], zero), zero);
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s_d[(16 * w + 4 * q + r) * kDiag + j] = x[0][r];
   }
   __syncthreads();
+  f32x4 row[4];   // by column tile: x[w - t], zeros right of the diagonal
+  by_wave(w, [&](auto W) {
 #pragma unroll
-  for (int d = 1; d < 4; ++d) {
-    x[d] = f32x4{0, 0, 0, 0};
-    const int jb = w - d;
-    if (jb < 0) continue;
-    f32x4 acc = {0, 0, 0, 0};
+    for (int d = 1; d <= W; ++d) {
+      const int jb = W - d;
+      f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-    for (int e = 0; e < d; ++e)
-      acc = mma16(*reinterpret_cast<const f32x4*>(&s_l[(16 * jb + j) * kPairStride + 16 * (w - e) + 4 * q]), x[e], acc);
-    x[d] = -mma16(*reinterpret_cast<const f32x4*>(&s_d[(16 * jb + j) * kDiag + 4 * q]), acc, f32x4{0, 0, 0, 0});
-  }
-  // by column tile: x[w - t], zeros right of the diagonal
-  f32x4 row[4];
+      for (int e = 0; e < d; ++e)
+        acc = mma16(*reinterpret_cast<const f32x4*>(&s_l[(16 * jb + j) * kPairStride + 16 * (W - e) + 4 * q]), x[e], acc);
+      x[d] = -mma16(*reinterpret_cast<const f32x4*>(&s_d[(16 * jb + j) * kDiag + 4 * q]), acc, f32x4{0, 0, 0, 0});
+    }
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < 4; ++t) row[t] = t <= W ? x[t <= W ? W - t : 0] : f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      row[t][r] = t == w ? x[0][r] : t == w - 1 ? x[1][r] : t == w - 2 ? x[2][r] : t == w - 3 ? x[3][r] : 0.0f;
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-    if (s <= (w >> 1)) store_frag(a.inv, at, lower_frag(w, s), lane, right_of<3>(row[2 * s], row[2 * s + 1]));
+    for (int s = 0; s <= W / 2; ++s) store_frag(a.inv, at, lower_frag(W, s), lane, right_of<3>(row[2 * s], row[2 * s + 1]));
+  });
 
   if constexpr (GRADS) {
     // both again, as rows in LDS and read by columns: row tiles 0 and 1 of the

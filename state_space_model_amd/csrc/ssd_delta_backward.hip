@@ -661,9 +661,8 @@ __global__ __launch_bounds__(kThreads) void k_delta_grads(DeltaArgs a) {
   bf16 *s_w = lds, *s_d = lds + L::tok, *s_s = lds + 2 * L::tok, *s_e = s_s + L::key;
   bf16 *s_k = lds, *s_q = lds + L::rows, *s_p = lds + 2 * L::rows, *s_l = s_p + L::pairs;
 
-  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
-  const int64_t h = id % a.H, c = id / a.H % a.Nc, b = id / a.H / a.Nc;
-  const int64_t g = h / (a.H / a.G), bh = b * a.H + h, at = chunk_at(a, bh, c);
+  const auto [b, c, h, g] = chunk_head(a);
+  const int64_t bh = b * a.H + h, at = chunk_at(a, bh, c);
   const int64_t t0 = c * C, row0 = b * a.T + t0, left = a.T - t0;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_of(tid), j = lane & 15, q = lane >> 4;
   if (tid < C) {
@@ -921,12 +920,13 @@ __global__ __launch_bounds__(kThreads) void k_delta_grads(DeltaArgs a) {
 // vectors of its heads: NL lanes of four keys a row.
 template <typename IO, int NL>
 __global__ __launch_bounds__(kThreads) void k_delta_unit_grads(DeltaArgs a) {
-  const int64_t id = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / NL;
-  const int64_t rows = a.Bt * a.T * a.G;
+  // rows below 2^27 (checked by the caller): divisions of 32 bits, which cost a fifth
+  const uint32_t id = (uint32_t)(((int64_t)blockIdx.x * kThreads + threadIdx.x) / NL);
+  const uint32_t rows = (uint32_t)(a.Bt * a.T * a.G);
   const bool in = id < 2 * rows;
   const bool is_q = id < rows;
-  const int64_t row = in ? (is_q ? id : id - rows) : 0;
-  const int64_t tok = row / a.G, g = row % a.G, per = a.H / a.G;
+  const uint32_t row = in ? (is_q ? id : id - rows) : 0, G = (uint32_t)a.G;
+  const int64_t tok = row / G, g = row % G, per = (uint32_t)a.H / G;
   const int key = 4 * (threadIdx.x % NL);
   const bool key_in = in && key < a.N;
   const int at = key_in ? key : 0;
