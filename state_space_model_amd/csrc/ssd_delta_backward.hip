@@ -622,49 +622,83 @@ __global__ __launch_bounds__(256 * NG) void k_delta_back_tokens(DeltaArgs a) {
 
 // ---------------------------------------------------------------------------
 // The gradients of one chunk of one head.  Wavefront w owns tokens 16 w .. + 15
-// of every result.  The contractions over the values run over slices of 32
-// value columns, whose operands are staged as planes and read transposed.
+// of every result, each formed transposed, lane (4 rows, own token): a pair's
+// gradients are then the right operand of the sums over earlier tokens as they
+// stand, and only those over later tokens go through LDS.  The contractions over
+// the values run over slices of 32 value columns, whose operands are staged as
+// planes and read transposed.  Contractions take their indices in the order
+// 4 q .. + 3, 16 + 4 q .. + 3, so that eight consecutive rows are read together,
+// which rows of 144 or 80 elements put into different banks.
+//
+// bfloat16 io: two workgroups to a compute unit (68 KB of LDS, the states that
+// enter and the gradients that leave through one buffer in turn).
 // ---------------------------------------------------------------------------
-constexpr int kSlice = 32;
+constexpr int kSlice = 32, kPairRow = C + 16;
 
 template <typename IO, int KP> struct GradsLds {
   static constexpr int PI = Planes<IO>::in;
-  // rows 8 words past a multiple of 64: the four rows of a transposed read take
-  // different banks (float32 keys of 128: 4 words, or the tiles would not fit)
-  static constexpr int KST = KP + (PI == 3 && KP == 128 ? 8 : 16);
-  static constexpr int tok = 3 * kSlice * kTokStride, key = 3 * kSlice * KST;  // staged slices
-  static constexpr int rows = PI * C * KST, pairs = 3 * C * kTokStride;        // k, q and the pairs
-  static constexpr int first = 2 * tok + 2 * key, second = 2 * rows + 2 * pairs;
+  static constexpr int KST = KP + (PI == 3 && KP == 128 ? 8 : 16);   // (float32 keys of 128: tiles would not fit)
+  static constexpr int tok = 3 * kSlice * kPairRow, key = 3 * kSlice * KST;    // staged slices
+  static constexpr int rows = PI * C * KST, pairs = 3 * C * kPairRow;          // k, q and the pairs
+  static constexpr int first = 2 * tok + key, second = 2 * rows + pairs;
   static constexpr int elems = first > second ? first : second;
 };
 
-// value (row, key) of an LDS tile of planes
+// rows r0 + 4 q .. + 3 and r0 + 16 + 4 q .. + 3 of column c0 + lane % 16
+template <int NP, int STRIDE>
+__device__ __forceinline__ Frag<NP> columns_of(const bf16* m, int plane, int r0, int c0, int lane) {
+  const int j = lane & 15, q = lane >> 4;
+  return read_tr<NP>(m + (r0 + 4 * q + (j >> 2)) * STRIDE + c0 + 4 * (j & 3), plane, 16 * STRIDE);
+}
+
+// four consecutive values of an LDS tile of planes
 template <int NP>
-__device__ __forceinline__ float plane_sum(const bf16* p, int plane) {
-  float x = (float)p[(NP - 1) * plane];
+__device__ __forceinline__ f32x4 plane_sum4(const bf16* p, int plane) {
+  f32x4 x = {0, 0, 0, 0};
 #pragma unroll
-  for (int i = NP - 2; i >= 0; --i) x += (float)p[i * plane];
+  for (int i = NP - 1; i >= 0; --i) {
+    const bf16x4 v = *reinterpret_cast<const bf16x4*>(p + i * plane);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] += (float)v[r];
+  }
   return x;
 }
-__device__ __forceinline__ float sum16(float v) {
-  for (int off = 8; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+
+// value columns 4 q .. + 3 and 16 + 4 q .. + 3 of a row's slice, zeros where there are none
+template <typename IO> struct Values8 {
+  float x[8];
+  __device__ __forceinline__ void load(const IO* p, bool lo, bool hi) {
+    using V = std::conditional_t<sizeof(IO) == 2, bf16x4, f32x4>;
+    const V a = *reinterpret_cast<const V*>(p), b = *reinterpret_cast<const V*>(hi ? p + 16 : p);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      x[r] = lo ? (float)a[r] : 0.0f;
+      x[4 + r] = hi ? (float)b[r] : 0.0f;
+    }
+  }
+};
+
+__device__ __forceinline__ float sum_q(float v) {   // over the lanes of a token
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
 }
 
 template <typename IO, int KP, bool FULL>
-__global__ __launch_bounds__(kThreads) void k_delta_grads(DeltaArgs a) {
+__global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_grads(DeltaArgs a) {
   using L = GradsLds<IO, KP>;
   constexpr int PI = L::PI, KST = L::KST, KT = KP / 16;
+  constexpr int kTokParts = kSlice * C / 4 / kThreads, kKeyParts = kSlice * KP / 4 / kThreads;
   __shared__ __align__(16) bf16 lds[L::elems];
   __shared__ float4 s_row[C];
   __shared__ float s_b[C], s_cum[C], s_beta[C], s_sum[2 * kThreads / 64];
-  bf16 *s_w = lds, *s_d = lds + L::tok, *s_s = lds + 2 * L::tok, *s_e = s_s + L::key;
-  bf16 *s_k = lds, *s_q = lds + L::rows, *s_p = lds + 2 * L::rows, *s_l = s_p + L::pairs;
+  bf16 *const s_w = lds, *const s_d = lds + L::tok, *const s_s = lds + 2 * L::tok;
+  bf16 *const s_k = lds, *const s_q = lds + L::rows, *const s_p = lds + 2 * L::rows;
 
   const auto [b, c, h, g] = chunk_head(a);
   const int64_t bh = b * a.H + h, at = chunk_at(a, bh, c);
   const int64_t t0 = c * C, row0 = b * a.T + t0, left = a.T - t0;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_of(tid), j = lane & 15, q = lane >> 4;
+  const int own = 16 * w + j;
   if (tid < C) {
     s_b[tid] = a.gate[at * kGates + kBeta + tid];
     s_row[tid] = a.row[at * C + tid];
@@ -675,216 +709,227 @@ __global__ __launch_bounds__(kThreads) void k_delta_grads(DeltaArgs a) {
   for (int i = 0; i < 4; ++i) dp[i] = dl[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < KT; ++i) dq[i] = z[i] = x[i] = f32x4{0, 0, 0, 0};
-  const bool row_in = 16 * w + j < left;
-  const int64_t my_row = row0 + (row_in ? 16 * w + j : 0);
+  const bool row_in = own < left;
+  const int64_t my_row = row0 + (row_in ? own : 0);
   const int64_t cols = padded_cols(a.P);
   float es = 0.0f, dr_v = 0.0f;
 
   for (int p0 = 0; p0 < a.P; p0 += kSlice) {
-    __syncthreads();
+    f32x4 vw[kTokParts], vd[kTokParts], vs[kKeyParts], ve[kKeyParts];
 #pragma unroll
-    for (int i = 0; i < kSlice * C / 4 / kThreads; ++i) {
+    for (int i = 0; i < kTokParts; ++i) {
       const int at4 = tid + i * kThreads, p = at4 / (C / 4), t = at4 % (C / 4) * 4;
       const bool in = p0 + p < a.P;
       const int64_t o = (at * cols + (in ? p0 + p : 0)) * C + t;
-      f32x4 vw = *reinterpret_cast<const f32x4*>(a.write + o), vd = *reinterpret_cast<const f32x4*>(a.dright + o);
-      if (!in) vw = vd = f32x4{0, 0, 0, 0};
-      store_split4<3>(&s_w[p * kTokStride + t], kSlice * kTokStride, vw);
-      store_split4<3>(&s_d[p * kTokStride + t], kSlice * kTokStride, vd);
+      vw[i] = *reinterpret_cast<const f32x4*>(a.write + o);
+      vd[i] = *reinterpret_cast<const f32x4*>(a.dright + o);
+      if (!in) vw[i] = vd[i] = f32x4{0, 0, 0, 0};
     }
 #pragma unroll
-    for (int i = 0; i < kSlice * KP / 4 / kThreads; ++i) {
+    for (int i = 0; i < kKeyParts; ++i) {
       const int at4 = tid + i * kThreads, p = at4 / (KP / 4), key = at4 % (KP / 4) * 4;
       const bool in = p0 + p < a.P && key < a.N;
       const int64_t o = (at * cols + (in ? p0 + p : 0)) * KP + (in ? key : 0);
-      f32x4 vs = *reinterpret_cast<const f32x4*>(a.enter + o), ve = *reinterpret_cast<const f32x4*>(a.leave + o);
-      if (!in) vs = ve = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) es = fmaf(vs[e], ve[e], es);
-      store_split4<3>(&s_s[p * KST + key], kSlice * KST, vs);
-      store_split4<3>(&s_e[p * KST + key], kSlice * KST, ve);
+      vs[i] = *reinterpret_cast<const f32x4*>(a.enter + o);
+      ve[i] = *reinterpret_cast<const f32x4*>(a.leave + o);
+      if (!in) vs[i] = ve[i] = f32x4{0, 0, 0, 0};
     }
-    const bool col_in = p0 + 8 * q < a.P;
-    const int64_t pc = h * a.P + (col_in ? p0 + 8 * q : 0);
-    const auto dyf = load_io8<IO>(static_cast<const IO*>(a.dy) + my_row * (a.H * a.P) + pc, row_in && col_in);
-    const auto vf = load_io8<IO>(static_cast<const IO*>(a.v) + my_row * a.v_stride + pc, row_in && col_in);
+    // P is a multiple of 8
+    const bool lo_in = row_in && p0 + 4 * q < a.P, hi_in = row_in && p0 + 16 + 4 * q < a.P;
+    const int64_t pc = h * a.P + (lo_in ? p0 + 4 * q : 0);
+    Values8<IO> dy, v;
+    dy.load(static_cast<const IO*>(a.dy) + my_row * (a.H * a.P) + pc, lo_in, hi_in);
+    v.load(static_cast<const IO*>(a.v) + my_row * a.v_stride + pc, lo_in, hi_in);
     __syncthreads();
-    const auto drf = load_planes_tr<3>(s_d, kSlice * kTokStride, kTokStride, 0, 16 * w, lane);
-    const auto wf = load_planes_tr<3>(s_w, kSlice * kTokStride, kTokStride, 0, 16 * w, lane);
+#pragma unroll
+    for (int i = 0; i < kTokParts; ++i) {
+      const int at4 = tid + i * kThreads, o = at4 / (C / 4) * kPairRow + at4 % (C / 4) * 4;
+      store_split4<3>(&s_w[o], kSlice * kPairRow, vw[i]);
+      store_split4<3>(&s_d[o], kSlice * kPairRow, vd[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kKeyParts; ++i) {
+      const int at4 = tid + i * kThreads, o = at4 / (KP / 4) * KST + at4 % (KP / 4) * 4;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) es = fmaf(vs[i][e], ve[i][e], es);
+      store_split4<3>(&s_s[o], kSlice * KST, vs[i]);
+    }
+    __syncthreads();
+    const auto dyf = split8<PI>(dy.x);
+    const auto drf = columns_of<3, kPairRow>(s_d, kSlice * kPairRow, 0, 16 * w, lane);
+    const auto wf = columns_of<3, kPairRow>(s_w, kSlice * kPairRow, 0, 16 * w, lane);
     {
-      const float beta = s_b[16 * w + j];
-      IO out[8];
+      const float beta = s_b[own];
+      float out[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float d = ((float)drf.p[2][e] + (float)drf.p[1][e]) + (float)drf.p[0][e];
-        float v = (float)vf.p[PI - 1][e];
-#pragma unroll
-        for (int i = PI - 2; i >= 0; --i) v += (float)vf.p[i][e];
-        dr_v = fmaf(d, v, dr_v);
-        out[e] = to_io<IO>(beta * d);
+        dr_v = fmaf(d, v.x[e], dr_v);
+        out[e] = beta * d;
       }
-      if (row_in && col_in) {
-        IO* to = static_cast<IO*>(a.dv) + my_row * a.dv_stride + pc;
-        if constexpr (sizeof(IO) == 2) {
-          *reinterpret_cast<bf16x8*>(to) = bf16x8{out[0], out[1], out[2], out[3], out[4], out[5], out[6], out[7]};
-        } else {
-          *reinterpret_cast<float4*>(to) = make_float4(out[0], out[1], out[2], out[3]);
-          *reinterpret_cast<float4*>(to + 4) = make_float4(out[4], out[5], out[6], out[7]);
-        }
+      IO* const to = static_cast<IO*>(a.dv) + my_row * a.dv_stride + pc;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        if (!(n ? hi_in : lo_in)) continue;
+        const float* o = out + 4 * n;
+        if constexpr (sizeof(IO) == 2)
+          *reinterpret_cast<bf16x4*>(to + 16 * n) = bf16x4{(bf16)o[0], (bf16)o[1], (bf16)o[2], (bf16)o[3]};
+        else
+          *reinterpret_cast<f32x4*>(to + 16 * n) = f32x4{o[0], o[1], o[2], o[3]};
       }
     }
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-      if (jt > w) continue;
-      const auto wb = load_planes_tr<3>(s_w, kSlice * kTokStride, kTokStride, 0, 16 * jt, lane);
-      dp[jt] = mma(dyf, wb, dp[jt]);
-      dl[jt] = mma(drf, wb, dl[jt]);
+    for (int j0 = 0; j0 < 4; j0 += 2) {
+      if (j0 > w) continue;
+      Frag<3> wb[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) wb[i] = columns_of<3, kPairRow>(s_w, kSlice * kPairRow, 0, 16 * (j0 + i), lane);
+      mma_tiles(wb, dyf, dp + j0);
+      mma_tiles(wb, drf, dl + j0);
     }
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-      const auto sb = load_planes_tr<3>(s_s, kSlice * KST, KST, 0, 16 * kt, lane);
-      dq[kt] = mma(dyf, sb, dq[kt]);
-      z[kt] = mma(drf, sb, z[kt]);
-      x[kt] = mma(wf, load_planes_tr<3>(s_e, kSlice * KST, KST, 0, 16 * kt, lane), x[kt]);
+    for (int k0 = 0; k0 < KT; k0 += 2) {
+      Frag<3> sb[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) sb[i] = columns_of<3, KST>(s_s, kSlice * KST, 0, 16 * (k0 + i), lane);
+      mma_tiles(sb, dyf, dq + k0);
+      mma_tiles(sb, drf, z + k0);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kKeyParts; ++i) {
+      const int at4 = tid + i * kThreads;
+      store_split4<3>(&s_s[at4 / (KP / 4) * KST + at4 % (KP / 4) * 4], kSlice * KST, ve[i]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k0 = 0; k0 < KT; k0 += 2) {
+      Frag<3> eb[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) eb[i] = columns_of<3, KST>(s_s, kSlice * KST, 0, 16 * (k0 + i), lane);
+      mma_tiles(eb, wf, x + k0);
     }
   }
-  __syncthreads();
-
   {
-    const int64_t row = row0 + (row_in ? 16 * w + j : left - 1), at = g * a.N + 8 * q;
+    const int64_t row = row0 + (row_in ? own : left - 1), at = g * a.N + 8 * q;
     KeyRow<IO, KP, FULL> kr, qr;
     kr.load(static_cast<const IO*>(a.k) + row * a.k_stride + at, a.N, q);
     qr.load(static_cast<const IO*>(a.q) + row * a.q_stride + at, a.N, q);
+    __syncthreads();
 #pragma unroll
     for (int s = 0; s < KP / 32; ++s) {
       const auto kf = kr.frag(s, a.N, q);
       const auto qf = qr.frag(s, a.N, q);
 #pragma unroll
       for (int i = 0; i < PI; ++i) {
-        const int o = i * C * KST + (16 * w + j) * KST + 32 * s + 8 * q;
+        const int o = i * C * KST + own * KST + 32 * s + 8 * q;
         *reinterpret_cast<bf16x8*>(&s_k[o]) = kf.p[i];
         *reinterpret_cast<bf16x8*>(&s_q[o]) = qf.p[i];
       }
     }
   }
-  // the pairs (i, j) of this wavefront's tokens i, over their decay, stored
-  // [j][i]; times 1/|k_j| for the sums over j
-  float4 rec[4];
-  float gamma[4], eta[4];
+  __syncthreads();
+
+  // the pairs (own token i, earlier token) over their decay; times 1/|k| of the
+  // earlier one they are the right operands of the sums over it
+  const float4 rec = s_row[own], last = s_row[C - 1];
+  const float beta = s_b[own], gamma = exp2_of(rec.z + rec.w), eta = exp2_of((last.z - rec.z) + (last.w - rec.w));
+  f32x4 rk[4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    rec[r] = s_row[16 * w + 4 * q + r];
-    gamma[r] = exp2_of(rec[r].z + rec[r].w);
-    eta[r] = exp2_of((s_row[C - 1].z - rec[r].z) + (s_row[C - 1].w - rec[r].w));
-  }
-#pragma unroll
-  for (int jt = 0; jt < 4; ++jt) {
-    const int cj = 16 * jt + j;
-    const float4 rj = s_row[cj];
-    f32x4 vp, vl;
+  for (int jt = 0; jt < 4; ++jt)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int ri = 16 * w + 4 * q + r;
-      const float dec = exp2_of((rec[r].z - rj.z) + (rec[r].w - rj.w));
-      dp[jt][r] = ri >= cj ? dec * dp[jt][r] : 0.0f;
-      dl[jt][r] = ri > cj ? dec * dl[jt][r] : 0.0f;
-      vp[r] = dp[jt][r] * rj.x;
-      vl[r] = dl[jt][r] * rj.x;
+      const int cj = 16 * jt + 4 * q + r;
+      const float4 rj = s_row[cj];
+      const float dec = exp2_of((rec.z - rj.z) + (rec.w - rj.w));
+      dp[jt][r] = own >= cj ? dec * dp[jt][r] : 0.0f;
+      dl[jt][r] = own > cj ? dec * dl[jt][r] : 0.0f;
+      rk[jt][r] = rj.x;
     }
-    store_split4<3>(&s_p[cj * kTokStride + 16 * w + 4 * q], C * kTokStride, vp);
-    store_split4<3>(&s_l[cj * kTokStride + 16 * w + 4 * q], C * kTokStride, vl);
-  }
-  __syncthreads();
   // K . (eta W E) for the gradient at the chunk's end
   float end_sum = 0.0f;
 #pragma unroll
-  for (int kt = 0; kt < KT; ++kt)
+  for (int kt = 0; kt < KT; ++kt) {
+    dq[kt] *= gamma;
+    z[kt] *= gamma;
+    x[kt] *= eta;
+    const f32x4 k = plane_sum4<PI>(&s_k[own * KST + 16 * kt + 4 * q], C * KST);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      dq[kt][r] *= gamma[r];
-      z[kt][r] *= gamma[r];
-      x[kt][r] *= eta[r];
-      const float k = rec[r].x * plane_sum<PI>(&s_k[(16 * w + 4 * q + r) * KST + 16 * kt + j], C * KST);
-      end_sum = fmaf(k, x[kt][r], end_sum);
-    }
+    for (int r = 0; r < 4; ++r) end_sum = fmaf(k[r], x[kt][r], end_sum);
+  }
+  end_sum *= rec.x;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     if (s > (w >> 1)) continue;
-    const auto pa = load_planes_tr<3>(s_p, C * kTokStride, kTokStride, 32 * s, 16 * w, lane);
-    const auto la = load_planes_tr<3>(s_l, C * kTokStride, kTokStride, 32 * s, 16 * w, lane);
+    const auto pf = right_of<3>(dp[2 * s] * rk[2 * s], dp[2 * s + 1] * rk[2 * s + 1]);
+    const auto lf = right_of<3>(dl[2 * s] * rk[2 * s], dl[2 * s + 1] * rk[2 * s + 1]);
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-      const auto kb = load_planes_tr<PI>(s_k, C * KST, KST, 32 * s, 16 * kt, lane);
-      dq[kt] = mma(pa, kb, dq[kt]);
-      z[kt] = mma(la, kb, z[kt]);
+    for (int k0 = 0; k0 < KT; k0 += 2) {
+      Frag<PI> kb[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) kb[i] = columns_of<PI, KST>(s_k, C * KST, 32 * s, 16 * (k0 + i), lane);
+      mma_tiles(kb, pf, dq + k0);
+      mma_tiles(kb, lf, z + k0);
     }
   }
-  __syncthreads();
-  // the same pairs for the sums over i
+  // the sums over later tokens: pairs [i][j], tiles that a reader of 32 rows meets
 #pragma unroll
-  for (int jt = 0; jt < 4; ++jt) {
-    const int cj = 16 * jt + j;
-    f32x4 vp, vl;
+  for (int pass = 0; pass < 2; ++pass) {
+    const float f = pass ? -beta * rec.x : rec.y;
+    if (pass) __syncthreads();
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      vp[r] = dp[jt][r] * rec[r].y;
-      vl[r] = -dl[jt][r] * s_b[16 * w + 4 * q + r] * rec[r].x;
-    }
-    store_split4<3>(&s_p[cj * kTokStride + 16 * w + 4 * q], C * kTokStride, vp);
-    store_split4<3>(&s_l[cj * kTokStride + 16 * w + 4 * q], C * kTokStride, vl);
-  }
-  __syncthreads();
+    for (int jt = 0; jt < 4; ++jt)
+      if (jt <= (w | 1)) store_split4<3>(&s_p[own * kPairRow + 16 * jt + 4 * q], C * kPairRow, (pass ? dl : dp)[jt] * f);
+    __syncthreads();
+    const bf16* const m = pass ? s_k : s_q;
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    if (s < (w >> 1)) continue;
-    const int o = (16 * w + j) * kTokStride + 32 * s + 8 * q;
-    const auto pa = load_planes<3>(&s_p[o], C * kTokStride);
-    const auto la = load_planes<3>(&s_l[o], C * kTokStride);
+    for (int s = 0; s < 2; ++s) {
+      if (s < (w >> 1)) continue;
+      const auto pf = columns_of<3, kPairRow>(s_p, C * kPairRow, 32 * s, 16 * w, lane);
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-      x[kt] = mma(pa, load_planes_tr<PI>(s_q, C * KST, KST, 32 * s, 16 * kt, lane), x[kt]);
-      x[kt] = mma(la, load_planes_tr<PI>(s_k, C * KST, KST, 32 * s, 16 * kt, lane), x[kt]);
+      for (int k0 = 0; k0 < KT; k0 += 4) {
+        Frag<PI> mb[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mb[i] = columns_of<PI, KST>(m, C * KST, 32 * s, 16 * (k0 + i), lane);
+        mma_tiles(mb, pf, x + k0);
+      }
     }
   }
 
   // row sums, and the gradients of unit keys and scaled unit queries
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int ri = 16 * w + 4 * q + r;
-    const float beta = s_b[ri];
+  {
     float kz = 0.0f, kx = 0.0f, qd = 0.0f;
-    float* pq = a.part_q + ((row0 + ri) * a.H + h) * a.N;
-    float* pk = a.part_k + ((row0 + ri) * a.H + h) * a.N;
+    const int64_t out = ((row0 + own) * a.H + h) * a.N;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
-      const int o = ri * KST + 16 * kt + j;
-      const float k = plane_sum<PI>(&s_k[o], C * KST), u = plane_sum<PI>(&s_q[o], C * KST);
-      kz = fmaf(k, z[kt][r], kz);
-      kx = fmaf(k, x[kt][r], kx);
-      qd = fmaf(u, dq[kt][r], qd);
-      if (ri < left && 16 * kt + j < a.N) {
-        pq[16 * kt + j] = dq[kt][r];
-        pk[16 * kt + j] = x[kt][r] - beta * z[kt][r];
+      const int key = 16 * kt + 4 * q, o = own * KST + key;
+      const f32x4 k = plane_sum4<PI>(&s_k[o], C * KST), u = plane_sum4<PI>(&s_q[o], C * KST);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        kz = fmaf(k[r], z[kt][r], kz);
+        kx = fmaf(k[r], x[kt][r], kx);
+        qd = fmaf(u[r], dq[kt][r], qd);
+      }
+      if (row_in && key < a.N) {
+        *reinterpret_cast<f32x4*>(a.part_q + out + key) = dq[kt];
+        *reinterpret_cast<f32x4*>(a.part_k + out + key) = x[kt] - beta * z[kt];
       }
     }
-    kz = rec[r].x * sum16(kz);
-    kx = rec[r].x * sum16(kx);
-    qd = rec[r].y * sum16(qd);
-    if (j == 0) {
-      s_cum[ri] = qd - beta * kz - kx;
-      s_beta[ri] = -kz;
+    kz = rec.x * sum_q(kz);
+    kx = rec.x * sum_q(kx);
+    qd = rec.y * sum_q(qd);
+    dr_v = sum_q(dr_v);
+    if (q == 0) {
+      s_cum[own] = qd - beta * kz - kx;
+      s_beta[own] = dr_v - kz;
     }
   }
   es = wave_sum64(es);
   end_sum = wave_sum64(end_sum);
-  dr_v += __shfl_xor(dr_v, 16, 64);
-  dr_v += __shfl_xor(dr_v, 32, 64);
   if (lane == 0) {
     s_sum[w] = es;
     s_sum[4 + w] = end_sum;
   }
-  __builtin_amdgcn_wave_barrier();
-  if (q == 0) s_beta[16 * w + j] += dr_v;   // rows of this wavefront
   __syncthreads();
   if (w != 0) return;
 
