@@ -938,62 +938,81 @@ __global__ __launch_bounds__(256 * NG) void k_delta_tokens(DeltaArgs a) {
 //   y = a S.q + u k.q,  S' = a S + u k,  u = b (v - a S.k)
 // NL lanes of four keys share a row; N / 4 of them have keys.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float lanes_sum(float v, int nl) {
-  for (int off = nl >> 1; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+template <int CTRL> __device__ __forceinline__ float dpp_add(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+// sum over aligned groups of NL lanes, 16 or 32: within 16 by lanes' neighbours
+// (quads, halves of 8, of 16) without a trip through LDS
+template <int NL> __device__ __forceinline__ float lanes_sum(float v) {
+  v = dpp_add<0xb1>(v);    // lane ^ 1
+  v = dpp_add<0x4e>(v);    // lane ^ 2
+  v = dpp_add<0x141>(v);   // mirrored within 8
+  v = dpp_add<0x140>(v);   // mirrored within 16
+  return NL == 16 ? v : v + __shfl_xor(v, 16, 64);
 }
 
 template <typename IO, int NL, int ROWS>
 __global__ __launch_bounds__(kThreads) void k_delta_step(DeltaArgs a) {
   constexpr int per_pass = kThreads / NL;
-  const int runs = (a.P + per_pass * ROWS - 1) / (per_pass * ROWS);
-  const int64_t bh = blockIdx.x / runs, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
+  const uint32_t runs = (uint32_t)(a.P + per_pass * ROWS - 1) / (per_pass * ROWS), H = (uint32_t)a.H;
+  const uint32_t slice = blockIdx.x / runs;
+  const int64_t bh = slice, b = slice / H, h = slice % H, g = (uint32_t)h / (H / (uint32_t)a.G);
   const int p0 = (int)(blockIdx.x % runs) * per_pass * ROWS + threadIdx.x / NL;
   const int key = 4 * (threadIdx.x % NL);
   const bool key_in = key < a.N;
   float4* state = reinterpret_cast<float4*>(a.state + bh * a.P * a.N) + (key_in ? key / 4 : 0);
-  float4 s[ROWS];
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int p = min(p0 + i * per_pass, a.P - 1);
-    const f32x4 t = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(state + (int64_t)p * (a.N / 4)));
-    s[i] = make_float4(t[0], t[1], t[2], t[3]);
-  }
-  float kv[4], qv[4], kk = 0.0f, qq = 0.0f, kq = 0.0f;
+  // all loads on every path, the token's before the state's: a wait for a row of
+  // the state then covers that row and no store
+  IO kraw[4], qraw[4], vraw[ROWS];
   const IO* kr = static_cast<const IO*>(a.k) + b * a.k_stride + g * a.N + (key_in ? key : 0);
   const IO* qr = static_cast<const IO*>(a.q) + b * a.q_stride + g * a.N + (key_in ? key : 0);
+  const IO* vr = static_cast<const IO*>(a.v) + b * a.v_stride + h * a.P;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    kv[e] = key_in ? to_f32(kr[e]) : 0.0f;
-    qv[e] = key_in ? to_f32(qr[e]) : 0.0f;
+    kraw[e] = kr[e];
+    qraw[e] = qr[e];
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) vraw[i] = vr[min(p0 + i * per_pass, a.P - 1)];
+  f32x4 s[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i)
+    s[i] = __builtin_nontemporal_load(
+        reinterpret_cast<const f32x4*>(state + (int64_t)min(p0 + i * per_pass, a.P - 1) * (a.N / 4)));
+  __builtin_amdgcn_sched_barrier(0);
+  float kv[4], qv[4], kk = 0.0f, qq = 0.0f, kq = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    kv[e] = key_in ? to_f32(kraw[e]) : 0.0f;
+    qv[e] = key_in ? to_f32(qraw[e]) : 0.0f;
     kk = fmaf(kv[e], kv[e], kk);
     qq = fmaf(qv[e], qv[e], qq);
     kq = fmaf(kv[e], qv[e], kq);
   }
-  kk = lanes_sum(kk, NL);
-  qq = lanes_sum(qq, NL);
-  kq = lanes_sum(kq, NL);
+  kk = lanes_sum<NL>(kk);
+  qq = lanes_sum<NL>(qq);
+  kq = lanes_sum<NL>(kq);
   const float rk = a.unit ? 1.0f / sqrtf(kk + a.norm_eps) : 1.0f;
   const float rq = a.scale * (a.unit ? 1.0f / sqrtf(qq + a.norm_eps) : 1.0f);
   const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
   const float d = delta_of(a.dt[bh] + bias, a.softplus, a.dt_min, a.dt_max);
   const float alpha = expf(d * a.A[h]);
   const float beta = a.sigmoid ? sigmoid_of(a.beta[bh]) : a.beta[bh];
-  const IO* vr = static_cast<const IO*>(a.v) + b * a.v_stride + h * a.P;
   IO* yr = static_cast<IO*>(a.y) + bh * a.P;
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     const int p = p0 + i * per_pass;
-    float sk = s[i].x * kv[0] + s[i].y * kv[1] + s[i].z * kv[2] + s[i].w * kv[3];
-    float sq = s[i].x * qv[0] + s[i].y * qv[1] + s[i].z * qv[2] + s[i].w * qv[3];
-    sk = lanes_sum(key_in ? sk : 0.0f, NL);
-    sq = lanes_sum(key_in ? sq : 0.0f, NL);
+    float sk = s[i][0] * kv[0] + s[i][1] * kv[1] + s[i][2] * kv[2] + s[i][3] * kv[3];
+    float sq = s[i][0] * qv[0] + s[i][1] * qv[1] + s[i][2] * qv[2] + s[i][3] * qv[3];
+    sk = lanes_sum<NL>(key_in ? sk : 0.0f);
+    sq = lanes_sum<NL>(key_in ? sq : 0.0f);
     if (p < a.P) {
-      const float u = beta * (to_f32(vr[p]) - alpha * rk * sk), uk = u * rk;
-      if (key_in)
-        __builtin_nontemporal_store(f32x4{fmaf(alpha, s[i].x, uk * kv[0]), fmaf(alpha, s[i].y, uk * kv[1]),
-                                          fmaf(alpha, s[i].z, uk * kv[2]), fmaf(alpha, s[i].w, uk * kv[3])},
-                                    reinterpret_cast<f32x4*>(state + (int64_t)p * (a.N / 4)));
+      const float u = beta * (to_f32(vraw[i]) - alpha * rk * sk), uk = u * rk;
+      if (key_in) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][e] = fmaf(alpha, s[i][e], uk * kv[e]);
+        __builtin_nontemporal_store(s[i], reinterpret_cast<f32x4*>(state + (int64_t)p * (a.N / 4)));
+      }
       if (threadIdx.x % NL == 0) yr[p] = to_io<IO>(rq * (alpha * sq + uk * kq));
     }
   }
@@ -1030,9 +1049,9 @@ hipError_t launch_scan(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
 template <typename IO>
 hipError_t launch_step(const DeltaArgs& a, hipStream_t stream) {
   auto go = [&](auto nl) {
-    constexpr int NL = decltype(nl)::value, per_pass = kThreads / NL;
-    const int64_t runs = (a.P + 2 * per_pass - 1) / (2 * per_pass);
-    hipLaunchKernelGGL((k_delta_step<IO, NL, 2>), dim3((unsigned)(a.Bt * a.H * runs)), dim3(kThreads), 0,
+    constexpr int NL = decltype(nl)::value, per_pass = kThreads / NL, ROWS = 2;
+    const int64_t runs = (a.P + ROWS * per_pass - 1) / (ROWS * per_pass);
+    hipLaunchKernelGGL((k_delta_step<IO, NL, ROWS>), dim3((unsigned)(a.Bt * a.H * runs)), dim3(kThreads), 0,
                        stream, a);
   };
   if (a.N <= 64) go(std::integral_constant<int, 16>{});
