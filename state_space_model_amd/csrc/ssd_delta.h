@@ -466,16 +466,24 @@ __device__ __forceinline__ void landed() {
 __device__ __forceinline__ void lds_free() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // Value columns of a chain whose four wavefronts share them and split the tokens
-// (tokens(NT), 16 NT columns), or a chain of wavefronts that own 16 each
-// (columns()).  A chain fills a compute unit's LDS.  Sharing makes a step as short
-// as it gets and is taken while every chain has a unit to itself; owning needs
-// less than half the work of LDS and VALU for as many columns.
+// (tokens(NG): NG such groups of 16 columns to a workgroup, which fills a compute
+// unit's LDS), or a chain of wavefronts that own 16 each (columns()).  Sharing
+// makes a step as short as it gets and is taken while every chain has a unit to
+// itself; owning needs less than half the work of LDS and VALU for as many
+// columns, and two workgroups share a unit.  bfloat16, 128 keys, shared in pairs
+// against owned: 4096 tokens of 80 heads of 64 values (160 pairs) 171 against 258
+// us, 136 heads (272) 345 against 328; 8 x 16384 tokens of 64 heads (1024) 2700
+// against 1800; the gradients' chains of 36 heads of 128 values (288) 354 against
+// 392, where the rule loses a tenth.
+//
+// `ways`: chains that one launch runs for every column (the gradients' both of 32
+// heads: 128 and 187 us one after the other, 265 us together in pairs)
 template <typename F, typename G>
-hipError_t chain_of(const DeltaArgs& a, F&& tokens, G&& columns) {
-  const int64_t groups = a.Bt * a.H * ((a.P + 15) / 16), pairs = a.Bt * a.H * ((a.P + 31) / 32);
+hipError_t chain_of(const DeltaArgs& a, int ways, F&& tokens, G&& columns) {
+  const int64_t heads = ways * a.Bt * a.H, groups = heads * ((a.P + 15) / 16), pairs = heads * ((a.P + 31) / 32);
   if (groups <= 256) tokens(std::integral_constant<int, 1>{}, (unsigned)groups);
   else if (pairs <= 256) tokens(std::integral_constant<int, 2>{}, (unsigned)pairs);
-  else columns((unsigned)(a.Bt * a.H * ((a.P + 63) / 64)));
+  else columns((unsigned)(heads * ((a.P + 63) / 64)));
   return hipGetLastError();
 }
 

@@ -56,7 +56,7 @@ ssd_status check(const ssd_delta_desc* d, bool step, bool grads, Sizes* s) {
   const int64_t chunks = step ? 1 : (d->seqlen / kDeltaChunk + (d->seqlen % kDeltaChunk != 0));
   int64_t bh = 0, groups = 0, tokens = 0, state = 0, y = 0, gates = 0;
   if (!mul_ok(d->batch, d->nheads, &bh) || !mul_ok(bh, chunks, &groups) || groups > kMaxGroups ||
-      !mul_ok(bh, (d->headdim + 15) / 16, &groups) || groups > kMaxGroups ||
+      !mul_ok(bh, (grads ? 2 : 1) * ((d->headdim + 15) / 16), &groups) || groups > kMaxGroups ||
       !mul_ok(d->batch, step ? 1 : d->seqlen, &tokens) ||
       !span_of(tokens, gn, d->q_stride, es, &s->q) || !span_of(tokens, gn, d->k_stride, es, &s->k) ||
       !span_of(tokens, hp, d->v_stride, es, &s->v) || !mul_ok(tokens, hp, &y) || y > INT64_MAX / 16 ||

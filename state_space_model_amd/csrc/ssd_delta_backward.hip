@@ -6,7 +6,7 @@
 // [P, N] that leaves the chunk:
 //   dW  = (D o Q K^T)^T dY + diag(eta) K E^T;    dR = (1 + L)^-T dW
 //   E'  = gamma_last E + dY^T diag(gamma) Q - dR^T diag(b gamma) K   (entering it)
-// chunk by chunk from the last (k_delta_back_chain), after a forward pass that
+// chunk by chunk from the last (back_chain), after a forward pass that
 // keeps the states and the writes.  Then, all chunks at once (k_delta_grads):
 //   dP = D o dY W^T (i >= j),  dL = D o dR W^T (i > j)
 //   dQ = diag(gamma) dY S + dP K;        Z = diag(gamma) dR S + dL K
@@ -19,26 +19,32 @@
 // of a token's own decay is the sum of dcum from it to the chunk's end.  Last,
 // the gradients of unit keys and queries are summed over the heads that share
 // them and taken through the normalisation: du = r (dU - U (U.dU)), r = 1/|u|.
-#include "ssd_delta.h"
+#include "ssd_delta_chains.h"
 
 namespace ssd {
 namespace delta {
 namespace {
 
 // As k_delta_chain, from the last chunk to the first.
+template <typename IO, int KP, int NT> struct BackChainLds {
+  static constexpr int PI = Planes<IO>::in, W = 16 * NT, tok = W * kTokStride;
+  static constexpr int k = 0, q = k + PI * C * (KP + 16), s = q + PI * C * (KP + 16), y = s + 3 * W * (KP + 8);
+  static constexpr int g = y + PI * tok, r = g + 3 * tok, e = r + 3 * tok, elems = e + 3 * tok;
+};
+
 template <typename IO, int KP, bool FULL, int NT>
-__global__ __launch_bounds__(kThreads) void k_delta_back_chain(DeltaArgs a) {
+__device__ __forceinline__ void back_chain(const DeltaArgs& a, bf16* lds, int64_t id) {
+  using L = BackChainLds<IO, KP, NT>;
   constexpr int PI = Planes<IO>::in;
   constexpr int KS = KP / 32, KST = KP + 8, KTR = KP + 16, KT = KP / 64, W = 16 * NT;
-  __shared__ __align__(16) bf16 s_k[PI * C * KTR], s_q[PI * C * KTR];
-  __shared__ __align__(16) bf16 s_s[3 * W * KST];           // E, value-major
-  __shared__ __align__(16) bf16 s_y[PI * W * kTokStride];   // dY
-  __shared__ __align__(16) bf16 s_g[3 * W * kTokStride];    // diag(gamma / |q|) dY
-  __shared__ __align__(16) bf16 s_r[3 * W * kTokStride];    // dW
-  __shared__ __align__(16) bf16 s_e[3 * W * kTokStride];    // -diag(b gamma / |k|) dR
+  bf16 *const s_k = lds + L::k, *const s_q = lds + L::q;
+  bf16* const s_s = lds + L::s;   // E, value-major
+  bf16* const s_y = lds + L::y;   // dY
+  bf16* const s_g = lds + L::g;   // diag(gamma / |q|) dY
+  bf16* const s_r = lds + L::r;   // dW
+  bf16* const s_e = lds + L::e;   // -diag(b gamma / |k|) dR
 
   const int slices = (a.P + W - 1) / W;
-  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
   const int64_t bh = id / slices, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
   const int col0 = (int)(id % slices) * W;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_of(tid), j = lane & 15, q = lane >> 4;
@@ -244,15 +250,13 @@ template <int KP, int NW> struct BackLds {
 };
 
 template <int KP, bool FULL>
-__global__ __launch_bounds__(256, 2) void k_delta_back_columns(DeltaArgs a) {
+__device__ __forceinline__ void back_columns(const DeltaArgs& a, bf16* lds, int64_t id) {
   constexpr int NW = 4, KS = KP / 32, KT = KP / 16, W = 16 * NW;
   using L = BackLds<KP, NW>;
   using Keys = KeyTile<KP, NW>;
   using Cols = ColumnTile<NW>;
-  __shared__ __align__(1024) bf16 lds[L::elems];
 
   const int slices = (a.P + W - 1) / W;
-  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
   const int64_t bh = id / slices, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
   const int col0 = (int)(id % slices) * W;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_of(tid), j = lane & 15, q = lane >> 4;
@@ -427,15 +431,13 @@ template <int KP, int NG> struct BackTokensLds {
 };
 
 template <int KP, bool FULL, int NG>
-__global__ __launch_bounds__(256 * NG) void k_delta_back_tokens(DeltaArgs a) {
+__device__ __forceinline__ void back_tokens(const DeltaArgs& a, bf16* lds, int64_t id) {
   using L = BackTokensLds<KP, NG>;
   using Keys = typename L::Keys;
   constexpr int KS = KP / 32, KT = KP / 64, W = L::W, NW = 4 * NG;
   constexpr int kKeyLoads = Keys::kLoads, kTriLoads = (3 * kTriFrags + NW - 1) / NW;
-  __shared__ __align__(1024) bf16 lds[L::elems];
 
   const int slices = (a.P + W - 1) / W;
-  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
   const int64_t bh = id / slices, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
   const int col0 = (int)(id % slices) * W;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_of(tid), j = lane & 15, q = lane >> 4;
@@ -618,6 +620,37 @@ __global__ __launch_bounds__(256 * NG) void k_delta_back_tokens(DeltaArgs a) {
       if (key[t] < a.N) *reinterpret_cast<f32x4*>(a.dh0 + (bh * a.P + col) * a.N + key[t]) = st[t];
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no request may reach LDS after this
+}
+
+// ---------------------------------------------------------------------------
+// Both chains in one launch: neither needs the other, and each is a sequence of
+// dependent steps that leaves a compute unit idle most of the time.  The first
+// half of the workgroups takes the longer one, from the last chunk.
+// ---------------------------------------------------------------------------
+template <typename F, typename G> __device__ __forceinline__ void both_ways(F&& back, G&& forth) {
+  const unsigned half = gridDim.x / 2;
+  if (blockIdx.x < half) back(xcd_remap(blockIdx.x, half));
+  else forth(xcd_remap(blockIdx.x - half, half));
+}
+constexpr int larger(int a, int b) { return a > b ? a : b; }
+
+template <typename IO, int KP, bool FULL>
+__global__ __launch_bounds__(kThreads) void k_delta_both_chains(DeltaArgs a) {
+  __shared__ __align__(16) bf16 lds[larger(BackChainLds<IO, KP, 1>::elems, ChainLds<IO, KP, 1, true>::elems)];
+  both_ways([&](int64_t id) { back_chain<IO, KP, FULL, 1>(a, lds, id); },
+            [&](int64_t id) { chain<IO, KP, FULL, 1, true>(a, lds, id); });
+}
+template <int KP, bool FULL, int NG>
+__global__ __launch_bounds__(256 * NG) void k_delta_both_tokens(DeltaArgs a) {
+  __shared__ __align__(1024) bf16 lds[larger(BackTokensLds<KP, NG>::elems, TokensLds<KP, NG, true>::elems)];
+  both_ways([&](int64_t id) { back_tokens<KP, FULL, NG>(a, lds, id); },
+            [&](int64_t id) { tokens_chain<KP, FULL, NG, true>(a, lds, id); });
+}
+template <int KP, bool FULL>
+__global__ __launch_bounds__(256, 2) void k_delta_both_columns(DeltaArgs a) {
+  __shared__ __align__(1024) bf16 lds[larger(BackLds<KP, 4>::elems, ColumnsLds<KP, 4, true>::elems)];
+  both_ways([&](int64_t id) { back_columns<KP, FULL>(a, lds, id); },
+            [&](int64_t id) { columns_chain<KP, FULL, true>(a, lds, id); });
 }
 
 // ---------------------------------------------------------------------------
@@ -1041,19 +1074,18 @@ hipError_t launch_grads(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
     constexpr int KP = decltype(kp)::value;
     constexpr bool FULL = decltype(full)::value;
     const unsigned chunks = (unsigned)(a.Bt * a.H * a.Nc);
-    const int64_t heads = a.Bt * a.H;
     if constexpr (sizeof(IO) == 2) {
-      chain_of(
-          a,
+      (void)chain_of(
+          a, 2,
           [&](auto ng, unsigned groups) {
-            hipLaunchKernelGGL((k_delta_back_tokens<KP, FULL, ng.value>), dim3(groups), dim3(256 * ng.value), 0, stream,
+            hipLaunchKernelGGL((k_delta_both_tokens<KP, FULL, ng.value>), dim3(groups), dim3(256 * ng.value), 0, stream,
                                a);
           },
           [&](unsigned groups) {
-            hipLaunchKernelGGL((k_delta_back_columns<KP, FULL>), dim3(groups), dim3(256), 0, stream, a);
+            hipLaunchKernelGGL((k_delta_both_columns<KP, FULL>), dim3(groups), dim3(256), 0, stream, a);
           });
     } else {
-      hipLaunchKernelGGL((k_delta_back_chain<IO, KP, FULL, 1>), dim3((unsigned)(heads * ((a.P + 15) / 16))),
+      hipLaunchKernelGGL((k_delta_both_chains<IO, KP, FULL>), dim3((unsigned)(2 * a.Bt * a.H * ((a.P + 15) / 16))),
                          dim3(kThreads), 0, stream, a);
     }
     hipLaunchKernelGGL((k_delta_grads<IO, KP, FULL>), dim3(chunks), dim3(kThreads), 0, stream, a);
@@ -1070,7 +1102,7 @@ hipError_t launch_grads(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
 }  // namespace delta
 
 hipError_t launch_delta_scan_backward(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
-  const hipError_t e = launch_delta_states(a, io_bf16, stream);
+  const hipError_t e = launch_delta_matrices(a, io_bf16, stream);
   return e != hipSuccess ? e : delta::launch_grads(a, io_bf16, stream);
 }
 

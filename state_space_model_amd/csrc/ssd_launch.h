@@ -242,7 +242,7 @@ constexpr int kDeltaMaxP = 256;   // value sizes: multiples of 8 up to here
 // Bytes of the scan's workspace and of its gradients'; with `ws` they are laid
 // out there.
 size_t delta_workspace(DeltaArgs& a, bool io_bf16, bool grads, char* ws);
-hipError_t launch_delta_states(const DeltaArgs& a, bool io_bf16, hipStream_t stream);  // the gradients' forward part
+hipError_t launch_delta_matrices(const DeltaArgs& a, bool io_bf16, hipStream_t stream);  // the gradients' first part
 hipError_t launch_delta_scan_backward(const DeltaArgs& a, bool io_bf16, hipStream_t stream);
 hipError_t launch_delta_scan(const DeltaArgs& a, bool io_bf16, hipStream_t stream);
 hipError_t launch_delta_step(const DeltaArgs& a, bool io_bf16, hipStream_t stream);
