@@ -264,6 +264,17 @@ template <typename F> __device__ __forceinline__ void by_wave(int w, F&& f) {
   else f(std::integral_constant<int, 3>{});
 }
 
+template <int CTRL> __device__ __forceinline__ float dpp_add(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+// sum over 16 lanes by neighbours (quads, halves of 8, of 16), without a trip through LDS
+__device__ __forceinline__ float sum_of_16(float v) {
+  v = dpp_add<0xb1>(v);           // lane ^ 1
+  v = dpp_add<0x4e>(v);           // lane ^ 2
+  v = dpp_add<0x141>(v);          // mirrored within 8
+  return dpp_add<0x140>(v);       // mirrored within 16
+}
+
 // sum over a wavefront
 __device__ __forceinline__ float wave_sum64(float v) {
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);

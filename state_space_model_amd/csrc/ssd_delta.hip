@@ -255,16 +255,9 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 4 : 2) void k_delta_pre
 //   y = a S.q + u k.q,  S' = a S + u k,  u = b (v - a S.k)
 // NL lanes of four keys share a row; N / 4 of them have keys.
 // ---------------------------------------------------------------------------
-template <int CTRL> __device__ __forceinline__ float dpp_add(float v) {
-  return v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
-}
-// sum over aligned groups of NL lanes, 16 or 32: within 16 by lanes' neighbours
-// (quads, halves of 8, of 16) without a trip through LDS
+// sum over aligned groups of NL lanes, 16 or 32
 template <int NL> __device__ __forceinline__ float lanes_sum(float v) {
-  v = dpp_add<0xb1>(v);    // lane ^ 1
-  v = dpp_add<0x4e>(v);    // lane ^ 2
-  v = dpp_add<0x141>(v);   // mirrored within 8
-  v = dpp_add<0x140>(v);   // mirrored within 16
+  v = sum_of_16(v);
   return NL == 16 ? v : v + __shfl_xor(v, 16, 64);
 }
 

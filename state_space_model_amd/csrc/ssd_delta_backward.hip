@@ -723,7 +723,8 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_gra
   constexpr int kTokParts = kSlice * C / 4 / kThreads, kKeyParts = kSlice * KP / 4 / kThreads;
   __shared__ __align__(16) bf16 lds[L::elems];
   __shared__ float4 s_row[C];
-  __shared__ float s_b[C], s_cum[C], s_beta[C], s_sum[2 * kThreads / 64];
+  __shared__ float s_b[C], s_from[C], s_to[C], s_beta[C], s_sum[kThreads / 64];
+  __shared__ __align__(16) float s_over[kThreads / 64][C];
   bf16 *const s_w = lds, *const s_d = lds + L::tok, *const s_s = lds + 2 * L::tok;
   bf16 *const s_k = lds, *const s_q = lds + L::rows, *const s_p = lds + 2 * L::rows;
 
@@ -879,18 +880,69 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_gra
       dl[jt][r] = own > cj ? dec * dl[jt][r] : 0.0f;
       rk[jt][r] = rj.x;
     }
-  // K . (eta W E) for the gradient at the chunk's end
-  float end_sum = 0.0f;
+  // What a decay's gradient is a sum of, for token t: pairs with t between them
+  // (below), what later tokens read of the entering state (from), what earlier
+  // ones wrote that reaches the end (to), and the state that passes through.  No
+  // term is in the sum and taken out again, which keeps float32's rounding at that
+  // of the result (differences of row and column sums: five times as much).
+  float from = 0.0f, to = 0.0f, kz = 0.0f;
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) {
     dq[kt] *= gamma;
     z[kt] *= gamma;
     x[kt] *= eta;
-    const f32x4 k = plane_sum4<PI>(&s_k[own * KST + 16 * kt + 4 * q], C * KST);
+    const int o = own * KST + 16 * kt + 4 * q;
+    const f32x4 k = plane_sum4<PI>(&s_k[o], C * KST), u = plane_sum4<PI>(&s_q[o], C * KST);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) end_sum = fmaf(k[r], x[kt][r], end_sum);
+    for (int r = 0; r < 4; ++r) {
+      from = fmaf(u[r], dq[kt][r], from);
+      kz = fmaf(k[r], z[kt][r], kz);
+      to = fmaf(k[r], x[kt][r], to);
+    }
   }
-  end_sum *= rec.x;
+  kz = rec.x * sum_q(kz);
+  from = rec.y * sum_q(from) - beta * kz;
+  to = rec.x * sum_q(to);
+  {
+    float before = 0.0f, pair_kz = 0.0f;   // the pairs (own, j) with j in earlier tiles
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) {
+      if (jt > w) continue;
+      f32x4 kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < KP / 32; ++s) {
+        const auto ka = load_planes<PI>(&s_k[(16 * jt + j) * KST + 32 * s + 8 * q], C * KST);
+        kk = mma(ka, load_planes<PI>(&s_k[own * KST + 32 * s + 8 * q], C * KST), kk);
+        qk = mma(ka, load_planes<PI>(&s_q[own * KST + 32 * s + 8 * q], C * KST), qk);
+      }
+      float sum = 0.0f, up[4];   // over the lane's pairs, up to each
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float lk = rec.x * dl[jt][r] * rk[jt][r] * kk[r];
+        pair_kz += lk;
+        up[r] = sum;
+        sum += fmaf(rec.y * dp[jt][r] * rk[jt][r], qk[r], -beta * lk);
+      }
+      float upto = sum;          // over the lanes of the token, up to this one
+      float o = __shfl_up(upto, 16, 64);
+      upto += q >= 1 ? o : 0.0f;
+      o = __shfl_up(upto, 32, 64);
+      upto += q >= 2 ? o : 0.0f;
+      o = __shfl_up(upto, 16, 64);
+      const float base = before + (q >= 1 ? o : 0.0f);
+      f32x4 over;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) over[r] = sum_of_16(own >= 16 * jt + 4 * q + r ? base + up[r] : 0.0f);
+      if (j == 0) *reinterpret_cast<f32x4*>(&s_over[w][16 * jt + 4 * q]) = over;
+      before += __shfl(upto, 48 + j, 64);
+    }
+    dr_v = sum_q(dr_v) - kz - sum_q(pair_kz);
+    if (q == 0) {
+      s_from[own] = from;
+      s_to[own] = to;
+      s_beta[own] = dr_v;
+    }
+  }
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     if (s > (w >> 1)) continue;
@@ -929,51 +981,35 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_gra
     }
   }
 
-  // row sums, and the gradients of unit keys and scaled unit queries
+  // the gradients of unit keys and scaled unit queries
   {
-    float kz = 0.0f, kx = 0.0f, qd = 0.0f;
     const int64_t out = ((row0 + own) * a.H + h) * a.N;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
-      const int key = 16 * kt + 4 * q, o = own * KST + key;
-      const f32x4 k = plane_sum4<PI>(&s_k[o], C * KST), u = plane_sum4<PI>(&s_q[o], C * KST);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        kz = fmaf(k[r], z[kt][r], kz);
-        kx = fmaf(k[r], x[kt][r], kx);
-        qd = fmaf(u[r], dq[kt][r], qd);
-      }
+      const int key = 16 * kt + 4 * q;
       if (row_in && key < a.N) {
         *reinterpret_cast<f32x4*>(a.part_q + out + key) = dq[kt];
         *reinterpret_cast<f32x4*>(a.part_k + out + key) = x[kt] - beta * z[kt];
       }
     }
-    kz = rec.x * sum_q(kz);
-    kx = rec.x * sum_q(kx);
-    qd = rec.y * sum_q(qd);
-    dr_v = sum_q(dr_v);
-    if (q == 0) {
-      s_cum[own] = qd - beta * kz - kx;
-      s_beta[own] = dr_v - kz;
-    }
   }
   es = wave_sum64(es);
-  end_sum = wave_sum64(end_sum);
-  if (lane == 0) {
-    s_sum[w] = es;
-    s_sum[4 + w] = end_sum;
-  }
+  if (lane == 0) s_sum[w] = es;
   __syncthreads();
   if (w != 0) return;
 
   // token `lane`: its decay and write strength
-  const float all = a.whole[at] * ((s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3])) +
-                    ((s_sum[4] + s_sum[5]) + (s_sum[6] + s_sum[7]));
-  float dg = s_cum[lane] + (lane == C - 1 ? all : 0.0f);
+  float from_on = s_from[lane], to_before = s_to[lane];
   for (int off = 1; off < 64; off <<= 1) {
-    const float o = __shfl_down(dg, off, 64);
-    if (lane + off < 64) dg += o;
+    const float later = __shfl_down(from_on, off, 64), earlier = __shfl_up(to_before, off, 64);
+    from_on += lane + off < 64 ? later : 0.0f;
+    to_before += lane >= off ? earlier : 0.0f;
   }
+  to_before = __shfl_up(to_before, 1, 64);
+  float dg = lane > 0 ? to_before : 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dg += i >= lane / 16 ? s_over[i][lane] : 0.0f;
+  dg += from_on + a.whole[at] * ((s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]));
   const bool in = lane < left;
   const int64_t th = (row0 + (in ? lane : 0)) * a.H + h;
   const float zt = a.dt[th] + (a.dt_bias ? a.dt_bias[h] : 0.0f);
