@@ -682,7 +682,8 @@ typedef struct {
  * of q, k, v, dt or beta reaches the outputs of its chunk, earlier tokens of
  * the chunk included, and of later ones; no other head that does not share it
  * and no other batch row.  The bits of a sequence do not depend on the batch.
- * Bt H ceil(T/64) and Bt H ceil(P/16) below 2^24, else SSD_ERR_UNSUPPORTED.
+ * Bt H ceil(T/64) and Bt H ceil(P/16) below 2^24 and strides up to 2^25 - 512
+ * elements, else SSD_ERR_UNSUPPORTED.
  */
 size_t ssd_delta_scan_workspace_bytes(const ssd_delta_desc* desc);
 ssd_status ssd_delta_scan(const ssd_delta_desc* desc, const void* q, const void* k, const void* v,
@@ -722,8 +723,8 @@ ssd_status ssd_delta_step(const ssd_delta_desc* desc, float* state, const void* 
  * All sums are float32 or wider in an order that depends on the shape alone
  * (no atomics).  Outputs may not overlap any input, the workspace or each
  * other.  batch == 0 or seqlen == 0 writes zeros to dA and ddt_bias, and
- * dfinal_state (or zeros) to dinitial_state.  Sizes as ssd_delta_scan, and
- * 2 Bt T G below 2^27.
+ * dfinal_state (or zeros) to dinitial_state.  Sizes as ssd_delta_scan, but
+ * 2 Bt H ceil(P/16) below 2^24, and 2 Bt T G below 2^27.
  */
 size_t ssd_delta_scan_backward_workspace_bytes(const ssd_delta_desc* desc);
 ssd_status ssd_delta_scan_backward(const ssd_delta_desc* desc, const void* q, const void* k,

@@ -9,8 +9,11 @@
 //   Y    = scale (diag(gamma) Q S^T + (D o Q K^T)_(i >= j) W)
 //   S'   = gamma_last S + W^T diag(e^(cum_last - cum)) K
 // k_delta_prep forms (1 + L)^-1 and D o Q K^T of every chunk, which need no
-// state, in parallel; k_delta_chain walks the chunks of one head and a slice of
-// its value columns in order, the state in matrix-core accumulators.
+// state, in parallel; a chain (ssd_delta_chains.h) walks the chunks of one head
+// and a slice of its value columns in order, the state in matrix-core
+// accumulators.  64 tokens: the work on states falls with the chunk's length, that
+// on pairs and the inverse grows with it, and a chunk of 128 would not leave its
+// matrices room in LDS.
 #include "ssd_delta_chains.h"
 
 namespace ssd {
@@ -24,13 +27,20 @@ namespace {
 // transposed: a result's lane then holds four consecutive columns of its row,
 // and two tiles of columns are a fragment of the matrix as it is (ssd_delta.h).
 //
-// The inverse X of 1 + L: the diagonal 16 x 16 blocks by back substitution, a
-// lane a row (X (1 + L) = 1: x_c = [c = row] - sum_{m > c} x_m L_mc); the blocks
-// left of them, nearest first, from X_ij = -(sum_{j < m <= i} X_im L_mj) X_jj on
-// the float32 matrix core, transposed.
+// The inverse X of 1 + L: the diagonal 8 x 8 blocks by back substitution, a
+// lane a row (X (1 + L) = 1: x_c = [c = row] - sum_{m > c} x_m L_mc); what is
+// left of them, first within blocks of 16, then by blocks of 16, nearest first,
+// from X_ij = -(sum_{j < m <= i} X_im L_mj) X_jj on the float32 matrix core,
+// transposed.  (16 x 16 blocks by substitution: a hundred dependent instructions
+// more a wavefront.)
 //
 // GRADS: for the gradients, whose chain from the last chunk needs both matrices
 // transposed and no output.
+//
+// Bound by its instructions: 8 x 16384 tokens of 64 heads in bfloat16 1440 us (the
+// vector units busy half of it, 3.2 TB/s), 4096 tokens of 80 heads with keys of
+// their own 64 us (5.0 TB/s).  bfloat16 keeps to 128 registers for six workgroups
+// to a compute unit; float32's planes need more.
 template <typename IO, int KP, bool FULL, bool GRADS>
 __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 4 : 2) void k_delta_prep(DeltaArgs a) {
   constexpr int PI = Planes<IO>::in, PY = Planes<IO>::y;
@@ -253,7 +263,11 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 4 : 2) void k_delta_pre
 // One token.  A row p of the state needs two dot products, S k and S q; the
 // token's own part of y is its write times k.q.
 //   y = a S.q + u k.q,  S' = a S + u k,  u = b (v - a S.k)
-// NL lanes of four keys share a row; N / 4 of them have keys.
+// NL lanes of four keys share a row; N / 4 of them have keys.  Bound by memory:
+// 64 sequences of 80 heads of 64 x 128 55 us, 6.1 TB/s of states read and written
+// (the token's loads behind the state's, and lane sums through LDS: 79); one
+// sequence 4.1 us, a launch.  Two rows a lane: four take 56 and 4.4, eight 56 and
+// 5.0.
 // ---------------------------------------------------------------------------
 // sum over aligned groups of NL lanes, 16 or 32
 template <int NL> __device__ __forceinline__ float lanes_sum(float v) {

@@ -46,7 +46,8 @@ ssd_status check(const ssd_delta_desc* d, bool step, bool grads, Sizes* s) {
     return SSD_ERR_INVALID_ARG;
   // the 64 rows of a chunk count in 32 bits of bytes
   constexpr int64_t kMaxStride = (1 << 25) - 512;
-  if (d->q_stride > kMaxStride || d->k_stride > kMaxStride || d->v_stride > kMaxStride || d->headdim % 8 != 0 || d->headdim > SSD_DELTA_MAX_P || d->dstate % 8 != 0 ||
+  if (d->q_stride > kMaxStride || d->k_stride > kMaxStride || d->v_stride > kMaxStride ||
+      d->headdim % 8 != 0 || d->headdim > SSD_DELTA_MAX_P || d->dstate % 8 != 0 ||
       d->dstate > SSD_DELTA_MAX_N || d->nheads > kMaxGroups)
     return SSD_ERR_UNSUPPORTED;
   const int64_t es = (int64_t)io_size(d->io_dtype);

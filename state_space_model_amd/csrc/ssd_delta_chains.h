@@ -10,7 +10,10 @@ namespace delta {
 namespace {
 
 // ---------------------------------------------------------------------------
-// The chunks of one (b, h) in order, 16 NT value columns.
+// The chunks of one (b, h) in order, 16 NT value columns, float32 io (keys and
+// queries are three planes there, and every product with them six).  Bound by a
+// step's chain of LDS, matrix instructions and barriers: 3 x 1001 tokens of 24
+// heads of 64 x 64 96 us, 6 us a chunk.
 //
 // The state's slice S^T [key, value] stays in accumulators (wavefront w: keys
 // KP / 4 w ..); its planes go to LDS value-major, key-contiguous, as the right
@@ -261,10 +264,12 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, bf16* lds, int64_t id)
 // columns alone.  The state, the right sides and the writes stay in its
 // registers (ssd_delta.h); what the wavefronts share, k, q and the two
 // matrices of a chunk, lands in LDS, half of a compute unit's, so that one
-// workgroup computes while another waits for its chunk (8 x 16384 x 64 heads of
-// 64 x 128: 1780 us; one
-// workgroup a unit that requests a chunk ahead 2270).  A
-// chunk takes a wavefront 182 matrix instructions (keys of 128), 2912 cycles.
+// workgroup computes while another waits for its chunk (8 x 16384 tokens of 64
+// heads of 64 x 128: 1780 us; one workgroup a unit that requests a chunk ahead
+// 2270).  A chunk takes a wavefront 182 matrix instructions (keys of 128), 2912
+// cycles, and as many cycles of vector instructions, most of them to split float32
+// into planes; that is what bounds it (the same chunk again and again, from the
+// L2: 13% less).
 // ---------------------------------------------------------------------------
 template <int KP, int NW, bool KEEP> struct ColumnsLds {
   using Keys = KeyTile<KP, NW>;
@@ -468,6 +473,11 @@ __device__ __forceinline__ void columns_chain(const DeltaArgs& a, bf16* lds, int
 //   barrier 3                              (waits for k, gates, q, v)
 // Every wavefront makes the same requests, so that the counts that the waits
 // leave outstanding are constants.
+//
+// Bound by the step's length: 4096 tokens of 80 heads of 64 x 128 171 us, 2.7 us a
+// chunk in pairs (2.0 alone), of which the requests account for a fifth (none in
+// the loop: 135 us); the rest is three products that wait for each other through
+// LDS.
 // ---------------------------------------------------------------------------
 template <int KP, int NG, bool KEEP> struct TokensLds {
   using Keys = KeyTile<KP, 4 * NG>;
