@@ -681,7 +681,9 @@ typedef struct {
  * both io types; a bfloat16 y is rounded once.  A NaN or an infinity in a token
  * of q, k, v, dt or beta reaches the outputs of its chunk, earlier tokens of
  * the chunk included, and of later ones; no other head that does not share it
- * and no other batch row.  The bits of a sequence do not depend on the batch.
+ * and no other batch row.  The bits of a sequence do not depend on what else is in
+ * its batch; in bfloat16 they depend on the batch's size through Bt H ceil(P/32)
+ * alone, where up to 256 and more (the gradients: 128) sum in different orders.
  * Bt H ceil(T/64) and Bt H ceil(P/16) below 2^24 and strides up to 2^25 - 512
  * elements, else SSD_ERR_UNSUPPORTED.
  */

@@ -424,8 +424,10 @@ size_t delta_workspace(DeltaArgs& a, bool io_bf16, bool grads, char* ws) {
     take(a.leave, n * state);
     take(a.write, n * cols);
     take(a.dright, n * cols);
-    take(a.part_q, keys);
-    take(a.part_k, keys);
+    if (a.H != a.G) {
+      take(a.part_q, keys);
+      take(a.part_k, keys);
+    }
     take(a.part_h, n * 2 * sizeof(float));
   }
   return at;
