@@ -13,7 +13,8 @@ namespace {
 // The chunks of one (b, h) in order, 16 NT value columns, float32 io (keys and
 // queries are three planes there, and every product with them six).  Bound by a
 // step's chain of LDS, matrix instructions and barriers: 3 x 1001 tokens of 24
-// heads of 64 x 64 96 us, 6 us a chunk.
+// heads of 64 x 64, 288 workgroups, 73 us (two to a compute unit, as keys are
+// written to LDS behind their first products and not a chunk ahead: 96 before).
 //
 // The state's slice S^T [key, value] stays in accumulators (wavefront w: keys
 // KP / 4 w ..); its planes go to LDS value-major, key-contiguous, as the right
@@ -32,7 +33,7 @@ namespace {
 // and no later request.
 template <typename IO, int KP, int NT, bool KEEP> struct ChainLds {
   static constexpr int PI = Planes<IO>::in, PY = Planes<IO>::y, W = 16 * NT;
-  static constexpr int k = 0, s = k + 2 * PI * C * (KP + 16), r = s + 3 * W * (KP + 8);
+  static constexpr int k = 0, s = k + PI * C * (KP + 16), r = s + 3 * W * (KP + 8);
   static constexpr int e = r + 3 * W * kTokStride, w = e + 3 * W * kTokStride;
   static constexpr int elems = w + (KEEP ? 0 : PY * W * kTokStride);
 };
@@ -127,20 +128,10 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, bf16* lds, int64_t id)
     pf[1] = load_planes<PY>(pp + second * (PY * kFrag), kFrag);
   };
   bf16* const put_k = &s_k[(16 * w + j) * KTR + 8 * q];
-  int k_at = 0;   // which half of s_k holds the chunk
-  auto store_k = [&](int at) {
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const auto f = kr.frag(s, a.N, q);
-#pragma unroll
-      for (int i = 0; i < PI; ++i) *reinterpret_cast<bf16x8*>(put_k + at + i * C * KTR + 32 * s) = f.p[i];
-    }
-  };
   rows_of(0);
   load_rows();
   load_x();
   if constexpr (!KEEP) load_p();
-  store_k(0);
   __syncthreads();
 
   const bf16* const get_s = &s_s[j * KST + 8 * q];
@@ -157,27 +148,35 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, bf16* lds, int64_t id)
           *reinterpret_cast<f32x4*>(state_at + 16 * n * KP + 16 * t) = st[n][t];
       state_at += cols * KP;
     }
-    // K S^T and Q S^T of the wavefront's tokens; the right sides b (v - gamma K S^T)
-    f32x4 y[NT];
+    // K S^T and Q S^T of the wavefront's tokens; the right sides b (v - gamma K S^T);
+    // the keys to LDS, where they are next read two barriers on
+    f32x4 y[NT], ks[NT], qs[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      f32x4 ks = {0, 0, 0, 0}, qs = {0, 0, 0, 0};
+    for (int n = 0; n < NT; ++n) ks[n] = qs[n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
+    for (int s = 0; s < KS; ++s) {
+      const auto kf = kr.frag(s, a.N, q);
+#pragma unroll
+      for (int i = 0; i < PI; ++i) *reinterpret_cast<bf16x8*>(put_k + i * C * KTR + 32 * s) = kf.p[i];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
         const auto sf = load_planes<3>(get_s + 16 * n * KST + 32 * s, W * KST);
-        ks = mma(kr.frag(s, a.N, q), sf, ks);
+        ks[n] = mma(kf, sf, ks[n]);
         if constexpr (!KEEP) {
           Frag<PY> sy;
 #pragma unroll
           for (int i = 0; i < PY; ++i) sy.p[i] = sf.p[i];
-          qs = mma(qr.frag(s, a.N, q), sy, qs);
+          qs[n] = mma(qr.frag(s, a.N, q), sy, qs[n]);
         }
       }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
       f32x4 rs;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        rs[r] = fmaf(-g_right[r], ks[r], g_beta[r] * to_f32(v[n][r]));
-        if constexpr (!KEEP) y[n][r] = g_out[r] * qs[r];
+        rs[r] = fmaf(-g_right[r], ks[n][r], g_beta[r] * to_f32(v[n][r]));
+        if constexpr (!KEEP) y[n][r] = g_out[r] * qs[n][r];
       }
       store_split4<3>(s_r + put_t + 16 * n * kTokStride, W * kTokStride, rs);
     }
@@ -217,7 +216,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, bf16* lds, int64_t id)
     for (int t = 0; t < KT; ++t) {
       Frag<PI> ka[2];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) ka[s] = read_tr<PI>(get_k + k_at + 32 * s * KTR + 16 * t, C * KTR, 16 * KTR);
+      for (int s = 0; s < 2; ++s) ka[s] = read_tr<PI>(get_k + 32 * s * KTR + 16 * t, C * KTR, 16 * KTR);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         f32x4 acc = {0, 0, 0, 0};
@@ -229,8 +228,6 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, bf16* lds, int64_t id)
         store_split4<3>(put_s + 16 * n * KST + 16 * t, W * KST, st[n][t]);
       }
     }
-    k_at = PI * C * KTR - k_at;
-    store_k(k_at);
     // outputs
     if constexpr (!KEEP) {
 #pragma unroll
