@@ -149,15 +149,6 @@ template <> struct Raw8<float> {
     return split8<3>(x);
   }
 };
-// zeros when !in; `p` is a valid address either way
-template <typename IO>
-__device__ __forceinline__ Frag<Planes<IO>::in> load_io8(const IO* p, bool in) {
-  Raw8<IO> r;
-  r.load(p);
-  r.keep(in);
-  return r.frag();
-}
-
 // ds_read_b64_tr_b16: within each group of 16 lanes, lane j addresses 4
 // elements and receives element j % 4 of the vectors addressed by lanes j / 4,
 // 4 + j / 4, 8 + j / 4 and 12 + j / 4.
@@ -180,12 +171,6 @@ __device__ __forceinline__ Frag<NP> read_tr(const bf16* p, int plane, int second
     f.p[i] = bf16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   }
   return f;
-}
-template <int NP>
-__device__ __forceinline__ Frag<NP> load_planes_tr(const bf16* m, int plane, int stride, int r0,
-                                                   int c0, int lane) {
-  const int j = lane & 15, q = lane >> 4;
-  return read_tr<NP>(m + (r0 + 8 * q + (j >> 2)) * stride + c0 + 4 * (j & 3), plane, 4 * stride);
 }
 
 // A 16 x 16 float32 product on the float32 matrix core, its right operand and
