@@ -24,6 +24,25 @@ namespace ssd {
 namespace delta {
 namespace {
 
+// The matrix cores do not round their sums to nearest: a sum comes out a little low
+// on the average, whatever its sign.  Through a sum of products with states, keys
+// and queries, whose elements have a mean, that shows in the decays' gradients,
+// and in those of A, a sum over all tokens, most.  So odd value columns of the
+// chains from the last chunk (what they leave in the workspace included) and odd
+// tokens of k_delta_grads are computed with the opposite sign: the bias of one half
+// takes that of the other back (dA of 4096 tokens of 32 heads: 1.3e-6 -> 2e-7).
+__device__ __forceinline__ float odd_sign(int i) { return i & 1 ? -1.0f : 1.0f; }
+__device__ __forceinline__ uint32_t odd_flip(int i) { return i & 1 ? 0x80008000u : 0u; }
+// the operand, negated where `flip` has the signs of two elements set
+template <int NP> __device__ __forceinline__ Frag<NP> with_sign(Frag<NP> f, uint32_t flip) {
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const uint4 v = __builtin_bit_cast(uint4, f.p[i]);
+    f.p[i] = __builtin_bit_cast(bf16x8, make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip));
+  }
+  return f;
+}
+
 // As chain, from the last chunk to the first.
 template <typename IO, int KP, int NT> struct BackChainLds {
   static constexpr int PI = Planes<IO>::in, W = 16 * NT, tok = W * kTokStride;
@@ -55,6 +74,7 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& a, bf16* lds, int64_
     col[n] = col_in[n] ? col0 + 16 * n + j : 0;
   }
 
+  const float sign = odd_sign(j);
   f32x4 st[NT][KT];
   const int key0 = 16 * KT * w + 4 * q;
   bf16* const put_s = &s_s[j * KST + key0];
@@ -64,7 +84,7 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& a, bf16* lds, int64_
     for (int t = 0; t < KT; ++t) {
       st[n][t] = f32x4{0, 0, 0, 0};
       if (a.dfinal && col_in[n] && key0 + 16 * t < a.N)
-        st[n][t] = *reinterpret_cast<const f32x4*>(a.dfinal + (bh * a.P + col[n]) * a.N + key0 + 16 * t);
+        st[n][t] = sign * *reinterpret_cast<const f32x4*>(a.dfinal + (bh * a.P + col[n]) * a.N + key0 + 16 * t);
       store_split4<3>(put_s + 16 * n * KST + 16 * t, W * KST, st[n][t]);
     }
 
@@ -129,7 +149,7 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& a, bf16* lds, int64_
     for (int n = 0; n < NT; ++n) {
       f32x4 v;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = to_f32(dy[n][r]);
+      for (int r = 0; r < 4; ++r) v[r] = sign * to_f32(dy[n][r]);
       store_split4<PI>(s_y + put_t + 16 * n * kTokStride, W * kTokStride, v);
 #pragma unroll
       for (int r = 0; r < 4; ++r) v[r] *= g_out[r];
@@ -234,7 +254,7 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& a, bf16* lds, int64_
 #pragma unroll
       for (int t = 0; t < KT; ++t)
         if (col_in[n] && key0 + 16 * t < a.N)
-          *reinterpret_cast<f32x4*>(a.dh0 + (bh * a.P + col[n]) * a.N + key0 + 16 * t) = st[n][t];
+          *reinterpret_cast<f32x4*>(a.dh0 + (bh * a.P + col[n]) * a.N + key0 + 16 * t) = sign * st[n][t];
   }
 }
 
@@ -294,13 +314,14 @@ __device__ __forceinline__ void back_columns(const DeltaArgs& a, bf16* lds, int6
   offsets((int)(a.T - c_last * C) - 1);
   request();
 
+  const float sign = odd_sign(j);
   f32x4 st[KT];
 #pragma unroll
   for (int t = 0; t < KT; ++t) {
     const int key = key_of(t, 4 * q);
     st[t] = f32x4{0, 0, 0, 0};
     if (a.dfinal && col_in && key < a.N)
-      st[t] = *reinterpret_cast<const f32x4*>(a.dfinal + (bh * a.P + col) * a.N + key);
+      st[t] = sign * *reinterpret_cast<const f32x4*>(a.dfinal + (bh * a.P + col) * a.N + key);
   }
   float* state_at = a.leave + (at * cols + col) * KP + 8 * q;
   float* right_at = a.dright + (at * cols + col) * C + 4 * q;
@@ -339,7 +360,7 @@ __device__ __forceinline__ void back_columns(const DeltaArgs& a, bf16* lds, int6
     Frag<3> rf[2], gf[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s)
-      dy[s] = read_tr2(lds + L::y + (32 * s + 4 * q + (j >> 2)) * W + 16 * w + 4 * (j & 3), 16 * W);
+      dy[s] = with_sign(read_tr2(lds + L::y + (32 * s + 4 * q + (j >> 2)) * W + 16 * w + 4 * (j & 3), 16 * W), odd_flip(j));
     mma_upper<3>(lds + L::p + lane * 8, dy, dw);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -408,7 +429,7 @@ __device__ __forceinline__ void back_columns(const DeltaArgs& a, bf16* lds, int6
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
       const int key = key_of(t, 4 * q);
-      if (key < a.N) *reinterpret_cast<f32x4*>(a.dh0 + (bh * a.P + col) * a.N + key) = st[t];
+      if (key < a.N) *reinterpret_cast<f32x4*>(a.dh0 + (bh * a.P + col) * a.N + key) = sign * st[t];
     }
   }
 }
@@ -481,6 +502,8 @@ __device__ __forceinline__ void back_tokens(const DeltaArgs& a, bf16* lds, int64
   request_py();
   request_x();
 
+  const float sign = odd_sign(j);
+  const uint32_t flip = odd_flip(j);
   f32x4 st[KT];
   const int col = col0 + row;
   const bool col_in = col < a.P;
@@ -491,7 +514,7 @@ __device__ __forceinline__ void back_tokens(const DeltaArgs& a, bf16* lds, int64
     put_s[t] = L::s + row_vec<KP>(row, key[t] / 8) + key[t] % 8;
     st[t] = f32x4{0, 0, 0, 0};
     if (a.dfinal && col_in && key[t] < a.N)
-      st[t] = *reinterpret_cast<const f32x4*>(a.dfinal + (bh * a.P + col) * a.N + key[t]);
+      st[t] = sign * *reinterpret_cast<const f32x4*>(a.dfinal + (bh * a.P + col) * a.N + key[t]);
   }
   auto store_s = [&]() {
 #pragma unroll
@@ -561,9 +584,9 @@ __device__ __forceinline__ void back_tokens(const DeltaArgs& a, bf16* lds, int64
           for (int o = 0; o < 2; ++o) ke[o] = mma(kf[o], ef[o].p[i], ke[o]);
       }
       const bf16* const lp = lds + L::p + upper_frag(w, first) * (3 * kFrag) + lane * 8;
-      dw[0] = mma(load_planes<3>(lp, kFrag), read_tr2(lds + dy_at + 32 * first * W, 16 * W), dw[0]);
-      if (w < 2) dw[1] = mma(load_planes<3>(lp + 3 * kFrag, kFrag), read_tr2(lds + dy_at + 32 * W, 16 * W), dw[1]);
-      const f32x4 ge = gates(kEnd), go = gates(kOut);
+      dw[0] = mma(load_planes<3>(lp, kFrag), with_sign(read_tr2(lds + dy_at + 32 * first * W, 16 * W), flip), dw[0]);
+      if (w < 2) dw[1] = mma(load_planes<3>(lp + 3 * kFrag, kFrag), with_sign(read_tr2(lds + dy_at + 32 * W, 16 * W), flip), dw[1]);
+      const f32x4 ge = gates(kEnd), go = sign * gates(kOut);
       const bf16x4 own = lds_read_tr4(lds + dy_at + 16 * w * W);
       f32x4 gy;
 #pragma unroll
@@ -616,7 +639,7 @@ __device__ __forceinline__ void back_tokens(const DeltaArgs& a, bf16* lds, int64
   if (a.dh0 && col_in) {
 #pragma unroll
     for (int t = 0; t < KT; ++t)
-      if (key[t] < a.N) *reinterpret_cast<f32x4*>(a.dh0 + (bh * a.P + col) * a.N + key[t]) = st[t];
+      if (key[t] < a.N) *reinterpret_cast<f32x4*>(a.dh0 + (bh * a.P + col) * a.N + key[t]) = sign * st[t];
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no request may reach LDS after this
 }
@@ -665,9 +688,11 @@ __global__ __launch_bounds__(256, 2) void k_delta_both_columns(DeltaArgs a) {
 //
 // bfloat16 io: two workgroups to a compute unit (69 KB of LDS, the states that
 // enter and the gradients that leave through one buffer in turn).  4096 tokens of
-// 32 heads of 128 x 128: 205 us (one workgroup a unit, results not transposed,
+// 32 heads of 128 x 128: 195-215 us (one workgroup a unit, results not transposed,
 // pairs through LDS both times: 323), of which vector instructions 60, matrix
-// instructions 40, LDS 40 and the 426 MB it moves 90.
+// instructions 40, LDS 40 and the 426 MB it moves 90.  The gradients that leave are
+// requested behind the first products' operands and not with them: those registers
+// would spill (20 us).
 // ---------------------------------------------------------------------------
 constexpr int kSlice = 32, kPairRow = C + 16;
 
@@ -741,6 +766,10 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_gra
   const int64_t t0 = c * C, row0 = b * a.T + t0, left = a.T - t0;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_of(tid), j = lane & 15, q = lane >> 4;
   const int own = 16 * w + j;
+  // odd tokens negated, until the decays are applied; odd value columns of what the
+  // chains left back to their signs
+  static_assert(kThreads / (C / 4) % 2 == 0 && kThreads / (KP / 4) % 2 == 0, "a thread's columns are all odd or all even");
+  const float sign = odd_sign(own), sign_t = odd_sign(tid / (C / 4)), sign_k = odd_sign(tid / (KP / 4));
   if (tid < C) {
     s_b[tid] = a.gate[at * kGates + kBeta + tid];
     s_row[tid] = a.row[at * C + tid];
@@ -757,14 +786,14 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_gra
   float es = 0.0f, dr_v = 0.0f;
 
   for (int p0 = 0; p0 < a.P; p0 += kSlice) {
-    f32x4 vw[kTokParts], vd[kTokParts], vs[kKeyParts], ve[kKeyParts];
+    f32x4 vw[kTokParts], vd[kTokParts], vs[kKeyParts];
 #pragma unroll
     for (int i = 0; i < kTokParts; ++i) {
       const int at4 = tid + i * kThreads, p = at4 / (C / 4), t = at4 % (C / 4) * 4;
       const bool in = p0 + p < a.P;
       const int64_t o = (at * cols + (in ? p0 + p : 0)) * C + t;
-      vw[i] = *reinterpret_cast<const f32x4*>(a.write + o);
-      vd[i] = *reinterpret_cast<const f32x4*>(a.dright + o);
+      vw[i] = *reinterpret_cast<const f32x4*>(a.write + o) * f32x4{1.0f, -1.0f, 1.0f, -1.0f};
+      vd[i] = *reinterpret_cast<const f32x4*>(a.dright + o) * f32x4{sign_t, -sign_t, sign_t, -sign_t};
       if (!in) vw[i] = vd[i] = f32x4{0, 0, 0, 0};
     }
 #pragma unroll
@@ -773,8 +802,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_gra
       const bool in = p0 + p < a.P && key < a.N;
       const int64_t o = (at * cols + (in ? p0 + p : 0)) * KP + (in ? key : 0);
       vs[i] = *reinterpret_cast<const f32x4*>(a.enter + o);
-      ve[i] = *reinterpret_cast<const f32x4*>(a.leave + o);
-      if (!in) vs[i] = ve[i] = f32x4{0, 0, 0, 0};
+      if (!in) vs[i] = f32x4{0, 0, 0, 0};
     }
     // P is a multiple of 8
     const bool lo_in = row_in && p0 + 4 * q < a.P, hi_in = row_in && p0 + 16 + 4 * q < a.P;
@@ -792,16 +820,23 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_gra
 #pragma unroll
     for (int i = 0; i < kKeyParts; ++i) {
       const int at4 = tid + i * kThreads, o = at4 / (KP / 4) * KST + at4 % (KP / 4) * 4;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) es = fmaf(vs[i][e], ve[i][e], es);
       store_split4<3>(&s_s[o], kSlice * KST, vs[i]);
     }
     __syncthreads();
-    const auto dyf = split8<PI>(dy.x);
+    f32x4 ve[kKeyParts];
+#pragma unroll
+    for (int i = 0; i < kKeyParts; ++i) {
+      const int at4 = tid + i * kThreads, p = at4 / (KP / 4), key = at4 % (KP / 4) * 4;
+      const bool in = p0 + p < a.P && key < a.N;
+      const int64_t o = (at * cols + (in ? p0 + p : 0)) * KP + (in ? key : 0);
+      ve[i] = *reinterpret_cast<const f32x4*>(a.leave + o);
+      if (!in) ve[i] = f32x4{0, 0, 0, 0};
+    }
+    const auto dyf = with_sign(split8<PI>(dy.x), odd_flip(own));
     const auto drf = columns_of<3, kPairRow>(s_d, kSlice * kPairRow, 0, 16 * w, lane);
     const auto wf = columns_of<3, kPairRow>(s_w, kSlice * kPairRow, 0, 16 * w, lane);
     {
-      const float beta = s_b[own];
+      const float beta = sign * s_b[own];
       float out[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -837,8 +872,11 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_gra
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kKeyParts; ++i) {
-      const int at4 = tid + i * kThreads;
-      store_split4<3>(&s_s[at4 / (KP / 4) * KST + at4 % (KP / 4) * 4], kSlice * KST, ve[i]);
+      const int at4 = tid + i * kThreads, o = at4 / (KP / 4) * KST + at4 % (KP / 4) * 4;
+      const f32x4 e = sign_k * ve[i], own_s = plane_sum4<3>(&s_s[o], kSlice * KST);   // what this thread put there
+#pragma unroll
+      for (int r = 0; r < 4; ++r) es = fmaf(own_s[r], e[r], es);
+      store_split4<3>(&s_s[o], kSlice * KST, e);
     }
     __syncthreads();
 #pragma unroll
@@ -872,7 +910,8 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_gra
   // the pairs (own token i, earlier token) over their decay; times 1/|k| of the
   // earlier one they are the right operands of the sums over it
   const float4 rec = s_row[own], last = s_row[C - 1];
-  const float beta = s_b[own], gamma = exp2_of(rec.z + rec.w), eta = exp2_of((last.z - rec.z) + (last.w - rec.w));
+  const float beta = s_b[own];
+  const float gamma = sign * exp2_of(rec.z + rec.w), eta = sign * exp2_of((last.z - rec.z) + (last.w - rec.w));
   f32x4 rk[4];
 #pragma unroll
   for (int jt = 0; jt < 4; ++jt)
@@ -880,7 +919,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_gra
     for (int r = 0; r < 4; ++r) {
       const int cj = 16 * jt + 4 * q + r;
       const float4 rj = s_row[cj];
-      const float dec = exp2_of((rec.z - rj.z) + (rec.w - rj.w));
+      const float dec = sign * odd_sign(r) * exp2_of((rec.z - rj.z) + (rec.w - rj.w));   // W's rows are cj, odd as r
       dp[jt][r] = own >= cj ? dec * dp[jt][r] : 0.0f;
       dl[jt][r] = own > cj ? dec * dl[jt][r] : 0.0f;
       rk[jt][r] = rj.x;
@@ -941,7 +980,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_gra
       if (j == 0) *reinterpret_cast<f32x4*>(&s_over[w][16 * jt + 4 * q]) = over;
       before += __shfl(upto, 48 + j, 64);
     }
-    dr_v = sum_q(dr_v) - kz - sum_q(pair_kz);
+    dr_v = sign * sum_q(dr_v) - kz - sum_q(pair_kz);
     if (q == 0) {
       s_from[own] = from;
       s_to[own] = to;
