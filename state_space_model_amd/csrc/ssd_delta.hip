@@ -39,15 +39,16 @@ namespace {
 //
 // Bound by its instructions: 8 x 16384 tokens of 64 heads in bfloat16 1440 us (the
 // vector units busy half of it, 3.2 TB/s), 4096 tokens of 80 heads with keys of
-// their own 64 us (5.0 TB/s).  bfloat16 keeps to 128 registers for six workgroups
-// to a compute unit; float32's planes need more.
+// their own 64 us (5.0 TB/s).  bfloat16 takes 96 registers, five workgroups to a
+// compute unit (held to the 80 of six it spills: 1740 and 79 us); float32's planes
+// need more.
 template <typename IO, int KP, bool FULL, bool GRADS>
 __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 4 : 2) void k_delta_prep(DeltaArgs a) {
   constexpr int PI = Planes<IO>::in, PY = Planes<IO>::y;
   constexpr int KS = KP / 32, KST = KP + 8, kDiag = 20;
   constexpr int k_bytes = PI * C * KST * 2, l_bytes = (GRADS ? 2 : 1) * C * kPairStride * 4;
   // the keys, then L transposed ([column][row]), then for GRADS both results: a
-  // workgroup in 24 KB (bfloat16), and six of them to a compute unit hide one
+  // workgroup in 24 KB (bfloat16), and five of them to a compute unit hide one
   // another's chain of dependent steps
   __shared__ __align__(16) char lds[k_bytes > l_bytes ? k_bytes : l_bytes];
   __shared__ __align__(16) float s_d[4 * 16 * kDiag];     // inverse diagonal blocks, transposed
