@@ -9,10 +9,11 @@
 // matrix core and accumulated in float32: six v_mfma_f32_16x16x32_bf16 (16
 // cycles each) where v_mfma_f32_16x16x4_f32 takes eight of 32 cycles.  An
 // operand that is bfloat16 already is one plane, and its product with a
-// float32 operand is exact up to the sum with three.  So states, writes and
-// their gradients keep float32 accuracy for both io types; only what ends in a
-// bfloat16 output is formed from two planes (2^-17 of it, against 2^-8 by the
-// rounding of the output).
+// float32 operand is exact up to the sum with three.  So states, writes, outputs
+// and all gradients keep float32 accuracy for both io types, and a bfloat16
+// output is rounded once, at its store.  (Outputs from two planes of the state,
+// the writes and q k^T would be a tenth faster, and off by up to 2^-15 of the terms'
+// magnitudes.)
 #pragma once
 
 #include <type_traits>
@@ -33,9 +34,9 @@ constexpr int kPairStride = C + 4; // LDS rows of C float32
 constexpr int kTriFrags = 6;
 constexpr int kFrag = 512;         // elements of one fragment: 8 per lane
 
-template <typename IO> struct Planes;
-template <> struct Planes<float> { static constexpr int in = 3, y = 3; };
-template <> struct Planes<bf16> { static constexpr int in = 1, y = 2; };
+template <typename IO> struct Planes;   // of an element of q, k or v
+template <> struct Planes<float> { static constexpr int in = 3; };
+template <> struct Planes<bf16> { static constexpr int in = 1; };
 
 template <int NP> struct Frag { bf16x8 p[NP]; };
 

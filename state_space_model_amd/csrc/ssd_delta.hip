@@ -44,7 +44,7 @@ namespace {
 // need more.
 template <typename IO, int KP, bool FULL, bool GRADS>
 __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 4 : 2) void k_delta_prep(DeltaArgs a) {
-  constexpr int PI = Planes<IO>::in, PY = Planes<IO>::y;
+  constexpr int PI = Planes<IO>::in;
   constexpr int KS = KP / 32, KST = KP + 8, kDiag = 20;
   constexpr int k_bytes = PI * C * KST * 2, l_bytes = (GRADS ? 2 : 1) * C * kPairStride * 4;
   // the keys, then L transposed ([column][row]), then for GRADS both results: a
@@ -157,7 +157,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 4 : 2) void k_delta_pre
   if constexpr (!GRADS) {
 #pragma unroll
     for (int s = 0; s < 2; ++s)
-      if (s <= (w >> 1)) store_frag(a.qk, at, lower_frag(w, s), lane, right_of<PY>(p[2 * s], p[2 * s + 1]));
+      if (s <= (w >> 1)) store_frag(a.qk, at, lower_frag(w, s), lane, right_of<3>(p[2 * s], p[2 * s + 1]));
   }
 
   __syncthreads();
@@ -402,7 +402,7 @@ hipError_t launch_step(const DeltaArgs& a, hipStream_t stream) {
 }  // namespace
 }  // namespace delta
 
-size_t delta_workspace(DeltaArgs& a, bool io_bf16, bool grads, char* ws) {
+size_t delta_workspace(DeltaArgs& a, bool grads, char* ws) {
   const size_t n = (size_t)(a.Bt * a.H * a.Nc), C = kDeltaChunk;
   const size_t frags = delta::kTriFrags * delta::kFrag * sizeof(bf16);
   size_t at = 0;
@@ -413,7 +413,7 @@ size_t delta_workspace(DeltaArgs& a, bool io_bf16, bool grads, char* ws) {
   take(a.gate, n * 4 * C * sizeof(float));
   take(a.whole, n * sizeof(float));
   take(a.inv, n * 3 * frags);
-  take(a.qk, n * (io_bf16 && !grads ? 2 : 3) * frags);
+  take(a.qk, n * 3 * frags);
   take(a.park, 64 * 16);
   if (grads) {
     const size_t P16 = (a.P + 15) / 16 * 16, KP = a.N > 64 ? 128 : 64;

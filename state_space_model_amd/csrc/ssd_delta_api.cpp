@@ -146,7 +146,7 @@ size_t ssd_delta_scan_workspace_bytes(const ssd_delta_desc* d) {
   Sizes s;
   if (check(d, false, false, &s) != SSD_OK) return 0;
   DeltaArgs a = args_of(d, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
-  return delta_workspace(a, d->io_dtype == SSD_BF16, false, nullptr);
+  return delta_workspace(a, false, nullptr);
 }
 
 ssd_status ssd_delta_scan(const ssd_delta_desc* d, const void* q, const void* k, const void* v,
@@ -179,7 +179,7 @@ ssd_status ssd_delta_scan(const ssd_delta_desc* d, const void* q, const void* k,
   const bool io_bf16 = d->io_dtype == SSD_BF16;
   DeltaArgs a = args_of(d, q, k, v, dt, dt_bias, A, beta);
   a.h0 = initial_state; a.y = y; a.state = final_state;
-  delta_workspace(a, io_bf16, false, static_cast<char*>(workspace));
+  delta_workspace(a, false, static_cast<char*>(workspace));
   return status_of(launch_delta_scan(a, io_bf16, stream));
 }
 
@@ -187,7 +187,7 @@ size_t ssd_delta_scan_backward_workspace_bytes(const ssd_delta_desc* d) {
   Sizes s;
   if (check(d, false, true, &s) != SSD_OK) return 0;
   DeltaArgs a = args_of(d, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
-  return delta_workspace(a, d->io_dtype == SSD_BF16, true, nullptr);
+  return delta_workspace(a, true, nullptr);
 }
 
 ssd_status ssd_delta_scan_backward(const ssd_delta_desc* d, const void* q, const void* k,
@@ -245,7 +245,7 @@ ssd_status ssd_delta_scan_backward(const ssd_delta_desc* d, const void* q, const
   a.dq = dq; a.dk = dk; a.dv = dv;
   a.dq_stride = d->dq_stride; a.dk_stride = d->dk_stride; a.dv_stride = d->dv_stride;
   a.ddt = ddt; a.dbeta = dbeta; a.dA = dA; a.ddt_bias = ddt_bias; a.dh0 = dinitial_state;
-  delta_workspace(a, io_bf16, true, static_cast<char*>(workspace));
+  delta_workspace(a, true, static_cast<char*>(workspace));
   return status_of(launch_delta_scan_backward(a, io_bf16, stream));
 }
 

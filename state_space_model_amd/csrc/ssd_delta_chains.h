@@ -32,16 +32,16 @@ namespace {
 // `park`; the workspace holds whole tiles), so that a wait covers what it is for
 // and no later request.
 template <typename IO, int KP, int NT, bool KEEP> struct ChainLds {
-  static constexpr int PI = Planes<IO>::in, PY = Planes<IO>::y, W = 16 * NT;
+  static constexpr int PI = Planes<IO>::in, W = 16 * NT;
   static constexpr int k = 0, s = k + PI * C * (KP + 16), r = s + 3 * W * (KP + 8);
   static constexpr int e = r + 3 * W * kTokStride, w = e + 3 * W * kTokStride;
-  static constexpr int elems = w + (KEEP ? 0 : PY * W * kTokStride);
+  static constexpr int elems = w + (KEEP ? 0 : 3 * W * kTokStride);
 };
 
 template <typename IO, int KP, bool FULL, int NT, bool KEEP>
 __device__ __forceinline__ void chain(const DeltaArgs& a, bf16* lds, int64_t id) {
   using L = ChainLds<IO, KP, NT, KEEP>;
-  constexpr int PI = Planes<IO>::in, PY = Planes<IO>::y;
+  constexpr int PI = Planes<IO>::in;
   constexpr int KS = KP / 32, KST = KP + 8, KTR = KP + 16, KT = KP / 64, W = 16 * NT;
   bf16 *const s_k = lds + L::k, *const s_s = lds + L::s;
   bf16* const s_r = lds + L::r;   // right sides
@@ -92,7 +92,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, bf16* lds, int64_t id)
   // the second fragment of wavefronts 0 and 1 is their first one again, unused
   const int second = w >= 2 ? 1 : 0;
   const bf16* xp = a.inv + (at0 * kTriFrags + lower_frag(w, 0)) * (3 * kFrag) + lane * 8;
-  const bf16* pp = a.qk + (at0 * kTriFrags + lower_frag(w, 0)) * (PY * kFrag) + lane * 8;
+  const bf16* pp = a.qk + (at0 * kTriFrags + lower_frag(w, 0)) * (3 * kFrag) + lane * 8;
   const float* ep = a.whole + at0;
   const int64_t y_row = a.H * a.P;
   IO* yp = KEEP ? nullptr : static_cast<IO*>(a.y) + (b * a.T + 16 * w + 4 * q) * y_row + h * a.P;
@@ -102,8 +102,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, bf16* lds, int64_t id)
   float* write_at = KEEP ? a.write + (at0 * cols + col0 + j) * C + 16 * w + 4 * q : nullptr;
 
   KeyRow<IO, KP, FULL> kr, qr;
-  Frag<3> xf[2];
-  Frag<PY> pf[2];
+  Frag<3> xf[2], pf[2];
   f32x4 g_beta, g_right, g_end, g_out;
   IO v[NT][4];
   float whole = *ep;
@@ -124,8 +123,8 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, bf16* lds, int64_t id)
     xf[1] = load_planes<3>(xp + second * (3 * kFrag), kFrag);
   };
   auto load_p = [&]() {
-    pf[0] = load_planes<PY>(pp, kFrag);
-    pf[1] = load_planes<PY>(pp + second * (PY * kFrag), kFrag);
+    pf[0] = load_planes<3>(pp, kFrag);
+    pf[1] = load_planes<3>(pp + second * (3 * kFrag), kFrag);
   };
   bf16* const put_k = &s_k[(16 * w + j) * KTR + 8 * q];
   rows_of(0);
@@ -162,12 +161,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, bf16* lds, int64_t id)
       for (int n = 0; n < NT; ++n) {
         const auto sf = load_planes<3>(get_s + 16 * n * KST + 32 * s, W * KST);
         ks[n] = mma(kf, sf, ks[n]);
-        if constexpr (!KEEP) {
-          Frag<PY> sy;
-#pragma unroll
-          for (int i = 0; i < PY; ++i) sy.p[i] = sf.p[i];
-          qs[n] = mma(qr.frag(s, a.N, q), sy, qs[n]);
-        }
+        if constexpr (!KEEP) qs[n] = mma(qr.frag(s, a.N, q), sf, qs[n]);
       }
     }
 #pragma unroll
@@ -201,7 +195,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, bf16* lds, int64_t id)
 #pragma unroll
       for (int r = 0; r < 4; ++r) es[r] = eta[r] * ws[r];
       store_split4<3>(s_e + put_t + 16 * n * kTokStride, W * kTokStride, es);
-      if constexpr (!KEEP) store_split4<PY>(s_w + put_t + 16 * n * kTokStride, W * kTokStride, ws);
+      if constexpr (!KEEP) store_split4<3>(s_w + put_t + 16 * n * kTokStride, W * kTokStride, ws);
       else *reinterpret_cast<f32x4*>(write_at + 16 * n * C) = ws;
     }
     if constexpr (KEEP) write_at += cols * C;
@@ -232,8 +226,8 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, bf16* lds, int64_t id)
     if constexpr (!KEEP) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        y[n] = mma(pf[0], load_planes<PY>(s_w + get_t + 16 * n * kTokStride, W * kTokStride), y[n]);
-        if (w >= 2) y[n] = mma(pf[1], load_planes<PY>(s_w + get_t + 16 * n * kTokStride + 32, W * kTokStride), y[n]);
+        y[n] = mma(pf[0], load_planes<3>(s_w + get_t + 16 * n * kTokStride, W * kTokStride), y[n]);
+        if (w >= 2) y[n] = mma(pf[1], load_planes<3>(s_w + get_t + 16 * n * kTokStride + 32, W * kTokStride), y[n]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           IO* const to = 16 * w + 4 * q + r < left && col_in[n] ? yp + r * y_row + col[n] : park;
@@ -241,7 +235,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, bf16* lds, int64_t id)
         }
       }
       yp += C * y_row;
-      pp += next * (kTriFrags * PY * kFrag);
+      pp += next * (kTriFrags * 3 * kFrag);
       load_p();
     }
     __syncthreads();
@@ -271,7 +265,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, bf16* lds, int64_t id)
 template <int KP, int NW, bool KEEP> struct ColumnsLds {
   using Keys = KeyTile<KP, NW>;
   static constexpr int k = 0, q = k + Keys::kElems, x = q + (KEEP ? 0 : Keys::kElems);
-  static constexpr int p = x + 3 * kTriFrags * kFrag, v = p + (KEEP ? 0 : 2 * kTriFrags * kFrag);
+  static constexpr int p = x + 3 * kTriFrags * kFrag, v = p + (KEEP ? 0 : 3 * kTriFrags * kFrag);
   static constexpr int gate = v + C * 16 * NW, elems = gate + 2 * kGates;
 };
 
@@ -307,14 +301,14 @@ __device__ __forceinline__ void columns_chain(const DeltaArgs& a, bf16* lds, int
   const bf16* qp = static_cast<const bf16*>(a.q) + b * a.T * a.q_stride + g * a.N;
   const bf16* vp = static_cast<const bf16*>(a.v) + b * a.T * a.v_stride + h * a.P + col0;
   const bf16* xp = a.inv + at0 * (3 * kTriFrags * kFrag) + w * 512;
-  const bf16* pp = a.qk + at0 * (2 * kTriFrags * kFrag) + w * 512;
+  const bf16* pp = a.qk + at0 * (3 * kTriFrags * kFrag) + w * 512;
   const float* gp = a.gate + at0 * kGates + w * 256;
   const bool all_cols = a.P - col0 >= W;
   auto request = [&]() {
     Keys::template request<FULL>(kp, k_off, lds0 + 2 * L::k);
     if constexpr (!KEEP) Keys::template request<FULL>(qp, q_off, lds0 + 2 * L::q);
     request_linear<3 * kTriFrags, NW>(xp, lds0 + 2 * L::x, w, lane);
-    if constexpr (!KEEP) request_linear<2 * kTriFrags, NW>(pp, lds0 + 2 * L::p, w, lane);
+    if constexpr (!KEEP) request_linear<3 * kTriFrags, NW>(pp, lds0 + 2 * L::p, w, lane);
     if (all_cols) Cols::template request<true>(vp, v_off, lds0 + 2 * L::v);
     else Cols::template request<false>(vp, v_off, lds0 + 2 * L::v);
     request_linear<1, NW>(gp, lds0 + 2 * L::gate, w, lane);
@@ -366,10 +360,9 @@ __device__ __forceinline__ void columns_chain(const DeltaArgs& a, bf16* lds, int
       for (int i = 0; i < 4; ++i) rows[i] = load_planes<1>(lds + L::k + row_at[s] + 16 * i * KP, 0);
       mma_tiles(rows, sf, ks);
       if constexpr (!KEEP) {
-        const Frag<2> sy = {{sf.p[0], sf.p[1]}};
 #pragma unroll
         for (int i = 0; i < 4; ++i) rows[i] = load_planes<1>(lds + L::q + row_at[s] + 16 * i * KP, 0);
-        mma_tiles(rows, sy, qs);
+        mma_tiles(rows, sf, qs);
       }
     }
     // the right sides, and the writes
@@ -415,13 +408,13 @@ __device__ __forceinline__ void columns_chain(const DeltaArgs& a, bf16* lds, int
     }
     // outputs, through the wavefront's own columns of v
     if constexpr (!KEEP) {
-      Frag<2> wf[2];
+      Frag<3> wf[2];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) wf[s] = right_of<2>(ws[2 * s], ws[2 * s + 1]);
+      for (int s = 0; s < 2; ++s) wf[s] = right_of<3>(ws[2 * s], ws[2 * s + 1]);
       bf16* const out = lds + L::v + 16 * w;
 #pragma unroll
       for (int i = 0; i < 4; ++i) qs[i] *= gates(kOut, i);
-      mma_lower<2>(lds + L::p + lane * 8, wf, qs);
+      mma_lower<3>(lds + L::p + lane * 8, wf, qs);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -443,7 +436,7 @@ __device__ __forceinline__ void columns_chain(const DeltaArgs& a, bf16* lds, int
       qp += C * a.q_stride;
       vp += C * a.v_stride;
       xp += 3 * kTriFrags * kFrag;
-      pp += 2 * kTriFrags * kFrag;
+      pp += 3 * kTriFrags * kFrag;
       gp += kGates;
       if (c + 2 == a.Nc) offsets(c + 1);
       request();
@@ -480,10 +473,10 @@ template <int KP, int NG, bool KEEP> struct TokensLds {
   using Keys = KeyTile<KP, 4 * NG>;
   static constexpr int W = 16 * NG;
   static constexpr int k = 0, q = k + 2 * Keys::kElems, x = q + (KEEP ? 0 : Keys::kElems);
-  static constexpr int p = x + 3 * kTriFrags * kFrag, v = p + (KEEP ? 0 : 2 * kTriFrags * kFrag);
+  static constexpr int p = x + 3 * kTriFrags * kFrag, v = p + (KEEP ? 0 : 3 * kTriFrags * kFrag);
   static constexpr int gate = v + C * W, s = gate + 4 * kGates, r = s + 3 * W * KP;
   static constexpr int e = r + 3 * W * C, wr = e + 3 * W * C;
-  static constexpr int y = wr + (KEEP ? 0 : 2 * W * C), elems = y + (KEEP ? 0 : C * W);
+  static constexpr int y = wr + (KEEP ? 0 : 3 * W * C), elems = y + (KEEP ? 0 : C * W);
 };
 
 template <int KP, bool FULL, int NG, bool KEEP>
@@ -491,7 +484,7 @@ __device__ __forceinline__ void tokens_chain(const DeltaArgs& a, bf16* lds, int6
   using L = TokensLds<KP, NG, KEEP>;
   using Keys = typename L::Keys;
   constexpr int KS = KP / 32, KT = KP / 64, W = L::W, NW = 4 * NG;
-  constexpr int kKeyLoads = Keys::kLoads, kXLoads = (3 * kTriFrags + NW - 1) / NW, kPLoads = (2 * kTriFrags + NW - 1) / NW;
+  constexpr int kKeyLoads = Keys::kLoads, kTriLoads = (3 * kTriFrags + NW - 1) / NW;
 
   const int slices = (a.P + W - 1) / W;
   const int64_t bh = id / slices, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
@@ -520,7 +513,7 @@ __device__ __forceinline__ void tokens_chain(const DeltaArgs& a, bf16* lds, int6
   const bf16* qp = static_cast<const bf16*>(a.q) + b * a.T * a.q_stride + g * a.N;
   const bf16* vp = static_cast<const bf16*>(a.v) + b * a.T * a.v_stride + h * a.P + col0;
   const bf16* xp = a.inv + at0 * (3 * kTriFrags * kFrag) + wave * 512;
-  const bf16* pp = a.qk + at0 * (2 * kTriFrags * kFrag) + wave * 512;
+  const bf16* pp = a.qk + at0 * (3 * kTriFrags * kFrag) + wave * 512;
   const float* gp = a.gate + at0 * kGates;
   const bool all_cols = a.P - col0 >= W;
   auto request_k = [&](int half) {
@@ -588,8 +581,8 @@ __device__ __forceinline__ void tokens_chain(const DeltaArgs& a, bf16* lds, int6
       for (int t = 0; t < KT; ++t) *reinterpret_cast<f32x4*>(kept ? state_at + key[t] : park) = st[t];
       state_at += cols * KP;
     } else {
-      request_evenly<2 * kTriFrags, NW>(pp, mine + 2 * L::p, wave, lane);
-      pp += 2 * kTriFrags * kFrag;
+      request_evenly<3 * kTriFrags, NW>(pp, mine + 2 * L::p, wave, lane);
+      pp += 3 * kTriFrags * kFrag;
     }
     // past the last chunk that one again, to where no one reads any more
     if (c + 1 < a.Nc) {
@@ -621,9 +614,8 @@ __device__ __forceinline__ void tokens_chain(const DeltaArgs& a, bf16* lds, int6
 #pragma unroll
           for (int o = 0; o < 2; ++o) ks[o] = mma(kf[o], sf[o].p[i], ks[o]);
           if constexpr (!KEEP)
-            if (i < 2)
 #pragma unroll
-              for (int o = 0; o < 2; ++o) qs[o] = mma(qf[o], sf[o].p[i], qs[o]);
+            for (int o = 0; o < 2; ++o) qs[o] = mma(qf[o], sf[o].p[i], qs[o]);
         }
       }
       const f32x4 gb = gates(kBeta), gr = gates(kRight);
@@ -634,7 +626,7 @@ __device__ __forceinline__ void tokens_chain(const DeltaArgs& a, bf16* lds, int6
       store_split4<3>(lds + L::r + put_t, W * C, rs);
       if constexpr (!KEEP) y = gates(kOut) * (qs[0] + qs[1]);
     }
-    landed<KEEP ? KT + kKeyLoads + 1 : 1 + kPLoads + kKeyLoads + 1>();
+    landed<KEEP ? KT + kKeyLoads + 1 : 1 + kTriLoads + kKeyLoads + 1>();
     request_qv();
     // the writes
     {
@@ -646,7 +638,7 @@ __device__ __forceinline__ void tokens_chain(const DeltaArgs& a, bf16* lds, int6
       ws += ws2;
       store_split4<3>(lds + L::e + put_t, W * C, ge * ws);
       if constexpr (!KEEP) {
-        store_split4<2>(lds + L::wr + put_t, W * C, ws);
+        store_split4<3>(lds + L::wr + put_t, W * C, ws);
       } else {
         *reinterpret_cast<f32x4*>(write_at) = ws;
         if (kept) write_at += cols * C;
@@ -676,10 +668,10 @@ __device__ __forceinline__ void tokens_chain(const DeltaArgs& a, bf16* lds, int6
     }
     // outputs
     if constexpr (!KEEP) {
-      const bf16* const lp = lds + L::p + lower_frag(w, 0) * (2 * kFrag) + lane * 8;
+      const bf16* const lp = lds + L::p + lower_frag(w, 0) * (3 * kFrag) + lane * 8;
       f32x4 y2 = {0, 0, 0, 0};
-      y = mma(load_planes<2>(lp, kFrag), load_planes<2>(lds + L::wr + get_t[0], W * C), y);
-      if (w >= 2) y2 = mma(load_planes<2>(lp + 2 * kFrag, kFrag), load_planes<2>(lds + L::wr + get_t[1], W * C), y2);
+      y = mma(load_planes<3>(lp, kFrag), load_planes<3>(lds + L::wr + get_t[0], W * C), y);
+      if (w >= 2) y2 = mma(load_planes<3>(lp + 3 * kFrag, kFrag), load_planes<3>(lds + L::wr + get_t[1], W * C), y2);
       // to rows of the output through LDS; only this wavefront touches these
       bf16* const out = lds + L::y + wave * 256;
 #pragma unroll
@@ -691,7 +683,7 @@ __device__ __forceinline__ void tokens_chain(const DeltaArgs& a, bf16* lds, int6
       bf16* const to = static_cast<bf16*>(a.y) + (b * a.T + c * C + 16 * w + tok) * (a.H * a.P) + h * a.P + col0 + 16 * n + part;
       *reinterpret_cast<uint4*>(in ? to : reinterpret_cast<bf16*>(park)) = val;
     }
-    landed<KEEP ? 1 + kXLoads : kXLoads + 1>();
+    landed<KEEP ? 1 + kTriLoads : kTriLoads + 1>();
   }
   if (!KEEP && a.state && col_in) {
 #pragma unroll

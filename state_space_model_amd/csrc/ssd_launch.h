@@ -213,7 +213,7 @@ struct DeltaArgs {
   float* gate;              // [4,C] factors of the tokens' rows (ssd_delta.hip)
   float* whole;             // decay over the chunk
   __bf16* inv;              // (1 + L)^-1, fragments of three planes
-  __bf16* qk;               // decayed q k^T, fragments (the gradients: of its transpose, three planes)
+  __bf16* qk;               // decayed q k^T, fragments of three planes (the gradients: of its transpose)
   void* park;               // [64] float: stores of tokens past the end go here, nothing reads it
   // the gradients (P16: P rounded up to 16; KP: N rounded up to 64)
   const void* dy;           // [Bt,T,H,P] io
@@ -241,7 +241,7 @@ constexpr int kDeltaMaxP = 256;   // value sizes: multiples of 8 up to here
 
 // Bytes of the scan's workspace and of its gradients'; with `ws` they are laid
 // out there.
-size_t delta_workspace(DeltaArgs& a, bool io_bf16, bool grads, char* ws);
+size_t delta_workspace(DeltaArgs& a, bool grads, char* ws);
 hipError_t launch_delta_matrices(const DeltaArgs& a, bool io_bf16, hipStream_t stream);  // the gradients' first part
 hipError_t launch_delta_scan_backward(const DeltaArgs& a, bool io_bf16, hipStream_t stream);
 hipError_t launch_delta_scan(const DeltaArgs& a, bool io_bf16, hipStream_t stream);
