@@ -678,10 +678,12 @@ typedef struct {
  * state as it is: batches of unequal lengths are padded with such tokens.
  *
  * Computed in chunks of 64 tokens.  States, writes and decays are float32 for
- * both io types; a bfloat16 y is rounded once.  A NaN or an infinity in a token
- * of q, k, v, dt or beta reaches the outputs of its chunk, earlier tokens of
- * the chunk included, and of later ones; no other head that does not share it
- * and no other batch row.  The bits of a sequence do not depend on what else is in
+ * both io types; a bfloat16 y is rounded once.  A NaN in a token of q, k, v,
+ * dt or beta, or an infinity in q, k or v, reaches the outputs of its chunk,
+ * which may include earlier tokens of the chunk, and of later ones; no head that
+ * does not share it and no other batch row.  A NaN in dt is not clipped to a
+ * bound.  An infinite dt is an ordinary gate, with dt_softplus one that keeps (-inf) or
+ * forgets (inf) everything, and so is an infinite beta with beta_sigmoid.  The bits of a sequence do not depend on what else is in
  * its batch; in bfloat16 they depend on the batch's size through Bt H ceil(P/32)
  * alone, where up to 256 and more (the gradients: 128) sum in different orders.
  * Bt H ceil(T/64) and Bt H ceil(P/16) below 2^24 and strides up to 2^25 - 512

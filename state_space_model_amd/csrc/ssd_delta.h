@@ -188,6 +188,13 @@ __device__ __forceinline__ f32x4 mma16(f32x4 a, f32x4 b, f32x4 acc) {
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// Delta of z = dt + dt_bias.  The clip's minimum and maximum return the other
+// operand of a NaN, which would make it a bound, an ordinary gate: it stays a NaN.
+__device__ __forceinline__ float rate_of(const DeltaArgs& a, float z) {
+  const float d = delta_of(z, a.softplus, a.dt_min, a.dt_max);
+  return z == z ? d : z;
+}
+
 // 1 / (1 + e^-z), also for -infinity (0)
 __device__ __forceinline__ float sigmoid_of(float z) {
   return 1.0f / (1.0f + exp2_of(-z * kLog2e));

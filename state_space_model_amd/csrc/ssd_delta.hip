@@ -84,7 +84,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 4 : 2) void k_delta_pre
     const bool in = lane < left;
     const int64_t th = (row0 + (in ? lane : 0)) * a.H + h;
     const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
-    const float d = delta_of(a.dt[th] + bias, a.softplus, a.dt_min, a.dt_max);
+    const float d = rate_of(a, a.dt[th] + bias);
     double sum = (double)d * (double)a.A[h] * 1.4426950408889634;
     sum = in ? (sum < -1e5 ? -1e5 : sum) : 0.0;
     for (int off = 1; off < 64; off <<= 1) {
@@ -320,7 +320,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_step(DeltaArgs a) {
   const float rk = a.unit ? 1.0f / sqrtf(kk + a.norm_eps) : 1.0f;
   const float rq = a.scale * (a.unit ? 1.0f / sqrtf(qq + a.norm_eps) : 1.0f);
   const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
-  const float d = delta_of(a.dt[bh] + bias, a.softplus, a.dt_min, a.dt_max);
+  const float d = rate_of(a, a.dt[bh] + bias);
   const float alpha = expf(d * a.A[h]);
   const float beta = a.sigmoid ? sigmoid_of(a.beta[bh]) : a.beta[bh];
   IO* yr = static_cast<IO*>(a.y) + bh * a.P;

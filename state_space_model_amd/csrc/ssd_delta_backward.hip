@@ -1094,8 +1094,8 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_gra
   const int64_t th = (row0 + (in ? lane : 0)) * a.H + h;
   const float zt = a.dt[th] + (a.dt_bias ? a.dt_bias[h] : 0.0f);
   const float pre = a.softplus ? softplus_of(zt) : zt;   // as in delta_of: the same clip decision
-  const float rate = fminf(fmaxf(pre, a.dt_min), a.dt_max);
-  float slope = pre >= a.dt_min && pre <= a.dt_max ? a.A[h] : 0.0f;
+  const float rate = rate_of(a, zt);
+  float slope = pre < a.dt_min || pre > a.dt_max ? 0.0f : a.A[h];   // a NaN is not clipped
   if (a.softplus) slope *= sigmoid_of(zt);
   const float ddt = in ? dg * slope : 0.0f;
   const float sum_a = wave_sum64(in ? dg * rate : 0.0f), sum_b = wave_sum64(ddt);
