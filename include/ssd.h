@@ -719,6 +719,7 @@ ssd_status ssd_delta_step(const ssd_delta_desc* desc, float* state, const void* 
  *        be disjoint columns of one tensor with one stride.  dq and dk are
  *        summed over the heads of a group and include the normalisation.
  *   ddt, dbeta [Bt,T,H], dA [H] f32 (written); ddt is zero where Delta was clipped
+ *        (a token whose infinite Delta forgets everything adds nothing to dA)
  *   ddt_bias [H] f32, dinitial_state [Bt,H,P,N] f32 (written) or NULL
  *   workspace: at least ssd_delta_scan_backward_workspace_bytes(desc),
  *        256-byte aligned; it holds the states and their gradients at every

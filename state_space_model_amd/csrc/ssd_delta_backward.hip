@@ -1098,7 +1098,8 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_gra
   float slope = pre < a.dt_min || pre > a.dt_max ? 0.0f : a.A[h];   // a NaN is not clipped
   if (a.softplus) slope *= sigmoid_of(zt);
   const float ddt = in ? dg * slope : 0.0f;
-  const float sum_a = wave_sum64(in ? dg * rate : 0.0f), sum_b = wave_sum64(ddt);
+  // an infinite rate forgets all: dg is 0, and so is what A's gradient has of it (x e^-x at infinity)
+  const float sum_a = wave_sum64(in && dg != 0.0f ? dg * rate : 0.0f), sum_b = wave_sum64(ddt);
   if (in) {
     const float beta = s_b[lane];
     a.ddt[th] = ddt;

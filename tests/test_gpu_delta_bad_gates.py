@@ -1,5 +1,5 @@
 """What is not finite among the gated delta rule's gates and values: a NaN reaches everything that
-depends on it and nothing else."""
+depends on it and nothing else; infinite gates are gates like large ones."""
 import math
 
 import pytest
@@ -108,3 +108,38 @@ def test_nan_in_a_step(io, name, mode):
         hit = torch.zeros_like(got, dtype=torch.bool)
         hit[rows, HEAD, cols] = True
         assert torch.equal(got[~hit], ref[~hit])
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("kind", KINDS, ids=str)
+def test_infinite_gates_are_gates(kind, mode):
+    """The bits of large finite gates: outputs, states, and every gradient, A's among them (the
+    gradient of a decay that forgets everything is 0, however large the rate)."""
+    need_gpu()
+    import state_space_model_amd as ssd
+    announce(f"delta infinite gates {kind} {mode}")
+    io, Bt, H, G, P = kind
+    x, u = make(81, Bt, T, H, G, P, N, io=io, bias=mode == "rates")
+    kw = MODES[mode]
+    if mode == "logs":
+        x["A"], x["dt"] = torch.ones(H), -x["dt"].abs()
+    dy, dfinal = cotangents(8, x)
+    out = []
+    for rate, write in ((math.inf, math.inf), (1e30, 1e4)):
+        x["dt"][:, 5::31] = -rate                  # keeps all; as a logarithm forgets all
+        if mode == "rates":
+            x["dt"][:, 11::37] = rate
+            x["dt"][0, 100:] = -rate
+        x["beta"][:, 3::17] = write
+        x["beta"][:, 7::19] = -write
+        d = on_device(x, u)
+        y, final = ssd.ssd_delta_scan(*args(d), **options(d), **kw)
+        grads = ssd.ssd_delta_scan_backward(*args(d), **options(d), **kw, dy=dy.cuda(), dfinal_state=dfinal.cuda())
+        state = d["h0"].clone()
+        t = 11 if mode == "rates" else 5
+        step = ssd.ssd_delta_step(state, d["q"][:, t], d["k"][:, t], d["v"][:, t], d["dt"][:, t].contiguous(),
+                                  d["A"], d["beta"][:, t].contiguous(), dt_bias=d["dt_bias"], **kw)
+        out.append({"y": y, "final": final, "step": step, "state": state, **grads})
+    for n in out[0]:
+        assert out[0][n].isfinite().all(), n
+        assert torch.equal(out[0][n], out[1][n]), n
