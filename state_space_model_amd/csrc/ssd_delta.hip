@@ -359,7 +359,8 @@ __global__ __launch_bounds__(256, 2) void k_delta_columns(DeltaArgs a) {
   columns_chain<KP, FULL, false>(a, lds, xcd_remap(blockIdx.x, gridDim.x));
 }
 
-// GRADS: what the gradients' chains need of a chunk, and no chain
+// GRADS: what the gradients' chains need of a chunk, and no chain.  Nothing is
+// launched behind a launch that failed: it would read what that one did not write.
 template <bool GRADS>
 hipError_t launch_scan(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
   return with_keys(a.N, io_bf16, [&](auto io, auto kp, auto full) {
@@ -368,7 +369,8 @@ hipError_t launch_scan(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
     constexpr bool FULL = decltype(full)::value;
     const unsigned chunks = (unsigned)(a.Bt * a.H * a.Nc);
     hipLaunchKernelGGL((k_delta_prep<IO, KP, FULL, GRADS>), dim3(chunks), dim3(kThreads), 0, stream, a);
-    if constexpr (GRADS) return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    if (GRADS || e != hipSuccess) return e;
     if constexpr (sizeof(IO) == 2) {
       return chain_of(
           a, 1,

@@ -1189,8 +1189,9 @@ hipError_t launch_grads(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
     constexpr int KP = decltype(kp)::value;
     constexpr bool FULL = decltype(full)::value;
     const unsigned chunks = (unsigned)(a.Bt * a.H * a.Nc);
+    hipError_t e;   // nothing is launched behind a launch that failed
     if constexpr (sizeof(IO) == 2) {
-      (void)chain_of(
+      e = chain_of(
           a, 2,
           [&](auto ng, unsigned groups) {
             hipLaunchKernelGGL((k_delta_both_tokens<KP, FULL, ng.value>), dim3(groups), dim3(256 * ng.value), 0, stream,
@@ -1202,13 +1203,17 @@ hipError_t launch_grads(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
     } else {
       hipLaunchKernelGGL((k_delta_both_chains<IO, KP, FULL>), dim3((unsigned)(2 * a.Bt * a.H * ((a.P + 15) / 16))),
                          dim3(kThreads), 0, stream, a);
+      e = hipGetLastError();
     }
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL((k_delta_grads<IO, KP, FULL>), dim3(chunks), dim3(kThreads), 0, stream, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
     if (a.H != a.G) {
       constexpr int per = kThreads / (KP / 4);
       const int64_t rows = 2 * a.Bt * a.T * a.G;
       hipLaunchKernelGGL((k_delta_unit_grads<IO, KP / 4>), dim3((unsigned)((rows + per - 1) / per)), dim3(kThreads),
                          0, stream, a);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     hipLaunchKernelGGL(k_delta_head_grads, dim3((unsigned)a.H), dim3(kThreads), 0, stream, a);
     return hipGetLastError();
