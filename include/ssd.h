@@ -729,7 +729,7 @@ ssd_status ssd_delta_step(const ssd_delta_desc* desc, float* state, const void* 
  * (no atomics).  Outputs may not overlap any input, the workspace or each
  * other.  batch == 0 or seqlen == 0 writes zeros to dA and ddt_bias, and
  * dfinal_state (or zeros) to dinitial_state.  Sizes as ssd_delta_scan, but
- * 2 Bt H ceil(P/16) below 2^24, and 2 Bt T G below 2^27.
+ * 2 Bt H ceil(P/16) below 2^24, and 2 Bt T G up to 2^27 - 8.
  */
 size_t ssd_delta_scan_backward_workspace_bytes(const ssd_delta_desc* desc);
 ssd_status ssd_delta_scan_backward(const ssd_delta_desc* desc, const void* q, const void* k,

@@ -20,6 +20,9 @@ inline ssd_status status_of(hipError_t e) { return e == hipSuccess ? SSD_OK : SS
 // workgroups of 256 threads: a grid's threads count in 32 bits
 constexpr int64_t kMaxGroups = (1 << 24) - 1;
 
+// of any length, also where a sum with it would overflow
+int64_t chunks_of(int64_t tokens) { return tokens / kDeltaChunk + (tokens % kDeltaChunk != 0); }
+
 // bytes that tensors and the spans of strided ones take
 struct Sizes {
   int64_t q, k, v, y, gates, heads, state;
@@ -54,7 +57,7 @@ ssd_status check(const ssd_delta_desc* d, bool step, bool grads, Sizes* s) {
   const int64_t gn = d->ngroups * d->dstate, hp = d->nheads * d->headdim;
   if (d->q_stride < gn || d->k_stride < gn || d->v_stride < hp) return SSD_ERR_SHAPE;
   if (grads && (d->dq_stride < gn || d->dk_stride < gn || d->dv_stride < hp)) return SSD_ERR_SHAPE;
-  const int64_t chunks = step ? 1 : (d->seqlen / kDeltaChunk + (d->seqlen % kDeltaChunk != 0));
+  const int64_t chunks = step ? 1 : chunks_of(d->seqlen);
   int64_t bh = 0, groups = 0, tokens = 0, state = 0, y = 0, gates = 0;
   if (!mul_ok(d->batch, d->nheads, &bh) || !mul_ok(bh, chunks, &groups) || groups > kMaxGroups ||
       !mul_ok(bh, (grads ? 2 : 1) * ((d->headdim + 15) / 16), &groups) || groups > kMaxGroups ||
@@ -67,9 +70,9 @@ ssd_status check(const ssd_delta_desc* d, bool step, bool grads, Sizes* s) {
                 !span_of(tokens, gn, d->dk_stride, es, &s->dk) ||
                 !span_of(tokens, hp, d->dv_stride, es, &s->dv)))
     return SSD_ERR_UNSUPPORTED;
-  // the gradients' workspace, in bytes (a bound), and a wavefront's half for each of 2 Bt T G rows
+  // the gradients' workspace, in bytes (a bound), and 2 Bt T G rows, up to 32 threads for each
   int64_t rows = 0, ws = 0;
-  if (grads && (!mul_ok(tokens, 2 * d->ngroups, &rows) || rows >= (int64_t{1} << 27) ||
+  if (grads && (!mul_ok(tokens, 2 * d->ngroups, &rows) || rows > (int64_t{1} << 27) - 8 ||
                 !mul_ok(bh * chunks, 8 * ((d->headdim + 8) * 128 + 64 * (d->headdim + d->dstate + 80)), &ws) ||
                 ws > INT64_MAX / 16))
     return SSD_ERR_UNSUPPORTED;
@@ -119,7 +122,7 @@ DeltaArgs args_of(const ssd_delta_desc* d, const void* q, const void* k, const v
   a.q_stride = d->q_stride; a.k_stride = d->k_stride; a.v_stride = d->v_stride;
   a.dt = dt; a.dt_bias = dt_bias; a.A = A; a.beta = beta;
   a.Bt = d->batch; a.T = d->seqlen; a.H = d->nheads; a.G = d->ngroups;
-  a.Nc = (d->seqlen + kDeltaChunk - 1) / kDeltaChunk;
+  a.Nc = chunks_of(d->seqlen);
   a.P = (int32_t)d->headdim; a.N = (int32_t)d->dstate;
   a.softplus = d->dt_softplus ? 1 : 0; a.sigmoid = d->beta_sigmoid ? 1 : 0;
   a.unit = d->qk_norm ? 1 : 0;

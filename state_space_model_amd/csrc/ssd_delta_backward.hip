@@ -1116,7 +1116,8 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_gra
 // of 32 heads of 128 in pairs 46 us, 4.4 TB/s.
 template <typename IO, int NL>
 __global__ __launch_bounds__(kThreads) void k_delta_unit_grads(DeltaArgs a) {
-  // rows below 2^27 (checked by the caller): divisions of 32 bits, which cost a fifth
+  // rows up to 2^27 - 8 (checked by the caller: a grid's threads count in 32 bits):
+  // divisions of 32 bits (64-bit ones cost a fifth)
   const uint32_t id = (uint32_t)(((int64_t)blockIdx.x * kThreads + threadIdx.x) / NL);
   const uint32_t rows = (uint32_t)(a.Bt * a.T * a.G);
   const bool in = id < 2 * rows;

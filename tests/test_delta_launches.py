@@ -11,7 +11,7 @@ import pytest
 import state_space_model_amd as ssd
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-OK, HIP = 0, 7
+OK, UNSUP, HIP = 0, 5, 7
 
 SHIM = r"""
 #include <stdint.h>
@@ -45,7 +45,7 @@ class Desc(ctypes.Structure):
                 + [(f"f{i}", ctypes.c_float) for i in range(4)])
 for fn, n in (("ssd_delta_scan_workspace_bytes", 0), ("ssd_delta_scan_backward_workspace_bytes", 0)):
     getattr(lib, fn).restype = ctypes.c_size_t
-at = lambda i: ctypes.c_void_p((1 << 45) + (i << 38))      # never read: nothing is launched
+at = lambda i: ctypes.c_void_p((1 << 45) + (i << 42))      # never read: nothing is launched
 out = []
 for name, io, Bt, T, H, G, P, K in json.loads(sys.argv[3]):
     d = Desc(Bt, T, H, P, K, G, G * K, G * K, H * P, G * K, G * K, H * P, io, 1, 1, 1, 0.0, float("inf"), 1e-6, 1.0)
@@ -102,3 +102,20 @@ def test_a_failed_launch_is_the_status(answers):
         for i, (code, count) in enumerate(failed):
             assert code == HIP, (call, i)
             assert count == i % len(grids) + 1, (call, i)     # nothing reads what a failed launch did not write
+
+
+# the largest sizes: rows of the keys' gradients up to 2^27 - 8 (eight to a workgroup of 256 threads,
+# and threads count in 32 bits), workgroups below 2^24
+LARGE = [("back", 0, 1, 22369621, 6, 3, 8, 128, UNSUP), ("back", 1, 1, 22369621, 6, 3, 8, 72, UNSUP),
+         ("back", 1, 1, 33554431, 4, 2, 8, 128, UNSUP), ("back", 1, 1, 33554430, 4, 2, 8, 128, OK),
+         ("back", 0, 1, 33554430, 4, 2, 8, 64, OK), ("scan", 1, 1, 64 * 4194303, 4, 4, 256, 128, OK),
+         ("scan", 0, 4194303, 64, 4, 1, 16, 128, OK), ("step", 1, 4194303, 1, 4, 1, 16, 128, OK),
+         ("step", 0, 1, 1, 2097151, 1, 128, 128, OK)]
+
+
+def test_grids_keep_to_the_limit(answers):
+    for call, (status, grids, failed) in zip(LARGE, answers([c[:-1] for c in LARGE])):
+        assert status == call[-1], (call, status)
+        assert bool(grids) == (status == OK), call
+        for groups, threads in grids:
+            assert 0 < groups * threads < 1 << 32, (call, groups, threads)
