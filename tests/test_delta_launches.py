@@ -110,7 +110,7 @@ LARGE = [("back", 0, 1, 22369621, 6, 3, 8, 128, UNSUP), ("back", 1, 1, 22369621,
          ("back", 1, 1, 33554431, 4, 2, 8, 128, UNSUP), ("back", 1, 1, 33554430, 4, 2, 8, 128, OK),
          ("back", 0, 1, 33554430, 4, 2, 8, 64, OK), ("scan", 1, 1, 64 * 4194303, 4, 4, 256, 128, OK),
          ("scan", 0, 4194303, 64, 4, 1, 16, 128, OK), ("step", 1, 4194303, 1, 4, 1, 16, 128, OK),
-         ("step", 0, 1, 1, 2097151, 1, 128, 128, OK)]
+         ("step", 0, 8191, 1, 256, 1, 128, 128, OK)]
 
 
 def test_grids_keep_to_the_limit(answers):
