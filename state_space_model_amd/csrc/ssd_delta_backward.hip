@@ -1045,8 +1045,11 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_gra
     }
     const float ru = 1.0f / sqrtf(sum_q(uu) + a.norm_eps), rk2 = rec.x * rec.x;
     const float tu = a.unit ? ru * sum_q(ud) * ru : 0.0f, tk = a.unit ? rk2 * sum_q(kd) : 0.0f;
-    IO* const to_q = static_cast<IO*>(a.dq) + my_row * a.dq_stride + g * a.N;
-    IO* const to_k = static_cast<IO*>(a.dk) + my_row * a.dk_stride + g * a.N;
+    int own_row = own;   // my_row formed again: kept over the slices it would spill
+    asm("" : "+v"(own_row));
+    const int64_t row = row0 + (own_row < left ? own_row : 0);
+    IO* const to_q = static_cast<IO*>(a.dq) + row * a.dq_stride + g * a.N;
+    IO* const to_k = static_cast<IO*>(a.dk) + row * a.dk_stride + g * a.N;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
       const int key = 16 * kt + 4 * q, o = own * KST + key;
