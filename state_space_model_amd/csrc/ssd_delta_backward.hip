@@ -1104,9 +1104,10 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 2 : 1) void k_delta_gra
   // an infinite rate forgets all: dg is 0, and so is what A's gradient has of it (x e^-x at infinity)
   const float sum_a = wave_sum64(in && dg != 0.0f ? dg * rate : 0.0f), sum_b = wave_sum64(ddt);
   if (in) {
-    const float beta = s_b[lane];
+    // the logistic's slope as a product: 1 - b would cancel where b is close to 1
+    const float zb = a.beta[th];
     a.ddt[th] = ddt;
-    a.dbeta[th] = s_beta[lane] * (a.sigmoid ? beta * (1.0f - beta) : 1.0f);
+    a.dbeta[th] = s_beta[lane] * (a.sigmoid ? sigmoid_of(zb) * sigmoid_of(-zb) : 1.0f);
   }
   if (lane == 0) {
     a.part_h[2 * at] = sum_a;
