@@ -9,6 +9,9 @@ import sys
 import pytest
 
 import state_space_model_amd as ssd
+import test_gpu_delta_chains
+import test_gpu_delta_pairs
+import test_gpu_delta_terms as terms
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 OK, UNSUP, HIP = 0, 5, 7
@@ -119,3 +122,21 @@ def test_grids_keep_to_the_limit(answers):
         assert bool(grids) == (status == OK), call
         for groups, threads in grids:
             assert 0 < groups * threads < 1 << 32, (call, groups, threads)
+
+
+def test_every_kind_of_chain_is_tested(answers):
+    """The launches of the GPU tests' sizes: a workgroup of 256 threads to 16 value columns, of 512 to
+    32, or of 256 to 64 (bfloat16)."""
+    kinds = {"alone": (256, 16), "pairs": (512, 32), "owned": (256, 64)}
+    asked = [("back", s, k) for k, shapes in (("alone", terms.ALONE), ("pairs", terms.PAIRS), ("owned", terms.OWNED))
+             for s in shapes]
+    for (Bt, H, G, P), back in zip(test_gpu_delta_chains.KINDS + test_gpu_delta_pairs.KINDS,
+                                   ("alone", "owned", "owned", "pairs", "pairs")):
+        asked.append(("back", (Bt, 130, H, G, P, 40), back))
+    for (Bt, H, G, P), scan in zip(test_gpu_delta_chains.KINDS, ("alone", "pairs", "owned")):
+        asked.append(("scan", (Bt, 130, H, G, P, 40), scan))
+    for (name, shape, kind), (_, grids, _) in zip(asked, answers([(n, 1, *s) for n, s, _ in asked])):
+        Bt, T, H, G, P, N = shape
+        threads, columns = kinds[kind]
+        ways = 2 if name == "back" else 1
+        assert grids[1] == [ways * Bt * H * ((P + columns - 1) // columns), threads], (name, shape, kind)
