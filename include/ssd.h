@@ -681,11 +681,13 @@ typedef struct {
  * both io types; a bfloat16 y is rounded once.  A NaN in a token of q, k, v,
  * dt or beta, or an infinity in q, k or v, reaches the outputs of its chunk,
  * which may include earlier tokens of the chunk, and of later ones; no head that
- * does not share it and no other batch row.  A NaN in dt is not clipped to a
- * bound.  An infinite dt is an ordinary gate, with dt_softplus one that keeps (-inf) or
- * forgets (inf) everything, and so is an infinite beta with beta_sigmoid.  The bits of a sequence do not depend on what else is in
- * its batch; in bfloat16 they depend on the batch's size through Bt H ceil(P/32)
- * alone, where up to 256 and more (the gradients: 128) sum in different orders.
+ * does not share it and no other batch row (float32 magnitudes past 3.39e38,
+ * bfloat16's largest, count as infinite).  A NaN in dt is not clipped to a
+ * bound.  An infinite dt is an ordinary gate (a = 0 or 1), and with beta_sigmoid
+ * an infinite beta (b = 0 or 1).  The bits of a sequence do not depend on what
+ * else is in its batch; in bfloat16 they depend on the batch's size through
+ * Bt H ceil(P/32) alone, where up to 256 and more (the gradients: 128) sum in
+ * different orders.
  * Bt H ceil(T/64) and Bt H ceil(P/16) below 2^24 and strides up to 2^25 - 512
  * elements, else SSD_ERR_UNSUPPORTED.
  */

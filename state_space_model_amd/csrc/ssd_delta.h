@@ -3,17 +3,21 @@
 // the bfloat16 matrix cores, and the layout of the chunks' workspace.
 //
 // Products.  A float32 number is the exact sum of three bfloat16 numbers of 8
-// significant bits each ("planes": h, m, l).  A product of two such
+// significant bits each ("planes": h, m, l), where none of them leaves bfloat16's
+// range: a magnitude past its largest number, 3.39e38, becomes infinite, and below
+// 2^-110 the last bits may be lost.  A product of two such
 // operands is formed from the plane products whose indices add to at most 2
-// (hh, hm, mh, hl, mm, lh; the rest is below 2^-26 of it), each exact in the
+// (hh, hm, mh, hl, mm, lh; ml and lm, the most of the rest, are 2^-8 2^-17 of it
+// each: 2^-24, half a step of float32), each exact in the
 // matrix core and accumulated in float32: six v_mfma_f32_16x16x32_bf16 (16
 // cycles each) where v_mfma_f32_16x16x4_f32 takes eight of 32 cycles.  An
 // operand that is bfloat16 already is one plane, and its product with a
 // float32 operand is exact up to the sum with three.  So states, writes, outputs
 // and all gradients keep float32 accuracy for both io types, and a bfloat16
 // output is rounded once, at its store.  (Outputs from two planes of the state,
-// the writes and q k^T would be a tenth faster, and off by up to 2^-15 of the terms'
-// magnitudes.)
+// the writes and q k^T would take a tenth less, 225 against 245 us for 4096 tokens
+// of 80 heads and 3210 against 3640 for 8 x 16384 of 64, and be off by up to 2^-15 of
+// the terms' magnitudes.)
 #pragma once
 
 #include <type_traits>
@@ -474,14 +478,16 @@ __device__ __forceinline__ void lds_free() { asm volatile("s_waitcnt lgkmcnt(0)\
 // unit's LDS), or a chain of wavefronts that own 16 each (columns()).  Sharing
 // makes a step as short as it gets and is taken while every chain has a unit to
 // itself; owning needs less than half the work of LDS and VALU for as many
-// columns, and two workgroups share a unit.  bfloat16, 128 keys, shared in pairs
-// against owned: 4096 tokens of 80 heads of 64 values (160 pairs) 171 against 258
-// us, 136 heads (272) 345 against 328; 8 x 16384 tokens of 64 heads (1024) 2700
-// against 1800; the gradients' chains of 36 heads of 128 values (288) 354 against
-// 392, where the rule loses a tenth.
+// columns, and two workgroups share a unit.  bfloat16, 4096 tokens, shared in pairs
+// against owned, in us: scans with 128 keys, 160 pairs 209 against 336, 256 pairs
+// 257 / 356, 272 384 / 359, 320 410 / 377, 384 440 / 406; with 64 keys, 256 177 / 293,
+// 272 310 / 297; 8 x 16384 tokens of 64 heads (1024 pairs) 3120 / 2145.  The gradients'
+// chains with 128 keys, 256 pairs 285 / 390, 288 353 / 410, 320 369 / 425, 384 447 / 438,
+// 512 486 / 455; with 64, 256 223 / 311, 288 274 / 322: between 256 and 384 pairs the rule
+// loses up to a seventh there.
 //
 // `ways`: chains that one launch runs for every column (the gradients' both of 32
-// heads: 128 and 187 us one after the other, 265 us together in pairs)
+// heads: 128 and 187 us one after the other, 265 to 285 us together in pairs)
 template <typename F, typename G>
 hipError_t chain_of(const DeltaArgs& a, int ways, F&& tokens, G&& columns) {
   const int64_t heads = ways * a.Bt * a.H, groups = heads * ((a.P + 15) / 16), pairs = heads * ((a.P + 31) / 32);

@@ -37,11 +37,11 @@ namespace {
 // GRADS: for the gradients, whose chain from the last chunk needs both matrices
 // transposed and no output.
 //
-// Bound by its instructions: 8 x 16384 tokens of 64 heads in bfloat16 1440 us (the
-// vector units busy half of it, 3.2 TB/s), 4096 tokens of 80 heads with keys of
-// their own 64 us (5.0 TB/s).  bfloat16 takes 96 registers, five workgroups to a
-// compute unit (held to the 80 of six it spills: 1740 and 79 us); float32's planes
-// need more.
+// Bound by its instructions and, with few heads to a key, by what it stores: 8 x
+// 16384 tokens of 64 heads in bfloat16 1540 us (3.6 TB/s), 4096 tokens of 80 heads
+// with keys of their own 68 us (5.3 TB/s).  bfloat16 takes 96 registers, five
+// workgroups to a compute unit (held to the 80 of six it spills and takes a fifth
+// more); float32's planes need more.
 template <typename IO, int KP, bool FULL, bool GRADS>
 __global__ __launch_bounds__(kThreads, sizeof(IO) == 2 ? 4 : 2) void k_delta_prep(DeltaArgs a) {
   constexpr int PI = Planes<IO>::in;

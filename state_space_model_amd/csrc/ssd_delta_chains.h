@@ -256,11 +256,11 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, bf16* lds, int64_t id)
 // registers (ssd_delta.h); what the wavefronts share, k, q and the two
 // matrices of a chunk, lands in LDS, half of a compute unit's, so that one
 // workgroup computes while another waits for its chunk (8 x 16384 tokens of 64
-// heads of 64 x 128: 1780 us; one workgroup a unit that requests a chunk ahead
-// 2270).  A chunk takes a wavefront 182 matrix instructions (keys of 128), 2912
-// cycles, and as many cycles of vector instructions, most of them to split float32
-// into planes; that is what bounds it (the same chunk again and again, from the
-// L2: 13% less).
+// heads of 64 x 128: 2100 us; one workgroup a unit that requests a chunk ahead
+// takes a quarter more).  A chunk takes a wavefront 216 matrix instructions (keys of
+// 128), 3456 cycles, and about as many cycles of its 800 vector instructions, most
+// of them to split float32 into planes; that is what bounds it (the same chunk
+// again and again, from the L2: an eighth less).
 // ---------------------------------------------------------------------------
 template <int KP, int NW, bool KEEP> struct ColumnsLds {
   using Keys = KeyTile<KP, NW>;
@@ -464,10 +464,9 @@ __device__ __forceinline__ void columns_chain(const DeltaArgs& a, bf16* lds, int
 // Every wavefront makes the same requests, so that the counts that the waits
 // leave outstanding are constants.
 //
-// Bound by the step's length: 4096 tokens of 80 heads of 64 x 128 171 us, 2.7 us a
-// chunk in pairs (2.0 alone), of which the requests account for a fifth (none in
-// the loop: 135 us); the rest is three products that wait for each other through
-// LDS.
+// Bound by the step's length: 4096 tokens of 80 heads of 64 x 128 190 us, 3.0 us a
+// chunk in pairs, of which the requests account for a fifth; the rest is three
+// products that wait for each other through LDS.
 // ---------------------------------------------------------------------------
 template <int KP, int NG, bool KEEP> struct TokensLds {
   using Keys = KeyTile<KP, 4 * NG>;
