@@ -683,8 +683,8 @@ typedef struct {
  * which may include earlier tokens of the chunk, and of later ones; no head that
  * does not share it and no other batch row (float32 magnitudes past 3.39e38,
  * bfloat16's largest, count as infinite).  A NaN in dt is not clipped to a
- * bound.  An infinite dt is an ordinary gate (a = 0 or 1), and with beta_sigmoid
- * an infinite beta (b = 0 or 1).  The bits of a sequence do not depend on what
+ * bound.  An infinite dt is an ordinary gate (a = 0 or 1; A not 0), with beta_sigmoid
+ * an infinite beta too (b = 0 or 1).  The bits of a sequence do not depend on what
  * else is in its batch; in bfloat16 they depend on the batch's size through
  * Bt H ceil(P/32) alone, where up to 256 and more (the gradients: 128) sum in
  * different orders.
